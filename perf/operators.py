@@ -180,7 +180,7 @@ def _quantise(x, fmt):
     g = x.unflatten(-1, (-1, GROUP))
     hi, lo = g.amax(-1, keepdim=True), g.amin(-1, keepdim=True)
     if fmt == "q8":
-        d = torch.maximum(hi, -lo) / 127
+        d = torch.maximum(hi, -lo) / torch.full_like(hi, 127)  # (a division, not a product with 1/127)
     else:
         d = torch.where(hi >= -lo, hi, lo) / -8
     d = d.clamp(-65504, 65504).half()
