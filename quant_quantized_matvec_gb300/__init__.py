@@ -8,6 +8,10 @@ their dtype/shape/device, and pass raw pointers through.
     import quant_quantized_matvec_gb300 as kq
     y = kq.matvec(kq.Q4_K, W, rows, cols, x)          # x: [ntok, cols] f32
     kq.matvec_set([(kq.Q4_K, Wq, 4096, 6656, x, yq), ...])
+
+The rest of a decode step (decode.py, include/kq_decode.h): rope, the
+quantised KVCache with kv_append / kv_read / kv_move, tree_attention over
+it, and verify_tree for drafted tokens.
 """
 from __future__ import annotations
 
@@ -224,3 +228,18 @@ def device_error(clear: bool = True) -> bool:
     if st == KQ_ERR_CUDA:
         raise KQError(st, "kq_device_error")
     return st == KQ_ERR_TIMEOUT
+
+
+# The decode step's other operators; decode.py needs torch, which this module
+# only imports when a function that takes tensors is called.
+_DECODE = ("KV_F16", "KV_Q4", "KV_Q8", "KV_PAGE", "MAX_DRAFT", "KVCache", "KVBatch", "rope_table",
+           "rope", "kv_append", "kv_read", "kv_move", "tree_mask", "tree_attention",
+           "attention_workspace_bytes", "verify_tree")
+
+
+def __getattr__(name):
+    if name not in _DECODE:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import decode
+    globals().update((n, getattr(decode, n)) for n in _DECODE)
+    return globals()[name]

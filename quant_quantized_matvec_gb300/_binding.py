@@ -25,6 +25,11 @@ SYMBOLS = ("kq_block_bytes", "kq_matrix_bytes", "kq_matvec",
            "kq_version")
 
 
+# include/kq_decode.h
+DECODE_SYMBOLS = ("kq_kv_page_bytes", "kq_rope_table", "kq_rope", "kq_kv_append", "kq_kv_read",
+                  "kq_kv_move", "kq_tree_attention", "kq_attn_workspace_bytes", "kq_verify_tree")
+
+
 class KqMat(ctypes.Structure):
     """Mirror of `kq_mat` in include/kq.h."""
     _fields_ = [
@@ -35,6 +40,43 @@ class KqMat(ctypes.Structure):
         ("cols", ctypes.c_int64),
         ("x", ctypes.c_void_p),
         ("y", ctypes.c_void_p),
+    ]
+
+
+class KqKv(ctypes.Structure):
+    """Mirror of `kq_kv` in include/kq_decode.h."""
+    _fields_ = [
+        ("fmt", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("data", ctypes.c_void_p),
+        ("pages", ctypes.c_int64),
+    ]
+
+
+class KqBatch(ctypes.Structure):
+    """Mirror of `kq_batch` in include/kq_decode.h."""
+    _fields_ = [
+        ("nseq", ctypes.c_int32),
+        ("max_new", ctypes.c_int32),
+        ("ntok", ctypes.c_int64),
+        ("start", ctypes.c_void_p),
+        ("ctx", ctypes.c_void_p),
+        ("pages", ctypes.c_void_p),
+        ("max_pages", ctypes.c_int64),
+    ]
+
+
+class KqRopeScaling(ctypes.Structure):
+    """Mirror of `kq_rope_scaling` in include/kq_decode.h."""
+    _fields_ = [
+        ("kind", ctypes.c_int32),
+        ("orig", ctypes.c_int32),
+        ("factor", ctypes.c_double),
+        ("fast", ctypes.c_double),
+        ("slow", ctypes.c_double),
+        ("magnitude", ctypes.c_double),
     ]
 
 
@@ -96,6 +138,24 @@ def load(path: str | None = None):
         lib.kq_last_launch_count.restype = i32
         lib.kq_version.argtypes = []
         lib.kq_version.restype = i32
+        kv, batch = ctypes.POINTER(KqKv), ctypes.POINTER(KqBatch)
+        lib.kq_kv_page_bytes.argtypes = [i32, i32, i32]
+        lib.kq_kv_page_bytes.restype = i64
+        lib.kq_rope_table.argtypes = [i64, i32, ctypes.c_double,
+                                      ctypes.POINTER(KqRopeScaling), vp, vp]
+        lib.kq_rope.argtypes = [vp, i64, vp, i64, i64, i32, i32, vp, vp, i64, i32, i32, i32, vp]
+        lib.kq_kv_append.argtypes = [kv, batch, vp, i64, vp, i64, vp, vp, i64, i32, i32, vp]
+        lib.kq_kv_read.argtypes = [kv, batch, vp, vp, vp]
+        lib.kq_kv_move.argtypes = [kv, batch, vp, vp, vp]
+        lib.kq_attn_workspace_bytes.argtypes = [kv, batch, i32]
+        lib.kq_attn_workspace_bytes.restype = i64
+        lib.kq_tree_attention.argtypes = [kv, batch, vp, i64, i32, vp, ctypes.c_float, vp, vp, i64,
+                                          vp]
+        lib.kq_verify_tree.argtypes = [i32, i64, i32, vp, vp, vp, vp, i64, vp, i64, i32, vp, vp,
+                                       vp, vp, vp, vp]
+        for name in ("kq_rope_table", "kq_rope", "kq_kv_append", "kq_kv_read", "kq_kv_move",
+                     "kq_tree_attention", "kq_verify_tree"):
+            getattr(lib, name).restype = i32
         if path is None:
             _lib = lib
         return lib

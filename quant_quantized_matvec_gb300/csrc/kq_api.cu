@@ -13,6 +13,7 @@
 #include <unordered_map>
 
 #include "kq.h"
+#include "kq_host.h"
 #include "kq_internal.h"
 #include "kq_launch.cuh"
 #include "kq_plan.h"
@@ -1231,6 +1232,27 @@ kq_status run_noalloc_chunk(const kq_mat &m, int ntok, void *stream) {
 }
 
 }  // namespace
+
+namespace kqhost {
+kq_status cuda_failed(cudaError_t e) {
+    g_last_cuda_error = (int)e;
+    return KQ_ERR_CUDA;
+}
+kq_status on_device(const void *p, int dev) {
+    const void *alias = nullptr;
+    bool host = false;
+    return device_address(p, dev, false, &alias, &host);
+}
+cudaError_t device(int *dev, int *sms, int *smem_optin, unsigned int **err) {
+    DeviceInfo info;
+    cudaError_t e = cudaGetDevice(dev);
+    if (e == cudaSuccess) e = device_info(*dev, info);
+    *sms = info.sms;
+    *smem_optin = info.smem_optin;
+    *err = info.err;
+    return e;
+}
+}  // namespace kqhost
 
 extern "C" {
 

@@ -1,0 +1,276 @@
+"""Attention of new tokens over the paged cache, against the formula in 64
+bits with the error bound that decode_ref.attention derives: every format,
+head layout and width, lengths from one token on, masks that leave a row
+empty, NaN and infinities in masked places, bad pages, long offsets."""
+import numpy as np
+import pytest
+
+import decode_ref as R
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import quant_quantized_matvec_gb300 as kq  # noqa: E402
+
+FMTS = [R.F16, R.Q8, R.Q4]
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+class Case:
+    """Sequences whose every place has been appended; k and v as the cache
+    holds them, per sequence."""
+
+    def __init__(self, fmt, hkv, g, dim, new, ctx, masks=None, seed=0, spread=1.0, garbage=0xFF,
+                 first_page=0, pages=None):
+        self.rng = rng = np.random.default_rng(seed)
+        self.new, self.ctx, self.fmt, self.dim = list(new), list(ctx), fmt, dim
+        self.start = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        self.ntok = int(self.start[-1])
+        need = [-(-(n + c) // 64) for n, c in zip(new, ctx)]
+        self.pages = pages or sum(need) + 2
+        order = first_page + rng.permutation(sum(need) + 2).astype(np.int32)
+        self.table = np.full((len(new), max(max(need), 1)), -1, np.int32)
+        at = 0
+        for b, n in enumerate(need):
+            self.table[b, :n] = order[at:at + n]
+            at += n
+        nb = kq.KVCache(fmt, hkv, dim, 1).page_bytes
+        data = torch.full((nb * self.pages,), garbage, dtype=torch.uint8, device="cuda")
+        self.cache = kq.KVCache(fmt, hkv, dim, self.pages, data)
+        self.hq = hkv * g
+        self.q = (spread * rng.standard_normal((self.ntok, self.hq, dim))).astype(np.float32)
+        # all places are written through a batch whose new tokens they are
+        total = [n + c for n, c in zip(new, ctx)]
+        starts = np.concatenate([[0], np.cumsum(total)]).astype(np.int32)
+        n = int(starts[-1])
+        self.k, self.v = (rng.standard_normal((n, hkv, dim)).astype(np.float32) for _ in range(2))
+        self.starts = starts
+        self.whole = kq.KVBatch(dev(starts), dev(np.zeros(len(new), np.int32)), dev(self.table), n,
+                                max(total))
+        self.batch = kq.KVBatch(dev(self.start), dev(np.asarray(ctx, np.int32)), dev(self.table),
+                                self.ntok, max(new))
+        if masks is None:  # random sets of the sequence's own new tokens
+            masks = [int(rng.integers(0, 1 << min(m, 62))) | 1 << j
+                     for m in new for j in range(m)]
+        self.masks = masks
+        self.write()
+
+    def write(self):
+        kq.kv_append(self.cache, self.whole, dev(self.k), dev(self.v))
+
+    def mask(self):
+        return dev(np.array([m - (1 << 64) if m >> 63 else m for m in self.masks], np.int64))
+
+    def run(self, **kw):
+        kw.setdefault("mask", self.mask())
+        return kq.tree_attention(self.cache, self.batch, dev(self.q), **kw)
+
+    def want(self, masks=None, scale=None):
+        masks = self.masks if masks is None else masks
+        ks, vs = (R.values(*R.quantise(x, self.fmt)) for x in (self.k, self.v))
+        outs, bounds = [], []
+        for b, (n, c) in enumerate(zip(self.new, self.ctx)):
+            lo, hi = self.starts[b], self.starts[b + 1]
+            seen = np.ones((n, n + c), bool)
+            for i in range(n):
+                for j in range(n):
+                    seen[i, c + j] = masks[self.start[b] + i] >> j & 1
+            o, e = R.attention(self.q[self.start[b]:self.start[b] + n], ks[lo:hi], vs[lo:hi], seen,
+                               self.dim ** -0.5 if scale is None else scale)
+            outs.append(o)
+            bounds.append(e)
+        return np.concatenate(outs), np.concatenate(bounds)
+
+    def check(self, got, want=None):
+        out, bound = self.want() if want is None else want
+        off = np.abs(got.cpu().numpy().astype(float) - out)
+        assert np.isfinite(off).all()
+        assert (off <= bound).all(), (float((off / np.maximum(bound, 1e-30)).max()))
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("hkv,g,new,ctx", [
+    (1, 1, [1], [0]), (2, 16, [1], [777]), (2, 4, [5, 1, 3], [63, 64, 0]),
+    (1, 8, [16], [1]), (3, 5, [7, 2], [190, 65]), (1, 16, [17], [300]), (8, 1, [1, 1], [62, 511])])
+def test_against_64_bits(fmt, dim, hkv, g, new, ctx):
+    c = Case(fmt, hkv, g, dim, new, ctx, seed=dim + g)
+    got = c.run()
+    c.check(got)
+    assert torch.equal(got, c.run())  # the same bits again
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
+@pytest.mark.parametrize("hkv,g,new,ctx", [
+    (1, 1, [64], [0]), (1, 4, [64, 33], [31, 64]), (1, 16, [64], [100]), (2, 7, [61], [3])])
+def test_many_new_tokens(fmt, hkv, g, new, ctx):
+    c = Case(fmt, hkv, g, 128, new, ctx, seed=g)
+    c.check(c.run())
+    causal = [(2 << j) - 1 for n in new for j in range(n)]
+    c.check(c.run(mask=None), c.want(causal))
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
+def test_long_and_ragged(fmt):
+    c = Case(fmt, 2, 4, 128, [2, 1, 4, 1, 1, 3], [9000, 1, 4097, 0, 2999, 640], seed=3, spread=4.0)
+    c.check(c.run())
+
+
+def test_a_batch_of_many_sequences():
+    rng = np.random.default_rng(8)
+    new, ctx = rng.integers(0, 4, 300).tolist(), rng.integers(0, 200, 300).tolist()
+    new[0] = 3
+    c = Case(R.Q8, 1, 4, 64, new, ctx, seed=9)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
+def test_empty_rows_are_zero(fmt):
+    c = Case(fmt, 2, 4, 128, [3, 2], [0, 5], masks=[0, 1, 0, 0, 0])
+    got = c.run()
+    assert (got[0] == 0).all() and (got[2] == 0).all()
+    c.check(got)
+    # bits beyond the sequence's own new tokens say nothing
+    c.masks = [~0 << 3 & (1 << 64) - 1, ~0 << 3 & (1 << 64) - 1 | 1, ~0 << 3 & (1 << 64) - 1,
+               1 << 63, 1 << 2]
+    assert torch.equal(c.run(), got)
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("ctx", [0, 61, 130])
+def test_masked_places_do_not_reach_a_row(fmt, bad, ctx):
+    """New token 2's key and value hold a NaN or an infinity; rows that attend
+    it show it, others are as without it."""
+    c = Case(fmt, 1, 4, 128, [6], [ctx], masks=[1, 3, 7, 9, 17, 37], seed=4)
+    clean = c.run()
+    c.k[ctx + 2, 0, 3], c.v[ctx + 2, 0, 40] = bad, bad
+    c.write()
+    got = c.run()
+    sees = [2, 5]
+    others = [0, 1, 3, 4]
+    assert torch.equal(got[others], clean[others])
+    assert torch.isnan(got[sees]).any(-1).all()
+    # the value alone: only the places of its own scale group (f16: itself)
+    c.k[ctx + 2, 0, 3] = 0.25
+    c.write()
+    got = c.run().cpu()
+    hit = torch.zeros(128, dtype=torch.bool)
+    hit[40 if fmt == R.F16 else slice(32, 64)] = True
+    if fmt == R.F16:
+        assert (~torch.isfinite(got[sees][..., hit])).all()
+        if bad == bad:
+            assert (got[sees][..., hit] == bad).all()
+    else:
+        assert torch.isnan(got[sees][..., hit]).all()
+    assert torch.isfinite(got[sees][..., ~hit]).all()
+    assert torch.isfinite(got[others]).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
+def test_extreme_logits(fmt):
+    c = Case(fmt, 1, 2, 64, [2], [200], seed=6, spread=3000.0)
+    c.check(c.run())
+    c.q[:] = 0
+    c.check(c.run())
+    c.q[:] = 1e-30
+    c.check(c.run())
+    c.q[0, 0, 5], c.q[1, 1, 7] = np.nan, np.inf
+    got = c.run()
+    assert torch.isnan(got[0, 0]).all() and torch.isnan(got[1, 1]).all()
+    assert torch.isfinite(got[0, 1]).all() and torch.isfinite(got[1, 0]).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
+def test_bad_pages(fmt):
+    c = Case(fmt, 2, 4, 64, [2, 1], [150, 150], masks=[1, 2, 1])
+    good = c.run()
+    table = c.table.copy()
+    table[0, 1] = c.pages
+    b = kq.KVBatch(c.batch.start, c.batch.ctx, dev(table), c.ntok, 2)
+    got = kq.tree_attention(c.cache, b, dev(c.q), mask=c.mask())
+    assert torch.isnan(got[:2]).all() and torch.equal(got[2], good[2])
+    # places past the table's end; lengths that are no lengths
+    b = kq.KVBatch(dev(np.array([0, 2, 9], np.int32)), dev(np.array([-3, 1 << 30], np.int32)),
+                   dev(c.table), c.ntok, 2)
+    out = torch.full((c.ntok, 8, 64), 5.0, device="cuda")
+    kq.tree_attention(c.cache, b, dev(c.q), mask=c.mask(), out=out)
+    assert torch.isfinite(out[:2]).all() and torch.isnan(out[2]).all()
+    # a token of no sequence is left alone
+    b = kq.KVBatch(dev(np.array([0, 1, 1], np.int32)), c.batch.ctx, dev(c.table), c.ntok, 2)
+    out.fill_(5.0)
+    kq.tree_attention(c.cache, b, dev(c.q), mask=c.mask(), out=out)
+    assert (out[1:] == 5).all() and torch.isfinite(out[0]).all()
+
+
+def test_masked_bad_page_is_not_attended():
+    c = Case(R.Q8, 1, 4, 64, [40], [50], masks=[1] * 40, seed=2)
+    good = c.run()
+    table = c.table.copy()
+    table[0, 1] = -1  # new tokens 14.. : none of them is attended
+    b = kq.KVBatch(c.batch.start, c.batch.ctx, dev(table), c.ntok, 40)
+    assert torch.equal(kq.tree_attention(c.cache, b, dev(c.q), mask=c.mask()), good)
+
+
+def test_large_offsets():
+    hkv, dim = 8, 256
+    nb = kq.KVCache(kq.KV_F16, hkv, dim, 1).page_bytes
+    pages = (9 << 29) // nb
+    c = Case(R.F16, hkv, 2, dim, [2], [700], first_page=pages - 14, pages=pages, garbage=0)
+    c.check(c.run())
+
+
+def test_strides_scale_out_and_workspace():
+    c = Case(R.Q4, 2, 4, 128, [3, 2], [700, 90], seed=11)
+    want = c.run()
+    wide = torch.zeros(c.ntok, c.hq + 4, 128, device="cuda")
+    wide[:, 2:2 + c.hq] = dev(c.q)
+    out = torch.empty_like(want)
+    ws = torch.full((kq.attention_workspace_bytes(c.cache, c.batch, c.hq) + 256,), 0xFF,
+                    dtype=torch.uint8, device="cuda")
+    got = kq.tree_attention(c.cache, c.batch, wide[:, 2:2 + c.hq], mask=c.mask(), out=out,
+                            workspace=ws)
+    assert got is out and torch.equal(got, want)
+    c.check(c.run(scale=0.7), c.want(scale=0.7))
+    need = kq.attention_workspace_bytes(c.cache, c.batch, c.hq)
+    if need:
+        with pytest.raises(kq.KQError, match="KQ_ERR_LIMIT"):
+            c.run(workspace=ws[:need - 1])
+
+
+def test_graph_serves_a_growing_sequence():
+    c = Case(R.Q8, 2, 8, 128, [2, 2], [500, 40], seed=12)
+    ws = torch.empty(max(256, kq.attention_workspace_bytes(c.cache, c.batch, c.hq)),
+                     dtype=torch.uint8, device="cuda")
+    q, m, out = dev(c.q), c.mask(), torch.empty(c.ntok, c.hq, 128, device="cuda")
+    kq.tree_attention(c.cache, c.batch, q, mask=m, out=out, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kq.tree_attention(c.cache, c.batch, q, mask=m, out=out, workspace=ws)
+    for ctx in ([500, 40], [130, 0], [64, 39]):
+        c.batch.ctx.copy_(dev(np.asarray(ctx, np.int32)))
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, c.run())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = c.run(stream=side)
+    side.synchronize()
+    assert torch.equal(got, out)
+
+
+def test_refusals():
+    c = Case(R.Q8, 2, 4, 64, [3], [10])
+    with pytest.raises(ValueError):
+        kq.tree_attention(c.cache, c.batch, dev(c.q)[:2])
+    with pytest.raises(ValueError):
+        kq.tree_attention(c.cache, c.batch, dev(c.q), mask=c.mask().int())
+    with pytest.raises(kq.KQError, match="KQ_ERR_SHAPE"):
+        kq.tree_attention(c.cache, c.batch, dev(c.q)[:, :7].contiguous())
+    with pytest.raises(kq.KQError, match="KQ_ERR_ALIAS"):
+        x = dev(c.q)
+        kq.tree_attention(c.cache, c.batch, x, out=x)
