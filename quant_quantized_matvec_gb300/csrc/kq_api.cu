@@ -1243,13 +1243,13 @@ kq_status on_device(const void *p, int dev) {
     bool host = false;
     return device_address(p, dev, false, &alias, &host);
 }
-cudaError_t device(int *dev, int *sms, int *smem_optin, unsigned int **err) {
+cudaError_t device(Device &d) {
+    int dev = 0;
     DeviceInfo info;
-    cudaError_t e = cudaGetDevice(dev);
-    if (e == cudaSuccess) e = device_info(*dev, info);
-    *sms = info.sms;
-    *smem_optin = info.smem_optin;
-    *err = info.err;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = device_info(dev, info);
+    const unsigned long long wl = g_wait_ns.load();
+    d = {info.sms, info.err, wl ? wl : kq::kWaitLimitNs};
     return e;
 }
 }  // namespace kqhost

@@ -1,0 +1,8 @@
+// kq_attn_q4.cu -- kq_attn.cuh for KQ_KV_Q4 caches.
+#include "kq_attn.cuh"
+
+namespace kqd {
+cudaError_t attn_q4(int dim, const AttnArgs &a, int sms, cudaStream_t s, int64_t *floats) {
+    return attn_format<KQ_KV_Q4>(dim, a, sms, s, floats);
+}
+}  // namespace kqd

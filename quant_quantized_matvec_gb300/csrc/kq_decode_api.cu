@@ -226,11 +226,10 @@ int64_t kq_attn_workspace_bytes(const kq_kv *kv, const kq_batch *batch, int q_he
     if (st == KQ_OK && (q_heads < 1 || q_heads > KQ_MAX_HEADS || q_heads % kv->kv_heads != 0))
         st = KQ_ERR_SHAPE;
     if (st != KQ_OK) return -(int64_t)st;
-    int dev = 0, sms = 0, smem = 0;
-    unsigned int *err = nullptr;
-    const cudaError_t e = kqhost::device(&dev, &sms, &smem, &err);
+    kqhost::Device dev{};
+    const cudaError_t e = kqhost::device(dev);
     if (e != cudaSuccess) return -(int64_t)kqhost::cuda_failed(e);
-    return kqd::attn_workspace(kv->head_dim, seqs_of(kv, batch), q_heads, sms);
+    return kqd::attn_workspace(kv->fmt, kv->head_dim, seqs_of(kv, batch), q_heads, dev.sms);
 }
 
 kq_status kq_tree_attention(const kq_kv *kv, const kq_batch *batch, const float *q,
@@ -246,12 +245,11 @@ kq_status kq_tree_attention(const kq_kv *kv, const kq_batch *batch, const float 
     if (!q || !out) return KQ_ERR_NULL;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(mask, 8) || !aligned(ws, 256))
         return KQ_ERR_ALIGN;
-    int dev = 0, sms = 0, smem = 0;
-    unsigned int *err = nullptr;
-    cudaError_t e = kqhost::device(&dev, &sms, &smem, &err);
+    kqhost::Device dev{};
+    cudaError_t e = kqhost::device(dev);
     if (e != cudaSuccess) return kqhost::cuda_failed(e);
     const kqd::Seqs seqs = seqs_of(kv, batch);
-    const int64_t need = kqd::attn_workspace(kv->head_dim, seqs, q_heads, sms);
+    const int64_t need = kqd::attn_workspace(kv->fmt, kv->head_dim, seqs, q_heads, dev.sms);
     if (ws && ws_bytes < need) return KQ_ERR_LIMIT;
     Pointers p;
     read_batch(p, batch);
@@ -269,7 +267,7 @@ kq_status kq_tree_attention(const kq_kv *kv, const kq_batch *batch, const float 
         if (e != cudaSuccess) return kqhost::cuda_failed(e);
     }
     e = kqd::attn(kv->fmt, kv->head_dim, seqs, q, q_stride, q_heads, mask, scale, out,
-                  ws ? ws : tmp, sms, err, s);
+                  ws ? ws : tmp, dev.sms, dev.err, dev.wait_ns, s);
     if (tmp) {
         const cudaError_t f = cudaFreeAsync(tmp, s);
         if (e == cudaSuccess) e = f;

@@ -33,10 +33,10 @@ cudaError_t kv_move(int fmt, int dim, const Seqs &q, const int32_t *path, const 
                     cudaStream_t s);
 
 // Attention: workspace bytes and the launches.
-int64_t attn_workspace(int dim, const Seqs &q, int q_heads, int sms);
+int64_t attn_workspace(int fmt, int dim, const Seqs &q, int q_heads, int sms);
 cudaError_t attn(int fmt, int dim, const Seqs &q, const float *x, int64_t x_stride, int q_heads,
                  const uint64_t *mask, float scale, float *out, void *ws, int sms,
-                 unsigned int *err, cudaStream_t s);
+                 unsigned int *err, unsigned long long wait_ns, cudaStream_t s);
 
 struct VerifyArgs {
     const int32_t *start, *token, *parent;

@@ -15,9 +15,14 @@ kq_status cuda_failed(cudaError_t e);
 // KQ_OK if p is memory of the current device or managed memory.
 kq_status on_device(const void *p, int dev);
 
-// The current device, its SM count, its opt-in shared memory per CTA, and
-// the device address of its error word (kq_device_error).
-cudaError_t device(int *dev, int *sms, int *smem_optin, unsigned int **err);
+// The current device: its SM count, the device address of its error word
+// (kq_device_error), and the wall-time limit of its kernels' waits.
+struct Device {
+    int sms;
+    unsigned int *err;
+    unsigned long long wait_ns;
+};
+cudaError_t device(Device &d);
 
 struct Span {
     uintptr_t lo, hi;  // [lo, hi)

@@ -37,6 +37,7 @@
 
 #include <cuda.h>
 
+#include "kq_async.cuh"
 #include "kq_blocks.cuh"
 #include "kq_tc.cuh"
 
@@ -54,7 +55,6 @@ constexpr int kMaxMaps = 4;
 constexpr int kMaxSlots = 32;
 constexpr int kOverlapPrefetch = 1;  // stages issued before the inputs (overlap)
 constexpr int kMaxHinv = 40;  // row-pair offsets hp of a stage are at most 17
-constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s (default)
 
 struct StreamMember {
     const uint8_t *W;
@@ -98,60 +98,6 @@ struct StreamParams {
 };
 
 // ------------------------------------------------------------ PTX helpers
-__device__ __forceinline__ uint32_t smem_addr(const void *p) {
-    return (uint32_t)__cvta_generic_to_shared(p);
-}
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
-}
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
-                 "r"(bytes)
-                 : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n"
-        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 100000;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ unsigned long long global_ns() {
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-// Wait for the phase of `parity` to complete; false once `limit_ns` of wall
-// time have passed.  Between polls the thread sleeps, doubling from 32 ns up
-// to `max_ns`, so that waiting warps leave the issue slots to working ones.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
-                                          unsigned long long limit_ns,
-                                          unsigned max_ns = 256) {
-    if (mbar_try(bar, parity)) return true;
-    const unsigned long long t0 = global_ns();
-    unsigned ns = 32;
-    while (!mbar_try(bar, parity)) {
-        __nanosleep(ns);
-        if (ns < max_ns) ns <<= 1;
-        if (global_ns() - t0 > limit_ns) return false;
-    }
-    return true;
-}
-__device__ __forceinline__ void bulk_g2s(uint32_t dst, const void *src,
-                                         uint32_t bytes, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1], %2, [%3];" ::"r"(dst),
-        "l"(src), "r"(bytes), "r"(bar)
-        : "memory");
-}
 __device__ __forceinline__ void tensor2d_g2s(uint32_t dst, const CUtensorMap *map,
                                              int c0, int c1, uint32_t bar) {
     asm volatile(
@@ -159,14 +105,6 @@ __device__ __forceinline__ void tensor2d_g2s(uint32_t dst, const CUtensorMap *ma
         " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
         "l"(map), "r"(c0), "r"(c1), "r"(bar)
         : "memory");
-}
-// Programmatic dependent launch: let the next kernel on the stream launch,
-// and wait for the preceding one (no-ops for an ordinary launch).
-__device__ __forceinline__ void allow_dependents() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void wait_prerequisites() {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 template <int NCW>
 __device__ __forceinline__ void consumer_sync() {

@@ -109,6 +109,7 @@ class KVBatch:
         self._c = _binding.KqBatch(nseq, self.max_new, self.ntok, start.data_ptr(),
                                    ctx.data_ptr(), pages.data_ptr(), pages.shape[1])
         self._p = ctypes.byref(self._c)
+        self._ws = {}  # workspace bytes of the attention calls made with it
 
 
 def rope_table(positions, rot, base=10000.0, scaling=None, factor=1.0, orig=1, fast=32.0,
@@ -211,9 +212,15 @@ def tree_mask(parents):
 
 
 def attention_workspace_bytes(cache, batch, q_heads):
-    n = int(_binding.load().kq_attn_workspace_bytes(cache._p, batch._p, int(q_heads)))
-    if n < 0:
-        raise KQError(-n, "kq_attn_workspace_bytes")
+    """Bytes of tree_attention's workspace (it depends on sizes alone, so the
+    batch keeps the answer)."""
+    key = (cache.fmt, cache.kv_heads, cache.head_dim, q_heads)
+    n = batch._ws.get(key)
+    if n is None:
+        n = int(_binding.load().kq_attn_workspace_bytes(cache._p, batch._p, int(q_heads)))
+        if n < 0:
+            raise KQError(-n, "kq_attn_workspace_bytes")
+        batch._ws[key] = n
     return n
 
 
@@ -223,8 +230,8 @@ def tree_attention(cache, batch, q, mask=None, scale=None, out=None, workspace=N
     over the committed tokens and the new ones whose bit is set in mask
     (int64 [ntok]; None: all up to the token itself).  scale: 1 /
     sqrt(head_dim) unless given.  workspace: a CUDA uint8 tensor of
-    attention_workspace_bytes(...) or more instead of a stream-ordered
-    temporary."""
+    attention_workspace_bytes(...) or more; otherwise torch's allocator gives
+    one for the call."""
     if q.dim() != 3:
         raise ValueError("q must be [ntok, q_heads, head_dim]")
     shape = (batch.ntok, q.shape[1], cache.head_dim)
@@ -235,9 +242,11 @@ def tree_attention(cache, batch, q, mask=None, scale=None, out=None, workspace=N
         with on:
             out = torch.empty(shape, dtype=torch.float32, device=q.device)
     op = _tensor(out, "out", torch.float32, shape)
-    wp, wn = None, 0
-    if workspace is not None:
-        wp, wn = _tensor(workspace, "workspace", torch.uint8), workspace.numel()
+    if workspace is None:
+        with on:
+            workspace = torch.empty(attention_workspace_bytes(cache, batch, q.shape[1]),
+                                    dtype=torch.uint8, device=q.device)
+    wp, wn = _tensor(workspace, "workspace", torch.uint8), workspace.numel()
     _call("kq_tree_attention", cache._p, batch._p, qp, qs, q.shape[1], mp,
           cache.head_dim ** -0.5 if scale is None else float(scale), op, wp, wn, st)
     return out
