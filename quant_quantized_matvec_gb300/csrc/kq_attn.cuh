@@ -45,7 +45,6 @@
 
 namespace kqd {
 
-constexpr int kGroupThreads = 128;  // four warps
 constexpr int kMaxGroups = 4;
 constexpr int kMaxSlots = 8;  // of a group's ring; a slot holds a page's keys or values
 
@@ -70,24 +69,26 @@ __host__ __device__ constexpr int part_floats(int rb, int d) { return rb * (d + 
 // ------------------------------------------------------------ shared memory
 // common | queries | per group: ring, probabilities, maxima
 struct AttnCommon {
-    uint64_t rowmask[64];
+    uint64_t rowmask[32];
     uint64_t bars[kMaxGroups * kMaxSlots];
-    long long scan[kMaxGroups * 4];
+    long long scan[16];
     long long start_unit;
     int start_seq;
     int dead;                              // a wait has expired
     int badpage[kMaxGroups * kMaxSlots];   // the slot's page is not valid
-    float rowfactor[64];
-    float ml[kMaxGroups][5][64];           // group's row maxima, warps' row sums
+    float rowfactor[32];
+    float ml[kMaxGroups][5][32];           // group's row maxima, warps' row sums
 };
 template <int FMT, int D, int MT>
 struct AttnSmem {
     static constexpr int kRows = 8 * MT;
+    static constexpr int kWg = 4;             // warps of a group
+    static constexpr int kGroups = 16 / kWg;  // groups of an SM
     static constexpr int kHalf = Kv<FMT, D>::kV;  // bytes of a slot
     static constexpr int kCommon = (sizeof(AttnCommon) + 127) / 128 * 128;
     static constexpr int kQ = kRows * D * 4;
     static constexpr int kP = kRows * kPage * 4;
-    static constexpr int kMax = 4 * kRows * 4;
+    static constexpr int kMax = kWg * kRows * 4;
     static __host__ __device__ int group(int nslot) { return nslot * kHalf + kP + kMax; }
     static __host__ __device__ int total(int ng, int nslot) {
         return kCommon + kQ + ng * group(nslot);
@@ -106,8 +107,16 @@ __device__ __forceinline__ float exp2_of(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ uint32_t bits_of(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
-__device__ __forceinline__ __half2 half2_of(uint32_t w) { return *reinterpret_cast<__half2 *>(&w); }
+__device__ __forceinline__ uint32_t bits_of(__half2 h) {
+    uint32_t w;
+    memcpy(&w, &h, 4);
+    return w;
+}
+__device__ __forceinline__ __half2 half2_of(uint32_t w) {
+    __half2 h;
+    memcpy(&h, &w, 4);
+    return h;
+}
 
 // hi and lo terms of a pair.
 __device__ __forceinline__ void split(float a, float b, uint32_t &hi, uint32_t &lo) {
@@ -152,8 +161,9 @@ __device__ __forceinline__ constexpr int pair_second(int s, int h) {
     return FMT == KQ_KV_Q4 ? 2 * s + h + 4 : 4 * s + 2 * h + 1;
 }
 
+template <int THREADS>
 __device__ __forceinline__ void group_sync(int g) {
-    asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "n"(kGroupThreads) : "memory");
+    asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "n"(THREADS) : "memory");
 }
 
 // Probabilities in shared memory, [row][16 chunks of 4 tokens]: lane c's
@@ -191,13 +201,15 @@ __device__ __forceinline__ int cta_of(long long u, long long total, int n) {
 
 // ------------------------------------------------------------------ kernel
 template <int FMT, int D, int MT>
-__global__ void __launch_bounds__(kMaxGroups *kGroupThreads, 1)
+__global__ void __launch_bounds__(AttnSmem<FMT, D, MT>::kGroups * AttnSmem<FMT, D, MT>::kWg * 32, 1)
     kq_attn_kernel(const __grid_constant__ AttnArgs a) {
     using L = Kv<FMT, D>;
     using M = AttnSmem<FMT, D, MT>;
     constexpr int RB = M::kRows;
     constexpr int kSteps = D / 16;          // k-steps of a logit
-    constexpr int kSlice = D / 4;           // values of a warp in part 3
+    constexpr int kWg = M::kWg, kGroupThreads = 32 * kWg;
+    constexpr int kTok = kPage / kWg, J = kTok / 8;  // tokens of a warp in part 1, in tiles
+    constexpr int kSlice = D / kWg;         // values of a warp in part 3
     constexpr int kTiles = kSlice / 8;      // its n-tiles
     constexpr int kSliceGroups = kSlice > kGroup ? kSlice / kGroup : 1;
     constexpr int kTilesG = kTiles / kSliceGroups;
@@ -206,7 +218,7 @@ __global__ void __launch_bounds__(kMaxGroups *kGroupThreads, 1)
     AttnCommon &cm = *reinterpret_cast<AttnCommon *>(smem);
     uint4 *qs = reinterpret_cast<uint4 *>(smem + M::kCommon);  // [tile][k-step][lane]
     const int tid = threadIdx.x, lane = tid & 31;
-    const int g = tid / kGroupThreads, w = (tid >> 5) & 3;
+    const int g = tid / kGroupThreads, w = (tid >> 5) % kWg;
     const int n8 = lane >> 2, c = lane & 3;  // row (or column) of an operand, and its quarter
     const int nthreads = a.ng * kGroupThreads;
     uint8_t *gbase = smem + M::kCommon + M::kQ + g * M::group(a.nslot);
@@ -262,7 +274,9 @@ __global__ void __launch_bounds__(kMaxGroups *kGroupThreads, 1)
     }
     if (u0 >= u1) return;
 
-    uint32_t op0 = 0;  // the group's copies before this segment
+    // the group's ring: next slot to fill and to use, and the use's parity
+    int fill = 0, use = 0;
+    uint32_t parity = 0, op0 = 0;  // op0: copies before this segment
     int b = cm.start_seq;
     long long off = cm.start_unit;
     for (long long u = u0; u < u1 && b < a.q.nseq;) {
@@ -294,14 +308,15 @@ __global__ void __launch_bounds__(kMaxGroups *kGroupThreads, 1)
             // (once a wait has expired nothing more is issued or waited for)
             if (lane == 0 && !*(volatile int *)&cm.dead) {
                 live = i + 1;
-                const uint32_t slot = (op0 + i) % a.nslot, bar = bars + 8 * slot;
-                cm.badpage[g * kMaxSlots + slot] = page < 0;
+                const uint32_t bar = bars + 8 * fill;
+                cm.badpage[g * kMaxSlots + fill] = page < 0;
                 kq::mbar_expect_tx(bar, M::kHalf);
-                kq::bulk_g2s(ring + slot * M::kHalf,
+                kq::bulk_g2s(ring + fill * M::kHalf,
                              a.q.data + (max(page, (int64_t)0) * a.q.heads + head) * L::kBlock +
                                  (i & 1) * M::kHalf,
                              M::kHalf, bar);
             }
+            if (++fill == a.nslot) fill = 0;
             __syncwarp();
         };
         int issued = 0;
@@ -372,12 +387,15 @@ __global__ void __launch_bounds__(kMaxGroups *kGroupThreads, 1)
             for (int i = 0; i < kTiles; ++i) O[t][i][0] = O[t][i][1] = 0.f;
         }
 
-        auto arrived = [&](uint32_t op) {
-            if (*(volatile int *)&cm.dead) return;
-            if (!kq::mbar_wait(bars + 8 * (op % a.nslot), (op / a.nslot) & 1, a.wait_ns)) {
+        // the next slot, once its copy has arrived
+        auto arrived = [&]() {
+            if (!*(volatile int *)&cm.dead && !kq::mbar_wait(bars + 8 * use, parity, a.wait_ns)) {
                 *(volatile int *)&cm.dead = 1;
                 atomicOr(a.err, 1u);
             }
+            const int slot = use;
+            if (++use == a.nslot) use = 0, parity ^= 1;
+            return slot;
         };
         for (int k = 0; k < count; ++k) {
             const int pg = pg0 + g + k * a.ng;
@@ -390,28 +408,28 @@ __global__ void __launch_bounds__(kMaxGroups *kGroupThreads, 1)
                 return (nw << left) | ~(~0ull << left);
             };
             // ---- 1. logits of tokens 16 w .. 16 w + 15
-            const uint32_t ks = (op0 + 2 * k) % a.nslot;
-            arrived(op0 + 2 * k);
+            const int ks = arrived();
             const uint8_t *kb = gbase + ks * M::kHalf;
             const bool badpage = cm.badpage[g * kMaxSlots + ks];
-            float S[MT][2][2];
+            float S[MT][J][2];
             {
-                float acc[MT][2][4];
+                float acc[MT][J][4];
                 constexpr int kLane = L::kSlabBytes / 4;  // bytes of a lane in a slab
 #pragma unroll
                 for (int t = 0; t < MT; ++t)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
+                    for (int j = 0; j < J; ++j) {
                         S[t][j][0] = S[t][j][1] = 0.f;
                         if (!L::kQuant) acc[t][j][0] = acc[t][j][1] = acc[t][j][2] = acc[t][j][3] = 0.f;
                     }
 #pragma unroll
                 for (int sl = 0; sl < L::kSlabs; ++sl) {
-                    uint32_t raw[2][kLane / 4];
+                    uint32_t raw[J][kLane / 4];
+                    uint32_t skw[J][2][(L::kSlabGroups + 1) / 2];  // scales, two groups a word
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
+                    for (int j = 0; j < J; ++j) {
                         const uint8_t *p = kb + sl * kPage * L::kSlabBytes +
-                                           (16 * w + 8 * j + n8) * L::kSlabBytes + c * kLane;
+                                           (kTok * w + 8 * j + n8) * L::kSlabBytes + c * kLane;
                         if constexpr (kLane == 16) {
                             const uint4 v = *reinterpret_cast<const uint4 *>(p);
                             raw[j][0] = v.x, raw[j][1] = v.y, raw[j][2] = v.z, raw[j][3] = v.w;
@@ -419,14 +437,27 @@ __global__ void __launch_bounds__(kMaxGroups *kGroupThreads, 1)
                             const uint2 v = *reinterpret_cast<const uint2 *>(p);
                             raw[j][0] = v.x, raw[j][1] = v.y;
                         }
+                        if constexpr (L::kQuant) {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const uint8_t *sp = kb + L::k_scale(kTok * w + 8 * j + 2 * c + i,
+                                                                    sl * L::kSlabGroups);
+                                if constexpr (L::kSlabGroups == 4) {
+                                    const uint2 v = *reinterpret_cast<const uint2 *>(sp);
+                                    skw[j][i][0] = v.x, skw[j][i][1] = v.y;
+                                } else {
+                                    skw[j][i][0] = *reinterpret_cast<const uint32_t *>(sp);
+                                }
+                            }
+                        }
                     }
 #pragma unroll
                     for (int gl = 0; gl < L::kSlabGroups; ++gl) {
                         const int gg = sl * L::kSlabGroups + gl;
-                        uint32_t bb[2][4];
-                        float sk[2][2];
+                        uint32_t bb[J][4];
+                        float sk[J][2];
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
+                        for (int j = 0; j < J; ++j) {
                             if constexpr (FMT == KQ_KV_F16) {
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) bb[j][i] = raw[j][i];
@@ -437,10 +468,11 @@ __global__ void __launch_bounds__(kMaxGroups *kGroupThreads, 1)
                                 codes4(raw[j][gl], bb[j]);
                             }
                             if constexpr (L::kQuant) {
-                                const __half *sp = reinterpret_cast<const __half *>(
-                                    kb + L::k_scale(16 * w + 8 * j + 2 * c, gg));
-                                sk[j][0] = __half2float(sp[0]);
-                                sk[j][1] = __half2float(sp[L::kGroups]);
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    const __half2 h = half2_of(skw[j][i][gl / 2]);
+                                    sk[j][i] = gl & 1 ? __high2float(h) : __low2float(h);
+                                }
                             }
                         }
 #pragma unroll
@@ -448,7 +480,7 @@ __global__ void __launch_bounds__(kMaxGroups *kGroupThreads, 1)
                             const uint4 q0 = qs[(t * kSteps + 2 * gg) * 32 + lane];
                             const uint4 q1 = qs[(t * kSteps + 2 * gg + 1) * 32 + lane];
 #pragma unroll
-                            for (int j = 0; j < 2; ++j) {
+                            for (int j = 0; j < J; ++j) {
                                 if constexpr (L::kQuant) {
                                     float d[4] = {0.f, 0.f, 0.f, 0.f};
                                     mma(d, q0, bb[j][0], bb[j][1]);
@@ -463,39 +495,41 @@ __global__ void __launch_bounds__(kMaxGroups *kGroupThreads, 1)
                         }
                     }
                 }
-                if constexpr (!L::kQuant)
+                if constexpr (!L::kQuant) {
 #pragma unroll
                     for (int t = 0; t < MT; ++t)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
+                        for (int j = 0; j < J; ++j) {
                             S[t][j][0] = acc[t][j][0] + acc[t][j][2];
                             S[t][j][1] = acc[t][j][1] + acc[t][j][3];
                         }
+                }
             }
             // ---- 2. row maxima, probabilities
-            float top[MT];
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
-                const float f = cm.rowfactor[8 * t + n8];
+                const float f = badpage ? quiet_nan() : cm.rowfactor[8 * t + n8];
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int j = 0; j < J; ++j)
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
-                        S[t][j][i] = badpage ? quiet_nan() : S[t][j][i] * f;
+                        S[t][j][i] *= f;
                 if (edge) {
-                    const uint32_t ok = (uint32_t)(allowed(8 * t + n8) >> (16 * w + 2 * c));
+                    const uint32_t ok = (uint32_t)(allowed(8 * t + n8) >> (kTok * w + 2 * c));
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
+                    for (int j = 0; j < J; ++j)
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
                             if (!((ok >> (8 * j + i)) & 1)) S[t][j][i] = -INFINITY;
                 }
-                float v = fmaxf(fmaxf(S[t][0][0], S[t][0][1]), fmaxf(S[t][1][0], S[t][1][1]));
+                float v = fmaxf(S[t][0][0], S[t][0][1]);
+#pragma unroll
+                for (int j = 1; j < J; ++j) v = fmaxf(v, fmaxf(S[t][j][0], S[t][j][1]));
                 v = fmaxf(v, __shfl_xor_sync(~0u, v, 1));
                 v = fmaxf(v, __shfl_xor_sync(~0u, v, 2));
                 if (c == 0) smax[w * RB + 8 * t + n8] = v;
             }
-            group_sync(g);
+            group_sync<kGroupThreads>(g);
             // every warp is done with these keys and the values before them
             if (w == 0)
                 for (; issued < min(2 * count, 2 * k + 1 + a.nslot); ++issued) copy(issued);
@@ -503,25 +537,26 @@ __global__ void __launch_bounds__(kMaxGroups *kGroupThreads, 1)
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 const int r = 8 * t + n8;
-                top[t] = fmaxf(fmaxf(smax[r], smax[RB + r]), fmaxf(smax[2 * RB + r], smax[3 * RB + r]));
-                const float now = fmaxf(m[t], top[t]);
+                float now = m[t];
+#pragma unroll
+                for (int i = 0; i < kWg; ++i) now = fmaxf(now, smax[i * RB + r]);
                 const float base = now == -INFINITY ? 0.f : now;
                 alpha[t] = exp2_of(m[t] - base);
                 m[t] = now;
+                const float high = base - 15.f;  // probabilities (and l, O) times 2^15
                 float sum = 0.f;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float p0 = exp2_of(S[t][j][0] - base), p1 = exp2_of(S[t][j][1] - base);
+                for (int j = 0; j < J; ++j) {
+                    const float p0 = exp2_of(S[t][j][0] - high), p1 = exp2_of(S[t][j][1] - high);
                     sum += p0 + p1;
-                    *reinterpret_cast<float2 *>(ps + p_at<FMT>(r, 16 * w + 8 * j + 2 * c)) =
+                    *reinterpret_cast<float2 *>(ps + p_at<FMT>(r, kTok * w + 8 * j + 2 * c)) =
                         make_float2(p0, p1);
                 }
                 l[t] = fmaf(l[t], alpha[t], sum);
             }
             // ---- 3. values kSlice w .. of all 64 tokens
-            const uint32_t vs = (op0 + 2 * k + 1) % a.nslot;
-            arrived(op0 + 2 * k + 1);
-            group_sync(g);
+            const int vs = arrived();
+            group_sync<kGroupThreads>(g);
             // (offsets of Kv count from the block's start; the slot starts at
             // the values)
             const uint8_t *vb = gbase + vs * M::kHalf - L::kV;
@@ -538,8 +573,8 @@ __global__ void __launch_bounds__(kMaxGroups *kGroupThreads, 1)
 #pragma unroll
             for (int sg = 0; sg < kSliceGroups; ++sg) {
                 const int group = w * kSlice / kGroup + sg;
-                float fac = 0x1p-15f;
-                float sn[16];
+                float fac = 1.f;
+                __half2 sn[8];     // scales of the lane's tokens, normalised
                 uint32_t keep[8];  // f16: pairs of tokens that stay
                 if constexpr (L::kQuant) {
                     const uint4 *sp = reinterpret_cast<const uint4 *>(vb + L::v_scale(16 * c, group));
@@ -561,21 +596,20 @@ __global__ void __launch_bounds__(kMaxGroups *kGroupThreads, 1)
                         bad |= __shfl_xor_sync(~0u, bad, 1);
                         bad |= __shfl_xor_sync(~0u, bad, 2);
                     }
+                    // |scales| of the page and group are below 2^ex: times
+                    // 2^-ex, they and a probability make less than 2^15
                     __half2 big = __habs2(half2_of(raw[0]));
 #pragma unroll
-                    for (int i = 1; i < 8; ++i) big = __hmax2_nan(big, __habs2(half2_of(raw[i])));
-                    big = __hmax2_nan(big, half2_of(__shfl_xor_sync(~0u, bits_of(big), 1)));
-                    big = __hmax2_nan(big, half2_of(__shfl_xor_sync(~0u, bits_of(big), 2)));
-                    const float smx = fmaxf(__low2float(big), __high2float(big));
-                    // every |scale| below 2^ex
-                    const int ex = max((int)((__float_as_uint(smx) >> 23) & 255) - 126, -24);
-                    const float up = __uint_as_float((uint32_t)(127 + 15 - ex) << 23);
-                    fac = __uint_as_float((uint32_t)(127 - 15 + ex) << 23);
+                    for (int i = 1; i < 8; ++i) big = __hmax2(big, __habs2(half2_of(raw[i])));
+                    big = __hmax2(big, half2_of(__shfl_xor_sync(~0u, bits_of(big), 1)));
+                    big = __hmax2(big, half2_of(__shfl_xor_sync(~0u, bits_of(big), 2)));
+                    const uint32_t top = bits_of(__hmax2(big, __lowhigh2highlow(big))) & 0xFFFFu;
+                    const int ex = max((int)(top >> 10) - 14, -15);
+                    const uint32_t up = ex <= 14 ? (uint32_t)(15 - ex) << 10 : 0x400u >> (ex - 14);
+                    fac = __uint_as_float((uint32_t)(127 + ex) << 23);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 f = __half22float2(half2_of(raw[i]));
-                        sn[2 * i] = f.x * up, sn[2 * i + 1] = f.y * up;
-                    }
+                    for (int i = 0; i < 8; ++i)
+                        sn[i] = __hmul2(half2_of(raw[i]), half2_of(up | up << 16));
                 } else if (edge) {
                     // (one pass over the slice's values, on edge pages only)
                     uint32_t b16 = 0;
@@ -606,39 +640,7 @@ __global__ void __launch_bounds__(kMaxGroups *kGroupThreads, 1)
                         keep[i] = (b16 >> (2 * i) & 1 ? 0u : 0xFFFFu) |
                                   (b16 >> (2 * i) & 2 ? 0u : 0xFFFF0000u);
                 }
-                // the slice's values, as operands
-                uint32_t vv[kTilesG][8];
-#pragma unroll
-                for (int nt = 0; nt < kTilesG; ++nt) {
-                    const int e = w * kSlice + 8 * (sg * kTilesG + nt) + n8;
-                    if constexpr (FMT == KQ_KV_F16) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint4 v = *reinterpret_cast<const uint4 *>(
-                                vb + L::v_word(e, token(8 * h) / 2));
-                            vv[nt][4 * h] = v.x, vv[nt][4 * h + 1] = v.y;
-                            vv[nt][4 * h + 2] = v.z, vv[nt][4 * h + 3] = v.w;
-                        }
-                        if (edge)
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) vv[nt][i] &= keep[i];
-                    } else if constexpr (FMT == KQ_KV_Q8) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(vb + L::v_word(e, 4 * c));
-                        codes8(v.x, vv[nt][0], vv[nt][1]);
-                        codes8(v.y, vv[nt][2], vv[nt][3]);
-                        codes8(v.z, vv[nt][4], vv[nt][5]);
-                        codes8(v.w, vv[nt][6], vv[nt][7]);
-                    } else {
-                        const uint2 v = *reinterpret_cast<const uint2 *>(vb + L::v_word(e, 2 * c));
-                        uint32_t x[4];
-                        codes4(v.x, x);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) vv[nt][i] = x[i];
-                        codes4(v.y, x);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) vv[nt][4 + i] = x[i];
-                    }
-                }
+                uint4 pa[MT][4];  // operands of the four k-steps
 #pragma unroll
                 for (int t = 0; t < MT; ++t) {
                     const int r = 8 * t + n8;
@@ -650,24 +652,71 @@ __global__ void __launch_bounds__(kMaxGroups *kGroupThreads, 1)
                         p[4 * i] = v.x, p[4 * i + 1] = v.y, p[4 * i + 2] = v.z, p[4 * i + 3] = v.w;
                     }
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) p[i] *= L::kQuant ? sn[i] : 0x1p15f;
-                    uint4 pa[4];  // operands of the four k-steps
-#pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int o = 8 * (i >> 1), st = i & 1;
-                        split(p[o + pair_first<FMT>(st, 0)], p[o + pair_second<FMT>(st, 0)], pa[i].x,
-                              pa[i].y);
-                        split(p[o + pair_first<FMT>(st, 1)], p[o + pair_second<FMT>(st, 1)], pa[i].z,
-                              pa[i].w);
+                        auto pair = [&](int h, uint32_t &hi, uint32_t &lo) {
+                            const int x = o + pair_first<FMT>(st, h), y = o + pair_second<FMT>(st, h);
+                            split(p[x], p[y], hi, lo);
+                            if constexpr (L::kQuant) {
+                                // (hi + lo) s as two terms: hi s is rounded,
+                                // what that loses (exact in f16) joins lo s
+                                const __half2 sc =
+                                    __halves2half2(x & 1 ? __high2half(sn[x / 2]) : __low2half(sn[x / 2]),
+                                                   y & 1 ? __high2half(sn[y / 2]) : __low2half(sn[y / 2]));
+                                const __half2 h2 = half2_of(hi), hs = __hmul2(h2, sc);
+                                lo = bits_of(__hfma2(half2_of(lo), sc, __hfma2(h2, sc, __hneg2(hs))));
+                                hi = bits_of(hs);
+                            }
+                        };
+                        pair(0, pa[t][i].x, pa[t][i].y);
+                        pair(1, pa[t][i].z, pa[t][i].w);
+                    }
+                }
+#pragma unroll
+                for (int nt = 0; nt < kTilesG; ++nt) {
+                    const int e = w * kSlice + 8 * (sg * kTilesG + nt) + n8;
+                    uint32_t vv[8];
+                    if constexpr (FMT == KQ_KV_F16) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint4 v = *reinterpret_cast<const uint4 *>(
+                                vb + L::v_word(e, token(8 * h) / 2));
+                            vv[4 * h] = v.x, vv[4 * h + 1] = v.y;
+                            vv[4 * h + 2] = v.z, vv[4 * h + 3] = v.w;
+                        }
+                        if (edge) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) vv[i] &= keep[i];
+                        }
+                    } else if constexpr (FMT == KQ_KV_Q8) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(vb + L::v_word(e, 4 * c));
+                        codes8(v.x, vv[0], vv[1]);
+                        codes8(v.y, vv[2], vv[3]);
+                        codes8(v.z, vv[4], vv[5]);
+                        codes8(v.w, vv[6], vv[7]);
+                    } else {
+                        const uint2 v = *reinterpret_cast<const uint2 *>(vb + L::v_word(e, 2 * c));
+                        uint32_t x[4];
+                        codes4(v.x, x);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) vv[i] = x[i];
+                        codes4(v.y, x);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) vv[4 + i] = x[i];
                     }
 #pragma unroll
-                    for (int nt = 0; nt < kTilesG; ++nt) {
+                    for (int t = 0; t < MT; ++t) {
                         float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) mma(d, pa[i], vv[nt][2 * i], vv[nt][2 * i + 1]);
+                        for (int i = 0; i < 4; ++i) mma(d, pa[t][i], vv[2 * i], vv[2 * i + 1]);
                         float *o = O[t][sg * kTilesG + nt];
-                        o[0] = fmaf(d[0] + d[2], fac, o[0] * alpha[t]);
-                        o[1] = fmaf(d[1] + d[3], fac, o[1] * alpha[t]);
+                        if constexpr (L::kQuant) {
+                            o[0] = fmaf(d[0] + d[2], fac, o[0] * alpha[t]);
+                            o[1] = fmaf(d[1] + d[3], fac, o[1] * alpha[t]);
+                        } else {
+                            o[0] = fmaf(o[0], alpha[t], d[0] + d[2]);
+                            o[1] = fmaf(o[1], alpha[t], d[1] + d[3]);
+                        }
                     }
                 }
                 // values that are not finite reach the rows that attend them
@@ -720,7 +769,7 @@ __global__ void __launch_bounds__(kMaxGroups *kGroupThreads, 1)
                 kq::mbar_wait(bars + 8 * ((op0 + i) % a.nslot), ((op0 + i) / a.nslot) & 1,
                               kq::kWaitLimitNs);
         op0 += 2 * count;
-        group_sync(g);
+        group_sync<kGroupThreads>(g);
         float *os = reinterpret_cast<float *>(gbase);
 #pragma unroll
         for (int t = 0; t < MT; ++t)
@@ -742,7 +791,10 @@ __global__ void __launch_bounds__(kMaxGroups *kGroupThreads, 1)
             for (int k = 0; k < a.ng; ++k) {
                 const float f = exp2_of(cm.ml[k][0][r] - base);
                 const float *lk = &cm.ml[k][1][r];
-                sum = fmaf(f, (lk[0] + lk[64]) + (lk[128] + lk[192]), sum);
+                float lsum = lk[0];
+#pragma unroll
+                for (int i = 1; i < kWg; ++i) lsum += lk[32 * i];
+                sum = fmaf(f, lsum, sum);
                 const float4 v = *reinterpret_cast<const float4 *>(
                     smem + M::kCommon + M::kQ + k * M::group(a.nslot) + 4 * (r * D + e));
                 y.x = fmaf(f, v.x, y.x), y.y = fmaf(f, v.y, y.y);
@@ -826,22 +878,22 @@ struct AttnShape {
 template <int FMT, int D, int MT>
 cudaError_t launch_attn(AttnArgs a, int sms, cudaStream_t s, int64_t *floats) {
     using M = AttnSmem<FMT, D, MT>;
-    // Four groups of an SM in all: in one CTA that joins them where there are
-    // fewer items than that, else in a CTA each, so that a CTA's items need
-    // no joining.  Fewer where a slot is too large for three a group.
+    // 16 warps of an SM in all: in one CTA that joins them where there are few
+    // items, else in four, so that a CTA's warps have fewer items to join.
+    // Fewer where a slot is too large for three a group.
     const int kSm = 227 * 1024;
-    int groups = kMaxGroups;
-    while (groups > 1 && (kSm / groups - 1024 - M::kCommon - M::kQ - M::kP - M::kMax) / M::kHalf < 3)
-        --groups;
     const int64_t items = (int64_t)a.q.nseq * a.q.heads *
                           (((int64_t)a.q.max_new * a.per + M::kRows - 1) / M::kRows);
     AttnShape sh;
-    const bool apart = items >= (int64_t)groups * sms;
-    sh.ng = apart ? 1 : groups;
-    const int ctas = apart ? groups : 1;  // of an SM
-    sh.ctas = ctas * sms;
-    sh.nslot = (kSm / ctas - 1024 - M::kCommon - M::kQ) / sh.ng;
-    sh.nslot = (sh.nslot - M::kP - M::kMax) / M::kHalf;
+    auto fit = [&](int ctas) {  // CTAs of an SM
+        const int room = kSm / ctas - 1024 - M::kCommon - M::kQ;
+        sh.ctas = ctas * sms;
+        sh.ng = M::kGroups / ctas;
+        while (sh.ng > 1 && room / sh.ng - M::kP - M::kMax < 3 * M::kHalf) --sh.ng;
+        sh.nslot = (room / sh.ng - M::kP - M::kMax) / M::kHalf;
+    };
+    fit(4);
+    if (items < 4 * (int64_t)sms || sh.nslot < 3) fit(1);
     if (sh.nslot > kMaxSlots) sh.nslot = kMaxSlots;
     *floats = 2 * (int64_t)sh.ctas * part_floats(M::kRows, D);
     if (!a.part) return cudaSuccess;
@@ -863,7 +915,7 @@ cudaError_t launch_attn(AttnArgs a, int sms, cudaStream_t s, int64_t *floats) {
             if (dev >= 0 && dev < 64) configured[dev] = smem;
         }
     }
-    kq_attn_kernel<FMT, D, MT><<<sh.ctas, sh.ng * kGroupThreads, smem, s>>>(a);
+    kq_attn_kernel<FMT, D, MT><<<sh.ctas, 32 * M::kWg * sh.ng, smem, s>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};

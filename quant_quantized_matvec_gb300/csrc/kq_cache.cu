@@ -144,19 +144,21 @@ __global__ void __launch_bounds__(kCacheThreads)
             const __half2 h0 = __floats2half2_rn(x[0], x[1]), h1 = __floats2half2_rn(x[2], x[3]);
             w[0] = *reinterpret_cast<const uint32_t *>(&h0);
             w[1] = *reinterpret_cast<const uint32_t *>(&h1);
-            if (on && values)
+            if (on && values) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     st.v[t][e + k] = (uint16_t)(w[k / 2] >> (16 * (k & 1)));
+            }
         } else {
             const Codes c = quantise<FMT>(x);
             const uint32_t m = FMT == KQ_KV_Q8 ? 0xFFu : 0xFu;
             w[0] = 0;
 #pragma unroll
             for (int k = 0; k < 4; ++k) w[0] |= ((uint32_t)c.c[k] & m) << (L::kBits * k);
-            if (on && values)
+            if (on && values) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) st.v[t][e + k] = (int8_t)c.c[k];
+            }
             if (on && l8 == 0)
                 *reinterpret_cast<__half *>(part.block +
                                             (values ? L::v_scale(t, g) : L::k_scale(t, g))) = c.d;
