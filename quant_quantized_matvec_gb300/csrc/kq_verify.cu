@@ -1,134 +1,265 @@
 // kq_verify.cu -- verification of drafted tokens (kq_verify_tree).
 //
-// One CTA per sequence walks the tree; r, the residual distribution, is
-// never stored: it is p[cur] less z_1 q[cur], less z_2 q[cur] ... for the
-// children rejected so far, formed again from p and q and the few z where
-// it is needed.  Sums are over whole multiples of 2^-44, so any order gives
+// A cluster of CTAs per sequence, each with a run of the vocabulary.  Every
+// CTA walks the tree itself: whether a child is accepted depends on its
+// token's entries in its parent's rows alone (and on the sums of what is left
+// after rejections), so those are fetched for all nodes at once and the walk
+// runs in shared memory.  Only a rejection and the final draw touch whole
+// rows: r, the residual distribution, is kept in shared memory, a run each
+// CTA, and sums go round the cluster through distributed shared memory, one
+// barrier each.  Sums are over whole multiples of 2^-44, so any order gives
 // the same.
+//
+// Bound by latency: a sequence reads two rows (1.6 MB at 202048 words) over
+// 16 SMs, after one dependent fetch of the nodes' entries.  16 CTAs a sequence
+// and r in shared memory against one CTA that forms r again from p and q for
+// each pass: 134 -> (see the measured table) us for one chain of 5 drafts.
+#include <cooperative_groups.h>
+
+#include <mutex>
+
 #include "kq_decode.cuh"
 #include "kq_decode_launch.h"
 
 namespace kqd {
 
-constexpr int kVerifyThreads = 1024;
+namespace cg = cooperative_groups;
 
+constexpr int kVerifyThreads = 512;
+constexpr int kMaxCluster = 16;
+constexpr int kBatch = 13;  // loads of a thread in flight
+
+// 0..1; NaN is 0.
 __device__ __forceinline__ float unit(float x) { return fminf(fmaxf(x, 0.f), 1.f); }
-
-// r at token x: row p less what each rejected child took out.
-struct Residual {
-    const float *p, *q;  // rows of the current node; q NULL: no distribution
-    int n;               // rejected children
-    const float *z;      // with q: the sums before each
-    const int32_t *out;  // without: their tokens
-    __device__ __forceinline__ float at(int x) const {
-        float r = unit(__ldg(p + x));
-        if (q) {
-            const float d = n ? unit(__ldg(q + x)) : 0.f;
-            for (int i = 0; i < n; ++i) r = fmaxf(__fsub_rn(r, __fmul_rn(z[i], d)), 0.f);
-        } else {
-            for (int i = 0; i < n; ++i) r = out[i] == x ? 0.f : r;
-        }
-        return r;
-    }
-};
 __device__ __forceinline__ unsigned long long fixed(float r) {
     return (unsigned long long)__float2ull_rz(r * 17592186044416.f);  // 2^44
 }
 
-__device__ unsigned long long block_sum(unsigned long long v, unsigned long long *tmp) {
-#pragma unroll
-    for (int o = 16; o; o /= 2) v += __shfl_xor_sync(~0u, v, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = v;
-    __syncthreads();
-    unsigned long long s = 0;
-    for (int i = 0; i < kVerifyThreads / 32; ++i) s += tmp[i];
-    return s;
-}
+struct VerifyShared {
+    unsigned long long warp[kVerifyThreads / 32];
+    unsigned long long cta[2];  // the CTA's sum, by turns
+    int32_t token[KQ_MAX_DRAFT], parent[KQ_MAX_DRAFT];
+    float u[KQ_MAX_DRAFT];
+    float pt[KQ_MAX_DRAFT], qt[KQ_MAX_DRAFT];  // parent's rows at the node's token
+    float z[KQ_MAX_DRAFT];                     // sums before each rejected child ...
+    int32_t out[KQ_MAX_DRAFT];                 // ... and its token
+};
 
 __global__ void __launch_bounds__(kVerifyThreads)
-    kq_verify_kernel(const __grid_constant__ VerifyArgs a) {
-    __shared__ unsigned long long tmp[kVerifyThreads / 32];
-    __shared__ float z[KQ_MAX_DRAFT];
-    __shared__ int32_t out[KQ_MAX_DRAFT];
-    const int b = blockIdx.x, tid = threadIdx.x, V = a.vocab;
+    kq_verify_kernel(const __grid_constant__ VerifyArgs a, int chunk) {
+    cg::cluster_group cluster = cg::this_cluster();
+    const int nrank = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    __shared__ VerifyShared sh;
+    extern __shared__ float r[];  // this CTA's run of the residual
+    const int b = blockIdx.x / nrank, tid = threadIdx.x, V = a.vocab;
+    const int lo = min(rank * chunk, V), n = min(lo + chunk, V) - lo;
     const Seq s = seq_of(a.start, nullptr, a.ntok, a.max_new, b);
-    if (s.n == 0) {
-        if (tid == 0) a.count[b] = 0, a.next[b] = -1;
+    if (s.n == 0) {  // the same for the whole cluster
+        if (rank == 0 && tid == 0) a.count[b] = 0, a.next[b] = -1;
         return;
     }
-    for (int i = tid; i < s.n; i += kVerifyThreads) a.path[s.first + i] = i ? -1 : 0;
+    for (int j = tid; j < s.n; j += kVerifyThreads) {
+        const int x = s.first + j, t = __ldg(a.token + x), p = __ldg(a.parent + x);
+        const bool ok = j > 0 && p >= 0 && p < j && t >= 0 && t < V;
+        sh.token[j] = t;
+        sh.parent[j] = ok ? p : -1;
+        sh.u[j] = unit(__ldg(a.u + x));
+        const int64_t row = s.first + (ok ? p : 0);
+        sh.pt[j] = ok ? unit(__ldg(a.p + row * a.p_stride + t)) : 0.f;
+        sh.qt[j] = ok && a.q ? unit(__ldg(a.q + row * a.q_stride + t)) : 0.f;
+    }
     __syncthreads();
-    int cur = 0, got = 1;
+
+    // The cluster's sum of one number a thread; `turn` counts the calls.
+    // before: the sum over the CTAs of lower rank.
+    int turn = 0;
+    unsigned long long before = 0;
+    auto cluster_sum = [&](unsigned long long v) {
+#pragma unroll
+        for (int o = 16; o; o /= 2) v += __shfl_xor_sync(~0u, v, o);
+        if ((tid & 31) == 0) sh.warp[tid >> 5] = v;
+        __syncthreads();
+        if (tid < 32) {
+            unsigned long long t = tid < kVerifyThreads / 32 ? sh.warp[tid] : 0;
+#pragma unroll
+            for (int o = 16; o; o /= 2) t += __shfl_xor_sync(~0u, t, o);
+            if (tid == 0) sh.cta[turn & 1] = t;
+        }
+        // (the entry written two calls ago was read before the last barrier)
+        cluster.sync();
+        // every warp fetches all entries at once, a lane each
+        const int lane = tid & 31;
+        unsigned long long t =
+            lane < nrank ? *cluster.map_shared_rank(&sh.cta[turn & 1], lane) : 0;
+        before = lane < rank ? t : 0;
+#pragma unroll
+        for (int o = 16; o; o /= 2) {
+            t += __shfl_xor_sync(~0u, t, o);
+            before += __shfl_xor_sync(~0u, before, o);
+        }
+        ++turn;
+        return t;
+    };
+    // r at a token of the vocabulary from a row of p and the rejections so far
+    int cur = 0, got = 1, rejected = 0;
     float zc = 1.f;
-    Residual r{a.p + (int64_t)s.first * a.p_stride, a.q ? a.q + (int64_t)s.first * a.q_stride : nullptr,
-               0, z, out};
+    auto left_of = [&](float p, float q, int t, int k) {
+        for (int i = 0; i < k; ++i) {
+            if (a.q) p = fmaxf(__fsub_rn(p, __fmul_rn(sh.z[i], q)), 0.f);
+            else p = sh.out[i] == t ? 0.f : p;
+        }
+        return p;
+    };
+    // the CTA's run of r after the first rej rejections; its sum's part
+    auto form = [&](int rej) {
+        const float *p = a.p + (int64_t)(s.first + cur) * a.p_stride + lo;
+        const float *q = a.q ? a.q + (int64_t)(s.first + cur) * a.q_stride + lo : nullptr;
+        unsigned long long sum = 0;
+        for (int i0 = tid; i0 < n; i0 += kBatch * kVerifyThreads) {
+            float pv[kBatch], qv[kBatch];  // loads first, all in flight
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int i = i0 + k * kVerifyThreads;
+                pv[k] = i < n ? __ldg(p + i) : 0.f;
+                qv[k] = i < n && q && rej ? __ldg(q + i) : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int i = i0 + k * kVerifyThreads;
+                if (i >= n) break;
+                const float x = left_of(unit(pv[k]), unit(qv[k]), lo + i, rej);
+                r[i] = x;
+                sum += fixed(x);
+            }
+        }
+        return sum;
+    };
+    int held = -1;  // rejections that r in shared memory has seen (-1: not formed)
     for (int j = 1; j < s.n; ++j) {
-        const int x = s.first + j;
-        if (__ldg(a.parent + x) != cur) continue;
-        const int t = __ldg(a.token + x);
-        if (t < 0 || t >= V) continue;
-        const float have = r.at(t);
-        const float d = r.q ? __fmul_rn(unit(__ldg(r.q + t)), zc) : zc;
-        if (__fmul_rn(unit(__ldg(a.u + x)), d) < have) {
-            cur = j;
-            r.p = a.p + (int64_t)x * a.p_stride;
-            if (a.q) r.q = a.q + (int64_t)x * a.q_stride;
-            r.n = 0, zc = 1.f;
-            if (tid == 0) a.path[s.first + got] = j;
+        if (sh.parent[j] != cur) continue;
+        const int t = sh.token[j];
+        const float have = left_of(sh.pt[j], sh.qt[j], t, rejected);
+        const float d = a.q ? __fmul_rn(sh.qt[j], zc) : zc;
+        if (__fmul_rn(sh.u[j], d) < have) {
+            if (rank == 0 && tid == 0) a.path[s.first + got] = j;
             ++got;
+            cur = j, rejected = 0, zc = 1.f, held = -1;
             continue;
         }
         // rejected: what is left without it
         __syncthreads();
-        if (tid == 0) z[r.n] = zc, out[r.n] = t;
+        if (tid == 0) sh.z[rejected] = zc, sh.out[rejected] = t;
         __syncthreads();
-        Residual left = r;
-        left.n = r.n + 1;
         unsigned long long sum = 0;
-        for (int i = tid; i < V; i += kVerifyThreads) sum += fixed(left.at(i));
-        sum = block_sum(sum, tmp);
+        if (held == rejected && a.q) {  // one step on from the r at hand
+            const float *q = a.q + (int64_t)(s.first + cur) * a.q_stride + lo;
+            for (int i0 = tid; i0 < n; i0 += kBatch * kVerifyThreads) {
+                float qv[kBatch];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int i = i0 + k * kVerifyThreads;
+                    qv[k] = i < n ? __ldg(q + i) : 0.f;
+                }
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int i = i0 + k * kVerifyThreads;
+                    if (i >= n) break;
+                    const float x = fmaxf(__fsub_rn(r[i], __fmul_rn(zc, unit(qv[k]))), 0.f);
+                    r[i] = x;
+                    sum += fixed(x);
+                }
+            }
+        } else {
+            sum = form(rejected + 1);
+        }
+        sum = cluster_sum(sum);
         if (sum) {
-            r = left;
+            held = ++rejected;
             zc = (float)((double)(long long)sum * 0x1p-44);
+        } else {
+            held = -1;  // r and z stay as they were
         }
     }
-    // the first token whose running sum passes the goal: each thread sums a
-    // run of tokens, the runs before it are added up, and the one run that
-    // holds the goal is walked
-    const int per = (V + kVerifyThreads - 1) / kVerifyThreads;
-    const int lo = min(tid * per, V), hi = min(lo + per, V);
+    if (held != rejected) form(rejected);
+    __syncthreads();
+    // the first token whose running sum passes the goal: a thread sums a run
+    // of tokens (an odd number, so that the threads' runs fall on different
+    // banks), the runs before it are added up, and the one that holds the
+    // goal is walked
+    const int per = ((chunk + kVerifyThreads - 1) / kVerifyThreads) | 1;
+    const int r0 = min(tid * per, n), r1 = min(r0 + per, n);
     unsigned long long mine = 0;
-    for (int i = lo; i < hi; ++i) mine += fixed(r.at(i));
-    const unsigned long long total = block_sum(mine, tmp);
+    for (int i = r0; i < r1; ++i) mine += fixed(r[i]);
+    const unsigned long long total = cluster_sum(mine);
     unsigned long long upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
         const unsigned long long v = __shfl_up_sync(~0u, upto, o);
         if ((tid & 31) >= o) upto += v;
     }
-    // (block_sum left every warp's sum in tmp)
-    for (int i = 0; i < (tid >> 5); ++i) upto += tmp[i];
-    const unsigned long long u = min((unsigned long long)(unit(__ldg(a.u_next + b)) * 0x1p31f), 0x7FFFFFFFull);
+    // (cluster_sum left every warp's sum)
+    for (int i = 0; i < (tid >> 5); ++i) upto += sh.warp[i];
+    upto += before;
+    const unsigned long long u =
+        min((unsigned long long)(unit(__ldg(a.u_next + b)) * 0x1p31f), 0x7FFFFFFFull);
     const unsigned long long goal = (total >> 31) * u + (((total & 0x7FFFFFFFull) * u) >> 31);
-    if (tid == 0) {
-        a.count[b] = got;
-        if (total == 0) a.next[b] = V - 1;
-    }
     if (goal >= upto - mine && goal < upto) {
         unsigned long long sum = upto - mine;
-        int i = lo;
-        for (; i < hi - 1; ++i) {
-            sum += fixed(r.at(i));
+        int i = r0;
+        for (; i < r1 - 1; ++i) {
+            sum += fixed(r[i]);
             if (sum > goal) break;
         }
-        a.next[b] = i;
+        a.next[b] = lo + i;
     }
+    if (rank == 0) {
+        for (int i = tid; i < s.n; i += kVerifyThreads)
+            if (i == 0 || i >= got) a.path[s.first + i] = i ? -1 : 0;
+        if (tid == 0) {
+            a.count[b] = got;
+            if (total == 0) a.next[b] = V - 1;
+        }
+    }
+    cluster.sync();  // no CTA leaves while another may read its sums
 }
 
 cudaError_t verify(const VerifyArgs &a, cudaStream_t s) {
-    kq_verify_kernel<<<a.nseq, kVerifyThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    // CTAs of a sequence: up to 16, each with 4096 words or more; a CTA's run
+    // fits in shared memory up to the largest vocabulary (128 KB)
+    int ctas = 1;
+    while (ctas < kMaxCluster && ctas * 4096 < a.vocab) ctas *= 2;
+    const int chunk = (a.vocab + ctas - 1) / ctas;
+    const int smem = 4 * chunk;
+    static std::mutex mu;
+    static bool configured[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (dev < 0 || dev >= 64 || !configured[dev]) {
+            e = cudaFuncSetAttribute(kq_verify_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     4 * (KQ_MAX_VOCAB / kMaxCluster));
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(kq_verify_kernel,
+                                         cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e != cudaSuccess) return e;
+            if (dev >= 0 && dev < 64) configured[dev] = true;
+        }
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.nseq * ctas));
+    cfg.blockDim = dim3(kVerifyThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kq_verify_kernel, a, chunk);
 }
 
 }  // namespace kqd

@@ -17,7 +17,6 @@ change in value from step to step, so a captured CUDA graph stays valid.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
@@ -30,27 +29,44 @@ MAX_DRAFT = 64
 SCALINGS = {None: 0, "linear": 1, "base": 2, "ramp": 3}
 
 
+# The library's functions, looked up once: the wrappers below run between
+# kernels of a few microseconds.
+_fn = {}
+
+
 def _call(name, *args):
-    st = getattr(_binding.load(), name)(*args)
+    f = _fn.get(name)
+    if f is None:
+        f = _fn[name] = getattr(_binding.load(), name)
+    st = f(*args)
     if st != 0:
         raise KQError(st, name)
 
 
 def _on(stream):
-    """The stream's pointer, and a context in which new tensors belong to it."""
+    """The stream's pointer, and a context in which new tensors belong to it
+    (None: they do already)."""
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream, contextlib.nullcontext()
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()), None
     return stream.cuda_stream, torch.cuda.stream(stream)
 
 
+def _empty(shape, dtype, device, on):
+    if on is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with on:
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _tensor(t, name, dtype, shape=None, dense=True):
+    """The address of a CUDA tensor after the checks."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if dense and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -58,16 +74,16 @@ def _tensor(t, name, dtype, shape=None, dense=True):
 
 
 def _heads(t, name, shape):
-    """Pointer and token stride of f32 [ntok, heads, dim] whose tokens may lie
+    """Address and token stride of f32 [ntok, heads, dim] whose tokens may lie
     apart (a slice of a fused projection's output)."""
     p = _tensor(t, name, torch.float32, shape, dense=False)
-    n, h, d = t.shape
-    s = t.stride()
-    if n == 0:
-        return p, h * d
-    if (d > 1 and s[2] != 1) or (h > 1 and s[1] != d):
+    n, h, d = shape
+    s0, s1, s2 = t.stride()
+    if (d > 1 and s2 != 1) or (h > 1 and s1 != d):
+        if n == 0:
+            return p, h * d
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    return p, s[0] if n > 1 else h * d
+    return p, s0 if n > 1 else h * d
 
 
 class KVCache:
@@ -122,8 +138,7 @@ def rope_table(positions, rot, base=10000.0, scaling=None, factor=1.0, orig=1, f
     if positions < 1 or rot < 2:
         raise ValueError("positions and rot must be positive")
     st, on = _on(stream)
-    with on:
-        table = torch.empty((positions, rot // 2, 2), dtype=torch.float32, device=device)
+    table = _empty((positions, rot // 2, 2), torch.float32, device, on)
     sc = _binding.KqRopeScaling(SCALINGS[scaling], int(orig), float(factor), float(fast),
                                 float(slow), float(magnitude))
     _call("kq_rope_table", int(positions), int(rot), float(base), ctypes.byref(sc),
@@ -132,26 +147,29 @@ def rope_table(positions, rot, base=10000.0, scaling=None, factor=1.0, orig=1, f
 
 
 def _table(table):
-    if table.dim() != 3 or table.shape[2] != 2:
+    s = table.shape
+    if len(s) != 3 or s[2] != 2:
         raise ValueError("table must be [positions, rot / 2, 2]")
-    return _tensor(table, "table", torch.float32), table.shape[0], 2 * table.shape[1]
+    return _tensor(table, "table", torch.float32), s[0], 2 * s[1]
 
 
 def rope(x, positions, table, interleaved=False, inverse=False, out=None, stream=None):
     """x f32 [ntok, heads, dim] with each head's first rot values turned by its
     token's position (int32 [ntok]); rot is the table's.  inverse turns back,
     and is the gradient.  out may be x."""
-    if x.dim() != 3:
+    shape = x.shape
+    if len(shape) != 3:
         raise ValueError("x must be [ntok, heads, dim]")
-    n, h, d = x.shape
-    xp, xs = _heads(x, "x", x.shape)
+    n, h, d = shape
+    xp, xs = _heads(x, "x", shape)
     tp, npos, rot = _table(table)
     pp = _tensor(positions, "positions", torch.int32, (n,))
     st, on = _on(stream)
     if out is None:
-        with on:
-            out = torch.empty((n, h, d), dtype=torch.float32, device=x.device)
-    op, os_ = _heads(out, "out", x.shape)
+        out = _empty(shape, torch.float32, x.device, on)
+        op, os_ = out.data_ptr(), h * d
+    else:
+        op, os_ = _heads(out, "out", shape)
     _call("kq_rope", xp, xs, op, os_, n, h, d, pp, tp, npos, rot, bool(interleaved),
           bool(inverse), st)
     return out
@@ -179,11 +197,10 @@ def kv_read(cache, batch, k=None, v=None, stream=None):
     """The batch's places read back: (k, v) f32 [ntok, kv_heads, head_dim]."""
     shape = (batch.ntok, cache.kv_heads, cache.head_dim)
     st, on = _on(stream)
-    with on:
-        if k is None:
-            k = torch.empty(shape, dtype=torch.float32, device=cache.data.device)
-        if v is None:
-            v = torch.empty(shape, dtype=torch.float32, device=cache.data.device)
+    if k is None:
+        k = _empty(shape, torch.float32, cache.data.device, on)
+    if v is None:
+        v = _empty(shape, torch.float32, cache.data.device, on)
     _call("kq_kv_read", cache._p, batch._p, _tensor(k, "k", torch.float32, shape),
           _tensor(v, "v", torch.float32, shape), st)
     return k, v
@@ -234,20 +251,18 @@ def tree_attention(cache, batch, q, mask=None, scale=None, out=None, workspace=N
     one for the call."""
     if q.dim() != 3:
         raise ValueError("q must be [ntok, q_heads, head_dim]")
-    shape = (batch.ntok, q.shape[1], cache.head_dim)
+    heads = q.shape[1]
+    shape = (batch.ntok, heads, cache.head_dim)
     qp, qs = _heads(q, "q", shape)
     mp = None if mask is None else _tensor(mask, "mask", torch.int64, (batch.ntok,))
     st, on = _on(stream)
     if out is None:
-        with on:
-            out = torch.empty(shape, dtype=torch.float32, device=q.device)
+        out = _empty(shape, torch.float32, q.device, on)
     op = _tensor(out, "out", torch.float32, shape)
     if workspace is None:
-        with on:
-            workspace = torch.empty(attention_workspace_bytes(cache, batch, q.shape[1]),
-                                    dtype=torch.uint8, device=q.device)
+        workspace = _empty(attention_workspace_bytes(cache, batch, heads), torch.uint8, q.device, on)
     wp, wn = _tensor(workspace, "workspace", torch.uint8), workspace.numel()
-    _call("kq_tree_attention", cache._p, batch._p, qp, qs, q.shape[1], mp,
+    _call("kq_tree_attention", cache._p, batch._p, qp, qs, heads, mp,
           cache.head_dim ** -0.5 if scale is None else float(scale), op, wp, wn, st)
     return out
 
@@ -273,13 +288,12 @@ def verify_tree(start, tokens, parents, p, q, u, u_next, max_new, path=None, cou
     pp, ps = rows(p, "p")
     qp, qs = (None, 0) if q is None else rows(q, "q")
     st, on = _on(stream)
-    with on:
-        if path is None:
-            path = torch.empty(ntok, dtype=torch.int32, device=p.device)
-        if count is None:
-            count = torch.empty(nseq, dtype=torch.int32, device=p.device)
-        if next_token is None:
-            next_token = torch.empty(nseq, dtype=torch.int32, device=p.device)
+    if path is None:
+        path = _empty(ntok, torch.int32, p.device, on)
+    if count is None:
+        count = _empty(nseq, torch.int32, p.device, on)
+    if next_token is None:
+        next_token = _empty(nseq, torch.int32, p.device, on)
     _call("kq_verify_tree", nseq, ntok, int(max_new),
           _tensor(start, "start", torch.int32, (nseq + 1,)),
           _tensor(tokens, "tokens", torch.int32, (ntok,)),
