@@ -7,10 +7,24 @@ namespace kqd {
 cudaError_t attn_f16(int dim, const AttnArgs &a, int sms, cudaStream_t s, int64_t *floats);
 cudaError_t attn_q8(int dim, const AttnArgs &a, int sms, cudaStream_t s, int64_t *floats);
 cudaError_t attn_q4(int dim, const AttnArgs &a, int sms, cudaStream_t s, int64_t *floats);
+cudaError_t attn_rows_f16(int dim, const AttnArgs &a, int64_t rows, int sms, cudaStream_t s,
+                          int64_t *floats);
+cudaError_t attn_rows_q8(int dim, const AttnArgs &a, int64_t rows, int sms, cudaStream_t s,
+                         int64_t *floats);
+cudaError_t attn_rows_q4(int dim, const AttnArgs &a, int64_t rows, int sms, cudaStream_t s,
+                         int64_t *floats);
 
 namespace {
+// Rows that a key head of a sequence may have.
+int64_t q_rows(const AttnArgs &a) { return (int64_t)a.q.max_new * a.per; }
+
 cudaError_t of_format(int fmt, int dim, const AttnArgs &a, int sms, cudaStream_t s,
                       int64_t *floats) {
+    const int64_t rows = q_rows(a);
+    if (dim <= 128 && rows > 16)
+        return fmt == KQ_KV_F16  ? attn_rows_f16(dim, a, rows, sms, s, floats)
+               : fmt == KQ_KV_Q8 ? attn_rows_q8(dim, a, rows, sms, s, floats)
+                                 : attn_rows_q4(dim, a, rows, sms, s, floats);
     return fmt == KQ_KV_F16  ? attn_f16(dim, a, sms, s, floats)
            : fmt == KQ_KV_Q8 ? attn_q8(dim, a, sms, s, floats)
                              : attn_q4(dim, a, sms, s, floats);

@@ -18,14 +18,19 @@
 //   3. each warp adds its quarter of the values' width, over all 64 tokens.
 //
 // Arithmetic.  The tensor cores take f16 operands, and codes are exact in
-// f16.  Queries and probabilities are f32, held as two f16 terms hi + lo (22
-// bits): an 8-row tile of them fills the 16 rows of an m16n8k16 operand, hi
-// above lo, so that one MMA forms both products and the two halves of its
-// result are added in f32.  A query row is scaled by a power of two first
-// (its largest magnitude below 2^15), probabilities times the values' scale
-// likewise by page and group.  Scales of quantised keys multiply the f32 sums
-// of their group.  Each page's sums start at zero and are added to the
-// running ones in f32, with the running maximum's correction.
+// f16.  Keys and values are the operand of 16 rows (tokens, or places of the
+// values' width), four rows of queries or probabilities that of eight
+// columns: they are f32, held as two f16 terms hi + lo (22 bits) side by
+// side, so that one m16n8k16 MMA forms both products and a lane adds the two
+// in f32.  (Eight rows as the operand of 16, hi above lo, gave half the useful
+// work to an MMA where a key head has four rows, and the rate of these MMAs,
+// one in eight clocks an SM, was what bounded the kernel.)  A query row is
+// scaled by a power of two first (its largest magnitude below 2^15), the
+// values' scales by page and group, probabilities by 2^15.  Scales of
+// quantised keys multiply the f32 sums of their group; those of values
+// multiply the probabilities' terms, whose rounding joins the lower term.
+// Each page's sums start at zero and are added to the running ones in f32,
+// with the running maximum's correction.
 //
 // The k index inside an MMA is any order that both operands share.  A lane
 // takes eight consecutive values of a key (an octet) or 16 tokens of a value
@@ -45,7 +50,7 @@
 
 namespace kqd {
 
-constexpr int kMaxGroups = 4;
+constexpr int kMaxGroups = 5;
 constexpr int kMaxSlots = 8;  // of a group's ring; a slot holds a page's keys or values
 
 struct AttnArgs {
@@ -68,27 +73,35 @@ __host__ __device__ constexpr int part_floats(int rb, int d) { return rb * (d + 
 
 // ------------------------------------------------------------ shared memory
 // common | queries | per group: ring, probabilities, maxima
+struct RunShared {
+    long long scan[32];
+    long long off;
+    int seq;
+};
 struct AttnCommon {
     uint64_t rowmask[32];
-    uint64_t bars[kMaxGroups * kMaxSlots];
-    long long scan[16];
-    long long start_unit;
-    int start_seq;
+    uint64_t bars[kMaxGroups * kMaxSlots];   // a slot's copy has arrived
+    uint64_t empty[kMaxGroups * kMaxSlots];  // and has been used
+    RunShared run;
     int dead;                              // a wait has expired
     int badpage[kMaxGroups * kMaxSlots];   // the slot's page is not valid
     float rowfactor[32];
     float ml[kMaxGroups][5][32];           // group's row maxima, warps' row sums
 };
-template <int FMT, int D, int MT>
+template <int FMT, int D, int NT>
 struct AttnSmem {
-    static constexpr int kRows = 8 * MT;
+    static constexpr int kRows = 4 * NT;
     static constexpr int kWg = 4;             // warps of a group
-    static constexpr int kGroups = 16 / kWg;  // groups of an SM
+// Groups of an SM: what registers (with the producer warp: 80 a thread for
+    // 20 warps, 96 for 16, 128 for 12) and, for f16, shared memory hold.
+    // One tile of an 8-bit cache: 157 us with four groups, 150 with five
+    // (32 sequences of 16384 tokens at most, 32 / 8 heads).
+    static constexpr int kGroups = NT == 1 ? (FMT == KQ_KV_F16 ? 4 : 5) : NT == 2 ? 4 : 3;
     static constexpr int kHalf = Kv<FMT, D>::kV;  // bytes of a slot
     static constexpr int kCommon = (sizeof(AttnCommon) + 127) / 128 * 128;
     static constexpr int kQ = kRows * D * 4;
-    static constexpr int kP = kRows * kPage * 4;
-    static constexpr int kMax = kWg * kRows * 4;
+    static constexpr int kP = 2 * 2 * kRows * kPage * 2;  // hi and lo columns, two pages
+    static constexpr int kMax = 2 * kWg * kRows * 4;
     static __host__ __device__ int group(int nslot) { return nslot * kHalf + kP + kMax; }
     static __host__ __device__ int total(int ng, int nslot) {
         return kCommon + kQ + ng * group(nslot);
@@ -151,33 +164,20 @@ __device__ __forceinline__ void codes4(uint32_t w, uint32_t (&b)[4]) {
     b[2] = bits_of(__hsub2(half2_of(nibble(v, 0x000F000Fu, 0x64086408u)), off));
     b[3] = bits_of(__hfma2(half2_of(nibble(v, 0x00F000F0u, 0x64806480u)), div, off16));
 }
-// Element pairs of the two k-steps of eight: pair h of step s.
-template <int FMT>
-__device__ __forceinline__ constexpr int pair_first(int s, int h) {
-    return FMT == KQ_KV_Q4 ? 2 * s + h : 4 * s + 2 * h;
-}
-template <int FMT>
-__device__ __forceinline__ constexpr int pair_second(int s, int h) {
-    return FMT == KQ_KV_Q4 ? 2 * s + h + 4 : 4 * s + 2 * h + 1;
-}
-
 template <int THREADS>
 __device__ __forceinline__ void group_sync(int g) {
     asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "n"(THREADS) : "memory");
 }
 
-// Probabilities in shared memory, [row][16 chunks of 4 tokens]: lane c's
-// tokens of a value (Kv order) are chunks 4 i + c, i = 0..3; odd rows are
-// turned by half a line.
+// Probabilities in shared memory: columns (row hi, row lo, next row hi, ...)
+// of 64 f16 in the order in which the values' operand takes the tokens: a
+// lane quarter's 16 are two chunks of eight; odd columns are turned by one.
 template <int FMT>
-__device__ __forceinline__ int p_at(int row, int tok) {
-    int c, i;
-    if (FMT == KQ_KV_F16) {
-        c = (tok >> 3) & 3, i = 2 * (tok >> 5) + ((tok >> 2) & 1);
-    } else {
-        c = tok >> 4, i = (tok >> 2) & 3;
-    }
-    return row * kPage + (((4 * i + c) ^ ((row & 1) << 2)) << 2) + (tok & 3);
+__device__ __forceinline__ int p_at(int col, int tok) {
+    int chunk = tok >> 3, k = tok & 7;
+    if (FMT == KQ_KV_F16) chunk = 2 * (chunk & 3) + (chunk >> 2);
+    if (FMT == KQ_KV_Q4) k = 2 * (k & 3) + (k >> 2);  // pairs (0, 4), (1, 5) ...
+    return col * kPage + ((chunk ^ (col & 1)) << 3) + k;
 }
 
 // ------------------------------------------------------------------- units
@@ -188,9 +188,9 @@ __device__ __forceinline__ int64_t pages_of(const Seqs &q, const Seq &s) {
     const int64_t n = ((int64_t)s.ctx + s.n + kPage - 1) / kPage;
     return s.ctx / kPage > q.max_pages ? q.max_pages + 1 : n;
 }
-template <int RB>
-__device__ __forceinline__ int64_t units_of(const AttnArgs &a, const Seq &s, int &blocks) {
-    blocks = (s.n * a.per + RB - 1) / RB;
+// (rb: rows of a block)
+__device__ __forceinline__ int64_t units_of(const AttnArgs &a, const Seq &s, int rb, int &blocks) {
+    blocks = (s.n * a.per + rb - 1) / rb;
     return s.n ? pages_of(a.q, s) * blocks * a.q.heads : 0;
 }
 // CTA that works on unit u, of `total` cut into n runs.
@@ -199,91 +199,109 @@ __device__ __forceinline__ int cta_of(long long u, long long total, int n) {
     return (int)(u < rem * (base + 1) ? u / (base + 1) : rem + (u - rem * (base + 1)) / base);
 }
 
+// This CTA's run [u0, u1) of all units; it begins at unit `off` of sequence
+// `seq`.  Every thread of the block takes part (nthreads, a multiple of 32).
+struct Run {
+    long long u0, u1, total, off;
+    int seq;
+};
+__device__ __forceinline__ Run run_of(const AttnArgs &a, int rb, int nthreads, RunShared &sh) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int each = (a.q.nseq + nthreads - 1) / nthreads;
+    const int b0 = min(tid * each, a.q.nseq), b1 = min(b0 + each, a.q.nseq);
+    long long mine = 0;
+    int blocks;
+    for (int b = b0; b < b1; ++b) mine += units_of(a, seq_of(a.q, b), rb, blocks);
+    long long upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const long long v = __shfl_up_sync(~0u, upto, o);
+        if (lane >= o) upto += v;
+    }
+    if (lane == 31) sh.scan[tid >> 5] = upto;
+    __syncthreads();
+    Run r;
+    r.total = 0;
+    for (int i = 0; i < nthreads / 32; ++i) {
+        if (i == (tid >> 5)) upto += r.total;
+        r.total += sh.scan[i];
+    }
+    const long long base = r.total / gridDim.x, rem = r.total % gridDim.x, k = blockIdx.x;
+    r.u0 = k * base + min(k, rem);
+    r.u1 = r.u0 + base + (k < rem ? 1 : 0);
+    if (r.u0 < r.u1 && r.u0 >= upto - mine && r.u0 < upto) {
+        long long at = upto - mine;
+        int b = b0;
+        for (;; ++b) {
+            const long long n = units_of(a, seq_of(a.q, b), rb, blocks);
+            if (r.u0 < at + n) break;
+            at += n;
+        }
+        sh.seq = b;
+        sh.off = r.u0 - at;
+    }
+    if (tid == 0) a.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
+    __syncthreads();
+    r.seq = sh.seq;
+    r.off = sh.off;
+    return r;
+}
+
 // ------------------------------------------------------------------ kernel
-template <int FMT, int D, int MT>
-__global__ void __launch_bounds__(AttnSmem<FMT, D, MT>::kGroups * AttnSmem<FMT, D, MT>::kWg * 32, 1)
+template <int FMT, int D, int NT>
+__global__ void __launch_bounds__(AttnSmem<FMT, D, NT>::kGroups * AttnSmem<FMT, D, NT>::kWg * 32 + 32, 1)
     kq_attn_kernel(const __grid_constant__ AttnArgs a) {
     using L = Kv<FMT, D>;
-    using M = AttnSmem<FMT, D, MT>;
+    using M = AttnSmem<FMT, D, NT>;
     constexpr int RB = M::kRows;
-    constexpr int kSteps = D / 16;          // k-steps of a logit
     constexpr int kWg = M::kWg, kGroupThreads = 32 * kWg;
-    constexpr int kTok = kPage / kWg, J = kTok / 8;  // tokens of a warp in part 1, in tiles
+    static_assert(kPage / kWg == 16, "one tile of tokens a warp in part 1");
     constexpr int kSlice = D / kWg;         // values of a warp in part 3
-    constexpr int kTiles = kSlice / 8;      // its n-tiles
+    constexpr int kTiles = kSlice / 16;     // its tiles
     constexpr int kSliceGroups = kSlice > kGroup ? kSlice / kGroup : 1;
     constexpr int kTilesG = kTiles / kSliceGroups;
 
     extern __shared__ __align__(128) uint8_t smem[];
     AttnCommon &cm = *reinterpret_cast<AttnCommon *>(smem);
-    uint4 *qs = reinterpret_cast<uint4 *>(smem + M::kCommon);  // [tile][k-step][lane]
+    uint4 *qs = reinterpret_cast<uint4 *>(smem + M::kCommon);  // [tile][group][lane]
     const int tid = threadIdx.x, lane = tid & 31;
-    const int g = tid / kGroupThreads, w = (tid >> 5) % kWg;
-    const int n8 = lane >> 2, c = lane & 3;  // row (or column) of an operand, and its quarter
-    const int nthreads = a.ng * kGroupThreads;
+    const int ntail = a.ng * kGroupThreads;   // threads of the groups
+    const bool producer = tid >= ntail;       // the last warp issues the copies
+    // (in the producer warp lane g serves group g)
+    const int g = producer ? min(tid - ntail, a.ng - 1) : tid / kGroupThreads;
+    const int w = (tid >> 5) % kWg;
+    const int n8 = lane >> 2, c = lane & 3;  // row or column of an operand, and its quarter;
+                                             // in results: token or place n8 (+ 8), row c of four
+    const int nthreads = ntail + 32;
     uint8_t *gbase = smem + M::kCommon + M::kQ + g * M::group(a.nslot);
-    float *ps = reinterpret_cast<float *>(gbase + a.nslot * M::kHalf);
-    float *smax = ps + RB * kPage;  // [warp][row]
+    __half *ps = reinterpret_cast<__half *>(gbase + a.nslot * M::kHalf);
+    float *smax = reinterpret_cast<float *>(gbase + a.nslot * M::kHalf + M::kP);  // [warp][row]
     const uint32_t ring = kq::smem_addr(gbase);
     const uint32_t bars = kq::smem_addr(&cm.bars[g * kMaxSlots]);
 
     if (tid < a.ng * kMaxSlots && (tid % kMaxSlots) < a.nslot) {
         kq::mbar_init(kq::smem_addr(&cm.bars[tid]), 1);
+        kq::mbar_init(kq::smem_addr(&cm.empty[tid]), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (tid == 0) cm.dead = 0;
     kq::allow_dependents();  // kq_attn_join waits for this kernel's end
 
-    // ---- this CTA's run of units
-    long long u0, u1, total;
-    {
-        const int each = (a.q.nseq + nthreads - 1) / nthreads;
-        const int b0 = min(tid * each, a.q.nseq), b1 = min(b0 + each, a.q.nseq);
-        long long mine = 0;
-        int blocks;
-        for (int b = b0; b < b1; ++b) mine += units_of<RB>(a, seq_of(a.q, b), blocks);
-        long long upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-            const long long v = __shfl_up_sync(~0u, upto, o);
-            if (lane >= o) upto += v;
-        }
-        if (lane == 31) cm.scan[tid >> 5] = upto;
-        __syncthreads();
-        total = 0;
-        for (int i = 0; i < nthreads / 32; ++i) {
-            if (i == (tid >> 5)) upto += total;
-            total += cm.scan[i];
-        }
-        const long long base = total / gridDim.x, rem = total % gridDim.x, k = blockIdx.x;
-        u0 = k * base + min(k, rem);
-        u1 = u0 + base + (k < rem ? 1 : 0);
-        if (u0 < u1 && u0 >= upto - mine && u0 < upto) {
-            long long at = upto - mine;
-            int b = b0;
-            for (;; ++b) {
-                const long long n = units_of<RB>(a, seq_of(a.q, b), blocks);
-                if (u0 < at + n) break;
-                at += n;
-            }
-            cm.start_seq = b;
-            cm.start_unit = u0 - at;
-        }
-        if (tid == 0) a.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
-        __syncthreads();
-    }
-    if (u0 >= u1) return;
+    const Run run = run_of(a, RB, nthreads, cm.run);
+    if (run.u0 >= run.u1) return;
 
-    // the group's ring: next slot to fill and to use, and the use's parity
-    int fill = 0, use = 0;
-    uint32_t parity = 0, op0 = 0;  // op0: copies before this segment
-    int b = cm.start_seq;
-    long long off = cm.start_unit;
-    for (long long u = u0; u < u1 && b < a.q.nseq;) {
+    // the group's ring: next slot to fill or to use, its turn's parity, and
+    // the first slot that is in use and not yet handed back
+    int use = 0, back = 0;
+    uint32_t parity = 0;
+    int primed = 0;  // (producer) slots of the ring that have been filled once
+    int b = run.seq;
+    long long off = run.off;
+    for (long long u = run.u0; u < run.u1 && b < a.q.nseq;) {
         // ---- the segment: pages [pg0, pg0 + npg) of one item
         int blocks;
         Seq s = seq_of(a.q, b);
-        const long long units = units_of<RB>(a, s, blocks);
+        const long long units = units_of(a, s, RB, blocks);
         if (off >= units) {
             ++b, off = 0;
             continue;
@@ -291,41 +309,57 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, MT>::kGroups * AttnSmem<FMT, 
         const int pages = (int)pages_of(a.q, s);
         const int item = (int)(off / pages);
         const int pg0 = (int)(off - (long long)item * pages);
-        const int npg = (int)min((long long)(pages - pg0), u1 - u);
+        const int npg = (int)min((long long)(pages - pg0), run.u1 - u);
         const int head = item / blocks, row0 = (item - head * blocks) * RB;
         const int nrows = min(RB, s.n * a.per - row0);
         const int count = npg > g ? (npg - g + a.ng - 1) / a.ng : 0;  // the group's pages
 
-        // ---- copies: warp 0 of the group looks up 32 pages at a time and
-        // one lane issues
-        int64_t found = -1;
-        int live = 0;  // copies issued (lane 0 of warp 0)
-        auto copy = [&](int i) {  // copy i of the segment: keys, then values, page by page
-            const int k = i >> 1;
-            if ((i & 1) == 0 && (k & 31) == 0)
-                found = k + lane < count ? page_of(a.q, b, pg0 + g + (int64_t)(k + lane) * a.ng) : -1;
-            const int64_t page = __shfl_sync(~0u, found, k & 31);
-            // (once a wait has expired nothing more is issued or waited for)
-            if (lane == 0 && !*(volatile int *)&cm.dead) {
-                live = i + 1;
-                const uint32_t bar = bars + 8 * fill;
-                cm.badpage[g * kMaxSlots + fill] = page < 0;
-                kq::mbar_expect_tx(bar, M::kHalf);
-                kq::bulk_g2s(ring + fill * M::kHalf,
-                             a.q.data + (max(page, (int64_t)0) * a.q.heads + head) * L::kBlock +
-                                 (i & 1) * M::kHalf,
-                             M::kHalf, bar);
-            }
-            if (++fill == a.nslot) fill = 0;
-            __syncwarp();
-        };
+        // ---- the producer warp: lane g copies group g's keys and values into
+        // its ring, in the order of their use: the first keys, then the next
+        // page's keys and a page's values by turns, the last values
+        const int mine = producer && tid - ntail < a.ng ? 2 * count : 0;
         int issued = 0;
-        if (w == 0)
-            for (; issued < min(2 * count, a.nslot); ++issued) copy(issued);
+        const int use0 = use;
+        const uint32_t parity0 = parity;
+        int64_t kpage = -1, vpage = -1, next = mine ? page_of(a.q, b, pg0 + g) : -1;
+        auto pump = [&](int until) {  // (the whole warp)
+            const unsigned long long t0 = kq::global_ns();
+            while (__any_sync(~0u, issued < until)) {
+                if (__any_sync(~0u, *(volatile int *)&cm.dead)) break;
+                bool late = false;
+                // (a slot's first filling waits for nothing)
+                if (issued < until &&
+                    (primed < a.nslot ||
+                     kq::mbar_test(kq::smem_addr(&cm.empty[g * kMaxSlots + use]), parity ^ 1))) {
+                    const int i = issued++;
+                    const bool values = i == mine - 1 || (i > 0 && (i & 1) == 0);
+                    if (!values) {
+                        vpage = kpage, kpage = next;
+                        const int k = (i + 1) / 2 + 1;  // the next page, looked up ahead
+                        if (k < count) next = page_of(a.q, b, pg0 + g + (int64_t)k * a.ng);
+                    }
+                    const int64_t page = !values || i == mine - 1 ? kpage : vpage;
+                    const uint32_t bar = bars + 8 * use;
+                    cm.badpage[g * kMaxSlots + use] = page < 0;
+                    kq::mbar_expect_tx(bar, M::kHalf);
+                    kq::bulk_g2s(ring + use * M::kHalf,
+                                 a.q.data + (max(page, (int64_t)0) * a.q.heads + head) * L::kBlock +
+                                     (values ? M::kHalf : 0),
+                                 M::kHalf, bar);
+                    if (primed < a.nslot) ++primed;
+                    if (++use == a.nslot) use = 0, parity ^= 1;
+                } else {
+                    // (the groups' own waits expire first, and say so)
+                    late = kq::global_ns() - t0 > 2 * kq::kWaitLimitNs;
+                }
+                if (__any_sync(~0u, late)) break;
+            }
+        };
+        if (producer) pump(min(mine, a.nslot));
 
         // ---- queries: rows scaled by a power of two, hi and lo terms, laid
         // out as the operands of part 1
-        for (int r = tid >> 5; r < RB; r += nthreads / 32) {
+        for (int r = tid >> 5; !producer && r < RB; r += ntail / 32) {
             const bool on = r < nrows;
             const int tok = on ? (row0 + r) / a.per : 0, hq = on ? (row0 + r) % a.per : 0;
             const float *row = a.x + (s.first + tok) * a.x_stride + (head * a.per + hq) * D;
@@ -368,20 +402,36 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, MT>::kGroups * AttnSmem<FMT, 
                     x[2] = odd ? r1 : m1, x[3] = odd ? m1 : r1;
                 }
                 if (e < D) {
-                    uint4 o;
-                    split(x[0], x[1], o.x, o.y);
-                    split(x[2], x[3], o.z, o.w);
+                    uint2 hi, lo;
+                    split(x[0], x[1], hi.x, lo.x);
+                    split(x[2], x[3], hi.y, lo.y);
                     const int octet = e >> 3;
-                    const int step = 2 * (octet >> 2) + ((e >> 2) & 1);
-                    qs[((r >> 3) * kSteps + step) * 32 + 4 * (r & 7) + (octet & 3)] = o;
+                    uint2 *o = reinterpret_cast<uint2 *>(
+                        qs + ((r >> 2) * L::kGroups + (octet >> 2)) * 32 + 8 * (r & 3) + (octet & 3));
+                    o[(e >> 2) & 1] = hi;      // column 2 r
+                    o[8 + ((e >> 2) & 1)] = lo;  // column 2 r + 1: four lanes on
                 }
             }
         }
         __syncthreads();
+        if (producer) {
+            pump(mine);
+            if (*(volatile int *)&cm.dead) {
+                // after an expired wait: no copy may land later than this
+                int slot = use0;
+                uint32_t ph = parity0;
+                for (int k = 0; k < issued; ++k) {
+                    if (k >= issued - a.nslot)
+                        kq::mbar_wait(bars + 8 * slot, ph, kq::kWaitLimitNs);
+                    if (++slot == a.nslot) slot = 0, ph ^= 1;
+                }
+            }
+            __syncwarp();
+        }
 
-        float m[MT], l[MT], O[MT][kTiles][2];
+        float m[NT], l[NT], O[NT][kTiles][2];  // rows 4 t + c
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
+        for (int t = 0; t < NT; ++t) {
             m[t] = -INFINITY, l[t] = 0.f;
 #pragma unroll
             for (int i = 0; i < kTiles; ++i) O[t][i][0] = O[t][i][1] = 0.f;
@@ -397,39 +447,44 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, MT>::kGroups * AttnSmem<FMT, 
             if (++use == a.nslot) use = 0, parity ^= 1;
             return slot;
         };
-        for (int k = 0; k < count; ++k) {
-            const int pg = pg0 + g + k * a.ng;
-            const int left = s.ctx - pg * kPage;      // committed tokens of the page and after
-            const bool edge = left < kPage;           // new tokens, or the end
-            // bit t: token t may be attended by row r (edge pages)
-            auto allowed = [&](int r) -> uint64_t {
-                const uint64_t nw = cm.rowmask[r] & (~0ull >> (64 - s.n));
-                if (left <= 0) return -left < 64 ? nw >> -left : 0;
-                return (nw << left) | ~(~0ull << left);
-            };
-            // ---- 1. logits of tokens 16 w .. 16 w + 15
+        // A turn forms page k's logits, adds page k - 1's values and forms page
+        // k's probabilities, with one barrier: maxima and probabilities are
+        // kept for two pages by turns.
+        float alpha[NT];
+        // bit t: row r may attend token t of a page with `left` committed
+        // tokens in it and after
+        auto allowed = [&](int left, int r) -> uint64_t {
+            const uint64_t nw = cm.rowmask[r] & (~0ull >> (64 - s.n));
+            if (left <= 0) return -left < 64 ? nw >> -left : 0;
+            return left >= kPage ? ~0ull : (nw << left) | ~(~0ull << left);
+        };
+        for (int k = 0; k <= (count && !producer ? count : -1); ++k) {
+            float S[NT][2];
+            float *sm = smax + (k & 1) * kWg * RB;
+            if (k < count) {
+            const int left = s.ctx - (pg0 + g + k * a.ng) * kPage;
+            const bool edge = left < kPage;  // new tokens, or the end
+            // ---- 1. logits of tokens 16 w + n8 (+ 8)
             const int ks = arrived();
             const uint8_t *kb = gbase + ks * M::kHalf;
             const bool badpage = cm.badpage[g * kMaxSlots + ks];
-            float S[MT][J][2];
             {
-                float acc[MT][J][4];
+                float acc[NT][4];
                 constexpr int kLane = L::kSlabBytes / 4;  // bytes of a lane in a slab
 #pragma unroll
-                for (int t = 0; t < MT; ++t)
-#pragma unroll
-                    for (int j = 0; j < J; ++j) {
-                        S[t][j][0] = S[t][j][1] = 0.f;
-                        if (!L::kQuant) acc[t][j][0] = acc[t][j][1] = acc[t][j][2] = acc[t][j][3] = 0.f;
-                    }
+                for (int t = 0; t < NT; ++t) {
+                    S[t][0] = S[t][1] = 0.f;
+                    acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
+                }
 #pragma unroll
                 for (int sl = 0; sl < L::kSlabs; ++sl) {
-                    uint32_t raw[J][kLane / 4];
-                    uint32_t skw[J][2][(L::kSlabGroups + 1) / 2];  // scales, two groups a word
+                    uint32_t raw[2][kLane / 4];
+                    uint32_t skw[2][(L::kSlabGroups + 1) / 2];  // scales, two groups a word
 #pragma unroll
-                    for (int j = 0; j < J; ++j) {
-                        const uint8_t *p = kb + sl * kPage * L::kSlabBytes +
-                                           (kTok * w + 8 * j + n8) * L::kSlabBytes + c * kLane;
+                    for (int j = 0; j < 2; ++j) {
+                        const int tok = 16 * w + 8 * j + n8;
+                        const uint8_t *p =
+                            kb + sl * kPage * L::kSlabBytes + tok * L::kSlabBytes + c * kLane;
                         if constexpr (kLane == 16) {
                             const uint4 v = *reinterpret_cast<const uint4 *>(p);
                             raw[j][0] = v.x, raw[j][1] = v.y, raw[j][2] = v.z, raw[j][3] = v.w;
@@ -438,26 +493,21 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, MT>::kGroups * AttnSmem<FMT, 
                             raw[j][0] = v.x, raw[j][1] = v.y;
                         }
                         if constexpr (L::kQuant) {
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const uint8_t *sp = kb + L::k_scale(kTok * w + 8 * j + 2 * c + i,
-                                                                    sl * L::kSlabGroups);
-                                if constexpr (L::kSlabGroups == 4) {
-                                    const uint2 v = *reinterpret_cast<const uint2 *>(sp);
-                                    skw[j][i][0] = v.x, skw[j][i][1] = v.y;
-                                } else {
-                                    skw[j][i][0] = *reinterpret_cast<const uint32_t *>(sp);
-                                }
+                            const uint8_t *sp = kb + L::k_scale(tok, sl * L::kSlabGroups);
+                            if constexpr (L::kSlabGroups == 4) {
+                                const uint2 v = *reinterpret_cast<const uint2 *>(sp);
+                                skw[j][0] = v.x, skw[j][1] = v.y;
+                            } else {
+                                skw[j][0] = *reinterpret_cast<const uint32_t *>(sp);
                             }
                         }
                     }
 #pragma unroll
                     for (int gl = 0; gl < L::kSlabGroups; ++gl) {
-                        const int gg = sl * L::kSlabGroups + gl;
-                        uint32_t bb[J][4];
-                        float sk[J][2];
+                        uint32_t bb[2][4];
+                        float sk[2];
 #pragma unroll
-                        for (int j = 0; j < J; ++j) {
+                        for (int j = 0; j < 2; ++j) {
                             if constexpr (FMT == KQ_KV_F16) {
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) bb[j][i] = raw[j][i];
@@ -468,95 +518,68 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, MT>::kGroups * AttnSmem<FMT, 
                                 codes4(raw[j][gl], bb[j]);
                             }
                             if constexpr (L::kQuant) {
-#pragma unroll
-                                for (int i = 0; i < 2; ++i) {
-                                    const __half2 h = half2_of(skw[j][i][gl / 2]);
-                                    sk[j][i] = gl & 1 ? __high2float(h) : __low2float(h);
-                                }
+                                const __half2 h = half2_of(skw[j][gl / 2]);
+                                sk[j] = gl & 1 ? __high2float(h) : __low2float(h);
                             }
                         }
+                        const uint4 k0 = make_uint4(bb[0][0], bb[1][0], bb[0][1], bb[1][1]);
+                        const uint4 k1 = make_uint4(bb[0][2], bb[1][2], bb[0][3], bb[1][3]);
 #pragma unroll
-                        for (int t = 0; t < MT; ++t) {
-                            const uint4 q0 = qs[(t * kSteps + 2 * gg) * 32 + lane];
-                            const uint4 q1 = qs[(t * kSteps + 2 * gg + 1) * 32 + lane];
-#pragma unroll
-                            for (int j = 0; j < J; ++j) {
-                                if constexpr (L::kQuant) {
-                                    float d[4] = {0.f, 0.f, 0.f, 0.f};
-                                    mma(d, q0, bb[j][0], bb[j][1]);
-                                    mma(d, q1, bb[j][2], bb[j][3]);
-                                    S[t][j][0] = fmaf(sk[j][0], d[0] + d[2], S[t][j][0]);
-                                    S[t][j][1] = fmaf(sk[j][1], d[1] + d[3], S[t][j][1]);
-                                } else {
-                                    mma(acc[t][j], q0, bb[j][0], bb[j][1]);
-                                    mma(acc[t][j], q1, bb[j][2], bb[j][3]);
-                                }
+                        for (int t = 0; t < NT; ++t) {
+                            const uint4 q = qs[(t * L::kGroups + sl * L::kSlabGroups + gl) * 32 + lane];
+                            if constexpr (L::kQuant) {
+                                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                                mma(d, k0, q.x, q.y);
+                                mma(d, k1, q.z, q.w);
+                                S[t][0] = fmaf(sk[0], d[0] + d[1], S[t][0]);
+                                S[t][1] = fmaf(sk[1], d[2] + d[3], S[t][1]);
+                            } else {
+                                mma(acc[t], k0, q.x, q.y);
+                                mma(acc[t], k1, q.z, q.w);
                             }
                         }
                     }
                 }
                 if constexpr (!L::kQuant) {
 #pragma unroll
-                    for (int t = 0; t < MT; ++t)
-#pragma unroll
-                        for (int j = 0; j < J; ++j) {
-                            S[t][j][0] = acc[t][j][0] + acc[t][j][2];
-                            S[t][j][1] = acc[t][j][1] + acc[t][j][3];
-                        }
+                    for (int t = 0; t < NT; ++t) {
+                        S[t][0] = acc[t][0] + acc[t][1];
+                        S[t][1] = acc[t][2] + acc[t][3];
+                    }
                 }
             }
-            // ---- 2. row maxima, probabilities
+            // ---- 2. row maxima
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                const float f = badpage ? quiet_nan() : cm.rowfactor[8 * t + n8];
-#pragma unroll
-                for (int j = 0; j < J; ++j)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        S[t][j][i] *= f;
+            for (int t = 0; t < NT; ++t) {
+                const float f = badpage ? quiet_nan() : cm.rowfactor[4 * t + c];
+                S[t][0] *= f, S[t][1] *= f;
                 if (edge) {
-                    const uint32_t ok = (uint32_t)(allowed(8 * t + n8) >> (kTok * w + 2 * c));
-#pragma unroll
-                    for (int j = 0; j < J; ++j)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            if (!((ok >> (8 * j + i)) & 1)) S[t][j][i] = -INFINITY;
+                    const uint64_t ok = allowed(left, 4 * t + c) >> (16 * w + n8);
+                    if (!(ok & 1)) S[t][0] = -INFINITY;
+                    if (!(ok & 256)) S[t][1] = -INFINITY;
                 }
-                float v = fmaxf(S[t][0][0], S[t][0][1]);
-#pragma unroll
-                for (int j = 1; j < J; ++j) v = fmaxf(v, fmaxf(S[t][j][0], S[t][j][1]));
-                v = fmaxf(v, __shfl_xor_sync(~0u, v, 1));
-                v = fmaxf(v, __shfl_xor_sync(~0u, v, 2));
-                if (c == 0) smax[w * RB + 8 * t + n8] = v;
+                float v = fmaxf(S[t][0], S[t][1]);
+                v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
+                v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
+                v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
+                if (n8 == 0) sm[w * RB + 4 * t + c] = v;
+            }
             }
             group_sync<kGroupThreads>(g);
-            // every warp is done with these keys and the values before them
-            if (w == 0)
-                for (; issued < min(2 * count, 2 * k + 1 + a.nslot); ++issued) copy(issued);
-            float alpha[MT];
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                const int r = 8 * t + n8;
-                float now = m[t];
-#pragma unroll
-                for (int i = 0; i < kWg; ++i) now = fmaxf(now, smax[i * RB + r]);
-                const float base = now == -INFINITY ? 0.f : now;
-                alpha[t] = exp2_of(m[t] - base);
-                m[t] = now;
-                const float high = base - 15.f;  // probabilities (and l, O) times 2^15
-                float sum = 0.f;
-#pragma unroll
-                for (int j = 0; j < J; ++j) {
-                    const float p0 = exp2_of(S[t][j][0] - high), p1 = exp2_of(S[t][j][1] - high);
-                    sum += p0 + p1;
-                    *reinterpret_cast<float2 *>(ps + p_at<FMT>(r, kTok * w + 8 * j + 2 * c)) =
-                        make_float2(p0, p1);
+            // every warp is done with page k's keys and page k - 2's values
+            if (w == 0 && lane == 0) {
+                const int n = (k < count) + (k > 1);
+                for (int i = 0; i < n; ++i) {
+                    kq::mbar_arrive(kq::smem_addr(&cm.empty[g * kMaxSlots + back]));
+                    if (++back == a.nslot) back = 0;
                 }
-                l[t] = fmaf(l[t], alpha[t], sum);
             }
+            if (k > 0) {
+            const int left = s.ctx - (pg0 + g + (k - 1) * a.ng) * kPage;
+            const bool edge = left < kPage;
+            const __half *pv = ps + ((k - 1) & 1) * 2 * RB * kPage;
             // ---- 3. values kSlice w .. of all 64 tokens
             const int vs = arrived();
-            group_sync<kGroupThreads>(g);
             // (offsets of Kv count from the block's start; the slot starts at
             // the values)
             const uint8_t *vb = gbase + vs * M::kHalf - L::kV;
@@ -614,7 +637,7 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, MT>::kGroups * AttnSmem<FMT, 
                     // (one pass over the slice's values, on edge pages only)
                     uint32_t b16 = 0;
 #pragma unroll 1
-                    for (int nt = 0; nt < kTiles; ++nt) {
+                    for (int nt = 0; nt < 2 * kTiles; ++nt) {
                         const int e = w * kSlice + 8 * nt + n8;
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
@@ -640,82 +663,96 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, MT>::kGroups * AttnSmem<FMT, 
                         keep[i] = (b16 >> (2 * i) & 1 ? 0u : 0xFFFFu) |
                                   (b16 >> (2 * i) & 2 ? 0u : 0xFFFF0000u);
                 }
-                uint4 pa[MT][4];  // operands of the four k-steps
+                // the slice's values, as operands of the four k-steps
+                uint4 vv[kTilesG][4];
 #pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    const int r = 8 * t + n8;
-                    float p[16];
+                for (int mt = 0; mt < kTilesG; ++mt) {
+                    uint32_t x[2][8];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 v = *reinterpret_cast<const float4 *>(
-                            ps + r * kPage + (((4 * i + c) ^ ((r & 1) << 2)) << 2));
-                        p[4 * i] = v.x, p[4 * i + 1] = v.y, p[4 * i + 2] = v.z, p[4 * i + 3] = v.w;
+                    for (int h = 0; h < 2; ++h) {
+                        const int e = w * kSlice + 16 * (sg * kTilesG + mt) + 8 * h + n8;
+                        if constexpr (FMT == KQ_KV_F16) {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const uint4 v = *reinterpret_cast<const uint4 *>(
+                                    vb + L::v_word(e, token(8 * i) / 2));
+                                x[h][4 * i] = v.x, x[h][4 * i + 1] = v.y;
+                                x[h][4 * i + 2] = v.z, x[h][4 * i + 3] = v.w;
+                            }
+                            if (edge) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) x[h][i] &= keep[i];
+                            }
+                        } else if constexpr (FMT == KQ_KV_Q8) {
+                            const uint4 v = *reinterpret_cast<const uint4 *>(vb + L::v_word(e, 4 * c));
+                            codes8(v.x, x[h][0], x[h][1]);
+                            codes8(v.y, x[h][2], x[h][3]);
+                            codes8(v.z, x[h][4], x[h][5]);
+                            codes8(v.w, x[h][6], x[h][7]);
+                        } else {
+                            const uint2 v = *reinterpret_cast<const uint2 *>(vb + L::v_word(e, 2 * c));
+                            uint32_t y[4];
+                            codes4(v.x, y);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) x[h][i] = y[i];
+                            codes4(v.y, y);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) x[h][4 + i] = y[i];
+                        }
                     }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int o = 8 * (i >> 1), st = i & 1;
-                        auto pair = [&](int h, uint32_t &hi, uint32_t &lo) {
-                            const int x = o + pair_first<FMT>(st, h), y = o + pair_second<FMT>(st, h);
-                            split(p[x], p[y], hi, lo);
-                            if constexpr (L::kQuant) {
-                                // (hi + lo) s as two terms: hi s is rounded,
-                                // what that loses (exact in f16) joins lo s
-                                const __half2 sc =
-                                    __halves2half2(x & 1 ? __high2half(sn[x / 2]) : __low2half(sn[x / 2]),
-                                                   y & 1 ? __high2half(sn[y / 2]) : __low2half(sn[y / 2]));
-                                const __half2 h2 = half2_of(hi), hs = __hmul2(h2, sc);
-                                lo = bits_of(__hfma2(half2_of(lo), sc, __hfma2(h2, sc, __hneg2(hs))));
-                                hi = bits_of(hs);
-                            }
-                        };
-                        pair(0, pa[t][i].x, pa[t][i].y);
-                        pair(1, pa[t][i].z, pa[t][i].w);
+                    for (int i = 0; i < 4; ++i)
+                        vv[mt][i] = make_uint4(x[0][2 * i], x[1][2 * i], x[0][2 * i + 1], x[1][2 * i + 1]);
+                }
+                // scales in the order of the probabilities' pairs
+                if constexpr (FMT == KQ_KV_Q4) {
+#pragma unroll
+                    for (int i = 0; i < 8; i += 4) {
+                        const __half2 s01 = sn[i], s23 = sn[i + 1], s45 = sn[i + 2], s67 = sn[i + 3];
+                        sn[i] = __lows2half2(s01, s45), sn[i + 1] = __highs2half2(s01, s45);
+                        sn[i + 2] = __lows2half2(s23, s67), sn[i + 3] = __highs2half2(s23, s67);
                     }
                 }
 #pragma unroll
-                for (int nt = 0; nt < kTilesG; ++nt) {
-                    const int e = w * kSlice + 8 * (sg * kTilesG + nt) + n8;
-                    uint32_t vv[8];
-                    if constexpr (FMT == KQ_KV_F16) {
+                for (int t = 0; t < NT; ++t) {
+                    // column n8: the hi or lo terms of row n8 / 2
+                    uint32_t pb[8];
+                    const int col = 8 * t + n8;
+                    auto load = [&](int of, uint32_t (&x)[8]) {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
+                        for (int i = 0; i < 2; ++i) {
                             const uint4 v = *reinterpret_cast<const uint4 *>(
-                                vb + L::v_word(e, token(8 * h) / 2));
-                            vv[4 * h] = v.x, vv[4 * h + 1] = v.y;
-                            vv[4 * h + 2] = v.z, vv[4 * h + 3] = v.w;
+                                pv + of * kPage + (((2 * c + i) ^ (of & 1)) << 3));
+                            x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
                         }
-                        if (edge) {
+                    };
+                    if constexpr (L::kQuant) {
+                        // (hi + lo) s as two terms: hi s is rounded, and what
+                        // that loses (exact in f16) joins lo s
+                        uint32_t hi[8], lo[8];
+                        load(col & ~1, hi);
+                        load(col | 1, lo);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) vv[i] &= keep[i];
+                        for (int i = 0; i < 8; ++i) {
+                            const __half2 h = half2_of(hi[i]), hs = __hmul2(h, sn[i]);
+                            const __half2 ls = __hfma2(half2_of(lo[i]), sn[i], __hfma2(h, sn[i], __hneg2(hs)));
+                            pb[i] = n8 & 1 ? bits_of(ls) : bits_of(hs);
                         }
-                    } else if constexpr (FMT == KQ_KV_Q8) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(vb + L::v_word(e, 4 * c));
-                        codes8(v.x, vv[0], vv[1]);
-                        codes8(v.y, vv[2], vv[3]);
-                        codes8(v.z, vv[4], vv[5]);
-                        codes8(v.w, vv[6], vv[7]);
                     } else {
-                        const uint2 v = *reinterpret_cast<const uint2 *>(vb + L::v_word(e, 2 * c));
-                        uint32_t x[4];
-                        codes4(v.x, x);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) vv[i] = x[i];
-                        codes4(v.y, x);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) vv[4 + i] = x[i];
+                        load(col, pb);
                     }
 #pragma unroll
-                    for (int t = 0; t < MT; ++t) {
+                    for (int mt = 0; mt < kTilesG; ++mt) {
                         float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) mma(d, pa[t][i], vv[2 * i], vv[2 * i + 1]);
-                        float *o = O[t][sg * kTilesG + nt];
+                        for (int i = 0; i < 4; ++i) mma(d, vv[mt][i], pb[2 * i], pb[2 * i + 1]);
+                        float *o = O[t][sg * kTilesG + mt];
                         if constexpr (L::kQuant) {
-                            o[0] = fmaf(d[0] + d[2], fac, o[0] * alpha[t]);
-                            o[1] = fmaf(d[1] + d[3], fac, o[1] * alpha[t]);
+                            o[0] = fmaf(d[0] + d[1], fac, o[0] * alpha[t]);
+                            o[1] = fmaf(d[2] + d[3], fac, o[1] * alpha[t]);
                         } else {
-                            o[0] = fmaf(o[0], alpha[t], d[0] + d[2]);
-                            o[1] = fmaf(o[1], alpha[t], d[1] + d[3]);
+                            o[0] = fmaf(o[0], alpha[t], d[0] + d[1]);
+                            o[1] = fmaf(o[1], alpha[t], d[2] + d[3]);
                         }
                     }
                 }
@@ -724,15 +761,16 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, MT>::kGroups * AttnSmem<FMT, 
                     const int tok = __ffsll((long long)bad) - 1;
                     bad &= bad - 1;
 #pragma unroll
-                    for (int t = 0; t < MT; ++t) {
-                        const int r = 8 * t + n8;
-                        if (!((allowed(r) >> tok) & 1)) continue;
-                        const float pv = ps[p_at<FMT>(r, tok)];
+                    for (int t = 0; t < NT; ++t) {
+                        const int r = 4 * t + c;
+                        if (!((allowed(left, r) >> tok) & 1)) continue;
+                        const float prob = __half2float(pv[p_at<FMT>(2 * r, tok)]) +
+                                           __half2float(pv[p_at<FMT>(2 * r + 1, tok)]);
 #pragma unroll
-                        for (int nt = 0; nt < kTilesG; ++nt)
+                        for (int mt = 0; mt < kTilesG; ++mt)
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const int e = w * kSlice + 8 * (sg * kTilesG + nt) + 2 * c + i;
+                            for (int h = 0; h < 2; ++h) {
+                                const int e = w * kSlice + 16 * (sg * kTilesG + mt) + 8 * h + n8;
                                 const uint32_t v = *reinterpret_cast<const uint32_t *>(
                                     vb + L::v_word(e, tok / L::kVPerWord));
                                 const int bit = tok % L::kVPerWord * L::kBits;
@@ -743,43 +781,70 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, MT>::kGroups * AttnSmem<FMT, 
                                             vb + L::v_scale(tok, group)));
                                 else
                                     x = __half2float(__ushort_as_half((uint16_t)(v >> bit)));
-                                float &o = O[t][sg * kTilesG + nt][i];
-                                o = fmaf(pv, x, o);
+                                float &o = O[t][sg * kTilesG + mt][h];
+                                o = fmaf(prob, x, o);
                             }
                     }
                 }
+            }
+            }
+            // ---- 2. probabilities
+            if (k < count) {
+                __half *pw = ps + (k & 1) * 2 * RB * kPage;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const int r = 4 * t + c;
+                float now = m[t];
+#pragma unroll
+                for (int i = 0; i < kWg; ++i) now = fmaxf(now, sm[i * RB + r]);
+                const float base = now == -INFINITY ? 0.f : now;
+                alpha[t] = exp2_of(m[t] - base);
+                m[t] = now;
+                const float high = base - 15.f;  // probabilities (and l, O) times 2^15
+                const float p0 = exp2_of(S[t][0] - high), p1 = exp2_of(S[t][1] - high);
+                l[t] = fmaf(l[t], alpha[t], p0 + p1);
+                const __half h0 = __float2half_rn(p0), h1 = __float2half_rn(p1);
+                const int tok = 16 * w + n8;
+                pw[p_at<FMT>(2 * r, tok)] = h0;
+                pw[p_at<FMT>(2 * r, tok + 8)] = h1;
+                pw[p_at<FMT>(2 * r + 1, tok)] = __float2half_rn(p0 - __half2float(h0));
+                pw[p_at<FMT>(2 * r + 1, tok + 8)] = __float2half_rn(p1 - __half2float(h1));
+            }
             }
         }
 
         // ---- the segment's rows: groups joined, then out or to a partial
         // result (the ring is idle now and holds the groups' values)
+        if (!producer) {
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
+        for (int t = 0; t < NT; ++t) {
             float v = l[t];
-            v += __shfl_xor_sync(~0u, v, 1);
-            v += __shfl_xor_sync(~0u, v, 2);
-            if (c == 0) {
-                cm.ml[g][1 + w][8 * t + n8] = v;
-                if (w == 0) cm.ml[g][0][8 * t + n8] = m[t];
+            v += __shfl_xor_sync(~0u, v, 4);
+            v += __shfl_xor_sync(~0u, v, 8);
+            v += __shfl_xor_sync(~0u, v, 16);
+            if (n8 == 0) {
+                cm.ml[g][1 + w][4 * t + c] = v;
+                if (w == 0) cm.ml[g][0][4 * t + c] = m[t];
             }
         }
-        // after an expired wait: no copy may land later than this
-        if (w == 0 && lane == 0 && *(volatile int *)&cm.dead)
-            for (int i = max(0, live - a.nslot); i < live; ++i)
-                kq::mbar_wait(bars + 8 * ((op0 + i) % a.nslot), ((op0 + i) / a.nslot) & 1,
-                              kq::kWaitLimitNs);
-        op0 += 2 * count;
+        // (all copies have been used; the last page's values are handed back)
         group_sync<kGroupThreads>(g);
+        if (count && w == 0 && lane == 0) {
+            kq::mbar_arrive(kq::smem_addr(&cm.empty[g * kMaxSlots + back]));
+            if (++back == a.nslot) back = 0;
+        }
         float *os = reinterpret_cast<float *>(gbase);
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int nt = 0; nt < kTiles; ++nt)
-                *reinterpret_cast<float2 *>(os + (8 * t + n8) * D + w * kSlice + 8 * nt + 2 * c) =
-                    make_float2(O[t][nt][0], O[t][nt][1]);
+            for (int mt = 0; mt < kTiles; ++mt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    os[(4 * t + c) * D + w * kSlice + 16 * mt + 8 * h + n8] = O[t][mt][h];
+        }
         __syncthreads();
         const bool whole = npg == pages;
-        const int slot = u == u0 ? 0 : 1;
+        const int slot = u == run.u0 ? 0 : 1;
         float *part = a.part + (2 * (int64_t)blockIdx.x + slot) * part_floats(RB, D);
         for (int i = tid; i < nrows * (D / 4); i += nthreads) {
             const int r = i / (D / 4), e = 4 * (i % (D / 4));
@@ -814,7 +879,7 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, MT>::kGroups * AttnSmem<FMT, 
         }
         if (tid == 0 && !whole && pg0 == 0) {
             a.meta[2 * blockIdx.x] =
-                make_int4(cta_of(u + pages - 1, total, gridDim.x), slot, nrows, head);
+                make_int4(cta_of(u + pages - 1, run.total, gridDim.x), slot, nrows, head);
             a.meta[2 * blockIdx.x + 1] = make_int4(s.first, row0, 0, 0);
         }
         // what was written to the ring comes before the next copies into it
@@ -825,48 +890,86 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, MT>::kGroups * AttnSmem<FMT, 
     }
 }
 
-// Joins the partial results of the item that begins in CTA blockIdx.x and
-// goes on: one row a block, four runs of parts at a time.
-template <int D, int RB>
-__global__ void __launch_bounds__(4 * D)
-    kq_attn_join(const __grid_constant__ AttnArgs a) {
-    __shared__ float acc[4][D], sums[4];
+// Joins partial results: a job is a row of an item that begins in one CTA and
+// goes on in others.  Every block counts the jobs of all CTAs and takes its
+// share; a row's parts are added in four runs side by side, in their order.
+// (A block per CTA and row, most of them with nothing to do, took 36 us for
+// 128 rows.)
+constexpr int kJoinRuns = 4;
+template <int D>
+__global__ void __launch_bounds__(kJoinRuns *D)
+    kq_attn_join(const __grid_constant__ AttnArgs a, int rb, int ctas) {
+    constexpr int kThreads = kJoinRuns * D, kWarps = kThreads / 32;
+    __shared__ float acc[kJoinRuns][D], sums[kJoinRuns], wt[kWarps];
+    __shared__ int scan[kWarps], job[2];
     kq::wait_prerequisites();
-    const int4 m0 = a.meta[2 * blockIdx.x];
-    const int r = blockIdx.y, e = threadIdx.x % D, run = threadIdx.x / D;
-    if (m0.x < 0 || r >= m0.z) return;
-    const int4 m1 = a.meta[2 * blockIdx.x + 1];
-    const int first = blockIdx.x, n = m0.x - first + 1;
-    // part i: slot m0.y of the first CTA, slot 0 of those after it
-    auto part = [&](int i) {
-        return a.part + (2 * (int64_t)(first + i) + (i ? 0 : m0.y)) * part_floats(RB, D);
-    };
-    float top = -INFINITY;
-    for (int i = threadIdx.x; i < n; i += 4 * D) top = fmaxf(top, part(i)[RB * D + r]);
+    const int tid = threadIdx.x, lane = tid & 31, e = tid % D, run = tid / D;
+    // this thread's CTAs, and the jobs before them
+    const int each = (ctas + kThreads - 1) / kThreads;
+    const int c0 = min(tid * each, ctas), c1 = min(c0 + each, ctas);
+    int mine = 0;
+    for (int i = c0; i < c1; ++i) mine += a.meta[2 * i].x < 0 ? 0 : a.meta[2 * i].z;
+    int upto = mine;
 #pragma unroll
-    for (int o = 16; o; o /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    __shared__ float wt[4 * D / 32];
-    if ((threadIdx.x & 31) == 0) wt[threadIdx.x / 32] = top;
-    __syncthreads();
-    for (int i = 0; i < 4 * D / 32; ++i) top = fmaxf(top, wt[i]);
-    const float base = top == -INFINITY ? 0.f : top;
-    float y = 0.f, sum = 0.f;
-#pragma unroll 4
-    for (int i = run; i < n; i += 4) {
-        const float *p = part(i);
-        const float f = exp2_of(p[RB * D + r] - base);
-        sum = fmaf(f, p[RB * D + RB + r], sum);
-        y = fmaf(f, p[r * D + e], y);
+    for (int o = 1; o < 32; o *= 2) {
+        const int v = __shfl_up_sync(~0u, upto, o);
+        if (lane >= o) upto += v;
     }
-    acc[run][e] = y;
-    if (e == 0) sums[run] = sum;
+    if (lane == 31) scan[tid >> 5] = upto;
     __syncthreads();
-    if (run) return;
-    sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
-    y = (acc[0][e] + acc[1][e]) + (acc[2][e] + acc[3][e]);
-    const int tok = (m1.y + r) / a.per, hq = (m1.y + r) % a.per;
-    a.out[((int64_t)(m1.x + tok) * a.q_heads + m0.w * a.per + hq) * D + e] =
-        sum == 0.f ? 0.f : __fdiv_rn(y, sum);
+    int total = 0;
+    for (int i = 0; i < kWarps; ++i) {
+        if (i == (tid >> 5)) upto += total;
+        total += scan[i];
+    }
+    for (int j = blockIdx.x; j < total; j += gridDim.x) {
+        if (j >= upto - mine && j < upto) {
+            int at = upto - mine;
+            for (int i = c0; i < c1; ++i) {
+                const int n = a.meta[2 * i].x < 0 ? 0 : a.meta[2 * i].z;
+                if (j < at + n) {
+                    job[0] = i, job[1] = j - at;
+                    break;
+                }
+                at += n;
+            }
+        }
+        __syncthreads();
+        const int first = job[0], r = job[1];
+        const int4 m0 = a.meta[2 * first], m1 = a.meta[2 * first + 1];
+        const int n = m0.x - first + 1;
+        // part i: slot m0.y of the first CTA, slot 0 of those after it
+        auto part = [&](int i) {
+            return a.part + (2 * (int64_t)(first + i) + (i ? 0 : m0.y)) * part_floats(rb, D);
+        };
+        float top = -INFINITY;
+        for (int i = tid; i < n; i += kThreads) top = fmaxf(top, part(i)[rb * D + r]);
+#pragma unroll
+        for (int o = 16; o; o /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+        if (lane == 0) wt[tid >> 5] = top;
+        __syncthreads();
+        for (int i = 0; i < kWarps; ++i) top = fmaxf(top, wt[i]);
+        const float base = top == -INFINITY ? 0.f : top;
+        float y = 0.f, sum = 0.f;
+#pragma unroll 8
+        for (int i = run; i < n; i += kJoinRuns) {
+            const float *p = part(i);
+            const float f = exp2_of(p[rb * D + r] - base);
+            sum = fmaf(f, p[rb * D + rb + r], sum);
+            y = fmaf(f, p[r * D + e], y);
+        }
+        acc[run][e] = y;
+        if (e == 0) sums[run] = sum;
+        __syncthreads();
+        if (run == 0) {
+            sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+            y = (acc[0][e] + acc[1][e]) + (acc[2][e] + acc[3][e]);
+            const int tok = (m1.y + r) / a.per, hq = (m1.y + r) % a.per;
+            a.out[((int64_t)(m1.x + tok) * a.q_heads + m0.w * a.per + hq) * D + e] =
+                sum == 0.f ? 0.f : __fdiv_rn(y, sum);
+        }
+        __syncthreads();
+    }
 }
 
 // ------------------------------------------------------------------ launch
@@ -875,9 +978,32 @@ struct AttnShape {
     int ctas, ng, nslot;
 };
 
-template <int FMT, int D, int MT>
+// The kernel and, after it, the join.
+template <int D>
+cudaError_t launch_pair(void (*kernel)(AttnArgs), const AttnArgs &a, int sms, int ctas, int threads,
+                        int smem, int rb, cudaStream_t s) {
+    // rows that may have parts to join: all there are, at most
+    const int64_t jobs = (int64_t)a.q.nseq * a.q.heads * a.q.max_new * a.per;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<ctas, threads, smem, s>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(jobs < 2 * sms ? jobs : 2 * sms));
+    cfg.blockDim = dim3(kJoinRuns * D);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kq_attn_join<D>, a, rb, ctas);
+}
+
+template <int FMT, int D, int NT>
 cudaError_t launch_attn(AttnArgs a, int sms, cudaStream_t s, int64_t *floats) {
-    using M = AttnSmem<FMT, D, MT>;
+    using M = AttnSmem<FMT, D, NT>;
     // 16 warps of an SM in all: in one CTA that joins them where there are few
     // items, else in four, so that a CTA's warps have fewer items to join.
     // Fewer where a slot is too large for three a group.
@@ -892,61 +1018,37 @@ cudaError_t launch_attn(AttnArgs a, int sms, cudaStream_t s, int64_t *floats) {
         while (sh.ng > 1 && room / sh.ng - M::kP - M::kMax < 3 * M::kHalf) --sh.ng;
         sh.nslot = (room / sh.ng - M::kP - M::kMax) / M::kHalf;
     };
-    fit(4);
-    if (items < 4 * (int64_t)sms || sh.nslot < 3) fit(1);
+    constexpr int kApart = M::kGroups < 4 ? M::kGroups : 4;
+    fit(kApart);
+    if (items < kApart * (int64_t)sms || sh.nslot < 3) fit(1);
     if (sh.nslot > kMaxSlots) sh.nslot = kMaxSlots;
     *floats = 2 * (int64_t)sh.ctas * part_floats(M::kRows, D);
     if (!a.part) return cudaSuccess;
     a.ng = sh.ng, a.nslot = sh.nslot;
     a.meta = reinterpret_cast<int4 *>(a.part);  // meta first, 16-byte aligned
     a.part += 8 * (int64_t)sh.ctas;
-    const int smem = M::total(sh.ng, sh.nslot);
-    static std::mutex mu;
-    static int configured[64] = {};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    {
-        std::lock_guard<std::mutex> lock(mu);
-        if (dev < 0 || dev >= 64 || configured[dev] < smem) {
-            e = cudaFuncSetAttribute(kq_attn_kernel<FMT, D, MT>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-            if (e != cudaSuccess) return e;
-            if (dev >= 0 && dev < 64) configured[dev] = smem;
-        }
-    }
-    kq_attn_kernel<FMT, D, MT><<<sh.ctas, 32 * M::kWg * sh.ng, smem, s>>>(a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(sh.ctas, M::kRows);
-    cfg.blockDim = dim3(4 * D);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kq_attn_join<D, M::kRows>, a);
+    return launch_pair<D>(kq_attn_kernel<FMT, D, NT>, a, sms, sh.ctas, 32 * M::kWg * sh.ng + 32,
+                          M::total(sh.ng, sh.nslot), M::kRows, s);
 }
 
-// The launch for a format and width: tiles of a row block by the rows that a
+// The launch for a format and width: tiles of four rows by the rows that a
 // key head has.
+template <int FMT, int D>
+cudaError_t attn_tiles(int64_t rows, const AttnArgs &a, int sms, cudaStream_t s, int64_t *floats) {
+    // (width 256: blocks of 16 rows for more; one of 32 spilled, 83 us against
+    // 59 for 8 sequences of 4100 tokens with 20 rows a key head)
+    return rows <= 4   ? launch_attn<FMT, D, 1>(a, sms, s, floats)
+           : rows <= 8 ? launch_attn<FMT, D, 2>(a, sms, s, floats)
+                       : launch_attn<FMT, D, 4>(a, sms, s, floats);
+}
+
 template <int FMT>
 cudaError_t attn_format(int dim, const AttnArgs &a, int sms, cudaStream_t s, int64_t *floats) {
     const int64_t rows = (int64_t)a.q.max_new * a.per;
     switch (dim) {
-    case 64:
-        return rows <= 8    ? launch_attn<FMT, 64, 1>(a, sms, s, floats)
-               : rows <= 16 ? launch_attn<FMT, 64, 2>(a, sms, s, floats)
-                            : launch_attn<FMT, 64, 4>(a, sms, s, floats);
-    case 128:
-        return rows <= 8    ? launch_attn<FMT, 128, 1>(a, sms, s, floats)
-               : rows <= 16 ? launch_attn<FMT, 128, 2>(a, sms, s, floats)
-                            : launch_attn<FMT, 128, 4>(a, sms, s, floats);
-    default:
-        return rows <= 8 ? launch_attn<FMT, 256, 1>(a, sms, s, floats)
-                         : launch_attn<FMT, 256, 2>(a, sms, s, floats);
+    case 64: return attn_tiles<FMT, 64>(rows, a, sms, s, floats);
+    case 128: return attn_tiles<FMT, 128>(rows, a, sms, s, floats);
+    default: return attn_tiles<FMT, 256>(rows, a, sms, s, floats);
     }
 }
 
