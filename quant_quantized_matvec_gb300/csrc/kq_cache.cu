@@ -6,8 +6,8 @@
 // values holds two tokens, and whole words are read, changed and written
 // where a call covers only some of their tokens.
 //
-// Quantisation: eight lanes hold a group of 32 values, four each; its
-// largest and smallest value come from three shuffles.
+// Quantisation: four lanes hold a group of 32 values, eight each; the value of
+// largest magnitude comes from two shuffles.
 // Bound by memory: 4 bytes a value on the f32 side, bits/8 on the other.
 #include "kq_decode.cuh"
 #include "kq_decode_launch.h"
@@ -17,83 +17,86 @@ namespace kqd {
 constexpr int kCacheThreads = 256;
 
 // ------------------------------------------------------------------ codes
-// The four codes of a lane (of eight that hold a group) and the group's
-// scale; every lane of the warp takes part.
+// The eight codes of a lane (of four that hold a group), in the low byte of
+// each, and the group's scale; every lane of the warp takes part.
 struct Codes {
-    int c[4];
+    int c[8];
     __half d;
 };
 template <int FMT>
-__device__ __forceinline__ Codes quantise(const float (&x)[4]) {
-    float hi = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-    float lo = fminf(fminf(x[0], x[1]), fminf(x[2], x[3]));
-    // a NaN or an infinity makes the sum of x * 0 a NaN
-    float bad = x[0] * 0.f + x[1] * 0.f + x[2] * 0.f + x[3] * 0.f;
+__device__ __forceinline__ Codes quantise(const float (&x)[8]) {
+    // The magnitudes as integers, a positive one before a negative one of the
+    // same size: one maximum gives the largest value with its sign, and
+    // whether any is a NaN or an infinity (their bits are the largest).
+    uint32_t key = 0;
 #pragma unroll
-    for (int o = 1; o < 8; o *= 2) {
-        hi = fmaxf(hi, __shfl_xor_sync(~0u, hi, o));
-        lo = fminf(lo, __shfl_xor_sync(~0u, lo, o));
-        bad += __shfl_xor_sync(~0u, bad, o);
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t b = __float_as_uint(x[i]);
+        key = max(key, FMT == KQ_KV_Q8 ? b << 1 : b << 1 | ((b >> 31) ^ 1));
     }
-    float d = FMT == KQ_KV_Q8 ? __fdiv_rn(fmaxf(hi, -lo), 127.f) : (hi >= -lo ? hi : lo) * -0.125f;
+    key = max(key, __shfl_xor_sync(~0u, key, 1));
+    key = max(key, __shfl_xor_sync(~0u, key, 2));
+    const bool bad = key >= 0xFF000000u;
+    const float top = __uint_as_float(key >> 1);
+    float d = FMT == KQ_KV_Q8 ? __fdiv_rn(top, 127.f) : (key & 1 ? top : -top) * -0.125f;
     d = fminf(fmaxf(d, -65504.f), 65504.f);
     Codes r;
-    r.d = __float2half_rn(bad == 0.f ? d : quiet_nan());
+    r.d = __float2half_rn(bad ? quiet_nan() : d);
     const float df = __half2float(r.d);
-    const float top = FMT == KQ_KV_Q8 ? 127.f : 7.f, bot = FMT == KQ_KV_Q8 ? -127.f : -8.f;
+    float inv;  // 1 / d to the last place or so; no scale, no codes
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(df));
+    inv = bad || df == 0.f ? 0.f : inv;
+    const float hi = FMT == KQ_KV_Q8 ? 127.f : 7.f, lo = FMT == KQ_KV_Q8 ? -127.f : -8.f;
+    // x / d rounded to nearest, by way of 1 / d: where the product is near a
+    // half, the division itself decides.  Added to 1.5 * 2^23 a number is
+    // rounded to a whole one, which then stands in the low bits.
+    constexpr float kWhole = 12582912.f;
+    float q[8], worst = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float c = df == 0.f || bad != 0.f ? 0.f : rintf(__fdiv_rn(x[i], df));
-        r.c[i] = (int)fminf(fmaxf(c, bot), top);
+    for (int i = 0; i < 8; ++i) {
+        q[i] = fminf(fmaxf(x[i] * inv, lo), hi);
+        worst = fmaxf(worst, fabsf(q[i] - ((q[i] + kWhole) - kWhole)));
     }
+    if (worst > 0.499f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (fabsf(q[i] - ((q[i] + kWhole) - kWhole)) > 0.499f)
+                q[i] = fminf(fmaxf(__fdiv_rn(x[i], df), lo), hi);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.c[i] = __float_as_int(q[i] + kWhole);
     return r;
 }
-
-__device__ __forceinline__ void load4(float (&x)[4], const float *p) {
-    const float4 v = *reinterpret_cast<const float4 *>(p);
-    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+// The low bytes of four numbers, side by side.
+__device__ __forceinline__ uint32_t bytes4(const int *c) {
+    return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
 }
 
-// Values e .. e+3 (e a multiple of 4) of the head at p, rotated.
-__device__ __forceinline__ void load4_rotated(float (&x)[4], const float *p, int e, int tok,
-                                              const AppendArgs &a) {
-    load4(x, p + e);
-    if (!a.table || e >= a.rot) return;
-    const int pos = __ldg(a.pos + tok);
-    if (pos < 0 || pos >= a.positions) {
-        x[0] = x[1] = x[2] = x[3] = quiet_nan();
-        return;
-    }
-    const float *row = a.table + (int64_t)pos * a.rot;
-    if (a.inter) {
-        const float4 cs = __ldg(reinterpret_cast<const float4 *>(row + e));
-        const float y[4] = {rot_a(x[0], x[1], cs.x, cs.y), rot_b(x[0], x[1], cs.x, cs.y),
-                            rot_a(x[2], x[3], cs.z, cs.w), rot_b(x[2], x[3], cs.z, cs.w)};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = y[i];
-        return;
-    }
-    const int half = a.rot / 2;
-    const bool first = e < half;
-    const int pair = first ? e : e - half;
-    float y[4];
-    load4(y, p + (first ? e + half : pair));
-    const float4 c0 = __ldg(reinterpret_cast<const float4 *>(row + 2 * pair));
-    const float4 c1 = __ldg(reinterpret_cast<const float4 *>(row + 2 * pair) + 1);
-    const float c[4] = {c0.x, c0.z, c1.x, c1.z}, s[4] = {c0.y, c0.w, c1.y, c1.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        x[i] = first ? rot_a(x[i], y[i], c[i], s[i]) : rot_b(y[i], x[i], c[i], s[i]);
+__device__ __forceinline__ float4 load4(const float *p) {
+    return *reinterpret_cast<const float4 *>(p);
 }
 
-// Values in shared memory on their way between [token][value] and the
-// cache's [value][token]: f16 bits or sign-extended codes.
+// Values on their way from [token][value] to the cache's [value][token], four
+// of a token a word (f16: two).
 template <int FMT, int D>
 struct Stage {
-    using T = typename std::conditional<FMT == KQ_KV_F16, uint16_t, int8_t>::type;
-    static constexpr int kPad = 4 / sizeof(T);
-    T v[kPage][D + kPad];
+    static constexpr int kWords = FMT == KQ_KV_F16 ? D / 2 : D / 4;
+    uint32_t v[kPage][kWords + 1];
 };
+
+// Bytes of four words turned: word i of the result has byte i of each.
+__device__ __forceinline__ void turn4(uint32_t (&w)[4]) {
+    const uint32_t a = __byte_perm(w[0], w[1], 0x5140), b = __byte_perm(w[0], w[1], 0x7362);
+    const uint32_t c = __byte_perm(w[2], w[3], 0x5140), d = __byte_perm(w[2], w[3], 0x7362);
+    w[0] = __byte_perm(a, c, 0x5410), w[1] = __byte_perm(a, c, 0x7632);
+    w[2] = __byte_perm(b, d, 0x5410), w[3] = __byte_perm(b, d, 0x7632);
+}
+// The low nibbles of four bytes, side by side.
+__device__ __forceinline__ uint32_t nibbles(uint32_t w) {
+    w &= 0x0F0F0F0Fu;
+    w = (w | w >> 4) & 0x00FF00FFu;
+    return (w | w >> 8) & 0xFFFFu;
+}
 
 // The part of a page that the CTA's sequence has new tokens in: its tokens
 // [t0, t1), the first of which is new token `tok` of the step.
@@ -116,7 +119,7 @@ __device__ __forceinline__ Part part_of(const Seqs &q, int b, int64_t rel, int h
 }
 
 template <int FMT, int D>
-__global__ void __launch_bounds__(kCacheThreads)
+__global__ void __launch_bounds__(kCacheThreads, 5)
     kq_kv_append_kernel(const __grid_constant__ Seqs q, const __grid_constant__ AppendArgs a) {
     using L = Kv<FMT, D>;
     __shared__ Stage<FMT, D> st;
@@ -125,75 +128,124 @@ __global__ void __launch_bounds__(kCacheThreads)
     const Part part = part_of<FMT, D>(q, blockIdx.z, blockIdx.x, head);
     if (!part.block) return;
     const int n = part.t1 - part.t0;
-    const int l8 = threadIdx.x & 7;
-    constexpr int kPer = kCacheThreads / 8;  // groups at a time
+    // a thread takes the same eight values of every kStep-th token
+    constexpr int kOctets = D / 8, kStep = kCacheThreads / kOctets;
+    const int e = 8 * (threadIdx.x % kOctets), j0 = threadIdx.x / kOctets;
+    const int64_t stride = values ? a.v_stride : a.k_stride;
+    const float *src = (values ? a.v : a.k) + (int64_t)(part.tok + j0) * stride + head * D + e;
+    const bool turn = !values && a.table && e < a.rot;
+    const int half = a.rot / 2;
+    // (halves may meet inside the eight values: each four has its partner)
+    const int to0 = e < half ? half : -half, to1 = e + 4 < half ? half : -half;
+    const int pair0 = e < half ? e : e - half, pair1 = e + 4 < half ? e + 4 : e + 4 - half;
+    uint8_t *kout = part.block + L::k_octet(part.t0 + j0, e / 8);
     // every lane runs every round: quantise() shuffles
-    for (int i0 = 0; i0 < n * L::kGroups; i0 += kPer) {
-        const int i = i0 + threadIdx.x / 8;
-        const bool on = i < n * L::kGroups;
-        const int j = on ? i / L::kGroups : 0, g = on ? i % L::kGroups : 0;
-        const int e = g * kGroup + 4 * l8, t = part.t0 + j;
-        float x[4] = {0.f, 0.f, 0.f, 0.f};
-        const int64_t row = part.tok + j;
+    for (int r = 0; r < (n + kStep - 1) / kStep; ++r) {
+        const int j = j0 + r * kStep, t = part.t0 + j;
+        const bool on = j < n;
+        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (on) {
-            if (values) load4(x, a.v + row * a.v_stride + head * D + e);
-            else load4_rotated(x, a.k + row * a.k_stride + head * D, e, (int)row, a);
+            const float4 u = load4(src), v = load4(src + 4);
+            x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
+            x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
         }
-        uint32_t w[2];  // the four values as the cache holds them
+        if (turn && on) {
+            const int pos = __ldg(a.pos + part.tok + j);
+            if (pos < 0 || pos >= a.positions) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = quiet_nan();
+            } else if (a.inter) {
+                const float4 *p =
+                    reinterpret_cast<const float4 *>(a.table + (int64_t)pos * a.rot + e);
+                const float4 c0 = __ldg(p), c1 = __ldg(p + 1);
+                const float y[8] = {rot_a(x[0], x[1], c0.x, c0.y), rot_b(x[0], x[1], c0.x, c0.y),
+                                    rot_a(x[2], x[3], c0.z, c0.w), rot_b(x[2], x[3], c0.z, c0.w),
+                                    rot_a(x[4], x[5], c1.x, c1.y), rot_b(x[4], x[5], c1.x, c1.y),
+                                    rot_a(x[6], x[7], c1.z, c1.w), rot_b(x[6], x[7], c1.z, c1.w)};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = y[k];
+            } else {
+                const float *row = a.table + (int64_t)pos * a.rot;
+                const float4 y0 = load4(src + to0), y1 = load4(src + 4 + to1);
+                const float4 *p0 = reinterpret_cast<const float4 *>(row + 2 * pair0);
+                const float4 *p1 = reinterpret_cast<const float4 *>(row + 2 * pair1);
+                const float4 c[4] = {__ldg(p0), __ldg(p0 + 1), __ldg(p1), __ldg(p1 + 1)};
+                const float y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float cc = k & 1 ? c[k / 2].z : c[k / 2].x;
+                    const float ss = k & 1 ? c[k / 2].w : c[k / 2].y;
+                    const bool first = (k < 4 ? to0 : to1) > 0;
+                    x[k] = first ? rot_a(x[k], y[k], cc, ss) : rot_b(y[k], x[k], cc, ss);
+                }
+            }
+        }
         if constexpr (FMT == KQ_KV_F16) {
-            const __half2 h0 = __floats2half2_rn(x[0], x[1]), h1 = __floats2half2_rn(x[2], x[3]);
-            w[0] = *reinterpret_cast<const uint32_t *>(&h0);
-            w[1] = *reinterpret_cast<const uint32_t *>(&h1);
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const __half2 h = __floats2half2_rn(x[2 * k], x[2 * k + 1]);
+                memcpy(&w[k], &h, 4);
+            }
             if (on && values) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    st.v[t][e + k] = (uint16_t)(w[k / 2] >> (16 * (k & 1)));
+                for (int k = 0; k < 4; ++k) st.v[t][e / 2 + k] = w[k];
+            } else if (on) {
+                *reinterpret_cast<uint4 *>(kout) = make_uint4(w[0], w[1], w[2], w[3]);
             }
         } else {
             const Codes c = quantise<FMT>(x);
-            const uint32_t m = FMT == KQ_KV_Q8 ? 0xFFu : 0xFu;
-            w[0] = 0;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) w[0] |= ((uint32_t)c.c[k] & m) << (L::kBits * k);
+            const uint32_t w0 = bytes4(c.c), w1 = bytes4(c.c + 4);
             if (on && values) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) st.v[t][e + k] = (int8_t)c.c[k];
+                st.v[t][e / 4] = w0, st.v[t][e / 4 + 1] = w1;
+            } else if (on) {
+                if constexpr (FMT == KQ_KV_Q8) *reinterpret_cast<uint2 *>(kout) = make_uint2(w0, w1);
+                else *reinterpret_cast<uint32_t *>(kout) = nibbles(w0) | nibbles(w1) << 16;
             }
-            if (on && l8 == 0)
+            if (on && (threadIdx.x & 3) == 0) {
+                const int g = e / kGroup;
                 *reinterpret_cast<__half *>(part.block +
                                             (values ? L::v_scale(t, g) : L::k_scale(t, g))) = c.d;
+            }
         }
-        if (on && !values) {
-            uint8_t *o = part.block + L::k_octet(t, e / 8) + (e & 4) * L::kBits / 8;
-            if constexpr (FMT == KQ_KV_F16)
-                *reinterpret_cast<uint2 *>(o) = make_uint2(w[0], w[1]);
-            else if constexpr (FMT == KQ_KV_Q8)
-                *reinterpret_cast<uint32_t *>(o) = w[0];
-            else
-                *reinterpret_cast<uint16_t *>(o) = (uint16_t)w[0];
-        }
+        src += kStep * stride;
+        kout += kStep * L::kSlabBytes;
     }
     if (!values) return;
     __syncthreads();
-    // words of the values' rows, along a row first (rows of a slab are
-    // contiguous); tokens of the word that this call does not write stay
-    constexpr int kWords = L::kVRow / 4;
-    for (int i = threadIdx.x; i < D * L::kVWords; i += kCacheThreads) {
-        const int slab = i / (D * kWords), r = i % (D * kWords);
-        const int e = r / kWords, w = slab * kWords + r % kWords;
+    // Words of the values' rows, along a row first (rows of a slab are
+    // contiguous); tokens of a word that this call does not write stay.
+    constexpr int kEach = FMT == KQ_KV_F16 ? 2 : 4;  // values of a staged word
+    constexpr int kWords = L::kVRow / 4;             // words of a row in a slab
+    for (int i = threadIdx.x; i < D / kEach * L::kVWords; i += kCacheThreads) {
+        const int slab = i / (D / kEach * kWords), r = i % (D / kEach * kWords);
+        const int e = r / kWords, w = slab * kWords + r % kWords;  // staged word, row word
         const int tw = w * L::kVPerWord;
         if (tw + L::kVPerWord <= part.t0 || tw >= part.t1) continue;
-        uint32_t word = 0, keep = 0;
+        uint32_t out[kEach];
+        if constexpr (FMT == KQ_KV_F16) {
+            const uint32_t x = st.v[tw][e], y = st.v[tw + 1][e];
+            out[0] = __byte_perm(x, y, 0x5410), out[1] = __byte_perm(x, y, 0x7632);
+        } else {
+            uint32_t x[4] = {st.v[tw][e], st.v[tw + 1][e], st.v[tw + 2][e], st.v[tw + 3][e]};
+            turn4(x);
 #pragma unroll
-        for (int k = 0; k < L::kVPerWord; ++k) {
-            const uint32_t m = L::kBits == 16 ? 0xFFFFu : (1u << L::kBits) - 1u;
-            if (tw + k >= part.t0 && tw + k < part.t1)
-                word |= ((uint32_t)st.v[tw + k][e] & m) << (L::kBits * k);
-            else
-                keep |= m << (L::kBits * k);
+            for (int k = 0; k < 4; ++k) out[k] = x[k];
+            if constexpr (FMT == KQ_KV_Q4) {
+                uint32_t y[4] = {st.v[tw + 4][e], st.v[tw + 5][e], st.v[tw + 6][e], st.v[tw + 7][e]};
+                turn4(y);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) out[k] = nibbles(x[k]) | nibbles(y[k]) << 16;
+            }
         }
-        uint32_t *o = reinterpret_cast<uint32_t *>(part.block + L::v_word(e, w));
-        *o = keep ? (*o & keep) | word : word;
+        uint32_t keep = 0;  // bits of tokens outside [t0, t1)
+        if (tw < part.t0) keep = ~(~0u << (L::kBits * (part.t0 - tw)));
+        if (tw + L::kVPerWord > part.t1) keep |= ~0u << (L::kBits * (part.t1 - tw));
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            uint32_t *o = reinterpret_cast<uint32_t *>(part.block + L::v_word(kEach * e + k, w));
+            *o = keep ? (*o & keep) | (out[k] & ~keep) : out[k];
+        }
     }
 }
 
@@ -202,67 +254,82 @@ __global__ void __launch_bounds__(kCacheThreads)
     kq_kv_read_kernel(const __grid_constant__ Seqs q, float *__restrict__ ko,
                       float *__restrict__ vo) {
     using L = Kv<FMT, D>;
-    __shared__ Stage<FMT, D> st;
     const int head = blockIdx.y >> 1;
     const bool values = blockIdx.y & 1;
     float *out = values ? vo : ko;
     if (!out) return;
     const Part part = part_of<FMT, D>(q, blockIdx.z, blockIdx.x, head);
     const int n = part.t1 - part.t0;
-    if (part.block && values) {
-        constexpr int kWords = L::kVRow / 4;
-        for (int i = threadIdx.x; i < D * L::kVWords; i += kCacheThreads) {
-            const int slab = i / (D * kWords), r = i % (D * kWords);
-            const int e = r / kWords, w = slab * kWords + r % kWords;
-            const int tw = w * L::kVPerWord;
-            if (tw + L::kVPerWord <= part.t0 || tw >= part.t1) continue;
-            const uint32_t word = *reinterpret_cast<const uint32_t *>(part.block + L::v_word(e, w));
-#pragma unroll
-            for (int k = 0; k < L::kVPerWord; ++k) {
-                if constexpr (FMT == KQ_KV_F16)
-                    st.v[tw + k][e] = (uint16_t)(word >> (16 * k));
-                else  // sign-extended
-                    st.v[tw + k][e] =
-                        (int8_t)((int)(word << (32 - L::kBits * (k + 1))) >> (32 - L::kBits));
-            }
-        }
-        __syncthreads();
+    const int64_t stride = (int64_t)q.heads * D;
+    out += (int64_t)part.tok * stride + head * D;
+    if (!part.block) {
+        const float x = quiet_nan();
+        for (int i = threadIdx.x; i < n * (D / 4); i += kCacheThreads)
+            *reinterpret_cast<float4 *>(out + i / (D / 4) * stride + 4 * (i % (D / 4))) =
+                make_float4(x, x, x, x);
+        return;
     }
+    if (values) {
+        // A warp takes a group of 32 values, a lane each, and eight tokens of
+        // its row at a time: a token's store is 128 contiguous bytes.
+        const int lane = threadIdx.x & 31;
+        for (int i = threadIdx.x / 32; i < L::kGroups * (kPage / 8); i += kCacheThreads / 32) {
+            const int g = i % L::kGroups, tw = i / L::kGroups * 8;
+            if (tw + 8 <= part.t0 || tw >= part.t1) continue;
+            const uint8_t *row = part.block + L::v_word(g * kGroup + lane, tw / L::kVPerWord);
+            float x[8];
+            if constexpr (FMT == KQ_KV_F16) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(row);
+                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    x[k] = __half2float(__ushort_as_half((uint16_t)(ws[k / 2] >> (16 * (k & 1)))));
+            } else {
+                uint32_t ws[2];
+                if constexpr (FMT == KQ_KV_Q8) {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(row);
+                    ws[0] = w.x, ws[1] = w.y;
+                } else {
+                    ws[0] = *reinterpret_cast<const uint32_t *>(row);
+                }
+                const uint4 s = *reinterpret_cast<const uint4 *>(part.block + L::v_scale(tw, g));
+                const uint32_t ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t w = ws[k * L::kBits / 32];
+                    const int c = (int)(w << (32 - L::kBits - k * L::kBits % 32)) >> (32 - L::kBits);
+                    x[k] = (float)c *
+                           __half2float(__ushort_as_half((uint16_t)(ss[k / 2] >> (16 * (k & 1)))));
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (tw + k >= part.t0 && tw + k < part.t1)
+                    out[(tw + k - part.t0) * stride + g * kGroup + lane] = x[k];
+        }
+        return;
+    }
+#pragma unroll 4
     for (int i = threadIdx.x; i < n * (D / 4); i += kCacheThreads) {
         const int j = i / (D / 4), e = 4 * (i % (D / 4)), t = part.t0 + j, g = e / kGroup;
+        const uint8_t *p = part.block + L::k_octet(t, e / 8) + (e & 4) * L::kBits / 8;
         float x[4];
-        if (!part.block) {
-            x[0] = x[1] = x[2] = x[3] = quiet_nan();
-        } else if constexpr (FMT == KQ_KV_F16) {
-            uint16_t h[4];
-            if (values) {
+        if constexpr (FMT == KQ_KV_F16) {
+            const uint2 w = *reinterpret_cast<const uint2 *>(p);
+            const uint32_t ws[2] = {w.x, w.y};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) h[k] = st.v[t][e + k];
-            } else {
-                const uint2 w = *reinterpret_cast<const uint2 *>(
-                    part.block + L::k_octet(t, e / 8) + (e & 4) * 2);
-                h[0] = (uint16_t)w.x, h[1] = (uint16_t)(w.x >> 16);
-                h[2] = (uint16_t)w.y, h[3] = (uint16_t)(w.y >> 16);
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) x[k] = __half2float(__ushort_as_half(h[k]));
+            for (int k = 0; k < 4; ++k)
+                x[k] = __half2float(__ushort_as_half((uint16_t)(ws[k / 2] >> (16 * (k & 1)))));
         } else {
-            const float d = __half2float(*reinterpret_cast<const __half *>(
-                part.block + (values ? L::v_scale(t, g) : L::k_scale(t, g))));
-            if (values) {
+            const float d =
+                __half2float(*reinterpret_cast<const __half *>(part.block + L::k_scale(t, g)));
+            const uint32_t w = FMT == KQ_KV_Q8 ? *reinterpret_cast<const uint32_t *>(p)
+                                               : *reinterpret_cast<const uint16_t *>(p);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) x[k] = (float)st.v[t][e + k] * d;
-            } else {
-                const uint8_t *p = part.block + L::k_octet(t, e / 8) + (e & 4) * L::kBits / 8;
-                const uint32_t w = FMT == KQ_KV_Q8 ? *reinterpret_cast<const uint32_t *>(p)
-                                                   : *reinterpret_cast<const uint16_t *>(p);
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    x[k] = (float)((int)(w << (32 - L::kBits * (k + 1))) >> (32 - L::kBits)) * d;
-            }
+            for (int k = 0; k < 4; ++k)
+                x[k] = (float)((int)(w << (32 - L::kBits * (k + 1))) >> (32 - L::kBits)) * d;
         }
-        *reinterpret_cast<float4 *>(out + ((int64_t)(part.tok + j) * q.heads + head) * D + e) =
-            make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4 *>(out + j * stride + e) = make_float4(x[0], x[1], x[2], x[3]);
     }
 }
 
