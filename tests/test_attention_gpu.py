@@ -15,6 +15,13 @@ import quant_quantized_matvec_gb300 as kq  # noqa: E402
 FMTS = [R.F16, R.Q8, R.Q4]
 
 
+@pytest.fixture(autouse=True)
+def no_expired_wait():
+    """Every wait inside the kernels is bounded; none may have run out."""
+    yield
+    assert not kq.device_error()
+
+
 def dev(a):
     return torch.from_numpy(np.ascontiguousarray(a)).cuda()
 
@@ -119,6 +126,30 @@ def test_long_and_ragged(fmt):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("g,new", [(17, 1), (8, 4), (11, 3), (16, 4), (13, 5), (16, 8), (43, 3)])
+def test_many_rows(fmt, dim, g, new):
+    """17..129 rows a key head, blocks of 32, 64 and 128: one sequence whose
+    pages are shared by CTAs, one of a few, one with nothing committed."""
+    c = Case(fmt, 2, g, dim, [new, new, 1], [1500, 130, 0], seed=g)
+    got = c.run()
+    c.check(got)
+    assert torch.equal(got, c.run())
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
+@pytest.mark.parametrize("g,new", [(4, 1), (8, 1), (16, 1), (5, 5), (12, 5), (16, 6)])
+def test_many_pages_a_cta(fmt, g, new):
+    """Enough pages that every ring goes round several times."""
+    c = Case(fmt, 1, g, 64, [new], [150000], seed=g, spread=3.0)
+    c.q[:, 1:] = c.q[:, :1]  # (the reference takes one head's time)
+    got = c.run()
+    assert torch.equal(got, got[:, :1].expand_as(got))
+    c.q, c.hq = c.q[:, :1], 1
+    c.check(got[:, :1])
+
+
 def test_a_batch_of_many_sequences():
     rng = np.random.default_rng(8)
     new, ctx = rng.integers(0, 4, 300).tolist(), rng.integers(0, 200, 300).tolist()
@@ -142,10 +173,18 @@ def test_empty_rows_are_zero(fmt):
 @pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("ctx", [0, 61, 130])
-def test_masked_places_do_not_reach_a_row(fmt, bad, ctx):
+def test_masked_places_do_not_reach_any_of_many_rows(fmt, bad, ctx):
+    """The same with 48 rows a key head."""
+    test_masked_places_do_not_reach_a_row(fmt, bad, ctx, g=8)
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("ctx", [0, 61, 130])
+def test_masked_places_do_not_reach_a_row(fmt, bad, ctx, g=4):
     """New token 2's key and value hold a NaN or an infinity; rows that attend
     it show it, others are as without it."""
-    c = Case(fmt, 1, 4, 128, [6], [ctx], masks=[1, 3, 7, 9, 17, 37], seed=4)
+    c = Case(fmt, 1, g, 128, [6], [ctx], masks=[1, 3, 7, 9, 17, 37], seed=4)
     clean = c.run()
     c.k[ctx + 2, 0, 3], c.v[ctx + 2, 0, 40] = bad, bad
     c.write()
@@ -171,8 +210,9 @@ def test_masked_places_do_not_reach_a_row(fmt, bad, ctx):
 
 
 @pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
-def test_extreme_logits(fmt):
-    c = Case(fmt, 1, 2, 64, [2], [200], seed=6, spread=3000.0)
+@pytest.mark.parametrize("g", [2, 20])
+def test_extreme_logits(fmt, g):
+    c = Case(fmt, 1, g, 64, [2], [200], seed=6, spread=3000.0)
     c.check(c.run())
     c.q[:] = 0
     c.check(c.run())
@@ -185,8 +225,9 @@ def test_extreme_logits(fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
-def test_bad_pages(fmt):
-    c = Case(fmt, 2, 4, 64, [2, 1], [150, 150], masks=[1, 2, 1])
+@pytest.mark.parametrize("g", [4, 20])
+def test_bad_pages(fmt, g):
+    c = Case(fmt, 2, g, 64, [2, 1], [150, 150], masks=[1, 2, 1])
     good = c.run()
     table = c.table.copy()
     table[0, 1] = c.pages
@@ -196,7 +237,7 @@ def test_bad_pages(fmt):
     # places past the table's end; lengths that are no lengths
     b = kq.KVBatch(dev(np.array([0, 2, 9], np.int32)), dev(np.array([-3, 1 << 30], np.int32)),
                    dev(c.table), c.ntok, 2)
-    out = torch.full((c.ntok, 8, 64), 5.0, device="cuda")
+    out = torch.full((c.ntok, 2 * g, 64), 5.0, device="cuda")
     kq.tree_attention(c.cache, b, dev(c.q), mask=c.mask(), out=out)
     assert torch.isfinite(out[:2]).all() and torch.isnan(out[2]).all()
     # a token of no sequence is left alone
@@ -206,8 +247,9 @@ def test_bad_pages(fmt):
     assert (out[1:] == 5).all() and torch.isfinite(out[0]).all()
 
 
-def test_masked_bad_page_is_not_attended():
-    c = Case(R.Q8, 1, 4, 64, [40], [50], masks=[1] * 40, seed=2)
+@pytest.mark.parametrize("dim", [64, 256])
+def test_masked_bad_page_is_not_attended(dim):
+    c = Case(R.Q8, 1, 4, dim, [40], [50], masks=[1] * 40, seed=2)
     good = c.run()
     table = c.table.copy()
     table[0, 1] = -1  # new tokens 14.. : none of them is attended
@@ -235,6 +277,11 @@ def test_strides_scale_out_and_workspace():
                             workspace=ws)
     assert got is out and torch.equal(got, want)
     c.check(c.run(scale=0.7), c.want(scale=0.7))
+    c.check(c.run(scale=-0.3), c.want(scale=-0.3))
+    c.check(c.run(scale=0.0), c.want(scale=0.0))
+    d = Case(R.Q8, 1, 24, 128, [2], [200], seed=14)  # many rows
+    d.check(d.run(scale=-0.3), d.want(scale=-0.3))
+    d.check(d.run(scale=0.0), d.want(scale=0.0))
     need = kq.attention_workspace_bytes(c.cache, c.batch, c.hq)
     if need:
         with pytest.raises(kq.KQError, match="KQ_ERR_LIMIT"):
@@ -261,6 +308,29 @@ def test_graph_serves_a_growing_sequence():
     got = c.run(stream=side)
     side.synchronize()
     assert torch.equal(got, out)
+
+
+@pytest.mark.parametrize("g", [4, 24])
+def test_an_expired_wait_is_reported(g):
+    """With a limit far below the time a page takes to arrive the call reports
+    it, gives NaN where it shows, and the next call is as always."""
+    c = Case(R.F16, 4, g, 128, [2], [60000], seed=15)
+    want = c.run()
+    from quant_quantized_matvec_gb300 import _binding
+    lib = _binding.load()
+    torch.cuda.synchronize()
+    lib.kq_set_wait_limit_ns(1)
+    try:
+        # (a page may come before its first test: then nothing expires)
+        got = c.run()
+        torch.cuda.synchronize()
+    finally:
+        lib.kq_set_wait_limit_ns(0)
+    expired = kq.device_error()
+    same = (got == want) | torch.isnan(got)
+    assert same.all()
+    assert torch.isnan(got).any() == expired
+    assert torch.equal(c.run(), want)
 
 
 def test_refusals():
