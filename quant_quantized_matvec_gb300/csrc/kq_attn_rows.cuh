@@ -52,7 +52,11 @@ struct RowsCommon {
     RunShared run;
     uint64_t rawfull[kRowSlots], rawempty[kRowSlots], scaled[kRowSlots];
     uint64_t kready[2], kfree[2], vready[2], vfree[2];
-    uint64_t sfree[2], sdone[4], pready[4], pvdone[4], ofree, drain[2];
+    // sdone: by tile & 3.  (A phase's parity tells it from the next only, so no
+    // barrier may complete twice before its waiter has looked, nor be waited for
+    // two phases ahead: S of tile t + 4 needs the buffer of tile t, or of a later
+    // one, back.)
+    uint64_t sfree[4], sdone[4], pready[4], pvdone[4], ofree, drain[2];
     uint32_t tmem;
     int dead;
     int badpage[4];          // of tile t & 3: the page is not valid
@@ -74,8 +78,9 @@ struct RowsSmem {
     static constexpr int kSlots = kRoom < kRowSlots ? kRoom : kRowSlots;
     static constexpr int kTotal = kRaw + kSlots * kHalf + 1024;  // (1024: alignment)
     // columns of tensor memory
-    static constexpr int kQ = 0, kP = D, kS = D + 64, kO = D + 192;
-    static_assert(sizeof(RowsCommon) <= kTiles0 && kSlots >= 3 && kO + D <= 512, "layout");
+    static constexpr int kQ = 0, kP = D, kO = D + 64, kS = 2 * D + 64;
+    static constexpr int kSBufs = D == 64 ? 4 : 3;
+    static_assert(sizeof(RowsCommon) <= kTiles0 && kSlots >= 3 && kS + 64 * kSBufs <= 512, "layout");
     static_assert(128 * (D + 4) * 4 <= 4 * kBuf + kSlots * kHalf, "the join's rows");
 };
 
@@ -201,10 +206,6 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     const int rb = 32 * qw;          // rows of a block
     const int ns = 4 / qw;           // sets
     const int nsl = ns == 4 ? 2 : ns == 2 ? 1 : 0;  // log2
-    // Barriers that tell a set its S: one a set, but two where there is one
-    // set, as both buffers may be done before it looks (a phase's parity tells
-    // it from the next only).
-    const int nd = ns == 1 ? 2 : ns, ndl = ns == 1 ? 1 : nsl;
     auto bar = [&](const uint64_t &b) { return kq::smem_addr(&b); };
 
     if (tid == 0) {
@@ -218,9 +219,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             kq::mbar_init(bar(cm.vready[i]), kConvWarps);
             kq::mbar_init(bar(cm.kfree[i]), 1);
             kq::mbar_init(bar(cm.vfree[i]), 1);
-            kq::mbar_init(bar(cm.sfree[i]), qw);
         }
         for (int i = 0; i < 4; ++i) {
+            kq::mbar_init(bar(cm.sfree[i]), qw);
             kq::mbar_init(bar(cm.sdone[i]), 1);
             kq::mbar_init(bar(cm.pvdone[i]), 1);
             kq::mbar_init(bar(cm.pready[i]), qw);
@@ -416,11 +417,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                     ok = left <= 0 ? (-left < 64 ? nw >> -left : 0) : (nw << left) | ~(~0ull << left);
                 }
                 // ---- S, maxima, probabilities times 2^15
-                wait(cm.sdone[t & (nd - 1)], t >> ndl);
+                const int sb = t % M::kSBufs;
+                wait(cm.sdone[t & 3], t >> 2);
                 tc_after();
                 float f = rowf * (L::kQuant ? *(volatile float *)&cm.kf[t & 7] : 1.f);
                 if (*(volatile int *)&cm.badpage[t & 3]) f = quiet_nan();
-                const uint32_t sa = mine + M::kS + 64 * (t & 1);
+                const uint32_t sa = mine + M::kS + 64 * sb;
                 // the half page's scores, those not attended as -infinity
                 auto scores = [&](int half, uint32_t (&d)[32]) {
                     tc_load32(d, sa + 32 * half);
@@ -515,7 +517,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                 tc_before();
                 __syncwarp();
                 if (lane == 0) {
-                    kq::mbar_arrive(bar(cm.sfree[t & 1]));
+                    kq::mbar_arrive(bar(cm.sfree[sb]));
                     kq::mbar_arrive(bar(cm.pready[t & (ns - 1)]));
                 }
             };
@@ -768,13 +770,14 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                 tc_after();
                 for (int t = g.t0; t < g.t0 + g.npg; ++t) {
                     wait(cm.kready[t & 1], t >> 1);
-                    if (t >= 2) wait(cm.sfree[t & 1], (t >> 1) - 1);
+                    const int sb = t % M::kSBufs;
+                    if (t >= M::kSBufs) wait(cm.sfree[sb], t / M::kSBufs - 1);
                     tc_after();
                     if (__any_sync(~0u, dead())) continue;
                     const uint32_t buf = uniform(t & 1);
-                    const uint32_t set = uniform(bar(cm.sdone[t & (nd - 1)]));
+                    const uint32_t usb = uniform(sb), done = uniform(t & 3);
                     const uint64_t kt = tile_desc(base + M::kTiles0 + buf * M::kBuf);
-                    const uint32_t d = tm + M::kS + 64 * buf;
+                    const uint32_t d = tm + M::kS + 64 * usb;
                     if (elected()) {
 #pragma unroll
                         for (int term = 0; term < kTerms; ++term)
@@ -787,7 +790,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                                 else tc_mma<false>(d, q, b, tile_idesc(kPage));
                             }
                         tc_commit(bar(cm.kfree[0]) + 8 * buf);
-                        tc_commit(set);
+                        tc_commit(bar(cm.sdone[0]) + 8 * done);
                     }
                     __syncwarp();
                 }
