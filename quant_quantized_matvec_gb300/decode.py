@@ -47,7 +47,7 @@ def _on(stream):
     """The stream's pointer, and a context in which new tensors belong to it
     (None: they do already)."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()), None
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()), None
     return stream.cuda_stream, torch.cuda.stream(stream)
 
 
@@ -60,6 +60,9 @@ def _empty(shape, dtype, device, on):
 
 def _tensor(t, name, dtype, shape=None, dense=True):
     """The address of a CUDA tensor after the checks."""
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype
+            and (shape is None or t.shape == shape) and (not dense or t.is_contiguous())):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -68,9 +71,15 @@ def _tensor(t, name, dtype, shape=None, dense=True):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if dense and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _out(t, name, dtype, shape, device, on):
+    """An output that was given, checked, or a new one; and its address."""
+    if t is None:
+        t = _empty(shape, dtype, device, on)
+        return t, t.data_ptr()
+    return t, _tensor(t, name, dtype, shape)
 
 
 def _heads(t, name, shape):
@@ -197,12 +206,9 @@ def kv_read(cache, batch, k=None, v=None, stream=None):
     """The batch's places read back: (k, v) f32 [ntok, kv_heads, head_dim]."""
     shape = (batch.ntok, cache.kv_heads, cache.head_dim)
     st, on = _on(stream)
-    if k is None:
-        k = _empty(shape, torch.float32, cache.data.device, on)
-    if v is None:
-        v = _empty(shape, torch.float32, cache.data.device, on)
-    _call("kq_kv_read", cache._p, batch._p, _tensor(k, "k", torch.float32, shape),
-          _tensor(v, "v", torch.float32, shape), st)
+    k, kp = _out(k, "k", torch.float32, shape, cache.data.device, on)
+    v, vp = _out(v, "v", torch.float32, shape, cache.data.device, on)
+    _call("kq_kv_read", cache._p, batch._p, kp, vp, st)
     return k, v
 
 
@@ -256,12 +262,13 @@ def tree_attention(cache, batch, q, mask=None, scale=None, out=None, workspace=N
     qp, qs = _heads(q, "q", shape)
     mp = None if mask is None else _tensor(mask, "mask", torch.int64, (batch.ntok,))
     st, on = _on(stream)
-    if out is None:
-        out = _empty(shape, torch.float32, q.device, on)
-    op = _tensor(out, "out", torch.float32, shape)
+    out, op = _out(out, "out", torch.float32, shape, q.device, on)
     if workspace is None:
-        workspace = _empty(attention_workspace_bytes(cache, batch, heads), torch.uint8, q.device, on)
-    wp, wn = _tensor(workspace, "workspace", torch.uint8), workspace.numel()
+        wn = attention_workspace_bytes(cache, batch, heads)
+        workspace = _empty(wn, torch.uint8, q.device, on)
+        wp = workspace.data_ptr()
+    else:
+        wp, wn = _tensor(workspace, "workspace", torch.uint8), workspace.numel()
     _call("kq_tree_attention", cache._p, batch._p, qp, qs, heads, mp,
           cache.head_dim ** -0.5 if scale is None else float(scale), op, wp, wn, st)
     return out
@@ -288,18 +295,14 @@ def verify_tree(start, tokens, parents, p, q, u, u_next, max_new, path=None, cou
     pp, ps = rows(p, "p")
     qp, qs = (None, 0) if q is None else rows(q, "q")
     st, on = _on(stream)
-    if path is None:
-        path = _empty(ntok, torch.int32, p.device, on)
-    if count is None:
-        count = _empty(nseq, torch.int32, p.device, on)
-    if next_token is None:
-        next_token = _empty(nseq, torch.int32, p.device, on)
+    dev = p.device
+    path, path_p = _out(path, "path", torch.int32, (ntok,), dev, on)
+    count, count_p = _out(count, "count", torch.int32, (nseq,), dev, on)
+    next_token, next_p = _out(next_token, "next_token", torch.int32, (nseq,), dev, on)
     _call("kq_verify_tree", nseq, ntok, int(max_new),
           _tensor(start, "start", torch.int32, (nseq + 1,)),
           _tensor(tokens, "tokens", torch.int32, (ntok,)),
           _tensor(parents, "parents", torch.int32, (ntok,)), pp, ps, qp, qs, shape[1],
           _tensor(u, "u", torch.float32, (ntok,)), _tensor(u_next, "u_next", torch.float32, (nseq,)),
-          _tensor(path, "path", torch.int32, (ntok,)),
-          _tensor(count, "count", torch.int32, (nseq,)),
-          _tensor(next_token, "next_token", torch.int32, (nseq,)), st)
+          path_p, count_p, next_p, st)
     return path, count, next_token
