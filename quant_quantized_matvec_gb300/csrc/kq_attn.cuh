@@ -92,7 +92,7 @@ template <int FMT, int D, int NT>
 struct AttnSmem {
     static constexpr int kRows = 4 * NT;
     static constexpr int kWg = 4;             // warps of a group
-// Groups of an SM: what registers (with the producer warp: 80 a thread for
+    // Groups of an SM: what registers (with the producer warp: 80 a thread for
     // 20 warps, 96 for 16, 128 for 12) and, for f16, shared memory hold.
     // One tile of an 8-bit cache: 157 us with four groups, 150 with five
     // (32 sequences of 16384 tokens at most, 32 / 8 heads).
@@ -462,108 +462,108 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, NT>::kGroups * AttnSmem<FMT, 
             float S[NT][2];
             float *sm = smax + (k & 1) * kWg * RB;
             if (k < count) {
-            const int left = s.ctx - (pg0 + g + k * a.ng) * kPage;
-            const bool edge = left < kPage;  // new tokens, or the end
-            // ---- 1. logits of tokens 16 w + n8 (+ 8)
-            const int ks = arrived();
-            const uint8_t *kb = gbase + ks * M::kHalf;
-            const bool badpage = cm.badpage[g * kMaxSlots + ks];
-            {
-                float acc[NT][4];
-                constexpr int kLane = L::kSlabBytes / 4;  // bytes of a lane in a slab
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    S[t][0] = S[t][1] = 0.f;
-                    acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
-                }
-#pragma unroll
-                for (int sl = 0; sl < L::kSlabs; ++sl) {
-                    uint32_t raw[2][kLane / 4];
-                    uint32_t skw[2][(L::kSlabGroups + 1) / 2];  // scales, two groups a word
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int tok = 16 * w + 8 * j + n8;
-                        const uint8_t *p =
-                            kb + sl * kPage * L::kSlabBytes + tok * L::kSlabBytes + c * kLane;
-                        if constexpr (kLane == 16) {
-                            const uint4 v = *reinterpret_cast<const uint4 *>(p);
-                            raw[j][0] = v.x, raw[j][1] = v.y, raw[j][2] = v.z, raw[j][3] = v.w;
-                        } else {
-                            const uint2 v = *reinterpret_cast<const uint2 *>(p);
-                            raw[j][0] = v.x, raw[j][1] = v.y;
-                        }
-                        if constexpr (L::kQuant) {
-                            const uint8_t *sp = kb + L::k_scale(tok, sl * L::kSlabGroups);
-                            if constexpr (L::kSlabGroups == 4) {
-                                const uint2 v = *reinterpret_cast<const uint2 *>(sp);
-                                skw[j][0] = v.x, skw[j][1] = v.y;
-                            } else {
-                                skw[j][0] = *reinterpret_cast<const uint32_t *>(sp);
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int gl = 0; gl < L::kSlabGroups; ++gl) {
-                        uint32_t bb[2][4];
-                        float sk[2];
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            if constexpr (FMT == KQ_KV_F16) {
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) bb[j][i] = raw[j][i];
-                            } else if constexpr (FMT == KQ_KV_Q8) {
-                                codes8(raw[j][2 * gl], bb[j][0], bb[j][1]);
-                                codes8(raw[j][2 * gl + 1], bb[j][2], bb[j][3]);
-                            } else {
-                                codes4(raw[j][gl], bb[j]);
-                            }
-                            if constexpr (L::kQuant) {
-                                const __half2 h = half2_of(skw[j][gl / 2]);
-                                sk[j] = gl & 1 ? __high2float(h) : __low2float(h);
-                            }
-                        }
-                        const uint4 k0 = make_uint4(bb[0][0], bb[1][0], bb[0][1], bb[1][1]);
-                        const uint4 k1 = make_uint4(bb[0][2], bb[1][2], bb[0][3], bb[1][3]);
-#pragma unroll
-                        for (int t = 0; t < NT; ++t) {
-                            const uint4 q = qs[(t * L::kGroups + sl * L::kSlabGroups + gl) * 32 + lane];
-                            if constexpr (L::kQuant) {
-                                float d[4] = {0.f, 0.f, 0.f, 0.f};
-                                mma(d, k0, q.x, q.y);
-                                mma(d, k1, q.z, q.w);
-                                S[t][0] = fmaf(sk[0], d[0] + d[1], S[t][0]);
-                                S[t][1] = fmaf(sk[1], d[2] + d[3], S[t][1]);
-                            } else {
-                                mma(acc[t], k0, q.x, q.y);
-                                mma(acc[t], k1, q.z, q.w);
-                            }
-                        }
-                    }
-                }
-                if constexpr (!L::kQuant) {
+                const int left = s.ctx - (pg0 + g + k * a.ng) * kPage;
+                const bool edge = left < kPage;  // new tokens, or the end
+                // ---- 1. logits of tokens 16 w + n8 (+ 8)
+                const int ks = arrived();
+                const uint8_t *kb = gbase + ks * M::kHalf;
+                const bool badpage = cm.badpage[g * kMaxSlots + ks];
+                {
+                    float acc[NT][4];
+                    constexpr int kLane = L::kSlabBytes / 4;  // bytes of a lane in a slab
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        S[t][0] = acc[t][0] + acc[t][1];
-                        S[t][1] = acc[t][2] + acc[t][3];
+                        S[t][0] = S[t][1] = 0.f;
+                        acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
+                    }
+#pragma unroll
+                    for (int sl = 0; sl < L::kSlabs; ++sl) {
+                        uint32_t raw[2][kLane / 4];
+                        uint32_t skw[2][(L::kSlabGroups + 1) / 2];  // scales, two groups a word
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const int tok = 16 * w + 8 * j + n8;
+                            const uint8_t *p =
+                                kb + sl * kPage * L::kSlabBytes + tok * L::kSlabBytes + c * kLane;
+                            if constexpr (kLane == 16) {
+                                const uint4 v = *reinterpret_cast<const uint4 *>(p);
+                                raw[j][0] = v.x, raw[j][1] = v.y, raw[j][2] = v.z, raw[j][3] = v.w;
+                            } else {
+                                const uint2 v = *reinterpret_cast<const uint2 *>(p);
+                                raw[j][0] = v.x, raw[j][1] = v.y;
+                            }
+                            if constexpr (L::kQuant) {
+                                const uint8_t *sp = kb + L::k_scale(tok, sl * L::kSlabGroups);
+                                if constexpr (L::kSlabGroups == 4) {
+                                    const uint2 v = *reinterpret_cast<const uint2 *>(sp);
+                                    skw[j][0] = v.x, skw[j][1] = v.y;
+                                } else {
+                                    skw[j][0] = *reinterpret_cast<const uint32_t *>(sp);
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int gl = 0; gl < L::kSlabGroups; ++gl) {
+                            uint32_t bb[2][4];
+                            float sk[2];
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                if constexpr (FMT == KQ_KV_F16) {
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) bb[j][i] = raw[j][i];
+                                } else if constexpr (FMT == KQ_KV_Q8) {
+                                    codes8(raw[j][2 * gl], bb[j][0], bb[j][1]);
+                                    codes8(raw[j][2 * gl + 1], bb[j][2], bb[j][3]);
+                                } else {
+                                    codes4(raw[j][gl], bb[j]);
+                                }
+                                if constexpr (L::kQuant) {
+                                    const __half2 h = half2_of(skw[j][gl / 2]);
+                                    sk[j] = gl & 1 ? __high2float(h) : __low2float(h);
+                                }
+                            }
+                            const uint4 k0 = make_uint4(bb[0][0], bb[1][0], bb[0][1], bb[1][1]);
+                            const uint4 k1 = make_uint4(bb[0][2], bb[1][2], bb[0][3], bb[1][3]);
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) {
+                                const uint4 q = qs[(t * L::kGroups + sl * L::kSlabGroups + gl) * 32 + lane];
+                                if constexpr (L::kQuant) {
+                                    float d[4] = {0.f, 0.f, 0.f, 0.f};
+                                    mma(d, k0, q.x, q.y);
+                                    mma(d, k1, q.z, q.w);
+                                    S[t][0] = fmaf(sk[0], d[0] + d[1], S[t][0]);
+                                    S[t][1] = fmaf(sk[1], d[2] + d[3], S[t][1]);
+                                } else {
+                                    mma(acc[t], k0, q.x, q.y);
+                                    mma(acc[t], k1, q.z, q.w);
+                                }
+                            }
+                        }
+                    }
+                    if constexpr (!L::kQuant) {
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            S[t][0] = acc[t][0] + acc[t][1];
+                            S[t][1] = acc[t][2] + acc[t][3];
+                        }
                     }
                 }
-            }
-            // ---- 2. row maxima
+                // ---- 2. row maxima
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const float f = badpage ? quiet_nan() : cm.rowfactor[4 * t + c];
-                S[t][0] *= f, S[t][1] *= f;
-                if (edge) {
-                    const uint64_t ok = allowed(left, 4 * t + c) >> (16 * w + n8);
-                    if (!(ok & 1)) S[t][0] = -INFINITY;
-                    if (!(ok & 256)) S[t][1] = -INFINITY;
+                for (int t = 0; t < NT; ++t) {
+                    const float f = badpage ? quiet_nan() : cm.rowfactor[4 * t + c];
+                    S[t][0] *= f, S[t][1] *= f;
+                    if (edge) {
+                        const uint64_t ok = allowed(left, 4 * t + c) >> (16 * w + n8);
+                        if (!(ok & 1)) S[t][0] = -INFINITY;
+                        if (!(ok & 256)) S[t][1] = -INFINITY;
+                    }
+                    float v = fmaxf(S[t][0], S[t][1]);
+                    v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
+                    v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
+                    v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
+                    if (n8 == 0) sm[w * RB + 4 * t + c] = v;
                 }
-                float v = fmaxf(S[t][0], S[t][1]);
-                v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
-                v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
-                v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
-                if (n8 == 0) sm[w * RB + 4 * t + c] = v;
-            }
             }
             group_sync<kGroupThreads>(g);
             // every warp is done with page k's keys and page k - 2's values
@@ -575,241 +575,243 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, NT>::kGroups * AttnSmem<FMT, 
                 }
             }
             if (k > 0) {
-            const int left = s.ctx - (pg0 + g + (k - 1) * a.ng) * kPage;
-            const bool edge = left < kPage;
-            const __half *pv = ps + ((k - 1) & 1) * 2 * RB * kPage;
-            // ---- 3. values kSlice w .. of all 64 tokens
-            const int vs = arrived();
-            // (offsets of Kv count from the block's start; the slot starts at
-            // the values)
-            const uint8_t *vb = gbase + vs * M::kHalf - L::kV;
-            auto token = [&](int i) {  // lane's token i of 16
-                return FMT == KQ_KV_F16 ? 32 * (i >> 3) + 8 * c + (i & 7) : 16 * c + i;
-            };
-            // tokens that no row may attend (past the end), or whose values
-            // are not finite: left out of the MMAs; the latter are added row
-            // by row below
-            uint64_t bad = 0;
-            const uint64_t held = !edge ? ~0ull
-                                  : left + s.n >= kPage ? ~0ull
-                                  : left + s.n <= 0 ? 0ull : ~(~0ull << (left + s.n));
+                const int left = s.ctx - (pg0 + g + (k - 1) * a.ng) * kPage;
+                const bool edge = left < kPage;
+                const __half *pv = ps + ((k - 1) & 1) * 2 * RB * kPage;
+                // ---- 3. values kSlice w .. of all 64 tokens
+                const int vs = arrived();
+                // (offsets of Kv count from the block's start; the slot starts at
+                // the values)
+                const uint8_t *vb = gbase + vs * M::kHalf - L::kV;
+                auto token = [&](int i) {  // lane's token i of 16
+                    return FMT == KQ_KV_F16 ? 32 * (i >> 3) + 8 * c + (i & 7) : 16 * c + i;
+                };
+                // tokens that no row may attend (past the end), or whose values
+                // are not finite: left out of the MMAs; the latter are added row
+                // by row below
+                uint64_t bad = 0;
+                const uint64_t held = !edge ? ~0ull
+                                      : left + s.n >= kPage ? ~0ull
+                                      : left + s.n <= 0 ? 0ull : ~(~0ull << (left + s.n));
 #pragma unroll
-            for (int sg = 0; sg < kSliceGroups; ++sg) {
-                const int group = w * kSlice / kGroup + sg;
-                float fac = 1.f;
-                __half2 sn[8];     // scales of the lane's tokens, normalised
-                uint32_t keep[8];  // f16: pairs of tokens that stay
-                if constexpr (L::kQuant) {
-                    const uint4 *sp = reinterpret_cast<const uint4 *>(vb + L::v_scale(16 * c, group));
-                    uint32_t raw[8];
-                    const uint4 s0 = sp[0], s1 = sp[1];
-                    raw[0] = s0.x, raw[1] = s0.y, raw[2] = s0.z, raw[3] = s0.w;
-                    raw[4] = s1.x, raw[5] = s1.y, raw[6] = s1.z, raw[7] = s1.w;
-                    if (edge) {
+                for (int sg = 0; sg < kSliceGroups; ++sg) {
+                    const int group = w * kSlice / kGroup + sg;
+                    float fac = 1.f;
+                    __half2 sn[8];     // scales of the lane's tokens, normalised
+                    uint32_t keep[8];  // f16: pairs of tokens that stay
+                    if constexpr (L::kQuant) {
+                        const uint4 *sp = reinterpret_cast<const uint4 *>(vb + L::v_scale(16 * c, group));
+                        uint32_t raw[8];
+                        const uint4 s0 = sp[0], s1 = sp[1];
+                        raw[0] = s0.x, raw[1] = s0.y, raw[2] = s0.z, raw[3] = s0.w;
+                        raw[4] = s1.x, raw[5] = s1.y, raw[6] = s1.z, raw[7] = s1.w;
+                        if (edge) {
+                            uint32_t b16 = 0;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const uint32_t h = (raw[i / 2] >> (16 * (i & 1))) & 0xFFFFu;
+                                const bool in = (held >> (16 * c + i)) & 1;
+                                const bool nf = (h & 0x7C00u) == 0x7C00u;
+                                if (in && nf) b16 |= 1u << i;
+                                if (!in || nf) raw[i / 2] &= i & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                            }
+                            bad = (uint64_t)b16 << (16 * c);
+                            bad |= __shfl_xor_sync(~0u, bad, 1);
+                            bad |= __shfl_xor_sync(~0u, bad, 2);
+                        }
+                        // |scales| of the page and group are below 2^ex: times
+                        // 2^-ex, they and a probability make less than 2^15
+                        __half2 big = __habs2(half2_of(raw[0]));
+#pragma unroll
+                        for (int i = 1; i < 8; ++i) big = __hmax2(big, __habs2(half2_of(raw[i])));
+                        big = __hmax2(big, half2_of(__shfl_xor_sync(~0u, bits_of(big), 1)));
+                        big = __hmax2(big, half2_of(__shfl_xor_sync(~0u, bits_of(big), 2)));
+                        const uint32_t top = bits_of(__hmax2(big, __lowhigh2highlow(big))) & 0xFFFFu;
+                        const int ex = max((int)(top >> 10) - 14, -15);
+                        const uint32_t up = ex <= 14 ? (uint32_t)(15 - ex) << 10 : 0x400u >> (ex - 14);
+                        fac = __uint_as_float((uint32_t)(127 + ex) << 23);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            sn[i] = __hmul2(half2_of(raw[i]), half2_of(up | up << 16));
+                    } else if (edge) {
+                        // (one pass over the slice's values, on edge pages only)
                         uint32_t b16 = 0;
+#pragma unroll 1
+                        for (int nt = 0; nt < 2 * kTiles; ++nt) {
+                            const int e = w * kSlice + 8 * nt + n8;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const uint32_t v = *reinterpret_cast<const uint32_t *>(
+                                    vb + L::v_word(e, token(2 * i) / 2));
+                                if ((v & 0x7C00u) == 0x7C00u) b16 |= 1u << (2 * i);
+                                if ((v & 0x7C000000u) == 0x7C000000u) b16 |= 2u << (2 * i);
+                            }
+                        }
+                        b16 |= __shfl_xor_sync(~0u, b16, 4);
+                        b16 |= __shfl_xor_sync(~0u, b16, 8);
+                        b16 |= __shfl_xor_sync(~0u, b16, 16);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const uint32_t h = (raw[i / 2] >> (16 * (i & 1))) & 0xFFFFu;
-                            const bool in = (held >> (16 * c + i)) & 1;
-                            const bool nf = (h & 0x7C00u) == 0x7C00u;
-                            if (in && nf) b16 |= 1u << i;
-                            if (!in || nf) raw[i / 2] &= i & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                            const bool in = (held >> token(i)) & 1;
+                            if (((b16 >> i) & 1) && in) bad |= 1ull << token(i);
+                            if (!in) b16 |= 1u << i;
                         }
-                        bad = (uint64_t)b16 << (16 * c);
                         bad |= __shfl_xor_sync(~0u, bad, 1);
                         bad |= __shfl_xor_sync(~0u, bad, 2);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            keep[i] = (b16 >> (2 * i) & 1 ? 0u : 0xFFFFu) |
+                                      (b16 >> (2 * i) & 2 ? 0u : 0xFFFF0000u);
                     }
-                    // |scales| of the page and group are below 2^ex: times
-                    // 2^-ex, they and a probability make less than 2^15
-                    __half2 big = __habs2(half2_of(raw[0]));
+                    // the slice's values, as operands of the four k-steps
+                    uint4 vv[kTilesG][4];
 #pragma unroll
-                    for (int i = 1; i < 8; ++i) big = __hmax2(big, __habs2(half2_of(raw[i])));
-                    big = __hmax2(big, half2_of(__shfl_xor_sync(~0u, bits_of(big), 1)));
-                    big = __hmax2(big, half2_of(__shfl_xor_sync(~0u, bits_of(big), 2)));
-                    const uint32_t top = bits_of(__hmax2(big, __lowhigh2highlow(big))) & 0xFFFFu;
-                    const int ex = max((int)(top >> 10) - 14, -15);
-                    const uint32_t up = ex <= 14 ? (uint32_t)(15 - ex) << 10 : 0x400u >> (ex - 14);
-                    fac = __uint_as_float((uint32_t)(127 + ex) << 23);
+                    for (int mt = 0; mt < kTilesG; ++mt) {
+                        uint32_t x[2][8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        sn[i] = __hmul2(half2_of(raw[i]), half2_of(up | up << 16));
-                } else if (edge) {
-                    // (one pass over the slice's values, on edge pages only)
-                    uint32_t b16 = 0;
-#pragma unroll 1
-                    for (int nt = 0; nt < 2 * kTiles; ++nt) {
-                        const int e = w * kSlice + 8 * nt + n8;
+                        for (int h = 0; h < 2; ++h) {
+                            const int e = w * kSlice + 16 * (sg * kTilesG + mt) + 8 * h + n8;
+                            if constexpr (FMT == KQ_KV_F16) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const uint32_t v = *reinterpret_cast<const uint32_t *>(
-                                vb + L::v_word(e, token(2 * i) / 2));
-                            if ((v & 0x7C00u) == 0x7C00u) b16 |= 1u << (2 * i);
-                            if ((v & 0x7C000000u) == 0x7C000000u) b16 |= 2u << (2 * i);
+                                for (int i = 0; i < 2; ++i) {
+                                    const uint4 v = *reinterpret_cast<const uint4 *>(
+                                        vb + L::v_word(e, token(8 * i) / 2));
+                                    x[h][4 * i] = v.x, x[h][4 * i + 1] = v.y;
+                                    x[h][4 * i + 2] = v.z, x[h][4 * i + 3] = v.w;
+                                }
+                                if (edge) {
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) x[h][i] &= keep[i];
+                                }
+                            } else if constexpr (FMT == KQ_KV_Q8) {
+                                const uint4 v = *reinterpret_cast<const uint4 *>(vb + L::v_word(e, 4 * c));
+                                codes8(v.x, x[h][0], x[h][1]);
+                                codes8(v.y, x[h][2], x[h][3]);
+                                codes8(v.z, x[h][4], x[h][5]);
+                                codes8(v.w, x[h][6], x[h][7]);
+                            } else {
+                                const uint2 v = *reinterpret_cast<const uint2 *>(vb + L::v_word(e, 2 * c));
+                                uint32_t y[4];
+                                codes4(v.x, y);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) x[h][i] = y[i];
+                                codes4(v.y, y);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) x[h][4 + i] = y[i];
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            vv[mt][i] =
+                            make_uint4(x[0][2 * i], x[1][2 * i], x[0][2 * i + 1], x[1][2 * i + 1]);
+                    }
+                    // scales in the order of the probabilities' pairs
+                    if constexpr (FMT == KQ_KV_Q4) {
+#pragma unroll
+                        for (int i = 0; i < 8; i += 4) {
+                            const __half2 s01 = sn[i], s23 = sn[i + 1], s45 = sn[i + 2], s67 = sn[i + 3];
+                            sn[i] = __lows2half2(s01, s45), sn[i + 1] = __highs2half2(s01, s45);
+                            sn[i + 2] = __lows2half2(s23, s67), sn[i + 3] = __highs2half2(s23, s67);
                         }
                     }
-                    b16 |= __shfl_xor_sync(~0u, b16, 4);
-                    b16 |= __shfl_xor_sync(~0u, b16, 8);
-                    b16 |= __shfl_xor_sync(~0u, b16, 16);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const bool in = (held >> token(i)) & 1;
-                        if (((b16 >> i) & 1) && in) bad |= 1ull << token(i);
-                        if (!in) b16 |= 1u << i;
-                    }
-                    bad |= __shfl_xor_sync(~0u, bad, 1);
-                    bad |= __shfl_xor_sync(~0u, bad, 2);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        keep[i] = (b16 >> (2 * i) & 1 ? 0u : 0xFFFFu) |
-                                  (b16 >> (2 * i) & 2 ? 0u : 0xFFFF0000u);
-                }
-                // the slice's values, as operands of the four k-steps
-                uint4 vv[kTilesG][4];
-#pragma unroll
-                for (int mt = 0; mt < kTilesG; ++mt) {
-                    uint32_t x[2][8];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int e = w * kSlice + 16 * (sg * kTilesG + mt) + 8 * h + n8;
-                        if constexpr (FMT == KQ_KV_F16) {
+                    for (int t = 0; t < NT; ++t) {
+                        // column n8: the hi or lo terms of row n8 / 2
+                        uint32_t pb[8];
+                        const int col = 8 * t + n8;
+                        auto load = [&](int of, uint32_t (&x)[8]) {
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
                                 const uint4 v = *reinterpret_cast<const uint4 *>(
-                                    vb + L::v_word(e, token(8 * i) / 2));
-                                x[h][4 * i] = v.x, x[h][4 * i + 1] = v.y;
-                                x[h][4 * i + 2] = v.z, x[h][4 * i + 3] = v.w;
+                                    pv + of * kPage + (((2 * c + i) ^ (of & 1)) << 3));
+                                x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
                             }
-                            if (edge) {
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) x[h][i] &= keep[i];
-                            }
-                        } else if constexpr (FMT == KQ_KV_Q8) {
-                            const uint4 v = *reinterpret_cast<const uint4 *>(vb + L::v_word(e, 4 * c));
-                            codes8(v.x, x[h][0], x[h][1]);
-                            codes8(v.y, x[h][2], x[h][3]);
-                            codes8(v.z, x[h][4], x[h][5]);
-                            codes8(v.w, x[h][6], x[h][7]);
-                        } else {
-                            const uint2 v = *reinterpret_cast<const uint2 *>(vb + L::v_word(e, 2 * c));
-                            uint32_t y[4];
-                            codes4(v.x, y);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) x[h][i] = y[i];
-                            codes4(v.y, y);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) x[h][4 + i] = y[i];
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        vv[mt][i] = make_uint4(x[0][2 * i], x[1][2 * i], x[0][2 * i + 1], x[1][2 * i + 1]);
-                }
-                // scales in the order of the probabilities' pairs
-                if constexpr (FMT == KQ_KV_Q4) {
-#pragma unroll
-                    for (int i = 0; i < 8; i += 4) {
-                        const __half2 s01 = sn[i], s23 = sn[i + 1], s45 = sn[i + 2], s67 = sn[i + 3];
-                        sn[i] = __lows2half2(s01, s45), sn[i + 1] = __highs2half2(s01, s45);
-                        sn[i + 2] = __lows2half2(s23, s67), sn[i + 3] = __highs2half2(s23, s67);
-                    }
-                }
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    // column n8: the hi or lo terms of row n8 / 2
-                    uint32_t pb[8];
-                    const int col = 8 * t + n8;
-                    auto load = [&](int of, uint32_t (&x)[8]) {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const uint4 v = *reinterpret_cast<const uint4 *>(
-                                pv + of * kPage + (((2 * c + i) ^ (of & 1)) << 3));
-                            x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
-                        }
-                    };
-                    if constexpr (L::kQuant) {
-                        // (hi + lo) s as two terms: hi s is rounded, and what
-                        // that loses (exact in f16) joins lo s
-                        uint32_t hi[8], lo[8];
-                        load(col & ~1, hi);
-                        load(col | 1, lo);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const __half2 h = half2_of(hi[i]), hs = __hmul2(h, sn[i]);
-                            const __half2 ls = __hfma2(half2_of(lo[i]), sn[i], __hfma2(h, sn[i], __hneg2(hs)));
-                            pb[i] = n8 & 1 ? bits_of(ls) : bits_of(hs);
-                        }
-                    } else {
-                        load(col, pb);
-                    }
-#pragma unroll
-                    for (int mt = 0; mt < kTilesG; ++mt) {
-                        float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) mma(d, vv[mt][i], pb[2 * i], pb[2 * i + 1]);
-                        float *o = O[t][sg * kTilesG + mt];
+                        };
                         if constexpr (L::kQuant) {
-                            o[0] = fmaf(d[0] + d[1], fac, o[0] * alpha[t]);
-                            o[1] = fmaf(d[2] + d[3], fac, o[1] * alpha[t]);
+                            // (hi + lo) s as two terms: hi s is rounded, and what
+                            // that loses (exact in f16) joins lo s
+                            uint32_t hi[8], lo[8];
+                            load(col & ~1, hi);
+                            load(col | 1, lo);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const __half2 h = half2_of(hi[i]), hs = __hmul2(h, sn[i]);
+                                const __half2 off = __hfma2(h, sn[i], __hneg2(hs));
+                                const __half2 ls = __hfma2(half2_of(lo[i]), sn[i], off);
+                                pb[i] = n8 & 1 ? bits_of(ls) : bits_of(hs);
+                            }
                         } else {
-                            o[0] = fmaf(o[0], alpha[t], d[0] + d[1]);
-                            o[1] = fmaf(o[1], alpha[t], d[2] + d[3]);
+                            load(col, pb);
+                        }
+#pragma unroll
+                        for (int mt = 0; mt < kTilesG; ++mt) {
+                            float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) mma(d, vv[mt][i], pb[2 * i], pb[2 * i + 1]);
+                            float *o = O[t][sg * kTilesG + mt];
+                            if constexpr (L::kQuant) {
+                                o[0] = fmaf(d[0] + d[1], fac, o[0] * alpha[t]);
+                                o[1] = fmaf(d[2] + d[3], fac, o[1] * alpha[t]);
+                            } else {
+                                o[0] = fmaf(o[0], alpha[t], d[0] + d[1]);
+                                o[1] = fmaf(o[1], alpha[t], d[2] + d[3]);
+                            }
+                        }
+                    }
+                    // values that are not finite reach the rows that attend them
+                    while (bad) {
+                        const int tok = __ffsll((long long)bad) - 1;
+                        bad &= bad - 1;
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            const int r = 4 * t + c;
+                            if (!((allowed(left, r) >> tok) & 1)) continue;
+                            const float prob = __half2float(pv[p_at<FMT>(2 * r, tok)]) +
+                                               __half2float(pv[p_at<FMT>(2 * r + 1, tok)]);
+#pragma unroll
+                            for (int mt = 0; mt < kTilesG; ++mt)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    const int e = w * kSlice + 16 * (sg * kTilesG + mt) + 8 * h + n8;
+                                    const uint32_t v = *reinterpret_cast<const uint32_t *>(
+                                        vb + L::v_word(e, tok / L::kVPerWord));
+                                    const int bit = tok % L::kVPerWord * L::kBits;
+                                    float x;
+                                    if constexpr (L::kQuant)
+                                        x = (float)((int)(v << (32 - L::kBits - bit)) >> (32 - L::kBits)) *
+                                            __half2float(*reinterpret_cast<const __half *>(
+                                                vb + L::v_scale(tok, group)));
+                                    else
+                                        x = __half2float(__ushort_as_half((uint16_t)(v >> bit)));
+                                    float &o = O[t][sg * kTilesG + mt][h];
+                                    o = fmaf(prob, x, o);
+                                }
                         }
                     }
                 }
-                // values that are not finite reach the rows that attend them
-                while (bad) {
-                    const int tok = __ffsll((long long)bad) - 1;
-                    bad &= bad - 1;
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        const int r = 4 * t + c;
-                        if (!((allowed(left, r) >> tok) & 1)) continue;
-                        const float prob = __half2float(pv[p_at<FMT>(2 * r, tok)]) +
-                                           __half2float(pv[p_at<FMT>(2 * r + 1, tok)]);
-#pragma unroll
-                        for (int mt = 0; mt < kTilesG; ++mt)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const int e = w * kSlice + 16 * (sg * kTilesG + mt) + 8 * h + n8;
-                                const uint32_t v = *reinterpret_cast<const uint32_t *>(
-                                    vb + L::v_word(e, tok / L::kVPerWord));
-                                const int bit = tok % L::kVPerWord * L::kBits;
-                                float x;
-                                if constexpr (L::kQuant)
-                                    x = (float)((int)(v << (32 - L::kBits - bit)) >> (32 - L::kBits)) *
-                                        __half2float(*reinterpret_cast<const __half *>(
-                                            vb + L::v_scale(tok, group)));
-                                else
-                                    x = __half2float(__ushort_as_half((uint16_t)(v >> bit)));
-                                float &o = O[t][sg * kTilesG + mt][h];
-                                o = fmaf(prob, x, o);
-                            }
-                    }
-                }
-            }
             }
             // ---- 2. probabilities
             if (k < count) {
                 __half *pw = ps + (k & 1) * 2 * RB * kPage;
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const int r = 4 * t + c;
-                float now = m[t];
+                for (int t = 0; t < NT; ++t) {
+                    const int r = 4 * t + c;
+                    float now = m[t];
 #pragma unroll
-                for (int i = 0; i < kWg; ++i) now = fmaxf(now, sm[i * RB + r]);
-                const float base = now == -INFINITY ? 0.f : now;
-                alpha[t] = exp2_of(m[t] - base);
-                m[t] = now;
-                const float high = base - 15.f;  // probabilities (and l, O) times 2^15
-                const float p0 = exp2_of(S[t][0] - high), p1 = exp2_of(S[t][1] - high);
-                l[t] = fmaf(l[t], alpha[t], p0 + p1);
-                const __half h0 = __float2half_rn(p0), h1 = __float2half_rn(p1);
-                const int tok = 16 * w + n8;
-                pw[p_at<FMT>(2 * r, tok)] = h0;
-                pw[p_at<FMT>(2 * r, tok + 8)] = h1;
-                pw[p_at<FMT>(2 * r + 1, tok)] = __float2half_rn(p0 - __half2float(h0));
-                pw[p_at<FMT>(2 * r + 1, tok + 8)] = __float2half_rn(p1 - __half2float(h1));
-            }
+                    for (int i = 0; i < kWg; ++i) now = fmaxf(now, sm[i * RB + r]);
+                    const float base = now == -INFINITY ? 0.f : now;
+                    alpha[t] = exp2_of(m[t] - base);
+                    m[t] = now;
+                    const float high = base - 15.f;  // probabilities (and l, O) times 2^15
+                    const float p0 = exp2_of(S[t][0] - high), p1 = exp2_of(S[t][1] - high);
+                    l[t] = fmaf(l[t], alpha[t], p0 + p1);
+                    const __half h0 = __float2half_rn(p0), h1 = __float2half_rn(p1);
+                    const int tok = 16 * w + n8;
+                    pw[p_at<FMT>(2 * r, tok)] = h0;
+                    pw[p_at<FMT>(2 * r, tok + 8)] = h1;
+                    pw[p_at<FMT>(2 * r + 1, tok)] = __float2half_rn(p0 - __half2float(h0));
+                    pw[p_at<FMT>(2 * r + 1, tok + 8)] = __float2half_rn(p1 - __half2float(h1));
+                }
             }
         }
 
@@ -817,30 +819,30 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, NT>::kGroups * AttnSmem<FMT, 
         // result (the ring is idle now and holds the groups' values)
         if (!producer) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            float v = l[t];
-            v += __shfl_xor_sync(~0u, v, 4);
-            v += __shfl_xor_sync(~0u, v, 8);
-            v += __shfl_xor_sync(~0u, v, 16);
-            if (n8 == 0) {
-                cm.ml[g][1 + w][4 * t + c] = v;
-                if (w == 0) cm.ml[g][0][4 * t + c] = m[t];
+            for (int t = 0; t < NT; ++t) {
+                float v = l[t];
+                v += __shfl_xor_sync(~0u, v, 4);
+                v += __shfl_xor_sync(~0u, v, 8);
+                v += __shfl_xor_sync(~0u, v, 16);
+                if (n8 == 0) {
+                    cm.ml[g][1 + w][4 * t + c] = v;
+                    if (w == 0) cm.ml[g][0][4 * t + c] = m[t];
+                }
             }
-        }
-        // (all copies have been used; the last page's values are handed back)
-        group_sync<kGroupThreads>(g);
-        if (count && w == 0 && lane == 0) {
-            kq::mbar_arrive(kq::smem_addr(&cm.empty[g * kMaxSlots + back]));
-            if (++back == a.nslot) back = 0;
-        }
-        float *os = reinterpret_cast<float *>(gbase);
+            // (all copies have been used; the last page's values are handed back)
+            group_sync<kGroupThreads>(g);
+            if (count && w == 0 && lane == 0) {
+                kq::mbar_arrive(kq::smem_addr(&cm.empty[g * kMaxSlots + back]));
+                if (++back == a.nslot) back = 0;
+            }
+            float *os = reinterpret_cast<float *>(gbase);
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int mt = 0; mt < kTiles; ++mt)
+                for (int mt = 0; mt < kTiles; ++mt)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    os[(4 * t + c) * D + w * kSlice + 16 * mt + 8 * h + n8] = O[t][mt][h];
+                    for (int h = 0; h < 2; ++h)
+                        os[(4 * t + c) * D + w * kSlice + 16 * mt + 8 * h + n8] = O[t][mt][h];
         }
         __syncthreads();
         const bool whole = npg == pages;
@@ -1035,11 +1037,16 @@ cudaError_t launch_attn(AttnArgs a, int sms, cudaStream_t s, int64_t *floats) {
 // key head has.
 template <int FMT, int D>
 cudaError_t attn_tiles(int64_t rows, const AttnArgs &a, int sms, cudaStream_t s, int64_t *floats) {
-    // (width 256: blocks of 16 rows for more; one of 32 spilled, 83 us against
-    // 59 for 8 sequences of 4100 tokens with 20 rows a key head)
-    return rows <= 4   ? launch_attn<FMT, D, 1>(a, sms, s, floats)
-           : rows <= 8 ? launch_attn<FMT, D, 2>(a, sms, s, floats)
-                       : launch_attn<FMT, D, 4>(a, sms, s, floats);
+    // Up to four tiles to a block, blocks alike.  (Width 256 has no other
+    // kernel for more rows; a block of 32 spilled, 83 us against 59 for 8
+    // sequences of 4100 tokens with 20 rows a key head.)
+    const int64_t tiles = (rows + 3) / 4, blocks = (tiles + 3) / 4;
+    switch ((int)((tiles + blocks - 1) / blocks)) {
+    case 1: return launch_attn<FMT, D, 1>(a, sms, s, floats);
+    case 2: return launch_attn<FMT, D, 2>(a, sms, s, floats);
+    case 3: return launch_attn<FMT, D, 3>(a, sms, s, floats);
+    default: return launch_attn<FMT, D, 4>(a, sms, s, floats);
+    }
 }
 
 template <int FMT>

@@ -139,6 +139,15 @@ def test_many_rows(fmt, dim, g, new):
 
 
 @pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("g,new", [(9, 1), (3, 4), (2, 6), (13, 1)])
+def test_some_rows(fmt, dim, g, new):
+    """9..13 rows a key head, tiles of four rows that are full and that are not."""
+    c = Case(fmt, 2, g, dim, [new, 1, new], [1500, 0, 129], seed=g)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
 @pytest.mark.parametrize("g,new", [(4, 1), (8, 1), (16, 1), (5, 5), (12, 5), (16, 6)])
 def test_many_pages_a_cta(fmt, g, new):
     """Enough pages that every ring goes round several times."""
@@ -176,6 +185,14 @@ def test_empty_rows_are_zero(fmt):
 def test_masked_places_do_not_reach_any_of_many_rows(fmt, bad, ctx):
     """The same with 48 rows a key head."""
     test_masked_places_do_not_reach_a_row(fmt, bad, ctx, g=8)
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
+@pytest.mark.parametrize("g", [1, 2])
+def test_masked_places_do_not_reach_any_of_few_rows(fmt, g):
+    """The same with 6 and 12 rows a key head."""
+    for ctx in (0, 61):
+        test_masked_places_do_not_reach_a_row(fmt, float("nan"), ctx, g=g)
 
 
 @pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
