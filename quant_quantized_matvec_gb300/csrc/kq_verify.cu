@@ -8,12 +8,18 @@
 // rows: r, the residual distribution, is kept in shared memory, a run each
 // CTA, and sums go round the cluster through distributed shared memory, one
 // barrier each.  Sums are over whole multiples of 2^-44, so any order gives
-// the same.
+// the same.  Each warp has a run of the CTA's words, and the sums by warp that
+// come with r's total are the draw's first two levels: only the warp whose run
+// holds the goal looks at words again.
 //
 // Bound by latency: a sequence reads two rows (1.6 MB at 202048 words) over
-// 16 SMs, after one dependent fetch of the nodes' entries.  16 CTAs a sequence
-// and r in shared memory against one CTA that forms r again from p and q for
-// each pass: 134 -> (see the measured table) us for one chain of 5 drafts.
+// 16 SMs, after one dependent fetch of the nodes' entries.  One chain of 5
+// drafts, 202048 words, one rejection, 12400 clocks: entries 2000, r 5700 (two
+// batches of loads), the sum round the cluster 2400, the draw 800.  Measured:
+// 10.3 us (one CTA that forms r again from p and q for each pass: 134); 16
+// trees of up to 16 nodes: 21.3 us.  More loads in flight, with 1024 threads
+// a CTA: 9% less for the chain, 28% more for the trees, whose clusters then
+// have no room side by side.
 #include <cooperative_groups.h>
 
 #include <mutex>
@@ -26,17 +32,23 @@ namespace kqd {
 namespace cg = cooperative_groups;
 
 constexpr int kVerifyThreads = 512;
+constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kBatch = 13;  // loads of a thread in flight
 
 // 0..1; NaN is 0.
 __device__ __forceinline__ float unit(float x) { return fminf(fmaxf(x, 0.f), 1.f); }
+// r (0..1) in whole multiples of 2^-44, rounded down: the significand, 24
+// bits, moved to its place.  (The conversion to 64 bits, two or so a clock,
+// took longer than all else of a pass over a row.)
 __device__ __forceinline__ unsigned long long fixed(float r) {
-    return (unsigned long long)__float2ull_rz(r * 17592186044416.f);  // 2^44
+    const uint32_t b = __float_as_uint(r);
+    const int down = 127 - (int)(b >> 23 & 255);
+    return (unsigned long long)(b & 0x7FFFFFu | 0x800000u) << 21 >> min(down, 63);
 }
 
 struct VerifyShared {
-    unsigned long long warp[kVerifyThreads / 32];
+    unsigned long long warp[kVerifyWarps];  // sums of the warps' runs
     unsigned long long cta[2];  // the CTA's sum, by turns
     int32_t token[KQ_MAX_DRAFT], parent[KQ_MAX_DRAFT];
     float u[KQ_MAX_DRAFT];
@@ -45,19 +57,25 @@ struct VerifyShared {
     int32_t out[KQ_MAX_DRAFT];                 // ... and its token
 };
 
-__global__ void __launch_bounds__(kVerifyThreads)
+__global__ void __launch_bounds__(kVerifyThreads, 2)
     kq_verify_kernel(const __grid_constant__ VerifyArgs a, int chunk) {
     cg::cluster_group cluster = cg::this_cluster();
     const int nrank = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     __shared__ VerifyShared sh;
     extern __shared__ float r[];  // this CTA's run of the residual
     const int b = blockIdx.x / nrank, tid = threadIdx.x, V = a.vocab;
+    const int lane = tid & 31, w = tid >> 5;
     const int lo = min(rank * chunk, V), n = min(lo + chunk, V) - lo;
+    // each warp has a run of the CTA's, [w0, w1)
+    const int seg = (chunk + kVerifyWarps - 1) / kVerifyWarps;
+    const int w0 = min(w * seg, n), w1 = min(w0 + seg, n);
     const Seq s = seq_of(a.start, nullptr, a.ntok, a.max_new, b);
     if (s.n == 0) {  // the same for the whole cluster
         if (rank == 0 && tid == 0) a.count[b] = 0, a.next[b] = -1;
         return;
     }
+    const unsigned long long u =
+        min((unsigned long long)(unit(__ldg(a.u_next + b)) * 0x1p31f), 0x7FFFFFFFull);
     for (int j = tid; j < s.n; j += kVerifyThreads) {
         const int x = s.first + j, t = __ldg(a.token + x), p = __ldg(a.parent + x);
         const bool ok = j > 0 && p >= 0 && p < j && t >= 0 && t < V;
@@ -77,10 +95,10 @@ __global__ void __launch_bounds__(kVerifyThreads)
     auto cluster_sum = [&](unsigned long long v) {
 #pragma unroll
         for (int o = 16; o; o /= 2) v += __shfl_xor_sync(~0u, v, o);
-        if ((tid & 31) == 0) sh.warp[tid >> 5] = v;
+        if (lane == 0) sh.warp[w] = v;
         __syncthreads();
         if (tid < 32) {
-            unsigned long long t = tid < kVerifyThreads / 32 ? sh.warp[tid] : 0;
+            unsigned long long t = lane < kVerifyWarps ? sh.warp[lane] : 0;
 #pragma unroll
             for (int o = 16; o; o /= 2) t += __shfl_xor_sync(~0u, t, o);
             if (tid == 0) sh.cta[turn & 1] = t;
@@ -88,7 +106,6 @@ __global__ void __launch_bounds__(kVerifyThreads)
         // (the entry written two calls ago was read before the last barrier)
         cluster.sync();
         // every warp fetches all entries at once, a lane each
-        const int lane = tid & 31;
         unsigned long long t =
             lane < nrank ? *cluster.map_shared_rank(&sh.cta[turn & 1], lane) : 0;
         before = lane < rank ? t : 0;
@@ -110,31 +127,40 @@ __global__ void __launch_bounds__(kVerifyThreads)
         }
         return p;
     };
-    // the CTA's run of r after the first rej rejections; its sum's part
+    // the warp's run of r after the first rej rejections; its sum's part
     auto form = [&](int rej) {
         const float *p = a.p + (int64_t)(s.first + cur) * a.p_stride + lo;
         const float *q = a.q ? a.q + (int64_t)(s.first + cur) * a.q_stride + lo : nullptr;
         unsigned long long sum = 0;
-        for (int i0 = tid; i0 < n; i0 += kBatch * kVerifyThreads) {
+        for (int i0 = w0 + lane; i0 < w1; i0 += kBatch * 32) {
             float pv[kBatch], qv[kBatch];  // loads first, all in flight
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
-                const int i = i0 + k * kVerifyThreads;
-                pv[k] = i < n ? __ldg(p + i) : 0.f;
-                qv[k] = i < n && q && rej ? __ldg(q + i) : 0.f;
+                const int i = i0 + k * 32;
+                pv[k] = i < w1 ? __ldg(p + i) : 0.f;
+                qv[k] = i < w1 && q && rej ? __ldg(q + i) : 0.f;
             }
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const int i = i0 + k * kVerifyThreads;
-                if (i >= n) break;
-                const float x = left_of(unit(pv[k]), unit(qv[k]), lo + i, rej);
-                r[i] = x;
-                sum += fixed(x);
+            for (int k = 0; k < kBatch; ++k) pv[k] = unit(pv[k]), qv[k] = unit(qv[k]);
+            for (int j = 0; j < rej; ++j) {  // left_of, all at once
+                const float z = sh.z[j];
+                const int out = q ? -1 : sh.out[j] - lo - i0;
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    if (q) pv[k] = fmaxf(__fsub_rn(pv[k], __fmul_rn(z, qv[k])), 0.f);
+                    else pv[k] = out == k * 32 ? 0.f : pv[k];
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {  // (past the run: 0)
+                if (i0 + k * 32 < w1) r[i0 + k * 32] = pv[k];
+                sum += fixed(pv[k]);
             }
         }
         return sum;
     };
     int held = -1;  // rejections that r in shared memory has seen (-1: not formed)
+    unsigned long long total = 0;  // the sum of that r
     for (int j = 1; j < s.n; ++j) {
         if (sh.parent[j] != cur) continue;
         const int t = sh.token[j];
@@ -153,19 +179,19 @@ __global__ void __launch_bounds__(kVerifyThreads)
         unsigned long long sum = 0;
         if (held == rejected && a.q) {  // one step on from the r at hand
             const float *q = a.q + (int64_t)(s.first + cur) * a.q_stride + lo;
-            for (int i0 = tid; i0 < n; i0 += kBatch * kVerifyThreads) {
+            for (int i0 = w0 + lane; i0 < w1; i0 += kBatch * 32) {
                 float qv[kBatch];
 #pragma unroll
                 for (int k = 0; k < kBatch; ++k) {
-                    const int i = i0 + k * kVerifyThreads;
-                    qv[k] = i < n ? __ldg(q + i) : 0.f;
+                    const int i = i0 + k * 32;
+                    qv[k] = i < w1 ? __ldg(q + i) : 0.f;
                 }
 #pragma unroll
                 for (int k = 0; k < kBatch; ++k) {
-                    const int i = i0 + k * kVerifyThreads;
-                    if (i >= n) break;
-                    const float x = fmaxf(__fsub_rn(r[i], __fmul_rn(zc, unit(qv[k]))), 0.f);
-                    r[i] = x;
+                    const int i = i0 + k * 32;
+                    const float have = i < w1 ? r[i] : 0.f;
+                    const float x = fmaxf(__fsub_rn(have, __fmul_rn(zc, unit(qv[k]))), 0.f);
+                    if (i < w1) r[i] = x;
                     sum += fixed(x);
                 }
             }
@@ -174,43 +200,44 @@ __global__ void __launch_bounds__(kVerifyThreads)
         }
         sum = cluster_sum(sum);
         if (sum) {
-            held = ++rejected;
+            held = ++rejected, total = sum;
             zc = (float)((double)(long long)sum * 0x1p-44);
         } else {
             held = -1;  // r and z stay as they were
         }
     }
-    if (held != rejected) form(rejected);
-    __syncthreads();
-    // the first token whose running sum passes the goal: a thread sums a run
-    // of tokens (an odd number, so that the threads' runs fall on different
-    // banks), the runs before it are added up, and the one that holds the
-    // goal is walked
-    const int per = ((chunk + kVerifyThreads - 1) / kVerifyThreads) | 1;
-    const int r0 = min(tid * per, n), r1 = min(r0 + per, n);
-    unsigned long long mine = 0;
-    for (int i = r0; i < r1; ++i) mine += fixed(r[i]);
-    const unsigned long long total = cluster_sum(mine);
-    unsigned long long upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-        const unsigned long long v = __shfl_up_sync(~0u, upto, o);
-        if ((tid & 31) >= o) upto += v;
-    }
-    // (cluster_sum left every warp's sum)
-    for (int i = 0; i < (tid >> 5); ++i) upto += sh.warp[i];
-    upto += before;
-    const unsigned long long u =
-        min((unsigned long long)(unit(__ldg(a.u_next + b)) * 0x1p31f), 0x7FFFFFFFull);
+    if (held != rejected) total = cluster_sum(form(rejected));
+    // The first token whose running sum passes the goal.  The warps' sums are
+    // there with the total; the warp whose run holds the goal gives its lanes
+    // a run each (an odd number of tokens, so that they fall on different
+    // banks), and the lane that holds it walks its own.
     const unsigned long long goal = (total >> 31) * u + (((total & 0x7FFFFFFFull) * u) >> 31);
-    if (goal >= upto - mine && goal < upto) {
-        unsigned long long sum = upto - mine;
-        int i = r0;
-        for (; i < r1 - 1; ++i) {
-            sum += fixed(r[i]);
-            if (sum > goal) break;
+    unsigned long long from = before;
+    for (int i = 0; i < w; ++i) from += sh.warp[i];
+    if (goal >= from && goal < from + sh.warp[w]) {
+        const int per = ((seg + 31) / 32) | 1;
+        const int r0 = min(w0 + lane * per, w1), r1 = min(r0 + per, w1);
+        unsigned long long mine = 0;
+        __syncwarp();
+        for (int i0 = r0; i0 < r1; i0 += kBatch) {
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) mine += i0 + k < r1 ? fixed(r[i0 + k]) : 0;
         }
-        a.next[b] = lo + i;
+        unsigned long long upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const unsigned long long v = __shfl_up_sync(~0u, upto, o);
+            if (lane >= o) upto += v;
+        }
+        unsigned long long sum = from + upto - mine;
+        if (goal >= sum && goal < sum + mine) {
+            int i = r0;
+            for (; i < r1 - 1; ++i) {
+                sum += fixed(r[i]);
+                if (sum > goal) break;
+            }
+            a.next[b] = lo + i;
+        }
     }
     if (rank == 0) {
         for (int i = tid; i < s.n; i += kVerifyThreads)
