@@ -1252,6 +1252,18 @@ cudaError_t device(Device &d) {
     d = {info.sms, info.err, wl ? wl : kq::kWaitLimitNs};
     return e;
 }
+cudaError_t rows_map(const void *data, int rows, int64_t blocks, int box, CUtensorMap *out) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {32, (cuuint64_t)rows, (cuuint64_t)blocks};
+    const cuuint64_t strides[2] = {64, 64 * (cuuint64_t)rows};
+    const cuuint32_t boxes[3] = {32, (cuuint32_t)box, 1}, each[3] = {1, 1, 1};
+    const CUresult r =
+        enc(out, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(data), dims, strides, boxes,
+            each, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
 }  // namespace kqhost
 
 extern "C" {

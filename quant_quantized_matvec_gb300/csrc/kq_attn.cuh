@@ -981,8 +981,8 @@ struct AttnShape {
 };
 
 // The kernel and, after it, the join.
-template <int D>
-cudaError_t launch_pair(void (*kernel)(AttnArgs), const AttnArgs &a, int sms, int ctas, int threads,
+template <int D, class ARGS>
+cudaError_t launch_pair(void (*kernel)(ARGS), const ARGS &a, int sms, int ctas, int threads,
                         int smem, int rb, cudaStream_t s) {
     // rows that may have parts to join: all there are, at most
     const int64_t jobs = (int64_t)a.q.nseq * a.q.heads * a.q.max_new * a.per;
@@ -1000,7 +1000,7 @@ cudaError_t launch_pair(void (*kernel)(AttnArgs), const AttnArgs &a, int sms, in
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kq_attn_join<D>, a, rb, ctas);
+    return cudaLaunchKernelEx(&cfg, kq_attn_join<D>, static_cast<const AttnArgs &>(a), rb, ctas);
 }
 
 template <int FMT, int D, int NT>

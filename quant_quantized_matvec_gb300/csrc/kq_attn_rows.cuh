@@ -33,9 +33,12 @@
 // quantised page of width 128 (1024 for f16) whatever the rows up to 128.
 #pragma once
 
+#include <cuda.h>
+
 #include <type_traits>
 
 #include "kq_attn.cuh"
+#include "kq_host.h"
 
 namespace kqd {
 
@@ -51,7 +54,7 @@ constexpr int kSoftRegs = 216, kConvRegs = 56, kOtherRegs = 32;
 struct RowsCommon {
     RunShared run;
     uint64_t rawfull[kRowSlots], rawempty[kRowSlots], scaled[kRowSlots];
-    uint64_t kready[2], kfree[2], vready[2], vfree[2];
+    uint64_t kready[2], kfree[2], vready[4], vfree[2], edge[4];
     // sdone: by tile & 3.  (A phase's parity tells it from the next only, so no
     // barrier may complete twice before its waiter has looked, nor be waited for
     // two phases ahead: S of tile t + 4 needs the buffer of tile t, or of a later
@@ -59,7 +62,7 @@ struct RowsCommon {
     uint64_t sfree[4], sdone[4], pready[4], pvdone[4], ofree, drain[2];
     uint32_t tmem;
     int dead;
-    int badpage[4];          // of tile t & 3: the page is not valid
+    int badpage[8];          // of tile t & 7: the page is not valid
     uint32_t badtok[4][2];   // values of these tokens are not finite (edge pages)
     float kf[8], vf[8];      // powers of two of the page's scales
     uint32_t up[kRowSlots];  // their inverse, as f16 pairs, by raw slot
@@ -69,8 +72,8 @@ struct RowsCommon {
 template <int FMT, int D>
 struct RowsSmem {
     using L = Kv<FMT, D>;
-    static constexpr int kTile = kPage * D * 2;                 // one f16 tile
-    static constexpr int kBuf = kTile * (L::kQuant ? 2 : 1);    // hi and lo
+    static constexpr int kTile = kPage * D * 2;         // one f16 tile
+    static constexpr int kBuf = L::kQuant ? 2 * kTile : 0;  // hi and lo (f16: the raw slots)
     static constexpr int kTiles0 = 4096;                        // after RowsCommon
     static constexpr int kRaw = kTiles0 + 4 * kBuf;             // K 0, K 1, V 0, V 1
     static constexpr int kHalf = L::kV;
@@ -149,6 +152,28 @@ __host__ __device__ constexpr uint32_t tile_idesc(int n) {
 __device__ __forceinline__ uint32_t tile_at(int row, int chunk) {
     return row * 128 + ((chunk ^ (row & 7)) << 4);
 }
+// The same with rows of 64 bytes, as an f16 page is copied.
+__device__ __forceinline__ uint64_t raw_desc(uint32_t addr) {
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(512 >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)4 << 61;
+}
+__device__ __forceinline__ uint32_t raw_at(int row, int chunk) {
+    return row * 64 + ((chunk ^ (row >> 1 & 3)) << 4);
+}
+// Box of half a block (keys or values), rows `y` on of block z.
+__device__ __forceinline__ void tensor3d_g2s(uint32_t dst, const CUtensorMap *map, int y, int z,
+                                             uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(0), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// The cache as rows of 64 bytes, for f16.
+struct RowsArgs : AttnArgs {
+    CUtensorMap map;
+};
 
 // Element pair h (0..3) of an octet as the converted tiles hold it.
 template <int FMT>
@@ -194,7 +219,7 @@ __device__ __noinline__ float add_not_finite(const uint8_t *block, int tok, int 
 
 template <int FMT, int D>
 __global__ void __launch_bounds__(kRowsThreads, 1)
-    kq_attn_rows_kernel(const __grid_constant__ AttnArgs a) {
+    kq_attn_rows_kernel(const __grid_constant__ RowsArgs a) {
     using L = Kv<FMT, D>;
     using M = RowsSmem<FMT, D>;
     extern __shared__ uint8_t smem_raw[];
@@ -211,18 +236,19 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < kRowSlots; ++i) {
             kq::mbar_init(bar(cm.rawfull[i]), 1);
-            kq::mbar_init(bar(cm.rawempty[i]), kConvWarps);
+            kq::mbar_init(bar(cm.rawempty[i]), L::kQuant ? kConvWarps : 1);
             kq::mbar_init(bar(cm.scaled[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             kq::mbar_init(bar(cm.kready[i]), kConvWarps);
-            kq::mbar_init(bar(cm.vready[i]), kConvWarps);
             kq::mbar_init(bar(cm.kfree[i]), 1);
             kq::mbar_init(bar(cm.vfree[i]), 1);
         }
         for (int i = 0; i < 4; ++i) {
             kq::mbar_init(bar(cm.sfree[i]), qw);
             kq::mbar_init(bar(cm.sdone[i]), 1);
+            kq::mbar_init(bar(cm.edge[i]), 1);
+            kq::mbar_init(bar(cm.vready[i]), kConvWarps);
             kq::mbar_init(bar(cm.pvdone[i]), 1);
             kq::mbar_init(bar(cm.pready[i]), qw);
             cm.badtok[i][0] = cm.badtok[i][1] = 0;
@@ -263,9 +289,10 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         int b, pages, pg0, npg, head, row0, nrows;
         long long u;
         int t0;
+        int pe, e0;  // first edge page, and edge tiles before the segment's
     };
     auto segments = [&](auto &&body) {
-        int b = run.seq, t0 = 0;
+        int b = run.seq, t0 = 0, e0 = 0;
         long long off = run.off;
         for (long long u = run.u0; u < run.u1 && b < a.q.nseq;) {
             int blocks;
@@ -283,9 +310,16 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             g.npg = (int)min((long long)(g.pages - g.pg0), run.u1 - u);
             g.head = item / blocks, g.row0 = (item - g.head * blocks) * rb;
             g.nrows = min(rb, g.s.n * a.per - g.row0);
+            g.pe = max(g.pg0, g.s.ctx / kPage), g.e0 = e0;
             body(g);
+            e0 += max(0, g.pg0 + g.npg - g.pe);
             u += g.npg, off += g.npg, t0 += g.npg;
         }
+    };
+    // The number of tile t's turn at the barriers of its converted values
+    // (f16: edge pages only have one; two a segment at most).
+    auto turn_of = [](const Seg &g, int t) {
+        return L::kQuant ? t : g.e0 + (g.pg0 + (t - g.t0) - g.pe);
     };
     // The end of a segment, for all threads: the softmax warps have left
     // their rows in shared memory (the tiles are idle now).
@@ -421,7 +455,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                 wait(cm.sdone[t & 3], t >> 2);
                 tc_after();
                 float f = rowf * (L::kQuant ? *(volatile float *)&cm.kf[t & 7] : 1.f);
-                if (*(volatile int *)&cm.badpage[t & 3]) f = quiet_nan();
+                if (*(volatile int *)&cm.badpage[t & 7]) f = quiet_nan();
                 const uint32_t sa = mine + M::kS + 64 * sb;
                 // the half page's scores, those not attended as -infinity
                 auto scores = [&](int half, uint32_t (&d)[32]) {
@@ -447,17 +481,19 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                 const float alpha = exp2_of(m - from);
                 m = now;
                 const float high = 15.f - from;
-                // Values that are not finite: the conversion left them out, and
-                // the rows that attend them take them below.  (Read before P
-                // goes out, after which the buffer's next page may come.)
-                uint64_t bad = 0;
-                if constexpr (kEdge) {
-                    wait(cm.vready[t & 1], t >> 1);
-                    bad = (uint64_t)*(volatile uint32_t *)&cm.badtok[t & 3][0] |
-                          (uint64_t)*(volatile uint32_t *)&cm.badtok[t & 3][1] << 32;
-                }
                 // ---- O of the page before, which also frees P
                 flush();
+                // Values that are not finite: the conversion left them out, and
+                // the rows that attend them take them below.  (Read before P
+                // goes out, after which the buffer's next page may come; after the
+                // flush, as with two sets the O warp gets to this page only then.)
+                uint64_t bad = 0;
+                if constexpr (kEdge) {
+                    const int n = turn_of(g, t);
+                    wait(cm.vready[n & 3], n >> 2);
+                    bad = (uint64_t)*(volatile uint32_t *)&cm.badtok[n & 3][0] |
+                          (uint64_t)*(volatile uint32_t *)&cm.badtok[n & 3][1] << 32;
+                }
                 // ---- P
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
@@ -544,7 +580,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         int use = 0, turn = 0;
         // the next raw slot's bytes, once they are there (and looked at)
         auto arrived = [&]() {
-            if constexpr (L::kQuant) wait(cm.scaled[use], turn);
+            wait(cm.scaled[use], turn);
             wait(cm.rawfull[use], turn);
             return smem + M::kRaw + use * M::kHalf;
         };
@@ -569,93 +605,118 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             *reinterpret_cast<uint4 *>(tile + at) = hi;
             *reinterpret_cast<uint4 *>(tile + M::kTile + at) = lo;
         };
-        segments([&](const Seg &g) {
-            __syncthreads();
-            for (int k = 0; k < g.npg; ++k) {
-                const int t = g.t0 + k, pg = g.pg0 + k;
-                const int left = g.s.ctx - pg * kPage;
-                const bool edge = left < kPage;
-                const int held = left + g.s.n;  // tokens of the page that exist
-                // ---- keys
-                const uint8_t *raw = arrived();
-                if (t >= 2) wait(cm.kfree[t & 1], (t >> 1) - 1);
-                uint8_t *kt = smem + M::kTiles0 + (t & 1) * M::kBuf;
-                if (ct == 0) {
-                    const int64_t page = page_of(a.q, g.b, pg);
-                    *(volatile int *)&cm.badpage[t & 3] = page < 0;
-                }
-                __half2 up = half2_of(*(volatile uint32_t *)&cm.up[use]);
-                constexpr int kOctets = D / 8;
-                constexpr int kN = kPage * kOctets / kConvThreads;
-                typename Octet<FMT>::T raws[kN];
-                __half sc1[kN];
+        // Which of the 8 tokens from `first` on are in the page but not finite,
+        // by the exponents of x; those and the ones past the page's end
+        // become zero.
+        auto clean = [](uint32_t (&x)[4], int first, int held) {
+            uint32_t bad = 0;
 #pragma unroll
-                for (int i = 0; i < kN; ++i) {
-                    const int at = ct + kConvThreads * i, row = at / kOctets, o = at % kOctets;
-                    raws[i] = *reinterpret_cast<const typename Octet<FMT>::T *>(raw + L::k_octet(row, o));
-                    if constexpr (L::kQuant)
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t m = 0xFFFFu << (16 * (k & 1));
+                const uint32_t inf = 0x7C00u << (16 * (k & 1));
+                const bool in = first + k < held;
+                const bool nf = (x[k >> 1] & inf) == inf;
+                if (in && nf) bad |= 1u << k;
+                if (!in || nf) x[k >> 1] &= ~m;
+            }
+            return bad;
+        };
+        if constexpr (!L::kQuant) {
+            // f16: the raw slots are the MMAs' operands; only an edge page's
+            // values are gone over, in place, when the O warp says so
+            segments([&](const Seg &g) {
+                __syncthreads();
+                for (int pg = g.pe; pg < g.pg0 + g.npg; ++pg) {
+                    const int t = g.t0 + (pg - g.pg0), n = turn_of(g, t);
+                    const int held = g.s.ctx + g.s.n - pg * kPage, slot = 2 * t + 1;
+                    wait(cm.edge[n & 3], n >> 2);
+                    wait(cm.rawfull[slot % M::kSlots], slot / M::kSlots);
+                    uint8_t *vt = smem + M::kRaw + slot % M::kSlots * M::kHalf;
+                    if (ct == 0) cm.badtok[(n + 2) & 3][0] = cm.badtok[(n + 2) & 3][1] = 0;
+                    for (int at = ct; at < D * 8; at += kConvThreads) {
+                        const int e = at >> 3, j = at & 7;  // tokens 8 j ..
+                        uint4 *p = reinterpret_cast<uint4 *>(vt + raw_at((j >> 2) * D + e, j & 3));
+                        uint4 v = *p;
+                        uint32_t x[4] = {v.x, v.y, v.z, v.w};
+                        const uint32_t bad = clean(x, 8 * j, held);
+                        if (bad) atomicOr(&cm.badtok[n & 3][j >> 2], bad << (8 * (j & 3)));
+                        *p = make_uint4(x[0], x[1], x[2], x[3]);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) kq::mbar_arrive(bar(cm.vready[n & 3]));
+                }
+                __syncthreads();
+                finish(g);
+            });
+        } else {
+            segments([&](const Seg &g) {
+                __syncthreads();
+                for (int k = 0; k < g.npg; ++k) {
+                    const int t = g.t0 + k, pg = g.pg0 + k;
+                    const int left = g.s.ctx - pg * kPage;
+                    const bool edge = left < kPage;
+                    const int held = left + g.s.n;  // tokens of the page that exist
+                    // ---- keys
+                    const uint8_t *raw = arrived();
+                    if (t >= 2) wait(cm.kfree[t & 1], (t >> 1) - 1);
+                    uint8_t *kt = smem + M::kTiles0 + (t & 1) * M::kBuf;
+                    if (ct == 0) {
+                        const int64_t page = page_of(a.q, g.b, pg);
+                        *(volatile int *)&cm.badpage[t & 7] = page < 0;
+                    }
+                    __half2 up = half2_of(*(volatile uint32_t *)&cm.up[use]);
+                    constexpr int kOctets = D / 8;
+                    constexpr int kN = kPage * kOctets / kConvThreads;
+                    typename Octet<FMT>::T raws[kN];
+                    __half sc1[kN];
+#pragma unroll
+                    for (int i = 0; i < kN; ++i) {
+                        const int at = ct + kConvThreads * i, row = at / kOctets, o = at % kOctets;
+                        raws[i] =
+                            *reinterpret_cast<const typename Octet<FMT>::T *>(raw + L::k_octet(row, o));
                         sc1[i] = *reinterpret_cast<const __half *>(raw + L::k_scale(row, o >> 2));
-                }
+                    }
 #pragma unroll
-                for (int i = 0; i < kN; ++i) {
-                    // 8 lanes make one 128-byte row of the tile
-                    const int at = ct + kConvThreads * i, row = at / kOctets, o = at % kOctets;
-                    uint8_t *half = kt + (o >> 3) * (kPage * 128);
-                    const uint32_t to = tile_at(row, o & 7);
-                    if constexpr (FMT == KQ_KV_F16) {
-                        *reinterpret_cast<uint4 *>(half + to) = raws[i];
-                    } else {
+                    for (int i = 0; i < kN; ++i) {
+                        // 8 lanes make one 128-byte row of the tile
+                        const int at = ct + kConvThreads * i, row = at / kOctets, o = at % kOctets;
+                        uint8_t *half = kt + (o >> 3) * (kPage * 128);
+                        const uint32_t to = tile_at(row, o & 7);
                         uint32_t c[4];
                         octet_codes<FMT>(raws[i], c);
                         const __half2 s2 = __hmul2(__half2half2(sc1[i]), up);
                         const __half2 sc[4] = {s2, s2, s2, s2};
                         put(half, to, c, sc);
                     }
-                }
-                release(cm.kready[t & 1]);
-                // ---- values
-                raw = arrived();
-                if (t >= 2) wait(cm.vfree[t & 1], (t >> 1) - 1);
-                uint8_t *vt = smem + M::kTiles0 + (2 + (t & 1)) * M::kBuf;
-                raw -= L::kV;
-                up = half2_of(*(volatile uint32_t *)&cm.up[use]);
-                if (ct == 0) cm.badtok[(t + 2) & 3][0] = cm.badtok[(t + 2) & 3][1] = 0;
-                constexpr int kM = D * 8 / kConvThreads;
-                typename Octet<FMT>::T vraw[kM];
-                uint4 svs[kM];
+                    release(cm.kready[t & 1]);
+                    // ---- values
+                    raw = arrived();
+                    if (t >= 2) wait(cm.vfree[t & 1], (t >> 1) - 1);
+                    uint8_t *vt = smem + M::kTiles0 + (2 + (t & 1)) * M::kBuf;
+                    raw -= L::kV;
+                    up = half2_of(*(volatile uint32_t *)&cm.up[use]);
+                    if (ct == 0) cm.badtok[(t + 2) & 3][0] = cm.badtok[(t + 2) & 3][1] = 0;
+                    constexpr int kM = D * 8 / kConvThreads;
+                    typename Octet<FMT>::T vraw[kM];
+                    uint4 svs[kM];
 #pragma unroll
-                for (int i = 0; i < kM; ++i) {
-                    const int at = ct + kConvThreads * i, e = at >> 3, j = at & 7;  // tokens 8 j ..
-                    vraw[i] = *reinterpret_cast<const typename Octet<FMT>::T *>(
-                        raw + L::v_word(e, 8 * j / L::kVPerWord));
-                    if constexpr (L::kQuant)
+                    for (int i = 0; i < kM; ++i) {
+                        const int at = ct + kConvThreads * i, e = at >> 3, j = at & 7;  // tokens 8 j ..
+                        vraw[i] = *reinterpret_cast<const typename Octet<FMT>::T *>(
+                            raw + L::v_word(e, 8 * j / L::kVPerWord));
                         svs[i] = *reinterpret_cast<const uint4 *>(raw + L::v_scale(8 * j, e / kGroup));
-                }
-#pragma unroll
-                for (int i = 0; i < kM; ++i) {
-                    const int at = ct + kConvThreads * i, e = at >> 3, j = at & 7;
-                    const uint32_t to = tile_at(e, j);
-                    if (edge) {
-                        uint32_t x[4];
-                        if constexpr (L::kQuant) memcpy(x, &svs[i], 16);
-                        else memcpy(x, &vraw[i], sizeof(vraw[i]));
-                        uint32_t bad = 0;
-#pragma unroll
-                        for (int k2 = 0; k2 < 8; ++k2) {
-                            const uint32_t m = 0xFFFFu << (16 * (k2 & 1));
-                            const uint32_t inf = 0x7C00u << (16 * (k2 & 1));
-                            const bool in = 8 * j + k2 < held;
-                            const bool nf = (x[k2 >> 1] & inf) == inf;
-                            if (in && nf) bad |= 1u << k2;
-                            if (!in || nf) x[k2 >> 1] &= ~m;
-                        }
-                        if (bad) atomicOr(&cm.badtok[t & 3][j >> 2], bad << (8 * (j & 3)));
-                        if constexpr (L::kQuant) memcpy(&svs[i], x, 16);
-                        else memcpy(&vraw[i], x, sizeof(vraw[i]));
                     }
-                    if constexpr (FMT == KQ_KV_F16) {
-                        *reinterpret_cast<uint4 *>(vt + to) = vraw[i];
-                    } else {
+#pragma unroll
+                    for (int i = 0; i < kM; ++i) {
+                        const int at = ct + kConvThreads * i, e = at >> 3, j = at & 7;
+                        const uint32_t to = tile_at(e, j);
+                        if (edge) {
+                            uint32_t x[4] = {svs[i].x, svs[i].y, svs[i].z, svs[i].w};
+                            const uint32_t bad = clean(x, 8 * j, held);
+                            if (bad) atomicOr(&cm.badtok[t & 3][j >> 2], bad << (8 * (j & 3)));
+                            svs[i] = make_uint4(x[0], x[1], x[2], x[3]);
+                        }
                         uint32_t c[4];
                         octet_codes<FMT>(vraw[i], c);
                         __half2 sc[4] = {half2_of(svs[i].x), half2_of(svs[i].y), half2_of(svs[i].z),
@@ -669,12 +730,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                         for (int k2 = 0; k2 < 4; ++k2) sc[k2] = __hmul2(sc[k2], up);
                         put(vt, to, c, sc);
                     }
+                    release(cm.vready[t & 3]);
                 }
-                release(cm.vready[t & 1]);
-            }
-            __syncthreads();
-            finish(g);
-        });
+                __syncthreads();
+                finish(g);
+            });
+        }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         int use = 0, turn = 0;  // (producer) the next raw slot and how often it was filled
@@ -720,11 +781,19 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                         if (issued + 2 < 2 * g.npg)
                             next = page_of(a.q, g.b, g.pg0 + (issued >> 1) + 1);
                     }
+                    // (f16: the entry of eight tiles ago has been read: the keys'
+                    // slot was given back by an S that needed a later one's)
+                    if (!L::kQuant && (issued & 1) == 0)
+                        *(volatile int *)&cm.badpage[(g.t0 + (issued >> 1)) & 7] = page < 0;
                     kq::mbar_expect_tx(bar(cm.rawfull[use]), M::kHalf);
-                    kq::bulk_g2s(base + M::kRaw + use * M::kHalf,
-                                 a.q.data + (max(page, (int64_t)0) * a.q.heads + g.head) * L::kBlock +
-                                     (issued & 1) * M::kHalf,
-                                 M::kHalf, bar(cm.rawfull[use]));
+                    const int64_t block = max(page, (int64_t)0) * a.q.heads + g.head;
+                    const uint32_t to = base + M::kRaw + use * M::kHalf;
+                    if constexpr (L::kQuant)
+                        kq::bulk_g2s(to, a.q.data + block * L::kBlock + (issued & 1) * M::kHalf,
+                                     M::kHalf, bar(cm.rawfull[use]));
+                    else
+                        tensor3d_g2s(to, &a.map, (issued & 1) * 2 * D, (int)block,
+                                     bar(cm.rawfull[use]));
                     if (++use == M::kSlots) use = 0, ++turn;
                 }
             };
@@ -769,14 +838,18 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             if (w == kFirstOther) {
                 tc_after();
                 for (int t = g.t0; t < g.t0 + g.npg; ++t) {
-                    wait(cm.kready[t & 1], t >> 1);
+                    const int slot = 2 * t;  // f16: the keys' raw slot
+                    if constexpr (L::kQuant) wait(cm.kready[t & 1], t >> 1);
+                    else wait(cm.rawfull[slot % M::kSlots], slot / M::kSlots);
                     const int sb = t % M::kSBufs;
                     if (t >= M::kSBufs) wait(cm.sfree[sb], t / M::kSBufs - 1);
                     tc_after();
                     if (__any_sync(~0u, dead())) continue;
                     const uint32_t buf = uniform(t & 1);
                     const uint32_t usb = uniform(sb), done = uniform(t & 3);
-                    const uint64_t kt = tile_desc(base + M::kTiles0 + buf * M::kBuf);
+                    const uint32_t raw = uniform(slot % M::kSlots);
+                    const uint64_t kt = L::kQuant ? tile_desc(base + M::kTiles0 + buf * M::kBuf)
+                                                  : raw_desc(base + M::kRaw + raw * M::kHalf);
                     const uint32_t d = tm + M::kS + 64 * usb;
                     if (elected()) {
 #pragma unroll
@@ -784,12 +857,13 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
 #pragma unroll
                             for (int i = 0; i < D / 16; ++i) {
                                 const uint32_t q = tm + M::kQ + (term == 1 ? D / 2 : 0) + 8 * i;
-                                const uint64_t b = kt + (((term == 2 ? M::kTile : 0) +
-                                                          (i >> 2) * (kPage * 128) + (i & 3) * 32) >> 4);
+                                const int at = L::kQuant ? (i >> 2) * (kPage * 128) + (i & 3) * 32
+                                                         : (i >> 1) * (kPage * 64) + (i & 1) * 32;
+                                const uint64_t b = kt + (((term == 2 ? M::kTile : 0) + at) >> 4);
                                 if (term + i) tc_mma<true>(d, q, b, tile_idesc(kPage));
                                 else tc_mma<false>(d, q, b, tile_idesc(kPage));
                             }
-                        tc_commit(bar(cm.kfree[0]) + 8 * buf);
+                        tc_commit(L::kQuant ? bar(cm.kfree[0]) + 8 * buf : bar(cm.rawempty[0]) + 8 * raw);
                         tc_commit(bar(cm.sdone[0]) + 8 * done);
                     }
                     __syncwarp();
@@ -797,25 +871,32 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             } else if (w == kFirstOther + 2) {
                 tc_after();
                 for (int t = g.t0; t < g.t0 + g.npg; ++t) {
-                    wait(cm.vready[t & 1], t >> 1);
+                    const int slot = 2 * t + 1, n = turn_of(g, t);
+                    if constexpr (!L::kQuant) wait(cm.rawfull[slot % M::kSlots], slot / M::kSlots);
+                    if (!L::kQuant && n >= g.e0 && lane == 0 && !dead())
+                        kq::mbar_arrive(bar(cm.edge[n & 3]));
+                    if (L::kQuant || n >= g.e0) wait(cm.vready[n & 3], n >> 2);
                     wait(cm.pready[t & (ns - 1)], t >> nsl);
                     if (t > 0) wait(cm.ofree, t - 1);
                     tc_after();
                     if (__any_sync(~0u, dead())) continue;
                     const uint32_t buf = uniform(t & 1);
                     const uint32_t set = uniform(bar(cm.pvdone[t & (ns - 1)]));
-                    const uint64_t vt = tile_desc(base + M::kTiles0 + (2 + buf) * M::kBuf);
+                    const uint32_t raw = uniform(slot % M::kSlots);
+                    const uint64_t vt = L::kQuant ? tile_desc(base + M::kTiles0 + (2 + buf) * M::kBuf)
+                                                  : raw_desc(base + M::kRaw + raw * M::kHalf);
                     if (elected()) {
 #pragma unroll
                         for (int term = 0; term < kTerms; ++term)
 #pragma unroll
                             for (int i = 0; i < kPage / 16; ++i) {
                                 const uint32_t p = tm + M::kP + (term == 1 ? 32 : 0) + 8 * i;
-                                const uint64_t b = vt + (((term == 2 ? M::kTile : 0) + i * 32) >> 4);
+                                const int at = L::kQuant ? i * 32 : (i >> 1) * (D * 64) + (i & 1) * 32;
+                                const uint64_t b = vt + (((term == 2 ? M::kTile : 0) + at) >> 4);
                                 if (term + i) tc_mma<true>(tm + M::kO, p, b, tile_idesc(D));
                                 else tc_mma<false>(tm + M::kO, p, b, tile_idesc(D));
                             }
-                        tc_commit(bar(cm.vfree[0]) + 8 * buf);
+                        tc_commit(L::kQuant ? bar(cm.vfree[0]) + 8 * buf : bar(cm.rawempty[0]) + 8 * raw);
                         tc_commit(set);
                     }
                     __syncwarp();
@@ -844,14 +925,20 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
 
 // Rows of a block: 32, 64 or 128, the least that hold a key head's rows.
 template <int FMT, int D>
-cudaError_t launch_rows(AttnArgs a, int64_t rows, int sms, cudaStream_t s, int64_t *floats) {
+cudaError_t launch_rows(const AttnArgs &args, int64_t rows, int sms, cudaStream_t s, int64_t *floats) {
     using M = RowsSmem<FMT, D>;
+    RowsArgs a;
+    static_cast<AttnArgs &>(a) = args;
     a.ng = rows <= 32 ? 1 : rows <= 64 ? 2 : 4;
     const int rb = 32 * a.ng;
     *floats = 2 * (int64_t)sms * part_floats(rb, D);
     if (!a.part) return cudaSuccess;
     a.meta = reinterpret_cast<int4 *>(a.part);
     a.part += 8 * (int64_t)sms;
+    if (FMT == KQ_KV_F16) {
+        const cudaError_t e = kqhost::rows_map(a.q.data, 4 * D, a.q.npages * a.q.heads, 2 * D, &a.map);
+        if (e != cudaSuccess) return e;
+    }
     return launch_pair<D>(kq_attn_rows_kernel<FMT, D>, a, sms, sms, kRowsThreads, M::kTotal, rb, s);
 }
 

@@ -2,6 +2,7 @@
 // (defined in kq_api.cu).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -23,6 +24,10 @@ struct Device {
     unsigned long long wait_ns;
 };
 cudaError_t device(Device &d);
+
+// A tensor map over `blocks` blocks of `rows` rows of 64 bytes (f16), boxes of
+// `box` rows, swizzled over 64 bytes.
+cudaError_t rows_map(const void *data, int rows, int64_t blocks, int box, CUtensorMap *out);
 
 struct Span {
     uintptr_t lo, hi;  // [lo, hi)
