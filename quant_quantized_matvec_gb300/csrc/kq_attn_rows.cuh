@@ -20,17 +20,26 @@
 // four warps take pages by turns, each with its own maxima and sums (32..64
 // rows: two pairs of warps); they are joined at the end of an item's pages.
 //
-// A page goes through: producer warp (bulk copies of the raw page) ->
-// conversion warps -> S -> softmax warps -> P -> O -> softmax warps; each
-// stage has two buffers but P and O.  Page k + 1's S is formed while page k's
-// probabilities are.
+// A page goes through: producer warp (copies of the raw page) -> conversion
+// warps -> S -> softmax warps -> P -> O -> softmax warps; each stage has two
+// buffers or more but O, so that S of the next pages is formed while a page's
+// probabilities are, and its O while the next page's are.  An f16 page is not
+// converted: tensor copies lay its rows of 64 bytes out as the MMAs take them,
+// and only the values of pages with new tokens, or that end, are gone over in
+// place (converted by a copy within shared memory: 365 us against 276 for 4
+// sequences of 131071 at most, 8 drafts, 32 / 8 heads).
 //
 // The softmax warps' code is kept short (loops over half a page, scores read
-// twice from tensor memory): four roles run side by side, and with the page
-// unrolled the warps waited for instructions.
+// twice from tensor memory), and the number of sets is fixed per instance:
+// four roles run side by side, and with the page unrolled, or the sets counted
+// at run time, the warps waited for instructions (32 sequences of 16384 at
+// most, 4 drafts, 64 / 8 heads, 8-bit: 427 us, 509 with sets at run time).
 //
 // Bound by: the MMAs of a page, 3 * 8 * 32 + 3 * 4 * 64 = 1536 clocks for a
-// quantised page of width 128 (1024 for f16) whatever the rows up to 128.
+// quantised page of width 128 (1024 for f16) whatever the rows up to 128, and
+// the shared memory that they and the conversion read and write (195 KB a
+// page, 1520 clocks; f16 96 KB); f16 with 32 rows by memory: 84% of the copy
+// rate in the case above.
 #pragma once
 
 #include <cuda.h>
@@ -217,7 +226,8 @@ __device__ __noinline__ float add_not_finite(const uint8_t *block, int tok, int 
     return fabsf(x) <= 3.4e38f ? o : fmaf(p, x, o);
 }
 
-template <int FMT, int D>
+// (QW: warps of a set, rows of a block / 32)
+template <int FMT, int D, int QW>
 __global__ void __launch_bounds__(kRowsThreads, 1)
     kq_attn_rows_kernel(const __grid_constant__ RowsArgs a) {
     using L = Kv<FMT, D>;
@@ -227,10 +237,16 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     RowsCommon &cm = *reinterpret_cast<RowsCommon *>(smem);
     const uint32_t base = kq::smem_addr(smem);
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-    const int qw = a.ng;             // warps of a set: rows of a block / 32
-    const int rb = 32 * qw;          // rows of a block
-    const int ns = 4 / qw;           // sets
-    const int nsl = ns == 4 ? 2 : ns == 2 ? 1 : 0;  // log2
+    constexpr int qw = QW, rb = 32 * QW;            // rows of a block
+    constexpr int ns = 4 / QW;                      // sets
+    constexpr int nsl = ns == 4 ? 2 : ns == 2 ? 1 : 0;  // log2
+    // Four sets take turns, so that a page's O is formed while others form P.
+    // With fewer, P has two buffers for that, one of them a buffer of S (8-bit,
+    // 128 rows: 55.2 us against 58.4 for a tree of 16 over 32001 tokens; not for
+    // f16, whose edge pages are gone over only after the O before them).
+    constexpr bool kTwoP = L::kQuant && ns < 4;
+    constexpr int kSB = kTwoP ? 2 : M::kSBufs;
+    auto pcol = [](int t) { return kTwoP && (t >> nsl & 1) ? M::kS + 128 : M::kP; };
     auto bar = [&](const uint64_t &b) { return kq::smem_addr(&b); };
 
     if (tid == 0) {
@@ -437,7 +453,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             float factor = 1.f;    // and its alpha
             auto flush = [&]() {
                 if (before < 0) return;
-                wait(cm.pvdone[before & (ns - 1)], before >> nsl);
+                wait(cm.pvdone[before & 3], before >> 2);
                 tc_after();
                 take(before, factor);
                 before = -1;
@@ -451,7 +467,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                     ok = left <= 0 ? (-left < 64 ? nw >> -left : 0) : (nw << left) | ~(~0ull << left);
                 }
                 // ---- S, maxima, probabilities times 2^15
-                const int sb = t % M::kSBufs;
+                const int sb = t % kSB;
                 wait(cm.sdone[t & 3], t >> 2);
                 tc_after();
                 float f = rowf * (L::kQuant ? *(volatile float *)&cm.kf[t & 7] : 1.f);
@@ -481,19 +497,23 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                 const float alpha = exp2_of(m - from);
                 m = now;
                 const float high = 15.f - from;
-                // ---- O of the page before, which also frees P
-                flush();
                 // Values that are not finite: the conversion left them out, and
                 // the rows that attend them take them below.  (Read before P
-                // goes out, after which the buffer's next page may come; after the
-                // flush, as with two sets the O warp gets to this page only then.)
+                // goes out, after which the buffer's next page may come.)
                 uint64_t bad = 0;
-                if constexpr (kEdge) {
-                    const int n = turn_of(g, t);
-                    wait(cm.vready[n & 3], n >> 2);
-                    bad = (uint64_t)*(volatile uint32_t *)&cm.badtok[n & 3][0] |
-                          (uint64_t)*(volatile uint32_t *)&cm.badtok[n & 3][1] << 32;
-                }
+                auto look = [&]() {
+                    if constexpr (kEdge) {
+                        const int n = turn_of(g, t);
+                        wait(cm.vready[n & 3], n >> 2);
+                        bad = (uint64_t)*(volatile uint32_t *)&cm.badtok[n & 3][0] |
+                              (uint64_t)*(volatile uint32_t *)&cm.badtok[n & 3][1] << 32;
+                    }
+                };
+                if constexpr (L::kQuant) look();
+                // ---- O of the page before, which also frees P
+                if constexpr (!kTwoP) flush();
+                // (f16: with two sets the O warp gets to this page only now)
+                if constexpr (!L::kQuant) look();
                 // ---- P
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
@@ -516,10 +536,20 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                             split(__uint_as_float(d[8 * o + oct_a<FMT>(h)]),
                                   __uint_as_float(d[8 * o + oct_b<FMT>(h)]), hi[4 * o + h],
                                   lo[4 * o + h]);
-                    tc_store16(mine + M::kP + 16 * half, hi);
-                    tc_store16(mine + M::kP + 32 + 16 * half, lo);
+                    tc_store16(mine + pcol(t) + 16 * half, hi);
+                    tc_store16(mine + pcol(t) + 32 + 16 * half, lo);
                 }
                 l = fmaf(l, alpha, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+                if constexpr (kTwoP) {
+                    tc_stored();
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (!kEdge) kq::mbar_arrive(bar(cm.sfree[sb]));
+                        kq::mbar_arrive(bar(cm.pready[t & 3]));
+                    }
+                    flush();
+                }
                 before = t, factor = alpha;
                 if constexpr (kEdge) {
                     if (bad && !dead()) {
@@ -552,9 +582,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                 tc_stored();
                 tc_before();
                 __syncwarp();
-                if (lane == 0) {
+                if (lane == 0 && (!kTwoP || kEdge)) {
                     kq::mbar_arrive(bar(cm.sfree[sb]));
-                    kq::mbar_arrive(bar(cm.pready[t & (ns - 1)]));
+                    if constexpr (!kTwoP) kq::mbar_arrive(bar(cm.pready[t & 3]));
                 }
             };
             for (int t = g.t0 + ((set - g.t0) & (ns - 1)); t < g.t0 + g.npg; t += ns) {
@@ -578,21 +608,6 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
         const int ct = tid - 128;
         int use = 0, turn = 0;
-        // the next raw slot's bytes, once they are there (and looked at)
-        auto arrived = [&]() {
-            wait(cm.scaled[use], turn);
-            wait(cm.rawfull[use], turn);
-            return smem + M::kRaw + use * M::kHalf;
-        };
-        auto release = [&](const uint64_t &ready) {
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) {
-                kq::mbar_arrive(bar(cm.rawempty[use]));
-                kq::mbar_arrive(bar(ready));
-            }
-            if (++use == M::kSlots) use = 0, ++turn;
-        };
         auto put = [&](uint8_t *tile, uint32_t at, const uint32_t (&c)[4], const __half2 (&sc)[4]) {
             uint4 hi, lo;
             uint32_t *h = &hi.x, *o = &lo.x;
@@ -650,87 +665,116 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                 finish(g);
             });
         } else {
+            // A page's keys, then its values; with fewer than four sets the next
+            // page's keys come before them, as the values wait for the O of two
+            // pages before and there are fewer pages on their way (64 rows, 16
+            // sequences of 16384 at most, 8 drafts, 8-bit: 174 us against 188;
+            // with four sets it would cost: 391 against 375 at 64 sequences of
+            // 20000, 32 rows, width 64).
+            constexpr int kOctets = D / 8;
+            constexpr int kN = kPage * kOctets / kConvThreads;  // octets of keys of a thread
+            constexpr int kM = D * 8 / kConvThreads;            // and of values
+            constexpr int ahead = ns < 4;
             segments([&](const Seg &g) {
                 __syncthreads();
-                for (int k = 0; k < g.npg; ++k) {
-                    const int t = g.t0 + k, pg = g.pg0 + k;
+                for (int k = -ahead; k < g.npg; ++k) {
+                    const int t = g.t0 + k, pg = g.pg0 + k, tk = t + ahead;
+                    const bool vals = k >= 0, keys = k + ahead < g.npg;
                     const int left = g.s.ctx - pg * kPage;
                     const bool edge = left < kPage;
                     const int held = left + g.s.n;  // tokens of the page that exist
-                    // ---- keys
-                    const uint8_t *raw = arrived();
-                    if (t >= 2) wait(cm.kfree[t & 1], (t >> 1) - 1);
-                    uint8_t *kt = smem + M::kTiles0 + (t & 1) * M::kBuf;
-                    if (ct == 0) {
-                        const int64_t page = page_of(a.q, g.b, pg);
-                        *(volatile int *)&cm.badpage[t & 7] = page < 0;
-                    }
-                    __half2 up = half2_of(*(volatile uint32_t *)&cm.up[use]);
-                    constexpr int kOctets = D / 8;
-                    constexpr int kN = kPage * kOctets / kConvThreads;
-                    typename Octet<FMT>::T raws[kN];
+                    // their raw slots: `use` and the one after it
+                    const bool second = use + 1 == M::kSlots;
+                    const int other = second ? 0 : use + 1;
+                    const bool kfirst = !ahead || !vals;
+                    const int ks = kfirst ? use : other, vs = ahead ? use : other;
+                    const int kturn = kfirst ? turn : turn + second;
+                    const int vturn = ahead ? turn : turn + second;
+                    typename Octet<FMT>::T raws[kN], vraw[kM];
                     __half sc1[kN];
-#pragma unroll
-                    for (int i = 0; i < kN; ++i) {
-                        const int at = ct + kConvThreads * i, row = at / kOctets, o = at % kOctets;
-                        raws[i] =
-                            *reinterpret_cast<const typename Octet<FMT>::T *>(raw + L::k_octet(row, o));
-                        sc1[i] = *reinterpret_cast<const __half *>(raw + L::k_scale(row, o >> 2));
-                    }
-#pragma unroll
-                    for (int i = 0; i < kN; ++i) {
-                        // 8 lanes make one 128-byte row of the tile
-                        const int at = ct + kConvThreads * i, row = at / kOctets, o = at % kOctets;
-                        uint8_t *half = kt + (o >> 3) * (kPage * 128);
-                        const uint32_t to = tile_at(row, o & 7);
-                        uint32_t c[4];
-                        octet_codes<FMT>(raws[i], c);
-                        const __half2 s2 = __hmul2(__half2half2(sc1[i]), up);
-                        const __half2 sc[4] = {s2, s2, s2, s2};
-                        put(half, to, c, sc);
-                    }
-                    release(cm.kready[t & 1]);
-                    // ---- values
-                    raw = arrived();
-                    if (t >= 2) wait(cm.vfree[t & 1], (t >> 1) - 1);
-                    uint8_t *vt = smem + M::kTiles0 + (2 + (t & 1)) * M::kBuf;
-                    raw -= L::kV;
-                    up = half2_of(*(volatile uint32_t *)&cm.up[use]);
-                    if (ct == 0) cm.badtok[(t + 2) & 3][0] = cm.badtok[(t + 2) & 3][1] = 0;
-                    constexpr int kM = D * 8 / kConvThreads;
-                    typename Octet<FMT>::T vraw[kM];
                     uint4 svs[kM];
+                    __half2 kup, vup;
+                    if (keys) {
+                        wait(cm.scaled[ks], kturn);
+                        wait(cm.rawfull[ks], kturn);
+                        const uint8_t *raw = smem + M::kRaw + ks * M::kHalf;
+                        kup = half2_of(*(volatile uint32_t *)&cm.up[ks]);
 #pragma unroll
-                    for (int i = 0; i < kM; ++i) {
-                        const int at = ct + kConvThreads * i, e = at >> 3, j = at & 7;  // tokens 8 j ..
-                        vraw[i] = *reinterpret_cast<const typename Octet<FMT>::T *>(
-                            raw + L::v_word(e, 8 * j / L::kVPerWord));
-                        svs[i] = *reinterpret_cast<const uint4 *>(raw + L::v_scale(8 * j, e / kGroup));
-                    }
-#pragma unroll
-                    for (int i = 0; i < kM; ++i) {
-                        const int at = ct + kConvThreads * i, e = at >> 3, j = at & 7;
-                        const uint32_t to = tile_at(e, j);
-                        if (edge) {
-                            uint32_t x[4] = {svs[i].x, svs[i].y, svs[i].z, svs[i].w};
-                            const uint32_t bad = clean(x, 8 * j, held);
-                            if (bad) atomicOr(&cm.badtok[t & 3][j >> 2], bad << (8 * (j & 3)));
-                            svs[i] = make_uint4(x[0], x[1], x[2], x[3]);
+                        for (int i = 0; i < kN; ++i) {
+                            const int at = ct + kConvThreads * i, row = at / kOctets, o = at % kOctets;
+                            raws[i] =
+                                *reinterpret_cast<const typename Octet<FMT>::T *>(raw + L::k_octet(row, o));
+                            sc1[i] = *reinterpret_cast<const __half *>(raw + L::k_scale(row, o >> 2));
                         }
-                        uint32_t c[4];
-                        octet_codes<FMT>(vraw[i], c);
-                        __half2 sc[4] = {half2_of(svs[i].x), half2_of(svs[i].y), half2_of(svs[i].z),
-                                         half2_of(svs[i].w)};
-                        if constexpr (FMT == KQ_KV_Q4) {
-                            const __half2 s01 = sc[0], s23 = sc[1], s45 = sc[2], s67 = sc[3];
-                            sc[0] = __lows2half2(s01, s45), sc[1] = __highs2half2(s01, s45);
-                            sc[2] = __lows2half2(s23, s67), sc[3] = __highs2half2(s23, s67);
-                        }
+                        if (tk >= 2) wait(cm.kfree[tk & 1], (tk >> 1) - 1);
+                        uint8_t *kt = smem + M::kTiles0 + (tk & 1) * M::kBuf;
 #pragma unroll
-                        for (int k2 = 0; k2 < 4; ++k2) sc[k2] = __hmul2(sc[k2], up);
-                        put(vt, to, c, sc);
+                        for (int i = 0; i < kN; ++i) {
+                            // 8 lanes make one 128-byte row of the tile
+                            const int at = ct + kConvThreads * i, row = at / kOctets, o = at % kOctets;
+                            uint8_t *half = kt + (o >> 3) * (kPage * 128);
+                            const uint32_t to = tile_at(row, o & 7);
+                            uint32_t c[4];
+                            octet_codes<FMT>(raws[i], c);
+                            const __half2 s2 = __hmul2(__half2half2(sc1[i]), kup);
+                            const __half2 sc[4] = {s2, s2, s2, s2};
+                            put(half, to, c, sc);
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) {
+                            kq::mbar_arrive(bar(cm.rawempty[ks]));
+                            kq::mbar_arrive(bar(cm.kready[tk & 1]));
+                        }
                     }
-                    release(cm.vready[t & 3]);
+                    if (vals) {
+                        wait(cm.scaled[vs], vturn);
+                        wait(cm.rawfull[vs], vturn);
+                        if (t >= 2) wait(cm.vfree[t & 1], (t >> 1) - 1);
+                        const uint8_t *raw = smem + M::kRaw + vs * M::kHalf - L::kV;
+                        vup = half2_of(*(volatile uint32_t *)&cm.up[vs]);
+#pragma unroll
+                        for (int i = 0; i < kM; ++i) {
+                            const int at = ct + kConvThreads * i, e = at >> 3, j = at & 7;  // tokens 8 j ..
+                            vraw[i] = *reinterpret_cast<const typename Octet<FMT>::T *>(
+                                raw + L::v_word(e, 8 * j / L::kVPerWord));
+                            svs[i] =
+                                *reinterpret_cast<const uint4 *>(raw + L::v_scale(8 * j, e / kGroup));
+                        }
+                        if (ct == 0) cm.badtok[(t + 2) & 3][0] = cm.badtok[(t + 2) & 3][1] = 0;
+                        uint8_t *vt = smem + M::kTiles0 + (2 + (t & 1)) * M::kBuf;
+#pragma unroll
+                        for (int i = 0; i < kM; ++i) {
+                            const int at = ct + kConvThreads * i, e = at >> 3, j = at & 7;
+                            const uint32_t to = tile_at(e, j);
+                            if (edge) {
+                                uint32_t x[4] = {svs[i].x, svs[i].y, svs[i].z, svs[i].w};
+                                const uint32_t bad = clean(x, 8 * j, held);
+                                if (bad) atomicOr(&cm.badtok[t & 3][j >> 2], bad << (8 * (j & 3)));
+                                svs[i] = make_uint4(x[0], x[1], x[2], x[3]);
+                            }
+                            uint32_t c[4];
+                            octet_codes<FMT>(vraw[i], c);
+                            __half2 sc[4] = {half2_of(svs[i].x), half2_of(svs[i].y), half2_of(svs[i].z),
+                                             half2_of(svs[i].w)};
+                            if constexpr (FMT == KQ_KV_Q4) {
+                                const __half2 s01 = sc[0], s23 = sc[1], s45 = sc[2], s67 = sc[3];
+                                sc[0] = __lows2half2(s01, s45), sc[1] = __highs2half2(s01, s45);
+                                sc[2] = __lows2half2(s23, s67), sc[3] = __highs2half2(s23, s67);
+                            }
+#pragma unroll
+                            for (int k2 = 0; k2 < 4; ++k2) sc[k2] = __hmul2(sc[k2], vup);
+                            put(vt, to, c, sc);
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) {
+                            kq::mbar_arrive(bar(cm.rawempty[vs]));
+                            kq::mbar_arrive(bar(cm.vready[t & 3]));
+                        }
+                    }
+                    for (int i = vals + keys; i; --i)
+                        if (++use == M::kSlots) use = 0, ++turn;
                 }
                 __syncthreads();
                 finish(g);
@@ -739,7 +783,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         int use = 0, turn = 0;  // (producer) the next raw slot and how often it was filled
-    // 2^(8 - ex) for the page's scales, all below 2^ex, and 2^(ex - 8):
+        // 2^(8 - ex) for the page's scales, all below 2^ex, and 2^(ex - 8):
         // a code times a scale then stays below 2^15.  (tokens from `held`
         // on and scales that are not finite do not count)
         auto normal = [&](const uint8_t *scales, bool keys, int held, uint32_t &up) {
@@ -781,9 +825,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                         if (issued + 2 < 2 * g.npg)
                             next = page_of(a.q, g.b, g.pg0 + (issued >> 1) + 1);
                     }
-                    // (f16: the entry of eight tiles ago has been read: the keys'
-                    // slot was given back by an S that needed a later one's)
-                    if (!L::kQuant && (issued & 1) == 0)
+                    // (the entry of eight tiles ago has been read: the keys' slot
+                    // was given back after an S or an O of a later tile was asked for)
+                    if ((issued & 1) == 0)
                         *(volatile int *)&cm.badpage[(g.t0 + (issued >> 1)) & 7] = page < 0;
                     kq::mbar_expect_tx(bar(cm.rawfull[use]), M::kHalf);
                     const int64_t block = max(page, (int64_t)0) * a.q.heads + g.head;
@@ -841,8 +885,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                     const int slot = 2 * t;  // f16: the keys' raw slot
                     if constexpr (L::kQuant) wait(cm.kready[t & 1], t >> 1);
                     else wait(cm.rawfull[slot % M::kSlots], slot / M::kSlots);
-                    const int sb = t % M::kSBufs;
-                    if (t >= M::kSBufs) wait(cm.sfree[sb], t / M::kSBufs - 1);
+                    const int sb = t % kSB;
+                    if (t >= kSB) wait(cm.sfree[sb], t / kSB - 1);
                     tc_after();
                     if (__any_sync(~0u, dead())) continue;
                     const uint32_t buf = uniform(t & 1);
@@ -876,12 +920,13 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                     if (!L::kQuant && n >= g.e0 && lane == 0 && !dead())
                         kq::mbar_arrive(bar(cm.edge[n & 3]));
                     if (L::kQuant || n >= g.e0) wait(cm.vready[n & 3], n >> 2);
-                    wait(cm.pready[t & (ns - 1)], t >> nsl);
+                    wait(cm.pready[t & 3], t >> 2);
                     if (t > 0) wait(cm.ofree, t - 1);
                     tc_after();
                     if (__any_sync(~0u, dead())) continue;
                     const uint32_t buf = uniform(t & 1);
-                    const uint32_t set = uniform(bar(cm.pvdone[t & (ns - 1)]));
+                    const uint32_t set = uniform(bar(cm.pvdone[t & 3]));
+                    const uint32_t pp = uniform(tm + pcol(t));
                     const uint32_t raw = uniform(slot % M::kSlots);
                     const uint64_t vt = L::kQuant ? tile_desc(base + M::kTiles0 + (2 + buf) * M::kBuf)
                                                   : raw_desc(base + M::kRaw + raw * M::kHalf);
@@ -890,7 +935,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                         for (int term = 0; term < kTerms; ++term)
 #pragma unroll
                             for (int i = 0; i < kPage / 16; ++i) {
-                                const uint32_t p = tm + M::kP + (term == 1 ? 32 : 0) + 8 * i;
+                                const uint32_t p = pp + (term == 1 ? 32 : 0) + 8 * i;
                                 const int at = L::kQuant ? i * 32 : (i >> 1) * (D * 64) + (i & 1) * 32;
                                 const uint64_t b = vt + (((term == 2 ? M::kTile : 0) + at) >> 4);
                                 if (term + i) tc_mma<true>(tm + M::kO, p, b, tile_idesc(D));
@@ -923,14 +968,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     }
 }
 
-// Rows of a block: 32, 64 or 128, the least that hold a key head's rows.
-template <int FMT, int D>
-cudaError_t launch_rows(const AttnArgs &args, int64_t rows, int sms, cudaStream_t s, int64_t *floats) {
+template <int FMT, int D, int QW>
+cudaError_t launch_block(const AttnArgs &args, int sms, cudaStream_t s, int64_t *floats) {
     using M = RowsSmem<FMT, D>;
+    constexpr int rb = 32 * QW;
     RowsArgs a;
     static_cast<AttnArgs &>(a) = args;
-    a.ng = rows <= 32 ? 1 : rows <= 64 ? 2 : 4;
-    const int rb = 32 * a.ng;
     *floats = 2 * (int64_t)sms * part_floats(rb, D);
     if (!a.part) return cudaSuccess;
     a.meta = reinterpret_cast<int4 *>(a.part);
@@ -939,7 +982,15 @@ cudaError_t launch_rows(const AttnArgs &args, int64_t rows, int sms, cudaStream_
         const cudaError_t e = kqhost::rows_map(a.q.data, 4 * D, a.q.npages * a.q.heads, 2 * D, &a.map);
         if (e != cudaSuccess) return e;
     }
-    return launch_pair<D>(kq_attn_rows_kernel<FMT, D>, a, sms, sms, kRowsThreads, M::kTotal, rb, s);
+    return launch_pair<D>(kq_attn_rows_kernel<FMT, D, QW>, a, sms, sms, kRowsThreads, M::kTotal, rb, s);
+}
+
+// Rows of a block: 32, 64 or 128, the least that hold a key head's rows.
+template <int FMT, int D>
+cudaError_t launch_rows(const AttnArgs &a, int64_t rows, int sms, cudaStream_t s, int64_t *floats) {
+    return rows <= 32   ? launch_block<FMT, D, 1>(a, sms, s, floats)
+           : rows <= 64 ? launch_block<FMT, D, 2>(a, sms, s, floats)
+                        : launch_block<FMT, D, 4>(a, sms, s, floats);
 }
 
 }  // namespace kqd
