@@ -92,16 +92,23 @@ template <int FMT, int D, int NT>
 struct AttnSmem {
     static constexpr int kRows = 4 * NT;
     static constexpr int kWg = 4;             // warps of a group
-    // Groups of an SM: what registers (with the producer warp: 80 a thread for
-    // 20 warps, 96 for 16, 128 for 12) and, for f16, shared memory hold.
-    // One tile of an 8-bit cache: 157 us with four groups, 150 with five
-    // (32 sequences of 16384 tokens at most, 32 / 8 heads).
-    static constexpr int kGroups = NT == 1 ? (FMT == KQ_KV_F16 ? 4 : 5) : NT == 2 ? 4 : 3;
     static constexpr int kHalf = Kv<FMT, D>::kV;  // bytes of a slot
     static constexpr int kCommon = (sizeof(AttnCommon) + 127) / 128 * 128;
     static constexpr int kQ = kRows * D * 4;
     static constexpr int kP = 2 * 2 * kRows * kPage * 2;  // hi and lo columns, two pages
     static constexpr int kMax = 2 * kWg * kRows * 4;
+    // Groups of an SM: what registers hold (with the producer warp: 80 a thread
+    // for 20 warps, 96 for 16, 128 for 12), less where shared memory holds
+    // fewer with three slots each; one less for f16, whose slots are twice as
+    // large.  5 / 4 groups, one tile, 8-bit: 150 / 157 us (32 sequences of
+    // 16384 tokens at most, 32 / 8 heads); 4 / 3, two tiles, 8-bit: 62.7 / 67.3,
+    // f16: 76.9 / 66.1 (16 sequences, 32 / 4 heads); 4 / 3 / 2, three tiles,
+    // 8-bit: 57.8 / 51.1 / 55.5, f16: 64.9 / 50.6 / 51.9 (24 / 2 heads).
+    static constexpr int kSm = 227 * 1024;
+    static constexpr int kMost = (NT == 1 ? 5 : NT == 2 ? 4 : 3) - (FMT == KQ_KV_F16 && NT < 3);
+    static constexpr int kFit = (kSm - 1024 - kCommon - kQ) / (3 * kHalf + kP + kMax);
+    static constexpr int kGroups = kFit < kMost ? kFit : kMost;
+    static_assert(kGroups >= 1, "a group");
     static __host__ __device__ int group(int nslot) { return nslot * kHalf + kP + kMax; }
     static __host__ __device__ int total(int ng, int nslot) {
         return kCommon + kQ + ng * group(nslot);
@@ -1006,23 +1013,23 @@ cudaError_t launch_pair(void (*kernel)(ARGS), const ARGS &a, int sms, int ctas, 
 template <int FMT, int D, int NT>
 cudaError_t launch_attn(AttnArgs a, int sms, cudaStream_t s, int64_t *floats) {
     using M = AttnSmem<FMT, D, NT>;
-    // 16 warps of an SM in all: in one CTA that joins them where there are few
-    // items, else in four, so that a CTA's warps have fewer items to join.
-    // Fewer where a slot is too large for three a group.
-    const int kSm = 227 * 1024;
+    // The groups of an SM stand in one CTA that joins them where there are few
+    // items, else in as many CTAs as there are groups (four at most), so that
+    // none waits for another at an item's end.  One / apart, 8-bit, 32 / 8
+    // heads: 256 items 152 / 158 us (of 16384 tokens at most), 512 items 33.0 /
+    // 24.4 (200), 1024 items 140 / 111 (2000) and 68.7 / 39.6 (300).
     const int64_t items = (int64_t)a.q.nseq * a.q.heads *
                           (((int64_t)a.q.max_new * a.per + M::kRows - 1) / M::kRows);
     AttnShape sh;
     auto fit = [&](int ctas) {  // CTAs of an SM
-        const int room = kSm / ctas - 1024 - M::kCommon - M::kQ;
+        const int room = M::kSm / ctas - 1024 - M::kCommon - M::kQ;
         sh.ctas = ctas * sms;
         sh.ng = M::kGroups / ctas;
-        while (sh.ng > 1 && room / sh.ng - M::kP - M::kMax < 3 * M::kHalf) --sh.ng;
         sh.nslot = (room / sh.ng - M::kP - M::kMax) / M::kHalf;
     };
     constexpr int kApart = M::kGroups < 4 ? M::kGroups : 4;
     fit(kApart);
-    if (items < kApart * (int64_t)sms || sh.nslot < 3) fit(1);
+    if (items < 3 * (int64_t)sms || sh.nslot < 3) fit(1);
     if (sh.nslot > kMaxSlots) sh.nslot = kMaxSlots;
     *floats = 2 * (int64_t)sh.ctas * part_floats(M::kRows, D);
     if (!a.part) return cudaSuccess;

@@ -18,7 +18,7 @@
 // batches of loads), the sum round the cluster 2400, the draw 800.  Measured:
 // 10.3 us (one CTA that forms r again from p and q for each pass: 134); 16
 // trees of up to 16 nodes: 21.3 us.  More loads in flight, with 1024 threads
-// a CTA: 9% less for the chain, 28% more for the trees, whose clusters then
+// a CTA: 8% less for the chain, 28% more for the trees, whose clusters then
 // have no room side by side.
 #include <cooperative_groups.h>
 
@@ -34,6 +34,8 @@ namespace cg = cooperative_groups;
 constexpr int kVerifyThreads = 512;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kMaxCluster = 16;
+constexpr int kMostWords = KQ_MAX_VOCAB / kMaxCluster;  // of a CTA
+constexpr int kMostCtas = 304;
 constexpr int kBatch = 13;  // loads of a thread in flight
 
 // 0..1; NaN is 0.
@@ -251,10 +253,15 @@ __global__ void __launch_bounds__(kVerifyThreads, 2)
 }
 
 cudaError_t verify(const VerifyArgs &a, cudaStream_t s) {
-    // CTAs of a sequence: up to 16, each with 4096 words or more; a CTA's run
-    // fits in shared memory up to the largest vocabulary (128 KB)
+    // CTAs of a sequence: up to 16, each with 4096 words or more, and about two
+    // an SM in all; a CTA's run is 32768 words (128 KB) at most.  (One chain of
+    // 32000 words: 8 CTAs 6.6 us, 16 6.4, 2 11.0; 32 chains: 8 each 9.4, 16
+    // 20.5, 2 12.1.  32 chains of 128256 words: 8 each 16.0 us, 16 28.0; 64 of
+    // 32000: 4 each 11.7, 8 15.1.)
     int ctas = 1;
-    while (ctas < kMaxCluster && ctas * 4096 < a.vocab) ctas *= 2;
+    while (ctas < kMaxCluster && ctas * 4096 < a.vocab &&
+           (2 * ctas * a.nseq <= kMostCtas || ctas * kMostWords < a.vocab))
+        ctas *= 2;
     const int chunk = (a.vocab + ctas - 1) / ctas;
     const int smem = 4 * chunk;
     static std::mutex mu;
@@ -266,7 +273,7 @@ cudaError_t verify(const VerifyArgs &a, cudaStream_t s) {
         std::lock_guard<std::mutex> lock(mu);
         if (dev < 0 || dev >= 64 || !configured[dev]) {
             e = cudaFuncSetAttribute(kq_verify_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     4 * (KQ_MAX_VOCAB / kMaxCluster));
+                                     4 * kMostWords);
             if (e == cudaSuccess)
                 e = cudaFuncSetAttribute(kq_verify_kernel,
                                          cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
