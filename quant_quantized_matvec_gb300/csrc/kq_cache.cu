@@ -8,7 +8,14 @@
 //
 // Quantisation: four lanes hold a group of 32 values, eight each; the value of
 // largest magnitude comes from two shuffles.
-// Bound by memory: 4 bytes a value on the f32 side, bits/8 on the other.
+//
+// Bound by: memory in principle, 4 bytes a value on the f32 side and bits/8 on
+// the other; in fact by the issue of the arithmetic on codes (write: ALU at
+// 56%) and, for short runs, by latency.  Up to 6001 tokens of three sequences,
+// 8 heads of 128, keys rotated: 4-bit write 37.1 us (floor 18), read 25.8 (18);
+// 8-bit 36.8 and 27.6.  16 sequences of up to 300 tokens, 8 heads of 64, f16:
+// 7.9 and 5.7 us.  With five CTAs an SM and no load ahead the 8-bit write took
+// 39.8 us, with six 39.5.
 #include "kq_decode.cuh"
 #include "kq_decode_launch.h"
 
@@ -119,7 +126,7 @@ __device__ __forceinline__ Part part_of(const Seqs &q, int b, int64_t rel, int h
 }
 
 template <int FMT, int D>
-__global__ void __launch_bounds__(kCacheThreads, 5)
+__global__ void __launch_bounds__(kCacheThreads, 4)
     kq_kv_append_kernel(const __grid_constant__ Seqs q, const __grid_constant__ AppendArgs a) {
     using L = Kv<FMT, D>;
     __shared__ Stage<FMT, D> st;
@@ -139,16 +146,15 @@ __global__ void __launch_bounds__(kCacheThreads, 5)
     const int to0 = e < half ? half : -half, to1 = e + 4 < half ? half : -half;
     const int pair0 = e < half ? e : e - half, pair1 = e + 4 < half ? e + 4 : e + 4 - half;
     uint8_t *kout = part.block + L::k_octet(part.t0 + j0, e / 8);
-    // every lane runs every round: quantise() shuffles
+    // every lane runs every round: quantise() shuffles; the next round's values
+    // are on their way meanwhile
+    float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
+    if (j0 < n) u = load4(src), v = load4(src + 4);
     for (int r = 0; r < (n + kStep - 1) / kStep; ++r) {
         const int j = j0 + r * kStep, t = part.t0 + j;
         const bool on = j < n;
-        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (on) {
-            const float4 u = load4(src), v = load4(src + 4);
-            x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
-            x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
-        }
+        float x[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+        if (j + kStep < n) u = load4(src + kStep * stride), v = load4(src + kStep * stride + 4);
         if (turn && on) {
             const int pos = __ldg(a.pos + part.tok + j);
             if (pos < 0 || pos >= a.positions) {
