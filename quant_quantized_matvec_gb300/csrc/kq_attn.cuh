@@ -9,13 +9,13 @@
 // falls into several runs leaves a partial result (row maxima, sums,
 // weighted values) in each, joined by kq_attn_join.
 //
-// A page.  A CTA has groups of four warps; a group takes whole pages, two
+// A page.  A CTA has groups of two or four warps; a group takes whole pages, two
 // bulk copies each (keys, values) into a ring of its own, and works on one
 // page at a time:
-//   1. each warp forms the logits of 16 of the page's 64 tokens,
+//   1. each warp forms the logits of its share of the page's 64 tokens,
 //   2. the warps exchange row maxima, form the probabilities and leave them
 //      in shared memory,
-//   3. each warp adds its quarter of the values' width, over all 64 tokens.
+//   3. each warp adds its share of the values' width, over all 64 tokens.
 //
 // Arithmetic.  The tensor cores take f16 operands, and codes are exact in
 // f16.  Keys and values are the operand of 16 rows (tokens, or places of the
@@ -50,7 +50,7 @@
 
 namespace kqd {
 
-constexpr int kMaxGroups = 5;
+constexpr int kMaxGroups = 8;
 constexpr int kMaxSlots = 8;  // of a group's ring; a slot holds a page's keys or values
 
 struct AttnArgs {
@@ -91,21 +91,29 @@ struct AttnCommon {
 template <int FMT, int D, int NT>
 struct AttnSmem {
     static constexpr int kRows = 4 * NT;
-    static constexpr int kWg = 4;             // warps of a group
+    // Warps of a group: two, so that less is waited for at its barrier and
+    // counted for a page; four for f16, of whose pages shared memory holds
+    // fewer, and for width 256 (registers).
+    static constexpr int kWg = FMT != KQ_KV_F16 && D <= 128 ? 2 : 4;
     static constexpr int kHalf = Kv<FMT, D>::kV;  // bytes of a slot
     static constexpr int kCommon = (sizeof(AttnCommon) + 127) / 128 * 128;
     static constexpr int kQ = kRows * D * 4;
     static constexpr int kP = 2 * 2 * kRows * kPage * 2;  // hi and lo columns, two pages
     static constexpr int kMax = 2 * kWg * kRows * 4;
-    // Groups of an SM: what registers hold (with the producer warp: 80 a thread
-    // for 20 warps, 96 for 16, 128 for 12), less where shared memory holds
-    // fewer with three slots each; one less for f16, whose slots are twice as
-    // large.  5 / 4 groups, one tile, 8-bit: 150 / 157 us (32 sequences of
-    // 16384 tokens at most, 32 / 8 heads); 4 / 3, two tiles, 8-bit: 62.7 / 67.3,
-    // f16: 76.9 / 66.1 (16 sequences, 32 / 4 heads); 4 / 3 / 2, three tiles,
-    // 8-bit: 57.8 / 51.1 / 55.5, f16: 64.9 / 50.6 / 51.9 (24 / 2 heads).
+    // Groups of an SM, by tiles: what registers hold (96 a thread for 20 warps,
+    // 128 for 16, 168 for 12), less where shared memory holds fewer with three
+    // slots each; of four warps one less for f16, whose slots are twice as
+    // large.  Four warps (5, 4, 3, 3 groups) / two warps (8, 7, 5, 5), 8-bit,
+    // 1..4 tiles: 153 / 139 us (32 sequences of 16384 tokens at most, 32 / 8
+    // heads), 62.8 / 59.7 (16 sequences, 32 / 4), 50.9 / 47.9 (24 / 2), 65.2 /
+    // 56.7 (32 / 2); 4-bit 165 / 145, 64.7 / 59.8, 49.7 / 51.2, 60.4 / 59.2.
+    // Two warps, one tile, 10 / 8 / 7 groups, 4-bit: 155 / 145 / 145, and 107 /
+    // 97 / 114 for 128 sequences of 2000; two tiles, 8 / 7 / 6: 64.9 / 59.8 /
+    // 60.3; four tiles, 6 / 5 / 4: 69.9 / 59.2 / 60.8.  Four warps, f16, two
+    // tiles, 4 / 3: 76.9 / 66.1; three tiles, 4 / 3 / 2: 64.9 / 50.6 / 51.9.
     static constexpr int kSm = 227 * 1024;
-    static constexpr int kMost = (NT == 1 ? 5 : NT == 2 ? 4 : 3) - (FMT == KQ_KV_F16 && NT < 3);
+    static constexpr int kMost = kWg == 2 ? (NT == 1 ? 8 : NT == 2 ? 7 : 5)
+                                 : (NT == 1 ? 5 : NT == 2 ? 4 : 3) - (FMT == KQ_KV_F16 && NT < 3);
     static constexpr int kFit = (kSm - 1024 - kCommon - kQ) / (3 * kHalf + kP + kMax);
     static constexpr int kGroups = kFit < kMost ? kFit : kMost;
     static_assert(kGroups >= 1, "a group");
@@ -262,7 +270,7 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, NT>::kGroups * AttnSmem<FMT, 
     using M = AttnSmem<FMT, D, NT>;
     constexpr int RB = M::kRows;
     constexpr int kWg = M::kWg, kGroupThreads = 32 * kWg;
-    static_assert(kPage / kWg == 16, "one tile of tokens a warp in part 1");
+    constexpr int kTok = kPage / 16 / kWg;  // tiles of 16 tokens of a warp in part 1
     constexpr int kSlice = D / kWg;         // values of a warp in part 3
     constexpr int kTiles = kSlice / 16;     // its tiles
     constexpr int kSliceGroups = kSlice > kGroup ? kSlice / kGroup : 1;
@@ -466,7 +474,7 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, NT>::kGroups * AttnSmem<FMT, 
             return left >= kPage ? ~0ull : (nw << left) | ~(~0ull << left);
         };
         for (int k = 0; k <= (count && !producer ? count : -1); ++k) {
-            float S[NT][2];
+            float S[NT][kTok][2];
             float *sm = smax + (k & 1) * kWg * RB;
             if (k < count) {
                 const int left = s.ctx - (pg0 + g + k * a.ng) * kPage;
@@ -475,12 +483,13 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, NT>::kGroups * AttnSmem<FMT, 
                 const int ks = arrived();
                 const uint8_t *kb = gbase + ks * M::kHalf;
                 const bool badpage = cm.badpage[g * kMaxSlots + ks];
-                {
+#pragma unroll
+                for (int tt = 0; tt < kTok; ++tt) {
                     float acc[NT][4];
                     constexpr int kLane = L::kSlabBytes / 4;  // bytes of a lane in a slab
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        S[t][0] = S[t][1] = 0.f;
+                        S[t][tt][0] = S[t][tt][1] = 0.f;
                         acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
                     }
 #pragma unroll
@@ -489,7 +498,7 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, NT>::kGroups * AttnSmem<FMT, 
                         uint32_t skw[2][(L::kSlabGroups + 1) / 2];  // scales, two groups a word
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            const int tok = 16 * w + 8 * j + n8;
+                            const int tok = 16 * (kTok * w + tt) + 8 * j + n8;
                             const uint8_t *p =
                                 kb + sl * kPage * L::kSlabBytes + tok * L::kSlabBytes + c * kLane;
                             if constexpr (kLane == 16) {
@@ -538,8 +547,8 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, NT>::kGroups * AttnSmem<FMT, 
                                     float d[4] = {0.f, 0.f, 0.f, 0.f};
                                     mma(d, k0, q.x, q.y);
                                     mma(d, k1, q.z, q.w);
-                                    S[t][0] = fmaf(sk[0], d[0] + d[1], S[t][0]);
-                                    S[t][1] = fmaf(sk[1], d[2] + d[3], S[t][1]);
+                                    S[t][tt][0] = fmaf(sk[0], d[0] + d[1], S[t][tt][0]);
+                                    S[t][tt][1] = fmaf(sk[1], d[2] + d[3], S[t][tt][1]);
                                 } else {
                                     mma(acc[t], k0, q.x, q.y);
                                     mma(acc[t], k1, q.z, q.w);
@@ -550,8 +559,8 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, NT>::kGroups * AttnSmem<FMT, 
                     if constexpr (!L::kQuant) {
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
-                            S[t][0] = acc[t][0] + acc[t][1];
-                            S[t][1] = acc[t][2] + acc[t][3];
+                            S[t][tt][0] = acc[t][0] + acc[t][1];
+                            S[t][tt][1] = acc[t][2] + acc[t][3];
                         }
                     }
                 }
@@ -559,13 +568,17 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, NT>::kGroups * AttnSmem<FMT, 
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     const float f = badpage ? quiet_nan() : cm.rowfactor[4 * t + c];
-                    S[t][0] *= f, S[t][1] *= f;
-                    if (edge) {
-                        const uint64_t ok = allowed(left, 4 * t + c) >> (16 * w + n8);
-                        if (!(ok & 1)) S[t][0] = -INFINITY;
-                        if (!(ok & 256)) S[t][1] = -INFINITY;
+                    float v = -INFINITY;
+#pragma unroll
+                    for (int tt = 0; tt < kTok; ++tt) {
+                        S[t][tt][0] *= f, S[t][tt][1] *= f;
+                        if (edge) {
+                            const uint64_t ok = allowed(left, 4 * t + c) >> (16 * (kTok * w + tt) + n8);
+                            if (!(ok & 1)) S[t][tt][0] = -INFINITY;
+                            if (!(ok & 256)) S[t][tt][1] = -INFINITY;
+                        }
+                        v = fmaxf(v, fmaxf(S[t][tt][0], S[t][tt][1]));
                     }
-                    float v = fmaxf(S[t][0], S[t][1]);
                     v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
                     v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
                     v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
@@ -810,14 +823,18 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, NT>::kGroups * AttnSmem<FMT, 
                     alpha[t] = exp2_of(m[t] - base);
                     m[t] = now;
                     const float high = base - 15.f;  // probabilities (and l, O) times 2^15
-                    const float p0 = exp2_of(S[t][0] - high), p1 = exp2_of(S[t][1] - high);
-                    l[t] = fmaf(l[t], alpha[t], p0 + p1);
-                    const __half h0 = __float2half_rn(p0), h1 = __float2half_rn(p1);
-                    const int tok = 16 * w + n8;
-                    pw[p_at<FMT>(2 * r, tok)] = h0;
-                    pw[p_at<FMT>(2 * r, tok + 8)] = h1;
-                    pw[p_at<FMT>(2 * r + 1, tok)] = __float2half_rn(p0 - __half2float(h0));
-                    pw[p_at<FMT>(2 * r + 1, tok + 8)] = __float2half_rn(p1 - __half2float(h1));
+                    l[t] *= alpha[t];
+#pragma unroll
+                    for (int tt = 0; tt < kTok; ++tt) {
+                        const float p0 = exp2_of(S[t][tt][0] - high), p1 = exp2_of(S[t][tt][1] - high);
+                        l[t] += p0 + p1;
+                        const __half h0 = __float2half_rn(p0), h1 = __float2half_rn(p1);
+                        const int tok = 16 * (kTok * w + tt) + n8;
+                        pw[p_at<FMT>(2 * r, tok)] = h0;
+                        pw[p_at<FMT>(2 * r, tok + 8)] = h1;
+                        pw[p_at<FMT>(2 * r + 1, tok)] = __float2half_rn(p0 - __half2float(h0));
+                        pw[p_at<FMT>(2 * r + 1, tok + 8)] = __float2half_rn(p1 - __half2float(h1));
+                    }
                 }
             }
         }
