@@ -42,7 +42,7 @@
 // conversions and MMAs for many.
 #pragma once
 
-#include <mutex>
+#include <atomic>
 
 #include "kq_async.cuh"
 #include "kq_decode.cuh"
@@ -1004,15 +1004,28 @@ struct AttnShape {
     int ctas, ng, nslot;
 };
 
+// Once per kernel and device: all of an SM's shared memory may be asked for.
+// (Two threads may both do it.)
+template <auto KERNEL>
+cudaError_t allow_shared(int bytes) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (done.load() >> dev & 1))) return e;
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev);
+    return e;
+}
+
 // The kernel and, after it, the join.
-template <int D, class ARGS>
-cudaError_t launch_pair(void (*kernel)(ARGS), const ARGS &a, int sms, int ctas, int threads,
+template <int D, auto KERNEL, class ARGS>
+cudaError_t launch_pair(const ARGS &a, int sms, int ctas, int threads,
                         int smem, int rb, cudaStream_t s) {
     // rows that may have parts to join: all there are, at most
     const int64_t jobs = (int64_t)a.q.nseq * a.q.heads * a.q.max_new * a.per;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_shared<KERNEL>(227 * 1024);
     if (e != cudaSuccess) return e;
-    kernel<<<ctas, threads, smem, s>>>(a);
+    KERNEL<<<ctas, threads, smem, s>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -1053,8 +1066,8 @@ cudaError_t launch_attn(AttnArgs a, int sms, cudaStream_t s, int64_t *floats) {
     a.ng = sh.ng, a.nslot = sh.nslot;
     a.meta = reinterpret_cast<int4 *>(a.part);  // meta first, 16-byte aligned
     a.part += 8 * (int64_t)sh.ctas;
-    return launch_pair<D>(kq_attn_kernel<FMT, D, NT>, a, sms, sh.ctas, 32 * M::kWg * sh.ng + 32,
-                          M::total(sh.ng, sh.nslot), M::kRows, s);
+    return launch_pair<D, kq_attn_kernel<FMT, D, NT>>(a, sms, sh.ctas, 32 * M::kWg * sh.ng + 32,
+                                                      M::total(sh.ng, sh.nslot), M::kRows, s);
 }
 
 // The launch for a format and width: tiles of four rows by the rows that a

@@ -982,7 +982,7 @@ cudaError_t launch_block(const AttnArgs &args, int sms, cudaStream_t s, int64_t 
         const cudaError_t e = kqhost::rows_map(a.q.data, 4 * D, a.q.npages * a.q.heads, 2 * D, &a.map);
         if (e != cudaSuccess) return e;
     }
-    return launch_pair<D>(kq_attn_rows_kernel<FMT, D, QW>, a, sms, sms, kRowsThreads, M::kTotal, rb, s);
+    return launch_pair<D, kq_attn_rows_kernel<FMT, D, QW>>(a, sms, sms, kRowsThreads, M::kTotal, rb, s);
 }
 
 // Rows of a block: 32, 64 or 128, the least that hold a key head's rows.
