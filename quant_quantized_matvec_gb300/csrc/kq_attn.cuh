@@ -5,9 +5,10 @@
 // Work.  An item is a key head of a sequence with a block of its rows (a row
 // is a new token and one of the query heads that share the key head); its
 // units are the sequence's pages.  All units in order are cut into as many
-// equal runs as there are CTAs, so ragged lengths balance; an item that
-// falls into several runs leaves a partial result (row maxima, sums,
-// weighted values) in each, joined by kq_attn_join.
+// equal runs as there are CTAs, so ragged lengths balance (each item by itself
+// where CTAs have few units); an item that falls into several runs leaves a
+// partial result (row maxima, sums, weighted values) in each, joined by
+// kq_attn_join.
 //
 // A page.  A CTA has groups of two or four warps; a group takes whole pages, two
 // bulk copies each (keys, values) into a ring of its own, and works on one
@@ -75,8 +76,9 @@ __host__ __device__ constexpr int part_floats(int rb, int d) { return rb * (d + 
 // common | queries | per group: ring, probabilities, maxima
 struct RunShared {
     long long scan[32];
+    uint32_t items[32], runs[32];
     long long off;
-    int seq;
+    int seq, pages, parts;
 };
 struct AttnCommon {
     uint64_t rowmask[32];
@@ -214,52 +216,122 @@ __device__ __forceinline__ int cta_of(long long u, long long total, int n) {
     return (int)(u < rem * (base + 1) ? u / (base + 1) : rem + (u - rem * (base + 1)) / base);
 }
 
-// This CTA's run [u0, u1) of all units; it begins at unit `off` of sequence
-// `seq`.  Every thread of the block takes part (nthreads, a multiple of 32).
+// This CTA's run [u0, u1) of units; it begins at unit `off` of sequence `seq`.
+// Every thread of the block takes part (nthreads, a multiple of 32).
+//
+// All units are cut evenly where CTAs have many.  Where they have few, a CTA
+// that ends one item and begins another would take the longer: then each item
+// is cut by itself into `parts` runs, none longer than `most` pages
+// (sum of ceil(pages / most) <= units / most + items <= CTAs).  A second item
+// costs a CTA 4 to 6 us or more, kApartPages pages' time: one sequence of 4000
+// tokens, 32 / 8 heads, 8-bit, 17.5 us cut evenly and 13.0 by items.
 struct Run {
     long long u0, u1, total, off;
     int seq;
+    int parts;  // runs of the item (0: cut evenly over all units)
 };
+constexpr int kApartPages = 8;
 __device__ __forceinline__ Run run_of(const AttnArgs &a, int rb, int nthreads, RunShared &sh) {
-    const int tid = threadIdx.x, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, nw = nthreads / 32;
     const int each = (a.q.nseq + nthreads - 1) / nthreads;
     const int b0 = min(tid * each, a.q.nseq), b1 = min(b0 + each, a.q.nseq);
-    long long mine = 0;
-    int blocks;
-    for (int b = b0; b < b1; ++b) mine += units_of(a, seq_of(a.q, b), rb, blocks);
+    if (tid == 0) a.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
+    // the last sequence looked at stays, as a thread mostly has one
+    int known = -1, pages = 0;
+    long long items = 0;
+    auto look = [&](int b) {
+        if (b == known) return;
+        const Seq s = seq_of(a.q, b);
+        known = b;
+        pages = s.n ? (int)pages_of(a.q, s) : 0;
+        items = s.n ? (int64_t)((s.n * a.per + rb - 1) / rb) * a.q.heads : 0;
+    };
+    long long mine = 0, count = 0;
+    for (int b = b0; b < b1; ++b) look(b), mine += pages * items, count += items;
     long long upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
         const long long v = __shfl_up_sync(~0u, upto, o);
         if (lane >= o) upto += v;
     }
-    if (lane == 31) sh.scan[tid >> 5] = upto;
+    const uint32_t some = __reduce_add_sync(~0u, (uint32_t)min(count, 1ll << 20));
+    if (lane == 31) sh.scan[w] = upto, sh.items[w] = some;
     __syncthreads();
     Run r;
     r.total = 0;
-    for (int i = 0; i < nthreads / 32; ++i) {
-        if (i == (tid >> 5)) upto += r.total;
+    uint32_t nitems = 0;
+    for (int i = 0; i < nw; ++i) {
+        if (i == w) upto += r.total;
         r.total += sh.scan[i];
+        nitems += sh.items[i];
     }
-    const long long base = r.total / gridDim.x, rem = r.total % gridDim.x, k = blockIdx.x;
-    r.u0 = k * base + min(k, rem);
-    r.u1 = r.u0 + base + (k < rem ? 1 : 0);
-    if (r.u0 < r.u1 && r.u0 >= upto - mine && r.u0 < upto) {
-        long long at = upto - mine;
-        int b = b0;
-        for (;; ++b) {
-            const long long n = units_of(a, seq_of(a.q, b), rb, blocks);
-            if (r.u0 < at + n) break;
-            at += n;
+    const uint32_t grid = gridDim.x, k = blockIdx.x;
+    uint32_t most = 0;
+    if (nitems < grid && r.total > grid && r.total < 1 << 30) {
+        const uint32_t n = (uint32_t)r.total, room = grid - nitems;
+        most = (n + room - 1) / room;
+        if (most > (n + grid - 1) / grid + kApartPages) most = 0;
+    }
+    r.parts = 0;
+    if (most) {
+        uint32_t runs = 0;
+        for (int b = b0; b < b1; ++b) look(b), runs += (uint32_t)items * ((pages + most - 1) / most);
+        uint32_t to = runs;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const uint32_t v = __shfl_up_sync(~0u, to, o);
+            if (lane >= o) to += v;
         }
-        sh.seq = b;
-        sh.off = r.u0 - at;
+        if (lane == 31) sh.runs[w] = to;
+        __syncthreads();
+        uint32_t all = 0;
+        for (int i = 0; i < nw; ++i) {
+            if (i == w) to += all;
+            all += sh.runs[i];
+        }
+        if (k >= to - runs && k < to) {
+            uint32_t at = to - runs;
+            for (int b = b0;; ++b) {
+                look(b);
+                const uint32_t parts = (pages + most - 1) / most, n = (uint32_t)items * parts;
+                if (k < at + n) {
+                    const uint32_t item = (k - at) / parts, j = (k - at) - item * parts;
+                    const uint32_t base = pages / parts, rem = pages - base * parts;
+                    sh.seq = b, sh.parts = (int)parts;
+                    sh.off = (long long)item * pages + j * base + min(j, rem);
+                    sh.pages = (int)(base + (j < rem));
+                    break;
+                }
+                at += n;
+            }
+        }
+        __syncthreads();
+        r.u0 = 0, r.u1 = k < all ? sh.pages : 0;
+        r.parts = sh.parts;
+    } else {
+        const long long base = r.total / grid, rem = r.total - base * grid;
+        r.u0 = k * base + min((long long)k, rem);
+        r.u1 = r.u0 + base + (k < rem ? 1 : 0);
+        if (r.u0 < r.u1 && r.u0 >= upto - mine && r.u0 < upto) {
+            long long at = upto - mine;
+            int b = b0;
+            for (;; ++b) {
+                look(b);
+                if (r.u0 < at + pages * items) break;
+                at += pages * items;
+            }
+            sh.seq = b;
+            sh.off = r.u0 - at;
+        }
+        __syncthreads();
     }
-    if (tid == 0) a.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
-    __syncthreads();
     r.seq = sh.seq;
     r.off = sh.off;
     return r;
+}
+// The last CTA of an item that begins in this one, at unit u.
+__device__ __forceinline__ int last_cta(const Run &run, long long u, int pages) {
+    return run.parts ? blockIdx.x + run.parts - 1 : cta_of(u + pages - 1, run.total, gridDim.x);
 }
 
 // ------------------------------------------------------------------ kernel
@@ -905,7 +977,7 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, NT>::kGroups * AttnSmem<FMT, 
         }
         if (tid == 0 && !whole && pg0 == 0) {
             a.meta[2 * blockIdx.x] =
-                make_int4(cta_of(u + pages - 1, run.total, gridDim.x), slot, nrows, head);
+                make_int4(last_cta(run, u, pages), slot, nrows, head);
             a.meta[2 * blockIdx.x + 1] = make_int4(s.first, row0, 0, 0);
         }
         // what was written to the ring comes before the next copies into it

@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         }
         if (tid == 0 && !whole && g.pg0 == 0) {
             a.meta[2 * blockIdx.x] =
-                make_int4(cta_of(g.u + g.pages - 1, run.total, gridDim.x), slot, g.nrows, g.head);
+                make_int4(last_cta(run, g.u, g.pages), slot, g.nrows, g.head);
             a.meta[2 * blockIdx.x + 1] = make_int4(g.s.first, g.row0, 0, 0);
         }
         // what was written comes before the next copies and MMAs there

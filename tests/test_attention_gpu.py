@@ -361,3 +361,14 @@ def test_refusals():
     with pytest.raises(kq.KQError, match="KQ_ERR_ALIAS"):
         x = dev(c.q)
         kq.tree_attention(c.cache, c.batch, x, out=x)
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
+@pytest.mark.parametrize("hkv,g,new,ctx,dim", [
+    (1, 4, [1], [64 * 152 - 1], 64), (1, 4, [1], [64 * 152], 64), (2, 8, [3], [64 * 300 + 7], 64),
+    (4, 1, [1] * 8, [2000, 0, 3000, 64, 1, 4000, 700, 63], 64), (1, 20, [2, 1], [64 * 200, 64 * 90], 128)])
+def test_few_items_cut_by_themselves(fmt, hkv, g, new, ctx, dim):
+    """Pages of few items, about as many as CTAs and some more: runs of one
+    item's pages, of lengths that differ by one."""
+    c = Case(fmt, hkv, g, dim, new, ctx, seed=hkv + g, spread=2.0)
+    c.check(c.run())
