@@ -240,11 +240,13 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     constexpr int qw = QW, rb = 32 * QW;            // rows of a block
     constexpr int ns = 4 / QW;                      // sets
     constexpr int nsl = ns == 4 ? 2 : ns == 2 ? 1 : 0;  // log2
-    // Four sets take turns, so that a page's O is formed while others form P.
-    // With fewer, P has two buffers for that, one of them a buffer of S (8-bit,
-    // 128 rows: 55.2 us against 58.4 for a tree of 16 over 32001 tokens; not for
-    // f16, whose edge pages are gone over only after the O before them).
-    constexpr bool kTwoP = L::kQuant && ns < 4;
+    // Sets take turns, so that a page's O is formed while others form P.  A
+    // single set has two buffers of P for that, one of them a buffer of S
+    // (8-bit, 128 rows: 45.8 us against 51.1 for a tree of 16 over 32001 tokens;
+    // with two sets 158.8 against 153.5 for 16 sequences of 16384 at most, 64
+    // rows; not for f16, whose edge pages are gone over only after the O before
+    // them).
+    constexpr bool kTwoP = L::kQuant && ns == 1;
     constexpr int kSB = kTwoP ? 2 : M::kSBufs;
     auto pcol = [](int t) { return kTwoP && (t >> nsl & 1) ? M::kS + 128 : M::kP; };
     auto bar = [&](const uint64_t &b) { return kq::smem_addr(&b); };
@@ -665,16 +667,16 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                 finish(g);
             });
         } else {
-            // A page's keys, then its values; with fewer than four sets the next
-            // page's keys come before them, as the values wait for the O of two
-            // pages before and there are fewer pages on their way (64 rows, 16
-            // sequences of 16384 at most, 8 drafts, 8-bit: 174 us against 188;
-            // with four sets it would cost: 391 against 375 at 64 sequences of
-            // 20000, 32 rows, width 64).
+            // A page's keys, then its values; with two sets the next page's keys
+            // come before them, as the values wait for the O of two pages before
+            // and fewer pages are on their way (64 rows, the case above, 8-bit:
+            // 158 us against 167; with one set 45.8 against 44.4 for the tree
+            // above, with four 460 against 413 for 32 sequences, 4 drafts, 64 / 8
+            // heads, though 355 against 376 for 64 of one token, 32 rows, width 64).
             constexpr int kOctets = D / 8;
             constexpr int kN = kPage * kOctets / kConvThreads;  // octets of keys of a thread
             constexpr int kM = D * 8 / kConvThreads;            // and of values
-            constexpr int ahead = ns < 4;
+            constexpr int ahead = ns == 2;
             segments([&](const Seg &g) {
                 __syncthreads();
                 for (int k = -ahead; k < g.npg; ++k) {
