@@ -5,8 +5,8 @@
 //
 // The rows are the 128 lanes of an accumulator.  Queries and probabilities
 // are the first operand, in tensor memory, as two f16 terms hi + lo; keys and
-// values the second, in shared memory, converted once for all rows by a
-// group of warps:
+// values the second, in shared memory, a quantised page converted once for
+// all rows by a group of warps:
 //   S [row][token]  = Qhi K + Qlo K        (f16 cache)
 //                   = Qhi Khi + Qhi Klo + Qlo Khi
 //   O [row][value]  = Phi V + Plo V,  Phi Vhi + Phi Vlo + Plo Vhi
@@ -194,11 +194,10 @@ __device__ __forceinline__ constexpr int oct_b(int h) {
     return FMT == KQ_KV_Q4 ? h + 4 : 2 * h + 1;
 }
 
-// Eight codes as they lie in the cache, and as f16 pairs.
+// Eight codes as they lie in a quantised cache, and as f16 pairs.
 template <int FMT>
 struct Octet {
-    using T = typename std::conditional<
-        FMT == KQ_KV_F16, uint4, typename std::conditional<FMT == KQ_KV_Q8, uint2, uint32_t>::type>::type;
+    using T = typename std::conditional<FMT == KQ_KV_Q8, uint2, uint32_t>::type;
 };
 template <int FMT>
 __device__ __forceinline__ void octet_codes(typename Octet<FMT>::T v, uint32_t (&c)[4]) {

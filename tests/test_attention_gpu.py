@@ -350,6 +350,28 @@ def test_an_expired_wait_is_reported(g):
     assert torch.equal(c.run(), want)
 
 
+@pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
+@pytest.mark.parametrize("g,new", [(4, 1), (16, 2), (16, 4), (16, 8)])
+def test_an_expired_wait_in_each_kernel(fmt, g, new):
+    """The same for few rows and for one, two and four warps of rows; NaN only
+    where the wait ran out, and nothing of it stays."""
+    from quant_quantized_matvec_gb300 import _binding
+    lib = _binding.load()
+    c = Case(fmt, 2, g, 128, [new], [40000], seed=16)
+    want = c.run()
+    torch.cuda.synchronize()
+    lib.kq_set_wait_limit_ns(1)
+    try:
+        got = c.run()
+        torch.cuda.synchronize()
+    finally:
+        lib.kq_set_wait_limit_ns(0)
+    expired = kq.device_error()
+    assert ((got == want) | torch.isnan(got)).all()
+    assert torch.isnan(got).any() == expired
+    assert torch.equal(c.run(), want)
+
+
 def test_refusals():
     c = Case(R.Q8, 2, 4, 64, [3], [10])
     with pytest.raises(ValueError):
