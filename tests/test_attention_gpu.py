@@ -394,3 +394,13 @@ def test_few_items_cut_by_themselves(fmt, hkv, g, new, ctx, dim):
     item's pages, of lengths that differ by one."""
     c = Case(fmt, hkv, g, dim, new, ctx, seed=hkv + g, spread=2.0)
     c.check(c.run())
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
+@pytest.mark.parametrize("nseq,hkv,most", [(116, 4, 200), (116, 4, 900), (160, 4, 600)])
+def test_many_items(fmt, nseq, hkv, most):
+    """More items than SMs have: groups in CTAs of their own, items cut by
+    themselves or not."""
+    ctx = [(37 * b * b + 11 * b) % most for b in range(nseq)]
+    c = Case(fmt, hkv, 2, 64, [1 + b % 2 for b in range(nseq)], ctx, seed=nseq)
+    c.check(c.run())
