@@ -222,3 +222,40 @@ def test_refusals():
     pinned = torch.zeros(3, 2, 64).pin_memory()
     with pytest.raises(ValueError):
         kq.kv_append(s.cache, s.batch, pinned, dev(s.v))
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
+def test_pages_past_32_bits(fmt):
+    """The last pages of a cache of more than 2^32 bytes: written, read back,
+    attended by few and by many rows and moved as those of a small one."""
+    heads, dim, new, ctx = 16, 128, 8, 130
+    each = kq.KVCache(fmt, heads, dim, 1).page_bytes
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    n = ctx + new
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=gen, device="cuda")
+
+    k, v = normal(n, heads, dim), normal(n, heads, dim)
+    q1, q4 = normal(1, heads, dim), normal(new, 4 * heads, dim)
+    path = torch.tensor([0, 2, 5, 6, -1, -1, -1, -1], dtype=torch.int32, device="cuda")
+    count = torch.tensor([4], dtype=torch.int32, device="cuda")
+    out = []
+    for pages in (3, (1 << 32) // each + 40):
+        cache = kq.KVCache(fmt, heads, dim, pages)
+        assert pages == 3 or cache.data.numel() > (1 << 32) + 30 * each
+
+        def batch(held, m):
+            return kq.KVBatch(*(torch.tensor(x, dtype=torch.int32, device="cuda") for x in (
+                [0, m], [held], [[pages - 2, pages - 1, pages - 3]])), m, m)
+
+        kq.kv_append(cache, batch(0, n), k, v)
+        kept = list(kq.kv_read(cache, batch(0, n)))
+        one, many = kq.tree_attention(cache, batch(n - 1, 1), q1), kq.tree_attention(cache, batch(ctx, new), q4)
+        kq.kv_move(cache, batch(ctx, new), path, count)
+        out.append(kept + [one, many] + list(kq.kv_read(cache, batch(0, n))))
+        del cache
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
+    assert torch.isfinite(out[0][2]).all() and torch.isfinite(out[0][3]).all()
+    assert not torch.equal(out[0][0], out[0][4])
