@@ -116,8 +116,19 @@ struct AttnSmem {
     static constexpr int kSm = 227 * 1024;
     static constexpr int kMost = kWg == 2 ? (NT == 1 ? 8 : NT == 2 ? 7 : 5)
                                  : (NT == 1 ? 5 : NT == 2 ? 4 : 3) - (FMT == KQ_KV_F16 && NT < 3);
-    static constexpr int kFit = (kSm - 1024 - kCommon - kQ) / (3 * kHalf + kP + kMax);
-    static constexpr int kGroups = kFit < kMost ? kFit : kMost;
+    // of each of `ctas` CTAs of an SM
+    static constexpr int groups(int ctas) {
+        const int fit = (kSm / ctas - 1024 - kCommon - kQ) / (3 * kHalf + kP + kMax);
+        return fit < kMost / ctas ? fit : kMost / ctas;
+    }
+    static constexpr int kGroups = groups(1);
+    // CTAs of an SM that hold the most groups, more than one if that can be
+    static constexpr int apart() {
+        int best = 1, most = 0;
+        for (int c = 4; c > 1; --c)
+            if (c * groups(c) > most) best = c, most = c * groups(c);
+        return best;
+    }
     static_assert(kGroups >= 1, "a group");
     static __host__ __device__ int group(int nslot) { return nslot * kHalf + kP + kMax; }
     static __host__ __device__ int total(int ng, int nslot) {
@@ -1116,22 +1127,22 @@ template <int FMT, int D, int NT>
 cudaError_t launch_attn(AttnArgs a, int sms, cudaStream_t s, int64_t *floats) {
     using M = AttnSmem<FMT, D, NT>;
     // The groups of an SM stand in one CTA that joins them where there are few
-    // items, else in as many CTAs as there are groups (four at most), so that
-    // none waits for another at an item's end.  One / apart, 8-bit, 32 / 8
-    // heads: 256 items 152 / 158 us (of 16384 tokens at most), 512 items 33.0 /
-    // 24.4 (200), 1024 items 140 / 111 (2000) and 68.7 / 39.6 (300).
+    // items, else in two to four CTAs, so that fewer wait for another at an
+    // item's end.  One / apart, 8-bit, 32 / 8 heads: 256 items 152 / 158 us (of
+    // 16384 tokens at most), 512 items 33.0 / 22.3 (200), 1024 items 140 / 95.9
+    // (2000).  Four / three / two CTAs: 8-bit 109 / 95.9 / 105 us (4, 6, 6
+    // groups), 4-bit 96.3 / 102 / 102 (8, 6, 8), f16 - / 77.0 / 75.2 (1024 items
+    // of 1000, 3 and 4 groups).
     const int64_t items = (int64_t)a.q.nseq * a.q.heads *
                           (((int64_t)a.q.max_new * a.per + M::kRows - 1) / M::kRows);
     AttnShape sh;
     auto fit = [&](int ctas) {  // CTAs of an SM
         const int room = M::kSm / ctas - 1024 - M::kCommon - M::kQ;
         sh.ctas = ctas * sms;
-        sh.ng = M::kGroups / ctas;
+        sh.ng = M::groups(ctas);
         sh.nslot = (room / sh.ng - M::kP - M::kMax) / M::kHalf;
     };
-    constexpr int kApart = M::kGroups < 4 ? M::kGroups : 4;
-    fit(kApart);
-    if (items < 3 * (int64_t)sms || sh.nslot < 3) fit(1);
+    fit(items < 3 * (int64_t)sms ? 1 : M::apart());
     if (sh.nslot > kMaxSlots) sh.nslot = kMaxSlots;
     *floats = 2 * (int64_t)sh.ctas * part_floats(M::kRows, D);
     if (!a.part) return cudaSuccess;
