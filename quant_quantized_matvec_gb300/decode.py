@@ -14,6 +14,8 @@ shapes, devices) and in the library (ranges, alignment, overlaps, memory).
 
 Descriptors (KVCache, KVBatch) are made once and kept; their tensors may
 change in value from step to step, so a captured CUDA graph stays valid.
+Their attributes cannot be set again: other tensors or sizes need another
+descriptor.
 """
 from __future__ import annotations
 
@@ -95,7 +97,19 @@ def _heads(t, name, shape):
     return p, s0 if n > 1 else h * d
 
 
-class KVCache:
+class _Fixed:
+    """A descriptor: the C struct behind it holds its tensors' addresses and
+    its sizes, so no attribute is set again after it was made."""
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"{type(self).__name__}.{name} is fixed: make another "
+                             f"{type(self).__name__}, or change the tensor's values in place")
+
+    def __delattr__(self, name):
+        raise AttributeError(f"{type(self).__name__}.{name} is fixed")
+
+
+class KVCache(_Fixed):
     """A paged key/value cache of one layer: `pages` pages of 64 tokens, in
     KV_F16, KV_Q8 or KV_Q4 (layout: include/kq_decode.h).  data: its bytes,
     a CUDA uint8 tensor (made, zeroed, if not given)."""
@@ -110,14 +124,13 @@ class KVCache:
         if data is None:
             data = torch.zeros(each * pages, dtype=torch.uint8, device=device)
         _tensor(data, "data", torch.uint8, (each * pages,))
-        self.fmt, self.kv_heads, self.head_dim = int(fmt), int(kv_heads), int(head_dim)
-        self.pages, self.page_bytes, self.data = int(pages), each, data
-        self._c = _binding.KqKv(self.fmt, self.kv_heads, self.head_dim, 0, data.data_ptr(),
-                                self.pages)
-        self._p = ctypes.byref(self._c)
+        c = _binding.KqKv(int(fmt), int(kv_heads), int(head_dim), 0, data.data_ptr(), int(pages))
+        self.__dict__.update(fmt=int(fmt), kv_heads=int(kv_heads), head_dim=int(head_dim),
+                             pages=int(pages), page_bytes=each, data=data, _c=c,
+                             _p=ctypes.byref(c))
 
 
-class KVBatch:
+class KVBatch(_Fixed):
     """The sequences of a step (kq_batch): start [nseq + 1], ctx [nseq] and
     pages [nseq, max_pages], int32 CUDA tensors; ntok new tokens in all, at
     most max_new of one sequence."""
@@ -129,12 +142,11 @@ class KVBatch:
         _tensor(start, "start", torch.int32, (nseq + 1,))
         _tensor(ctx, "ctx", torch.int32, (nseq,))
         _tensor(pages, "pages", torch.int32, (nseq, pages.shape[1]))
-        self.start, self.ctx, self.pages = start, ctx, pages
-        self.nseq, self.ntok, self.max_new = nseq, int(ntok), int(max_new)
-        self._c = _binding.KqBatch(nseq, self.max_new, self.ntok, start.data_ptr(),
-                                   ctx.data_ptr(), pages.data_ptr(), pages.shape[1])
-        self._p = ctypes.byref(self._c)
-        self._ws = {}  # workspace bytes of the attention calls made with it
+        c = _binding.KqBatch(nseq, int(max_new), int(ntok), start.data_ptr(), ctx.data_ptr(),
+                             pages.data_ptr(), pages.shape[1])
+        self.__dict__.update(start=start, ctx=ctx, pages=pages, nseq=nseq, ntok=int(ntok),
+                             max_new=int(max_new), _c=c, _p=ctypes.byref(c),
+                             _ws={})  # workspace bytes of the attention calls made with it
 
 
 def rope_table(positions, rot, base=10000.0, scaling=None, factor=1.0, orig=1, fast=32.0,

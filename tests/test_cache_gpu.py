@@ -259,3 +259,24 @@ def test_pages_past_32_bits(fmt):
         assert torch.equal(a, b)
     assert torch.isfinite(out[0][2]).all() and torch.isfinite(out[0][3]).all()
     assert not torch.equal(out[0][0], out[0][4])
+
+
+def test_descriptors_follow_values_and_refuse_other_tensors():
+    s = Setup(R.Q8, 2, 64, [3], [10])
+    with pytest.raises(AttributeError):
+        s.batch.ctx = dev(np.array([20], np.int32))
+    with pytest.raises(AttributeError):
+        s.batch.ntok = 2  # (the kernels would read three tokens of k and v)
+    with pytest.raises(AttributeError):
+        s.cache.data = torch.zeros_like(s.cache.data)
+    assert s.batch.ntok == 3 and (s.batch.nseq, s.batch.max_new) == (1, 3)
+    with pytest.raises(ValueError):
+        kq.kv_append(s.cache, s.batch, dev(s.k[:2]), dev(s.v[:2]))
+    kq.kv_append(s.cache, s.batch, dev(s.k), dev(s.v))
+    want = kq.kv_read(s.cache, s.batch)
+    s.batch.ctx.fill_(12)  # values may change
+    kq.kv_append(s.cache, s.batch, dev(s.k), dev(s.v))
+    got = kq.kv_read(s.cache, s.batch)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    s.batch.ctx.fill_(10)
+    assert torch.equal(kq.kv_read(s.cache, s.batch)[0][2], want[0][0])

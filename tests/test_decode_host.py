@@ -188,3 +188,21 @@ def test_tree_mask():
     for bad in ([0], [-2], [-1, 1], [-1] * 65):
         with pytest.raises(ValueError):
             kq.tree_mask(bad)
+
+
+def test_descriptors_cannot_be_changed():
+    """The C structs hold addresses and sizes: an attribute that could be set
+    would leave them with those of tensors that are gone, or let smaller
+    tensors through the checks than the kernels read."""
+    torch = pytest.importorskip("torch")
+    import quant_quantized_matvec_gb300 as kq
+    for cls, names in ((kq.KVCache, ("fmt", "kv_heads", "head_dim", "pages", "page_bytes", "data")),
+                       (kq.KVBatch, ("start", "ctx", "pages", "nseq", "ntok", "max_new"))):
+        made = object.__new__(cls)
+        made.__dict__.update({n: torch.zeros(3) for n in names})
+        for n in names:
+            with pytest.raises(AttributeError, match="fixed"):
+                setattr(made, n, torch.zeros(2))
+            with pytest.raises(AttributeError, match="fixed"):
+                delattr(made, n)
+            assert getattr(made, n).shape == (3,)
