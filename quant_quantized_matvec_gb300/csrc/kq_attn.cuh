@@ -417,8 +417,6 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, NT>::kGroups * AttnSmem<FMT, 
         // page's keys and a page's values by turns, the last values
         const int mine = producer && tid - ntail < a.ng ? 2 * count : 0;
         int issued = 0;
-        const int use0 = use;
-        const uint32_t parity0 = parity;
         int64_t kpage = -1, vpage = -1, next = mine ? page_of(a.q, b, pg0 + g) : -1;
         auto pump = [&](int until) {  // (the whole warp)
             const unsigned long long t0 = kq::global_ns();
@@ -514,16 +512,6 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, NT>::kGroups * AttnSmem<FMT, 
         __syncthreads();
         if (producer) {
             pump(mine);
-            if (*(volatile int *)&cm.dead) {
-                // after an expired wait: no copy may land later than this
-                int slot = use0;
-                uint32_t ph = parity0;
-                for (int k = 0; k < issued; ++k) {
-                    if (k >= issued - a.nslot)
-                        kq::mbar_wait(bars + 8 * slot, ph, kq::kWaitLimitNs);
-                    if (++slot == a.nslot) slot = 0, ph ^= 1;
-                }
-            }
             __syncwarp();
         }
 
@@ -952,6 +940,14 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, NT>::kGroups * AttnSmem<FMT, 
                         os[(4 * t + c) * D + w * kSlice + 16 * mt + 8 * h + n8] = O[t][mt][h];
         }
         __syncthreads();
+        // After an expired wait no copy may land later than this.  (Not before
+        // the barrier: a group's wait may expire when the producer is done, with
+        // copies on their way.  The last one of a slot is this lap's before `use`,
+        // else the lap's before.)
+        if (producer && tid - ntail < a.ng && *(volatile int *)&cm.dead) {
+            for (int k = 0; k < primed; ++k)
+                kq::mbar_wait(bars + 8 * k, parity ^ (k >= use), kq::kWaitLimitNs);
+        }
         const bool whole = npg == pages;
         const int slot = u == run.u0 ? 0 : 1;
         float *part = a.part + (2 * (int64_t)blockIdx.x + slot) * part_floats(RB, D);

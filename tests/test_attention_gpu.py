@@ -404,3 +404,50 @@ def test_many_items(fmt, nseq, hkv, most):
     ctx = [(37 * b * b + 11 * b) % most for b in range(nseq)]
     c = Case(fmt, hkv, 2, 64, [1 + b % 2 for b in range(nseq)], ctx, seed=nseq)
     c.check(c.run())
+
+
+def _expire(c, tries=8):
+    """The case's call with a limit far below the time a page takes to arrive,
+    over data that is not in L2: rows are NaN where a wait ran out, else as
+    always, the call ends at once, and nothing of it stays.  Returns how often
+    a wait ran out."""
+    from quant_quantized_matvec_gb300 import _binding
+    lib = _binding.load()
+    want = c.run()
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    q, mask, out = dev(c.q), c.mask(), torch.empty_like(want)
+    ends = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    times = 0
+    for _ in range(tries):
+        flush.fill_(1)
+        out.fill_(5.0)
+        torch.cuda.synchronize()
+        lib.kq_set_wait_limit_ns(1)
+        try:
+            ends[0].record()
+            kq.tree_attention(c.cache, c.batch, q, mask=mask, out=out)
+            ends[1].record()
+            torch.cuda.synchronize()
+        finally:
+            lib.kq_set_wait_limit_ns(0)
+        expired = kq.device_error()
+        times += expired
+        assert ends[0].elapsed_time(ends[1]) < 1000.0
+        assert ((out == want) | torch.isnan(out)).all()
+        assert torch.isnan(out).any() == expired
+        for _ in range(2):  # the same SMs again, at once
+            assert torch.equal(c.run(), want)
+    return times
+
+
+def _many_segments(fmt, g, dim, nseq=600, most=900):
+    """A batch of which each CTA has several items, some of them of one page."""
+    ctx = [(37 * b * b + 11 * b) % most for b in range(nseq)]
+    return Case(fmt, 2, g, dim, [1 + b % 2 for b in range(nseq)], ctx, seed=18)
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
+@pytest.mark.parametrize("dim,g", [(64, 2), (128, 4), (128, 7), (256, 8)])
+def test_expired_waits_with_few_rows(fmt, dim, g):
+    _expire(Case(fmt, 2, g, dim, [2], [40000], seed=19))
+    _expire(_many_segments(fmt, g, dim))
