@@ -70,7 +70,7 @@ struct RowsCommon {
     // one, back.)
     uint64_t sfree[4], sdone[4], pready[4], pvdone[4], ofree, drain[2];
     uint32_t tmem;
-    int dead;
+    int dead, drained[2];
     int badpage[8];          // of tile t & 7: the page is not valid
     uint32_t badtok[4][2];   // values of these tokens are not finite (edge pages)
     float kf[8], vf[8];      // powers of two of the page's scales
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         kq::mbar_init(bar(cm.ofree), qw);
         kq::mbar_init(bar(cm.drain[0]), 1);
         kq::mbar_init(bar(cm.drain[1]), 1);
-        cm.dead = 0;
+        cm.dead = cm.drained[0] = cm.drained[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     kq::allow_dependents();
@@ -949,11 +949,16 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                 }
             }
             if ((w == kFirstOther || w == kFirstOther + 2) && __any_sync(~0u, dead())) {
-                // nothing of the MMAs may run after this
-                const uint64_t &b = cm.drain[w == kFirstOther ? 0 : 1];
-                if (elected()) tc_commit(bar(b));
-                __syncwarp();
-                kq::mbar_wait(bar(b), 0, kq::kWaitLimitNs);
+                // nothing of the MMAs may run after this (once: the segments
+                // after this one issue none)
+                const int k = w == kFirstOther ? 0 : 1;
+                if (!*(volatile int *)&cm.drained[k]) {
+                    if (elected()) tc_commit(bar(cm.drain[k]));
+                    __syncwarp();
+                    kq::mbar_wait(bar(cm.drain[k]), 0, kq::kWaitLimitNs);
+                    __syncwarp();
+                    if (lane == 0) *(volatile int *)&cm.drained[k] = 1;
+                }
             }
             __syncwarp();
             __syncthreads();

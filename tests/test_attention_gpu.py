@@ -451,3 +451,11 @@ def _many_segments(fmt, g, dim, nseq=600, most=900):
 def test_expired_waits_with_few_rows(fmt, dim, g):
     _expire(Case(fmt, 2, g, dim, [2], [40000], seed=19))
     _expire(_many_segments(fmt, g, dim))
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
+@pytest.mark.parametrize("dim,g", [(64, 20), (128, 20), (128, 50), (64, 100), (128, 100)])
+def test_expired_waits_in_batches_of_many_rows(fmt, dim, g):
+    """Blocks of 32, 64 and 128 rows, and several items a CTA: those after
+    the one whose wait ran out wait for nothing."""
+    _expire(_many_segments(fmt, g, dim, nseq=300, most=300))
