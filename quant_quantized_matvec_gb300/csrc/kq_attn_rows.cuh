@@ -814,7 +814,6 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         segments([&](const Seg &g) {
             // --------------------------------------------- producer warp
             int issued = 0;
-            const int use0 = use, turn0 = turn;
             const bool issuer = w == kFirstOther + 1 && lane == 0;
             int64_t page = -1, next = issuer ? page_of(a.q, g.b, g.pg0) : -1;
             auto pump = [&](int until) {
@@ -844,17 +843,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             };
             if (issuer) pump(min(2 * g.npg, M::kSlots));
             __syncthreads();
-            if (issuer) {
-                pump(2 * g.npg);
-                if (dead()) {  // no copy may land after this
-                    int slot = use0, n = turn0;
-                    for (int k = 0; k < issued; ++k) {
-                        if (k >= issued - M::kSlots)
-                            kq::mbar_wait(bar(cm.rawfull[slot]), n & 1, kq::kWaitLimitNs);
-                        if (++slot == M::kSlots) slot = 0, ++n;
-                    }
-                }
-            }
+            if (issuer) pump(2 * g.npg);
             // ------- scale warp: each raw slot's powers of two, ahead of the
             // conversion (a quantised cache's only)
             if (L::kQuant && w == kFirstOther + 3) {
@@ -948,20 +937,29 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                     __syncwarp();
                 }
             }
-            if ((w == kFirstOther || w == kFirstOther + 2) && __any_sync(~0u, dead())) {
-                // nothing of the MMAs may run after this (once: the segments
-                // after this one issue none)
+            __syncwarp();
+            __syncthreads();
+            // After an expired wait no copy and no MMA may run on past this.
+            // (Not before the barrier: another role's wait may expire when the
+            // producer or an MMA warp is done, with work of theirs on its way.)
+            if (dead()) {
+                if (issuer) {  // each slot's last copy: this turn's before `use`
+                    for (int k = 0; k < M::kSlots; ++k) {
+                        const int n = k < use ? turn : turn - 1;
+                        if (n >= 0) kq::mbar_wait(bar(cm.rawfull[k]), n & 1, kq::kWaitLimitNs);
+                    }
+                }
+                // (once: the segments after this one issue no MMAs)
                 const int k = w == kFirstOther ? 0 : 1;
-                if (!*(volatile int *)&cm.drained[k]) {
+                if ((w == kFirstOther || w == kFirstOther + 2) && !*(volatile int *)&cm.drained[k]) {
                     if (elected()) tc_commit(bar(cm.drain[k]));
                     __syncwarp();
                     kq::mbar_wait(bar(cm.drain[k]), 0, kq::kWaitLimitNs);
                     __syncwarp();
                     if (lane == 0) *(volatile int *)&cm.drained[k] = 1;
                 }
+                __syncwarp();
             }
-            __syncwarp();
-            __syncthreads();
             finish(g);
         });
     }

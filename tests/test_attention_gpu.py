@@ -459,3 +459,11 @@ def test_expired_waits_in_batches_of_many_rows(fmt, dim, g):
     """Blocks of 32, 64 and 128 rows, and several items a CTA: those after
     the one whose wait ran out wait for nothing."""
     _expire(_many_segments(fmt, g, dim, nseq=300, most=300))
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
+@pytest.mark.parametrize("dim,g", [(64, 20), (128, 10), (128, 50), (64, 100), (128, 100)])
+def test_expired_waits_with_many_rows(fmt, dim, g):
+    """One item's pages in every CTA: its copies and MMAs end with the call
+    (the next one takes the same shared and tensor memory at once)."""
+    _expire(Case(fmt, 2, g, dim, [2], [30000], seed=20))
