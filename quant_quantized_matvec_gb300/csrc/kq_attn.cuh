@@ -419,10 +419,9 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, NT>::kGroups * AttnSmem<FMT, 
         int issued = 0;
         int64_t kpage = -1, vpage = -1, next = mine ? page_of(a.q, b, pg0 + g) : -1;
         auto pump = [&](int until) {  // (the whole warp)
-            const unsigned long long t0 = kq::global_ns();
+            unsigned long long since = 0;  // the lane waits for its slot (0: it does not)
             while (__any_sync(~0u, issued < until)) {
                 if (__any_sync(~0u, *(volatile int *)&cm.dead)) break;
-                bool late = false;
                 // (a slot's first filling waits for nothing)
                 if (issued < until &&
                     (primed < a.nslot ||
@@ -444,11 +443,15 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, NT>::kGroups * AttnSmem<FMT, 
                                  M::kHalf, bar);
                     if (primed < a.nslot) ++primed;
                     if (++use == a.nslot) use = 0, parity ^= 1;
-                } else {
-                    // (the groups' own waits expire first, and say so)
-                    late = kq::global_ns() - t0 > 2 * kq::kWaitLimitNs;
+                    since = 0;
+                } else if (issued < until) {
+                    const unsigned long long now = kq::global_ns();
+                    if (!since) since = now;
+                    if (now - since > a.wait_ns) {
+                        *(volatile int *)&cm.dead = 1;
+                        atomicOr(a.err, 1u);
+                    }
                 }
-                if (__any_sync(~0u, late)) break;
             }
         };
         if (producer) pump(min(mine, a.nslot));

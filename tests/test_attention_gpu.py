@@ -467,3 +467,35 @@ def test_expired_waits_with_many_rows(fmt, dim, g):
     """One item's pages in every CTA: its copies and MMAs end with the call
     (the next one takes the same shared and tensor memory at once)."""
     _expire(Case(fmt, 2, g, dim, [2], [30000], seed=20))
+
+
+@pytest.mark.parametrize("g", [4, 20])
+def test_the_limit_is_a_waits_not_the_calls(g):
+    """A call whose items take several times the limit each, no wait of which
+    is long: nothing expires.  (One page stands for all 800000 of a sequence.)"""
+    from quant_quantized_matvec_gb300 import _binding
+    lib = _binding.load()
+    nseq, hkv = 4, torch.cuda.get_device_properties(0).multi_processor_count // 4
+    pages = 800000 if g == 4 else 100000
+    cache = kq.KVCache(kq.KV_Q4, hkv, 64, 1)
+    one = kq.KVBatch(dev(np.array([0, 64], np.int32)), dev(np.zeros(1, np.int32)),
+                     dev(np.zeros((1, 1), np.int32)), 64, 64)
+    gen = torch.Generator(device="cuda").manual_seed(21)
+    kq.kv_append(cache, one, *(torch.randn(64, hkv, 64, generator=gen, device="cuda") for _ in range(2)))
+    batch = kq.KVBatch(dev(np.arange(nseq + 1, dtype=np.int32)),
+                       dev(np.full(nseq, 64 * pages - 1, np.int32)),
+                       torch.zeros(nseq, pages, dtype=torch.int32, device="cuda"), nseq, 1)
+    q = torch.randn(nseq, hkv * g, 64, generator=gen, device="cuda")
+    want = kq.tree_attention(cache, batch, q)
+    ends = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    torch.cuda.synchronize()
+    lib.kq_set_wait_limit_ns(20 * 10 ** 6)
+    try:
+        ends[0].record()
+        got = kq.tree_attention(cache, batch, q)
+        ends[1].record()
+        torch.cuda.synchronize()
+    finally:
+        lib.kq_set_wait_limit_ns(0)
+    assert ends[0].elapsed_time(ends[1]) > 60.0  # ms
+    assert torch.isfinite(want).all() and torch.equal(got, want)
