@@ -423,9 +423,14 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, NT>::kGroups * AttnSmem<FMT, 
             while (__any_sync(~0u, issued < until)) {
                 if (__any_sync(~0u, *(volatile int *)&cm.dead)) break;
                 // (a slot's first filling waits for nothing)
-                if (issued < until &&
-                    (primed < a.nslot ||
-                     kq::mbar_test(kq::smem_addr(&cm.empty[g * kMaxSlots + use]), parity ^ 1))) {
+                bool room = issued < until &&
+                            (primed < a.nslot ||
+                             kq::mbar_test(kq::smem_addr(&cm.empty[g * kMaxSlots + use]), parity ^ 1));
+                // (a group whose wait ran out hands back slots whose copies may be
+                // on their way: it sets `dead` first, so this look comes after
+                // the one at the slot)
+                room = room && !*(volatile int *)&cm.dead;
+                if (room) {
                     const int i = issued++;
                     const bool values = i == mine - 1 || (i > 0 && (i & 1) == 0);
                     if (!values) {
