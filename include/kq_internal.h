@@ -55,7 +55,8 @@ int kq_plan_describe(const kq_mat *mats, int n, int ntok, int sms, int smem_opti
 /*
  * Test hook for failure reporting: the wall-time limit, in nanoseconds, of
  * every wait the streaming kernel makes on a shared-memory barrier (and of
- * its producer's wait for the input loads), for launches enqueued after
+ * its producer's wait for the input loads), and of every wait of
+ * kq_tree_attention's kernels, for launches enqueued after
  * this call; 0 restores the default of 2 s.  Returns the previous setting
  * (0 = default).  Process-wide.
  *
@@ -65,7 +66,8 @@ int kq_plan_describe(const kq_mat *mats, int n, int ntok, int sms, int smem_opti
  * KQ_ERR_TIMEOUT), stops issuing copies, waits -- always with the default
  * limit -- for the copies it had issued, and writes NaN to the rows it had
  * not finished.  Nothing hangs or faults, and the next launch made with the
- * default limit computes normally.
+ * default limit computes normally.  (Attention: NaN to the rows of the items
+ * whose wait ran out, and of those that the CTA had not begun.)
  */
 unsigned long long kq_set_wait_limit_ns(unsigned long long ns);
 

@@ -7,6 +7,7 @@
 namespace kq {
 
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s (default)
+constexpr unsigned kSuspendNs = 100000;  // a thread's suspension by mbar_try
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
     return (uint32_t)__cvta_generic_to_shared(p);
@@ -63,6 +64,31 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
         __nanosleep(ns);
         if (ns < max_ns) ns <<= 1;
         if (global_ns() - t0 > limit_ns) return false;
+    }
+    return true;
+}
+// mbar_wait with a limit that may be shorter than the 100 us for which
+// mbar_try may suspend the thread (suspend_ns: the lesser of the two).
+__device__ __forceinline__ bool mbar_wait_for(uint32_t bar, uint32_t parity,
+                                              unsigned long long limit_ns, uint32_t suspend_ns) {
+    auto arrived = [&]() {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n"
+            " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(suspend_ns)
+            : "memory");
+        return ok != 0;
+    };
+    if (arrived()) return true;
+    const unsigned long long t0 = global_ns();
+    unsigned ns = 32;
+    while (!arrived()) {
+        if (global_ns() - t0 > limit_ns) return false;
+        __nanosleep(ns);
+        if (ns < 256) ns <<= 1;
     }
     return true;
 }

@@ -48,6 +48,7 @@ cudaError_t attn(int fmt, int dim, const Seqs &q, const float *x, int64_t x_stri
     a.x = x, a.x_stride = x_stride, a.mask = mask, a.out = out;
     a.part = static_cast<float *>(ws);
     a.err = err, a.wait_ns = wait_ns;
+    a.suspend_ns = wait_ns < kq::kSuspendNs ? (uint32_t)wait_ns : kq::kSuspendNs;
     a.q_heads = q_heads, a.per = q_heads / q.heads;
     a.scale = scale * 1.44269504088896340736f;
     int64_t floats = 0;

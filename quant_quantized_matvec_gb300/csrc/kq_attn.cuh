@@ -64,6 +64,7 @@ struct AttnArgs {
     int4 *meta;     // two entries a CTA: the item that begins in it and goes on
     unsigned int *err;
     unsigned long long wait_ns;
+    uint32_t suspend_ns;  // the lesser of it and kq::kSuspendNs
     int32_t q_heads, per;  // query heads; of them to a key head
     float scale;           // times log2 e
     int32_t ng, nslot;     // groups a CTA, slots of a group's ring
@@ -533,7 +534,8 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, NT>::kGroups * AttnSmem<FMT, 
 
         // the next slot, once its copy has arrived
         auto arrived = [&]() {
-            if (!*(volatile int *)&cm.dead && !kq::mbar_wait(bars + 8 * use, parity, a.wait_ns)) {
+            if (!*(volatile int *)&cm.dead &&
+                !kq::mbar_wait_for(bars + 8 * use, parity, a.wait_ns, a.suspend_ns)) {
                 *(volatile int *)&cm.dead = 1;
                 atomicOr(a.err, 1u);
             }

@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     auto dead = [&]() { return *(volatile int *)&cm.dead != 0; };
     auto wait = [&](const uint64_t &b, int phase) {  // the completion of the barrier's phase
         if (kq::mbar_test(bar(b), phase & 1) || dead()) return;
-        if (!kq::mbar_wait(bar(b), phase & 1, a.wait_ns)) {
+        if (!kq::mbar_wait_for(bar(b), phase & 1, a.wait_ns, a.suspend_ns)) {
             *(volatile int *)&cm.dead = 1;
             atomicOr(a.err, 1u);
         }

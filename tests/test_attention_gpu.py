@@ -499,3 +499,20 @@ def test_the_limit_is_a_waits_not_the_calls(g):
         lib.kq_set_wait_limit_ns(0)
     assert ends[0].elapsed_time(ends[1]) > 60.0  # ms
     assert torch.isfinite(want).all() and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
+@pytest.mark.parametrize("dim,g", [(64, 2), (128, 4), (128, 7), (256, 8), (64, 20), (128, 10),
+                                   (128, 20), (128, 50), (64, 100), (128, 100)])
+def test_a_short_limit_is_kept(fmt, dim, g):
+    """1 ns is shorter than any page takes: each kernel's waits do run out,
+    where CTAs have one item of many pages and where they have several."""
+    c = Case(fmt, 2, g, dim, [2], [62], seed=22)
+    pages = 20000  # one page stands for all of them
+    c.batch = kq.KVBatch(dev(c.start), dev(np.array([64 * pages - 2], np.int32)),
+                         dev(np.full((1, pages), c.table[0, 0], np.int32)), 2, 2)
+    assert _expire(c, tries=3) == 3
+    c = Case(fmt, 2, g, dim, [1] * 200, [63] * 200, seed=23)
+    c.batch = kq.KVBatch(dev(c.start), dev(np.full(200, 64 * 200 - 1, np.int32)),
+                         dev(np.repeat(c.table, 200, 1)), 200, 1)
+    assert _expire(c, tries=3) == 3
