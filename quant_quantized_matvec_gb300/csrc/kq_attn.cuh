@@ -903,11 +903,15 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, NT>::kGroups * AttnSmem<FMT, 
                     const float base = now == -INFINITY ? 0.f : now;
                     alpha[t] = exp2_of(m[t] - base);
                     m[t] = now;
-                    const float high = base - 15.f;  // probabilities (and l, O) times 2^15
                     l[t] *= alpha[t];
 #pragma unroll
                     for (int tt = 0; tt < kTok; ++tt) {
-                        const float p0 = exp2_of(S[t][tt][0] - high), p1 = exp2_of(S[t][tt][1] - high);
+                        // probabilities (and l, O) times 2^15.  The maximum is taken off
+                        // by itself, which gives 0 for the largest whatever its size;
+                        // together with the 15 it would be rounded past 2^24, and the
+                        // largest be infinite as an f16
+                        const float p0 = exp2_of(S[t][tt][0] - base) * 32768.f;
+                        const float p1 = exp2_of(S[t][tt][1] - base) * 32768.f;
                         l[t] += p0 + p1;
                         const __half h0 = __float2half_rn(p0), h1 = __float2half_rn(p1);
                         const int tok = 16 * (kTok * w + tt) + n8;

@@ -516,3 +516,35 @@ def test_a_short_limit_is_kept(fmt, dim, g):
     c.batch = kq.KVBatch(dev(c.start), dev(np.full(200, 64 * 200 - 1, np.int32)),
                          dev(np.repeat(c.table, 200, 1)), 200, 1)
     assert _expire(c, tries=3) == 3
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("by", ["query", "scale"])
+@pytest.mark.parametrize("top", [2.0 ** 24 + 10, 2.0 ** 25 + 4, 1e8, 2.0 ** 27, 3e9, 1e30])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_logits_past_24_bits(fmt, dim, by, top, sign, g=2):
+    """Finite logits (in units of log 2) that f32 holds in steps of 2 and
+    more: the row is the mean of the values at its largest logit, of which
+    three are the same to the bit, in three pages.
+
+    Queries and keys have one factor of a logit that is not zero, so equal
+    keys give equal logits, whatever their size, and the other logits are
+    smaller by half the largest: their probabilities are 0 in f32.  What is
+    left of the error is the sums', as decode_ref.attention derives it with
+    logits that are exact."""
+    c = Case(fmt, 2, g, dim, [2], [200], seed=17)
+    at = [5, 70, 130]
+    c.k[..., 0] = 0.5 if sign > 0 else 1.0
+    c.k[..., 1:] *= 0.01
+    c.k[at, :, 0] = 1.0 if sign > 0 else 0.5
+    c.write()
+    big = sign * top / 1.4427 / (1.0 if sign > 0 else 0.5)
+    c.q[:] = 0
+    c.q[..., 0] = big if by == "query" else 1.0
+    got = c.run(scale=1.0 if by == "query" else big, mask=None).cpu().numpy().astype(float)
+    v = R.values(*R.quantise(c.v, fmt)).astype(float)
+    want, size = (np.repeat(f(v)[at].mean(0), g, 0) for f in (np.asarray, np.abs))
+    bound = size * (2 * 2.0 ** -21 + (64 + 4 + 304) * 2.0 ** -22) + 202 * 2.0 ** -38 * np.abs(v).max()
+    assert np.isfinite(got).all()
+    assert (np.abs(got - want) <= bound).all()
