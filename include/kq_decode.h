@@ -195,10 +195,11 @@ kq_status kq_kv_move(const kq_kv *kv, const kq_batch *batch, const int32_t *path
  *
  * A row that attends a place without a valid page is NaN.  max_new <=
  * KQ_MAX_DRAFT.  Queries and probabilities are held as two f16 terms (22
- * bits; queries after scaling a row by a power of two), and so is code *
- * scale, or a probability times its value's scale, where that is formed before
- * the product (what is dropped is below 2^-22 of it, or 2^-39 of the page's
- * largest).  Products are exact, sums are f32.
+ * bits; queries after scaling a row by a power of two, and with many rows by
+ * the fraction of `scale` too, rounded to f32), and so is code * scale, or a
+ * probability times its value's scale, where that is formed before the product
+ * (what is dropped is below 2^-22 of it, or 2^-39 of the page's largest).
+ * Products are exact, sums are f32.  Logits may have any finite size.
  */
 kq_status kq_tree_attention(const kq_kv *kv, const kq_batch *batch, const float *q,
                             int64_t q_stride, int q_heads, const uint64_t *mask, float scale,

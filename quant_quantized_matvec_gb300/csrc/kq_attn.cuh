@@ -67,6 +67,8 @@ struct AttnArgs {
     uint32_t suspend_ns;  // the lesser of it and kq::kSuspendNs
     int32_t q_heads, per;  // query heads; of them to a key head
     float scale;           // times log2 e
+    float scale_m;         // the same as scale_m * 2^scale_e, |scale_m| in 0.5..1 or 0
+    int32_t scale_e;
     int32_t ng, nslot;     // groups a CTA, slots of a group's ring
 };
 

@@ -404,11 +404,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                 top = fmaxf(top, fmaxf(fmaxf(fabsf(v[i].x), fabsf(v[i].y)),
                                        fmaxf(fabsf(v[i].z), fabsf(v[i].w))));
             const int ex = max((int)((__float_as_uint(top) >> 23) & 255) - 126, -111);
-            float up = __uint_as_float((uint32_t)(127 + 15 - ex) << 23);
-            // (a negative scale goes to the query, so that maxima stay maxima)
-            const float rowf = fabsf(a.scale) * __uint_as_float((uint32_t)(127 + (ex >> 1)) << 23) *
-                               __uint_as_float((uint32_t)(127 + (ex - (ex >> 1)) - 15) << 23);
-            if (a.scale < 0.f) up = -up;
+            // The query is multiplied by the fraction of the scale (which has its
+            // sign) as well, so that the factor of the scores is a power of two
+            // and their product with it exact.
+            const float up = a.scale_m * __uint_as_float((uint32_t)(127 + 15 - ex) << 23);
+            const float rowf =
+                __uint_as_float((uint32_t)(127 + min(max(ex - 15 + a.scale_e, -126), 127)) << 23);
             const uint64_t nw = (!on      ? 0
                                  : a.mask ? __ldg(a.mask + g.s.first + tok)
                                           : ~0ull >> (63 - tok)) &
@@ -493,11 +494,15 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                     for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(d[i]));
                 }
                 mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                const float now = fmaxf(m, mx[0] == -INFINITY ? mx[0] : mx[0] * f);
+                // Probabilities are held times 2^15.  The row's reference is its
+                // maximum less 15, rounded up, and all that follows goes by the
+                // reference: however large the logits are, and the steps in which
+                // f32 holds them, none passes 2^15.
+                const float now =
+                    fmaxf(m, mx[0] == -INFINITY ? mx[0] : __fsub_ru(mx[0] * f, 15.f));
                 const float from = now == -INFINITY ? 0.f : now;
                 const float alpha = exp2_of(m - from);
                 m = now;
-                const float high = 15.f - from;
                 // Values that are not finite: the conversion left them out, and
                 // the rows that attend them take them below.  (Read before P
                 // goes out, after which the buffer's next page may come.)
@@ -523,7 +528,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                     scores(half, d);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        float p = exp2_of(fmaf(__uint_as_float(d[i]), f, high));
+                        float p = exp2_of(fmaf(__uint_as_float(d[i]), f, -from));
                         if constexpr (kEdge)  // (f may be a NaN)
                             if (!((uint32_t)(ok >> (32 * half)) >> i & 1)) p = 0.f;
                         sum[i & 3] += p;
@@ -568,7 +573,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                                 float p = 0.f;
 #pragma unroll
                                 for (int i = 0; i < 32; ++i) p = i == (at & 31) ? __uint_as_float(d[i]) : p;
-                                p = exp2_of(fmaf(p, f, high));
+                                p = exp2_of(fmaf(p, f, -from));
                                 if ((ok >> at) & 1) {
 #pragma unroll
                                     for (int i = 0; i < D; ++i)

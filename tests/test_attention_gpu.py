@@ -548,3 +548,14 @@ def test_logits_past_24_bits(fmt, dim, by, top, sign, g=2):
     bound = size * (2 * 2.0 ** -21 + (64 + 4 + 304) * 2.0 ** -22) + 202 * 2.0 ** -38 * np.abs(v).max()
     assert np.isfinite(got).all()
     assert (np.abs(got - want) <= bound).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("g", [10, 30, 60])
+@pytest.mark.parametrize("top", [2.0 ** 24 + 10, 2.0 ** 25 + 4, 1e8, 2.0 ** 27, 3e9, 1e30])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_logits_past_24_bits_in_many_rows(fmt, dim, top, sign, g):
+    """The same with 20, 60 and 120 rows a key head."""
+    for by in ("query", "scale"):
+        test_logits_past_24_bits(fmt, dim, by, top, sign, g=g)
