@@ -899,21 +899,21 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, NT>::kGroups * AttnSmem<FMT, 
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     const int r = 4 * t + c;
-                    float now = m[t];
+                    // Probabilities (and l, O) are held times 2^15.  The row's reference
+                    // is its maximum less 15, rounded up, and all that follows goes by
+                    // the reference: however large the logits are, and the steps in
+                    // which f32 holds them, none passes 2^15.
+                    float top = sm[r];
 #pragma unroll
-                    for (int i = 0; i < kWg; ++i) now = fmaxf(now, sm[i * RB + r]);
+                    for (int i = 1; i < kWg; ++i) top = fmaxf(top, sm[i * RB + r]);
+                    const float now = fmaxf(m[t], __fsub_ru(top, 15.f));
                     const float base = now == -INFINITY ? 0.f : now;
                     alpha[t] = exp2_of(m[t] - base);
                     m[t] = now;
                     l[t] *= alpha[t];
 #pragma unroll
                     for (int tt = 0; tt < kTok; ++tt) {
-                        // probabilities (and l, O) times 2^15.  The maximum is taken off
-                        // by itself, which gives 0 for the largest whatever its size;
-                        // together with the 15 it would be rounded past 2^24, and the
-                        // largest be infinite as an f16
-                        const float p0 = exp2_of(S[t][tt][0] - base) * 32768.f;
-                        const float p1 = exp2_of(S[t][tt][1] - base) * 32768.f;
+                        const float p0 = exp2_of(S[t][tt][0] - base), p1 = exp2_of(S[t][tt][1] - base);
                         l[t] += p0 + p1;
                         const __half h0 = __float2half_rn(p0), h1 = __float2half_rn(p1);
                         const int tok = 16 * (kTok * w + tt) + n8;
