@@ -232,7 +232,8 @@ int64_t kq_attn_workspace_bytes(const kq_kv *kv, const kq_batch *batch, int q_he
  * taken as the nearer bound, NaN as 0; the same for u, which stays below 1.
  *
  *   start   device int32 [nseq + 1] as in kq_batch; 1..KQ_MAX_DRAFT nodes a
- *           sequence (max_new), one with none gets count 0 and next -1
+ *           sequence (max_new), one with none gets count 0 and next -1 (with
+ *           ntok = 0 all of them; token, parent, p, u and path may be NULL)
  *   token   device int32 [ntok]; a draft outside the vocabulary is rejected
  *           (and nothing is taken out for it)
  *   parent  device int32 [ntok], a node of lower index in the sequence; a

@@ -285,21 +285,29 @@ kq_status kq_verify_tree(int nseq, int64_t ntok, int max_new, const int32_t *sta
     if (vocab < 1 || vocab > KQ_MAX_VOCAB || p_stride < vocab || p_stride > kMaxStride ||
         (q && (q_stride < vocab || q_stride > kMaxStride)))
         return KQ_ERR_SHAPE;
-    if (ntok == 0) return KQ_OK;
-    if (!start || !token || !parent || !p || !u || !u_next || !path || !count || !next)
+    // (without nodes token, parent, p, u and path have no elements to point at)
+    if (!start || !u_next || !count || !next ||
+        (ntok > 0 && (!token || !parent || !p || !u || !path)))
         return KQ_ERR_NULL;
     const void *four[] = {start, token, parent, p, q, u, u_next, path, count, next};
     for (const void *a : four)
         if (!aligned(a, 4)) return KQ_ERR_ALIGN;
+    int devices = 0;
+    if (ntok == 0 && (cudaGetDeviceCount(&devices) != cudaSuccess || devices == 0)) {
+        cudaGetLastError();
+        return KQ_OK;  // no memory that a result could be written to
+    }
     Pointers a;
     a.read(start, 4 * ((int64_t)nseq + 1));
-    a.read(token, 4 * ntok);
-    a.read(parent, 4 * ntok);
-    a.read(p, rows_bytes(ntok, p_stride, vocab));
-    if (q) a.read(q, rows_bytes(ntok, q_stride, vocab));
-    a.read(u, 4 * ntok);
+    if (ntok > 0) {
+        a.read(token, 4 * ntok);
+        a.read(parent, 4 * ntok);
+        a.read(p, rows_bytes(ntok, p_stride, vocab));
+        if (q) a.read(q, rows_bytes(ntok, q_stride, vocab));
+        a.read(u, 4 * ntok);
+        a.write(path, 4 * ntok);
+    }
     a.read(u_next, 4 * (int64_t)nseq);
-    a.write(path, 4 * ntok);
     a.write(count, 4 * (int64_t)nseq);
     a.write(next, 4 * (int64_t)nseq);
     const kq_status st = a.check();

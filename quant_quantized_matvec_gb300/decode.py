@@ -300,7 +300,7 @@ def verify_tree(start, tokens, parents, p, q, u, u_next, max_new, path=None, cou
 
     def rows(t, name):
         ptr = _tensor(t, name, torch.float32, shape, dense=False)
-        if shape[1] > 1 and t.stride(1) != 1:
+        if ntok and shape[1] > 1 and t.stride(1) != 1:
             raise ValueError(f"{name}: a row must be contiguous")
         return ptr, t.stride(0) if ntok > 1 else shape[1]
 

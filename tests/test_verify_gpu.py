@@ -179,3 +179,29 @@ def test_refusals():
         kq.verify_tree(*a[:4], a[4][:, :10], *a[5:], 3)
     with pytest.raises(kq.KQError, match="KQ_ERR_NTOK"):
         kq.verify_tree(*a, 65)
+
+
+@pytest.mark.parametrize("q", [True, False], ids=["probs", "tokens"])
+def test_no_nodes_in_any_sequence(q):
+    """A step whose sequences are all idle: count 0 and next -1 for each, as
+    for one idle sequence among others."""
+    c = Case([0, 0, 0], 100, "chain")
+    count, nxt = (torch.full((3,), 7, dtype=torch.int32, device="cuda") for _ in range(2))
+    path, _, _ = c.run(q, count=count, next_token=nxt)
+    assert path.shape == (0,)
+    assert count.tolist() == [0, 0, 0] and nxt.tolist() == [-1, -1, -1]
+    many = Case([0] * 4096, 5, "chain")
+    _, got, nxt = many.run(q)
+    assert (got == 0).all() and (nxt == -1).all()
+
+
+def test_no_nodes_with_torchs_strides_and_starts_of_any_kind():
+    c = Case([0, 0], 100, "chain")
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    p = torch.empty(0, 100, device="cuda")
+    for start in ([0, 0, 0], [7, 3, 1 << 30]):  # (cut to the ntok tokens there are)
+        out = kq.verify_tree(dev(np.array(start, np.int32)), none, none, p, None, p[:, 0], dev(c.un), 4)
+        assert [x.tolist() for x in out] == [[], [0, 0], [-1, -1]]
+    with pytest.raises(kq.KQError, match="KQ_ERR_ALIAS"):
+        kq.verify_tree(dev(c.start), none, none, p, None, p[:, 0], dev(c.un), 4,
+                       count=out[2], next_token=out[2])
