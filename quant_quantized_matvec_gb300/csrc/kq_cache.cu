@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kCacheThreads, 4)
     const int e = 8 * (threadIdx.x % kOctets), j0 = threadIdx.x / kOctets;
     const int64_t stride = values ? a.v_stride : a.k_stride;
     const float *src = (values ? a.v : a.k) + (int64_t)(part.tok + j0) * stride + head * D + e;
-    const bool turn = !values && a.table && e < a.rot;
+    const bool keys = !values && a.table, turn = keys && e < a.rot;
     const int half = a.rot / 2;
     // (halves may meet inside the eight values: each four has its partner)
     const int to0 = e < half ? half : -half, to1 = e + 4 < half ? half : -half;
@@ -155,12 +155,13 @@ __global__ void __launch_bounds__(kCacheThreads, 4)
         const bool on = j < n;
         float x[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
         if (j + kStep < n) u = load4(src + kStep * stride), v = load4(src + kStep * stride + 4);
-        if (turn && on) {
+        if (keys && on) {
             const int pos = __ldg(a.pos + part.tok + j);
             if (pos < 0 || pos >= a.positions) {
+                // (all of the key, also what is not rotated)
 #pragma unroll
                 for (int k = 0; k < 8; ++k) x[k] = quiet_nan();
-            } else if (a.inter) {
+            } else if (turn && a.inter) {
                 const float4 *p =
                     reinterpret_cast<const float4 *>(a.table + (int64_t)pos * a.rot + e);
                 const float4 c0 = __ldg(p), c1 = __ldg(p + 1);
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(kCacheThreads, 4)
                                     rot_a(x[6], x[7], c1.z, c1.w), rot_b(x[6], x[7], c1.z, c1.w)};
 #pragma unroll
                 for (int k = 0; k < 8; ++k) x[k] = y[k];
-            } else {
+            } else if (turn) {
                 const float *row = a.table + (int64_t)pos * a.rot;
                 const float4 y0 = load4(src + to0), y1 = load4(src + 4 + to1);
                 const float4 *p0 = reinterpret_cast<const float4 *>(row + 2 * pair0);

@@ -280,3 +280,24 @@ def test_descriptors_follow_values_and_refuse_other_tensors():
     assert all(torch.equal(a, b) for a, b in zip(want, got))
     s.batch.ctx.fill_(10)
     assert torch.equal(kq.kv_read(s.cache, s.batch)[0][2], want[0][0])
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("dim,rot", [(128, 32), (64, 24), (256, 128), (128, 128)])
+def test_a_bad_position_stores_a_key_of_nan(fmt, inter, dim, rot):
+    """The whole key, as kq_rope gives it, also where a part of it is not
+    rotated; its value, and the other tokens, are as ever."""
+    s = Setup(fmt, 2, dim, [9, 66], [5, 62], seed=rot)
+    a = s.rng.uniform(0, 6.3, (40, rot // 2))
+    table = np.stack([np.cos(a), np.sin(a)], -1).astype(np.float32)
+    pos = s.rng.integers(0, 40, s.ntok).astype(np.int32)
+    kq.kv_append(s.cache, s.batch, dev(s.k), dev(s.v), dev(pos), dev(table), inter)
+    k, v = (x.cpu().numpy() for x in kq.kv_read(s.cache, s.batch))
+    bad = [1, 2, 70]
+    pos[bad] = [40, -1, 1 << 30]
+    kq.kv_append(s.cache, s.batch, dev(s.k), dev(s.v), dev(pos), dev(table), inter)
+    k2, v2 = (x.cpu().numpy() for x in kq.kv_read(s.cache, s.batch))
+    assert np.isnan(k2[bad]).all()
+    rest = [i for i in range(s.ntok) if i not in bad]
+    assert np.array_equal(k2[rest], k[rest]) and np.array_equal(v2, v)
