@@ -559,3 +559,22 @@ def test_logits_past_24_bits_in_many_rows(fmt, dim, top, sign, g):
     """The same with 20, 60 and 120 rows a key head."""
     for by in ("query", "scale"):
         test_logits_past_24_bits(fmt, dim, by, top, sign, g=g)
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("g,new", [(1, 3), (3, 2), (5, 2), (2, 8)])
+@pytest.mark.parametrize("most", [150, 700])
+def test_many_items_of_each_tile(fmt, dim, g, new, most):
+    """More items than three an SM, so that an SM's groups stand in CTAs of
+    their own, for each number of tiles of four rows and each width."""
+    nseq = 120
+    ctx = [(37 * b * b + 11 * b) % most for b in range(nseq)]
+    c = Case(fmt, 4, g, dim, [1 + (b + new - 1) % new for b in range(nseq)], ctx, seed=nseq + g)
+    got = c.run()
+    assert torch.equal(got, c.run())
+    # (the reference takes one head of the first and the last key head's time)
+    heads = [0, c.hq - 1]
+    c.q, c.hq = np.ascontiguousarray(c.q[:, heads]), 2
+    c.k, c.v = (np.ascontiguousarray(x[:, [0, -1]]) for x in (c.k, c.v))
+    c.check(got[:, heads])

@@ -301,3 +301,28 @@ def test_a_bad_position_stores_a_key_of_nan(fmt, inter, dim, rot):
     assert np.isnan(k2[bad]).all()
     rest = [i for i in range(s.ntok) if i not in bad]
     assert np.array_equal(k2[rest], k[rest]) and np.array_equal(v2, v)
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
+def test_only_the_sequences_pages_are_written(fmt):
+    """Of a cache of more than 4 GiB nothing but the pages that the calls are
+    about is touched."""
+    heads, dim = 8, 256
+    each = kq.KVCache(fmt, heads, dim, 1).page_bytes
+    pages = (9 << 29) // each
+    cache = kq.KVCache(fmt, heads, dim, pages)
+    table = np.array([[pages - 1, 0, pages - 2]], np.int32)
+    b = kq.KVBatch(dev(np.array([0, 62], np.int32)), dev(np.array([66], np.int32)), dev(table), 62, 62)
+    x = torch.randn(62, heads, dim, device="cuda")
+    path = torch.full((62,), -1, dtype=torch.int32, device="cuda")
+    path[:4] = torch.tensor([0, 3, 30, 61])
+    kq.kv_append(cache, b, x, -x)
+    kq.kv_move(cache, b, path, torch.tensor([4], dtype=torch.int32, device="cuda"))
+    k, _ = kq.kv_read(cache, b)
+    y = kq.tree_attention(cache, b, torch.randn(62, 2 * heads, dim, device="cuda"))
+    assert torch.isfinite(y).all() and (k != 0).any()
+    held = cache.data.view(pages, each)
+    assert (held[0] != 0).any()
+    assert not (held[pages - 1] != 0).any() and not (held[pages - 2] != 0).any()
+    held[0] = 0  # places 66..127 are the second page's
+    assert int(cache.data.view(torch.int64).count_nonzero()) == 0
