@@ -83,8 +83,10 @@ typedef struct kq_kv {
  * t lies in page pages[b * max_pages + t / 64], token t % 64.
  *
  * Sequences whose start is not within 0..ntok in rising order, whose new
- * tokens pass max_new, or whose ctx is negative are cut to what is.  No page
- * may be written through two sequences of one call.
+ * tokens pass max_new, or whose ctx is negative are cut to what is.  (Starts
+ * that fall and rise again can give a token to two sequences; what a call
+ * writes for it is then either's.)  A call that writes the cache needs a page of
+ * its own for each entry of its tables; calls that read it do not.
  */
 typedef struct kq_batch {
     int32_t nseq;         /* 1..KQ_MAX_SEQS */
@@ -106,7 +108,9 @@ typedef struct kq_rope_scaling {
                      base * factor^(rot / (rot - 2)); 3 ramp: pairs that turn
                      more than `fast` times in `orig` positions keep theta,
                      those that turn less than `slow` times get theta /
-                     factor, those between a linear blend by their turns */
+                     factor, those between a blend that is linear in their
+                     turns (one that is linear in the pair's index, as some
+                     models have it, needs a table of the caller's) */
     int32_t orig; /* ramp: positions the model was trained on, >= 1 */
     double factor; /* > 0 (kinds 1..3) */
     double fast, slow; /* ramp: fast > slow >= 0 */
@@ -144,9 +148,10 @@ kq_status kq_rope(const float *x, int64_t stride, float *out, int64_t out_stride
  * Quantise the new tokens' keys and values into the cache at places ctx[b] +
  * j.  With a table (not NULL) the keys are rotated first, as kq_rope does,
  * with position pos[t] of each new token (in a tree of drafts that is not
- * its place).  k and v: device f32 [ntok][kv_heads][head_dim], strides
- * (multiples of 4) from token to token, 16-byte aligned.  Tokens whose place
- * has no valid page are skipped; a bad position stores a key of NaN.
+ * its place); without a table pos is not looked at.  k and v: device f32
+ * [ntok][kv_heads][head_dim], strides (multiples of 4) from token to token,
+ * 16-byte aligned.  Tokens whose place has no valid page are skipped; a bad
+ * position stores a key of NaN, all of it.
  */
 kq_status kq_kv_append(const kq_kv *kv, const kq_batch *batch, const float *k, int64_t k_stride,
                        const float *v, int64_t v_stride, const int32_t *pos, const float *table,
@@ -199,7 +204,10 @@ kq_status kq_kv_move(const kq_kv *kv, const kq_batch *batch, const int32_t *path
  * the fraction of `scale` too, rounded to f32), and so is code * scale, or a
  * probability times its value's scale, where that is formed before the product
  * (what is dropped is below 2^-22 of it, or 2^-39 of the page's largest).
- * Products are exact, sums are f32.  Logits may have any finite size.
+ * Products are exact, sums are f32.  Logits may be as large as f32 holds, as
+ * long as scale * q is finite too.  A row that attends an infinity (an f16 key
+ * or value past 65504) may be NaN where the formula gives it an infinite value
+ * or a weight of zero.
  */
 kq_status kq_tree_attention(const kq_kv *kv, const kq_batch *batch, const float *q,
                             int64_t q_stride, int q_heads, const uint64_t *mask, float scale,

@@ -23,6 +23,12 @@ int64_t q_rows(const AttnArgs &a) { return (int64_t)a.q.max_new * a.per; }
 cudaError_t of_format(int fmt, int dim, const AttnArgs &a, int sms, cudaStream_t s,
                       int64_t *floats) {
     const int64_t rows = q_rows(a);
+    // Up to 16 rows fit one block of mma.sync tiles; more are tcgen05's, but for
+    // width 256, which its tensor memory does not hold.  Measured, mma.sync /
+    // tcgen05, 16 rows (16 sequences of 16384 at most, 2 key heads of 128): 8-bit
+    // 56.2 / 72.2 us, 4-bit 58.3 / 69.6; 12 rows 47.6 / 70.2.  f16 goes the same
+    // way although 16 rows took 51.2 us with tcgen05 and 59.3 here (12 rows
+    // 50.2 / 50.5).
     if (dim <= 128 && rows > 16)
         return fmt == KQ_KV_F16  ? attn_rows_f16(dim, a, rows, sms, s, floats)
                : fmt == KQ_KV_Q8 ? attn_rows_q8(dim, a, rows, sms, s, floats)

@@ -31,7 +31,9 @@
 // quantised keys multiply the f32 sums of their group; those of values
 // multiply the probabilities' terms, whose rounding joins the lower term.
 // Each page's sums start at zero and are added to the running ones in f32,
-// with the running maximum's correction.
+// with the correction of the row's running reference, its maximum less 15.
+// (The maximum and the 15 together, taken off each logit, lost the 15 to
+// rounding past 2^24.)
 //
 // The k index inside an MMA is any order that both operands share.  A lane
 // takes eight consecutive values of a key (an octet) or 16 tokens of a value
@@ -1144,7 +1146,9 @@ cudaError_t launch_attn(AttnArgs a, int sms, cudaStream_t s, int64_t *floats) {
     // 16384 tokens at most), 512 items 33.0 / 22.3 (200), 1024 items 140 / 95.9
     // (2000).  Four / three / two CTAs: 8-bit 109 / 95.9 / 105 us (4, 6, 6
     // groups), 4-bit 96.3 / 102 / 102 (8, 6, 8), f16 - / 77.0 / 75.2 (1024 items
-    // of 1000, 3 and 4 groups).
+    // of 1000, 3 and 4 groups).  (The rule counts items and not their pages: where
+    // CTAs apart hold fewer groups in all, as with 8 bits and width 128, 6 for
+    // 7, many long items lose some.)
     const int64_t items = (int64_t)a.q.nseq * a.q.heads *
                           (((int64_t)a.q.max_new * a.per + M::kRows - 1) / M::kRows);
     AttnShape sh;

@@ -14,7 +14,12 @@
 // (scales after a power of two a page; what is dropped is below 2^-22).  A
 // thread of the four softmax warps has a row: no reduction across lanes.
 // Each page's O starts at zero and is added to the row's f32 sums in
-// registers, with the running maximum's correction.
+// registers, with the correction of the running reference, the row's maximum
+// less 15.  Queries are multiplied by the fraction of the scale as they are
+// brought in (one f32 rounding), so that scores are multiplied by powers of
+// two alone, exactly: fma(score, factor, -reference) is at most 15 whatever the
+// size of both.  (A rounded product, the maximum taken off and the result
+// multiplied by 2^15: 480 us against 418 in the 8-bit case below.)
 //
 // Blocks of up to 32 rows stand in all four quarters of the lanes, and the
 // four warps take pages by turns, each with its own maxima and sums (32..64

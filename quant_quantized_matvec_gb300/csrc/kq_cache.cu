@@ -10,11 +10,14 @@
 // largest magnitude comes from two shuffles.
 //
 // Bound by: memory in principle, 4 bytes a value on the f32 side and bits/8 on
-// the other; in fact by the issue of the arithmetic on codes (write: ALU at
-// 56%) and, for short runs, by latency.  Up to 6001 tokens of three sequences,
-// 8 heads of 128, keys rotated: 4-bit write 37.1 us (floor 18), read 25.8 (18);
-// 8-bit 36.8 and 27.6.  16 sequences of up to 300 tokens, 8 heads of 64, f16:
-// 7.9 and 5.7 us.  With five CTAs an SM and no load ahead the 8-bit write took
+// the other; in fact by the issue of the arithmetic on codes (8-bit write:
+// 70% of the issue slots, ALU at 51%) and, for short runs, by latency.  Up to
+// 6001 tokens of three sequences, 8 heads of 128, keys rotated: 4-bit write 37.2
+// us (floor 18), read 25.8 (18); 8-bit 37.0 and 27.7.  16 sequences of up to
+// 300 tokens, 8 heads of 64, f16: 7.9 and 5.8 us.  Move, 8-bit, 2 heads of 128, 1
+// / 4 / 16 tokens: 2.9 / 4.6 / 12.1 us for one sequence, 3.2 / 5.6 / 12.6 for
+// 32: a token's fetches (path, page, word) one behind the other, as one token
+// is moved after the other.  With five CTAs an SM and no load ahead the 8-bit write took
 // 39.8 us, with six 39.5.
 #include "kq_decode.cuh"
 #include "kq_decode_launch.h"
@@ -55,7 +58,9 @@ __device__ __forceinline__ Codes quantise(const float (&x)[8]) {
     inv = bad || df == 0.f ? 0.f : inv;
     const float hi = FMT == KQ_KV_Q8 ? 127.f : 7.f, lo = FMT == KQ_KV_Q8 ? -127.f : -8.f;
     // x / d rounded to nearest, by way of 1 / d: where the product is near a
-    // half, the division itself decides.  Added to 1.5 * 2^23 a number is
+    // half, the division itself decides.  (0.499 is far from what the product's
+    // error needs, below 3e-5 at 127: one value in 500 passes it, so two rounds
+    // of a warp in five divide.)  Added to 1.5 * 2^23 a number is
     // rounded to a whole one, which then stands in the low bits.
     constexpr float kWhole = 12582912.f;
     float q[8], worst = 0.f;

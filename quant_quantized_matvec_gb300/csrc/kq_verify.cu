@@ -14,9 +14,9 @@
 //
 // Bound by latency: a sequence reads two rows (1.6 MB at 202048 words) over
 // 16 SMs, after one dependent fetch of the nodes' entries.  One chain of 5
-// drafts, 202048 words, one rejection, 12400 clocks: entries 2000, r 5700 (two
-// batches of loads), the sum round the cluster 2400, the draw 800.  Measured:
-// 10.3 us (one CTA that forms r again from p and q for each pass: 134); 16
+// drafts, 202048 words, one rejection, rows not in L2, by clock64 in a copy:
+// 15700 clocks, entries 3500, r 8100 (two batches of loads), the sum round the
+// cluster 2700, the draw 1400.  Measured, rows in L2: 10.2 us (one CTA that forms r again from p and q for each pass: 134); 16
 // trees of up to 16 nodes: 21.3 us.  More loads in flight, with 1024 threads
 // a CTA: 8% less for the chain, 28% more for the trees, whose clusters then
 // have no room side by side.
@@ -35,8 +35,10 @@ constexpr int kVerifyThreads = 512;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kMostWords = KQ_MAX_VOCAB / kMaxCluster;  // of a CTA
-constexpr int kMostCtas = 304;
-constexpr int kBatch = 13;  // loads of a thread in flight
+constexpr int kMostCtas = 304;  // two an SM of this chip
+// Loads of a thread in flight, of p and of q: what 64 registers hold, two CTAs
+// an SM, and half of the 25 rounds of a warp's run at 202048 words in 16 CTAs.
+constexpr int kBatch = 13;
 
 // 0..1; NaN is 0.
 __device__ __forceinline__ float unit(float x) { return fminf(fmaxf(x, 0.f), 1.f); }

@@ -152,8 +152,8 @@ class KVBatch(_Fixed):
 def rope_table(positions, rot, base=10000.0, scaling=None, factor=1.0, orig=1, fast=32.0,
                slow=1.0, magnitude=1.0, device="cuda", stream=None):
     """(cos, sin) of positions 0..positions-1: f32 [positions, rot / 2, 2].
-    scaling for long contexts: None, "linear", "base" or "ramp"
-    (kq_rope_scaling)."""
+    scaling for long contexts: None, "linear", "base" or "ramp", a blend that
+    is linear in a pair's turns (kq_rope_scaling)."""
     if scaling not in SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(map(str, SCALINGS))}")
     if positions < 1 or rot < 2:
@@ -198,7 +198,8 @@ def rope(x, positions, table, interleaved=False, inverse=False, out=None, stream
 
 def kv_append(cache, batch, k, v, positions=None, table=None, interleaved=False, stream=None):
     """Quantise the new tokens' keys and values, f32 [ntok, kv_heads,
-    head_dim], into the cache; with a table the keys are rotated first."""
+    head_dim], into the cache; with a table the keys are rotated first, by
+    positions (which are not looked at without one)."""
     shape = (batch.ntok, cache.kv_heads, cache.head_dim)
     kp, ks = _heads(k, "k", shape)
     vp, vs = _heads(v, "v", shape)
