@@ -58,10 +58,8 @@ cudaError_t attn(int fmt, int dim, const Seqs &q, const float *x, int64_t x_stri
     a.err = err, a.wait_ns = wait_ns;
     a.suspend_ns = wait_ns < kq::kSuspendNs ? (uint32_t)wait_ns : kq::kSuspendNs;
     a.q_heads = q_heads, a.per = q_heads / q.heads;
-    const double scale2 = scale * 1.44269504088896340736;
     int e = 0;
-    a.scale = (float)scale2;
-    a.scale_m = (float)std::frexp(scale2, &e);
+    a.scale_m = (float)std::frexp(scale * 1.44269504088896340736, &e);
     a.scale_e = e;
     int64_t floats = 0;
     return of_format(fmt, dim, a, sms, s, &floats);

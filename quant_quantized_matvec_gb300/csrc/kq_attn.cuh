@@ -68,9 +68,8 @@ struct AttnArgs {
     unsigned long long wait_ns;
     uint32_t suspend_ns;  // the lesser of it and kq::kSuspendNs
     int32_t q_heads, per;  // query heads; of them to a key head
-    float scale;           // times log2 e
-    float scale_m;         // the same as scale_m * 2^scale_e, |scale_m| in 0.5..1 or 0
-    int32_t scale_e;
+    float scale_m;         // scale times log2 e = scale_m * 2^scale_e,
+    int32_t scale_e;       // |scale_m| in 0.5..1, or 0
     int32_t ng, nslot;     // groups a CTA, slots of a group's ring
 };
 
@@ -196,6 +195,12 @@ __device__ __forceinline__ void codes4(uint32_t w, uint32_t (&b)[4]) {
     b[1] = bits_of(__hfma2(half2_of(nibble(w, 0x00F000F0u, 0x64806480u)), div, off16));
     b[2] = bits_of(__hsub2(half2_of(nibble(v, 0x000F000Fu, 0x64086408u)), off));
     b[3] = bits_of(__hfma2(half2_of(nibble(v, 0x00F000F0u, 0x64806480u)), div, off16));
+}
+// The exponent of 2 in a row's factor, for queries below 2^ex that were brought
+// below 2^15: past either end the scaled query is not finite, or the logits
+// vanish.
+__device__ __forceinline__ int factor_exponent(int ex, int scale_e) {
+    return min(max(ex - 15 + scale_e, -126), 127);
 }
 template <int THREADS>
 __device__ __forceinline__ void group_sync(int g) {
@@ -489,9 +494,8 @@ __global__ void __launch_bounds__(AttnSmem<FMT, D, NT>::kGroups * AttnSmem<FMT, 
             const int ex = max((int)((__float_as_uint(top) >> 23) & 255) - 126, -111);
             const float up = __uint_as_float((uint32_t)(127 + 15 - ex) << 23);
             if (lane == 0) {
-                // (2^(ex - 15) in two steps: it may be below the normal range)
-                cm.rowfactor[r] = a.scale * __uint_as_float((uint32_t)(127 + (ex >> 1)) << 23) *
-                                  __uint_as_float((uint32_t)(127 + (ex - (ex >> 1)) - 15) << 23);
+                cm.rowfactor[r] = a.scale_m *
+                                  __uint_as_float((uint32_t)(127 + factor_exponent(ex, a.scale_e)) << 23);
                 cm.rowmask[r] = !on ? 0
                                 : a.mask ? __ldg(a.mask + s.first + tok)
                                          : ~0ull >> (63 - tok);

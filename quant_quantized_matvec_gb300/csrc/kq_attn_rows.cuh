@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             // and their product with it exact.
             const float up = a.scale_m * __uint_as_float((uint32_t)(127 + 15 - ex) << 23);
             const float rowf =
-                __uint_as_float((uint32_t)(127 + min(max(ex - 15 + a.scale_e, -126), 127)) << 23);
+                __uint_as_float((uint32_t)(127 + factor_exponent(ex, a.scale_e)) << 23);
             const uint64_t nw = (!on      ? 0
                                  : a.mask ? __ldg(a.mask + g.s.first + tok)
                                           : ~0ull >> (63 - tok)) &

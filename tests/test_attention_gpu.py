@@ -578,3 +578,14 @@ def test_many_items_of_each_tile(fmt, dim, g, new, most):
     c.q, c.hq = np.ascontiguousarray(c.q[:, heads]), 2
     c.k, c.v = (np.ascontiguousarray(x[:, [0, -1]]) for x in (c.k, c.v))
     c.check(got[:, heads])
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
+@pytest.mark.parametrize("dim,g", [(64, 2), (128, 7), (256, 4), (64, 20), (128, 50)])
+@pytest.mark.parametrize("scale", [3e38, -3e38, 1e-38])
+def test_scales_at_the_ends_of_f32(fmt, dim, g, scale):
+    """Any finite scale, as long as its product with a query is finite."""
+    scale = float(np.float32(scale))
+    c = Case(fmt, 1, g, dim, [2], [200], seed=24, spread=0.25 / abs(scale))
+    got = c.run(scale=scale)
+    c.check(got, c.want(scale=scale))
