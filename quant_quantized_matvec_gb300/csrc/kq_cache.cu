@@ -10,15 +10,15 @@
 // largest magnitude comes from two shuffles.
 //
 // Bound by: memory in principle, 4 bytes a value on the f32 side and bits/8 on
-// the other; in fact by the issue of the arithmetic on codes (8-bit write:
-// 70% of the issue slots, ALU at 51%) and, for short runs, by latency.  Up to
-// 6001 tokens of three sequences, 8 heads of 128, keys rotated: 4-bit write 37.2
-// us (floor 18), read 25.8 (18); 8-bit 37.0 and 27.7.  16 sequences of up to
-// 300 tokens, 8 heads of 64, f16: 7.9 and 5.8 us.  Move, 8-bit, 2 heads of 128, 1
+// the other; in fact by the issue of the arithmetic on codes (8-bit write: 70%
+// of the issue slots, ALU at 51%) and, for short runs, by latency.  Up to 6001
+// tokens of three sequences, 8 heads of 128, keys rotated: 4-bit write 37.2 us
+// (floor 18), read 25.8 (18); 8-bit 37.0 and 27.7.  16 sequences of up to 300
+// tokens, 8 heads of 64, f16: 7.9 and 5.8 us.  Move, 8-bit, 2 heads of 128, 1
 // / 4 / 16 tokens: 2.9 / 4.6 / 12.1 us for one sequence, 3.2 / 5.6 / 12.6 for
 // 32: a token's fetches (path, page, word) one behind the other, as one token
-// is moved after the other.  With five CTAs an SM and no load ahead the 8-bit write took
-// 39.8 us, with six 39.5.
+// is moved after the other.  With five CTAs an SM and no load ahead the 8-bit
+// write took 39.8 us, with six 39.5.
 #include "kq_decode.cuh"
 #include "kq_decode_launch.h"
 

@@ -12,14 +12,15 @@
 // come with r's total are the draw's first two levels: only the warp whose run
 // holds the goal looks at words again.
 //
-// Bound by latency: a sequence reads two rows (1.6 MB at 202048 words) over
-// 16 SMs, after one dependent fetch of the nodes' entries.  One chain of 5
+// Bound by latency: a sequence reads two rows (1.6 MB at 202048 words) over 16
+// SMs, after one dependent fetch of the nodes' entries.  One chain of 5
 // drafts, 202048 words, one rejection, rows not in L2, by clock64 in a copy:
 // 15700 clocks, entries 3500, r 8100 (two batches of loads), the sum round the
-// cluster 2700, the draw 1400.  Measured, rows in L2: 10.2 us (one CTA that forms r again from p and q for each pass: 134); 16
-// trees of up to 16 nodes: 21.3 us.  More loads in flight, with 1024 threads
-// a CTA: 8% less for the chain, 28% more for the trees, whose clusters then
-// have no room side by side.
+// cluster 2700, the draw 1400.  Measured, rows in L2: 10.2 us (one CTA that
+// forms r again from p and q for each pass: 134); 16 trees of up to 16 nodes:
+// 21.3 us.  More loads in flight, with 1024 threads a CTA: 8% less for the
+// chain, 28% more for the trees, whose clusters then have no room side by
+// side.
 #include <cooperative_groups.h>
 
 #include <mutex>
