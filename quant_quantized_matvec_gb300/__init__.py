@@ -11,7 +11,8 @@ their dtype/shape/device, and pass raw pointers through.
 
 The rest of a decode step (decode.py, include/kq_decode.h): rope, the
 quantised KVCache with kv_append / kv_read / kv_move, tree_attention over
-it, and verify_tree for drafted tokens.
+it, and verify_tree for drafted tokens.  A prompt (prompt.py,
+include/kq_prompt.h): norm_rope, prompt_attention, token_logprobs.
 """
 from __future__ import annotations
 
@@ -230,16 +231,23 @@ def device_error(clear: bool = True) -> bool:
     return st == KQ_ERR_TIMEOUT
 
 
-# The decode step's other operators; decode.py needs torch, which this module
-# only imports when a function that takes tensors is called.
+# The decode step's other operators and a prompt's; decode.py and prompt.py need
+# torch, which this module only imports when a function that takes tensors is
+# called.
 _DECODE = ("KV_F16", "KV_Q4", "KV_Q8", "KV_PAGE", "MAX_DRAFT", "KVCache", "KVBatch", "rope_table",
            "rope", "kv_append", "kv_read", "kv_move", "tree_mask", "tree_attention",
            "attention_workspace_bytes", "verify_tree")
+_PROMPT = ("MAX_TOP", "norm_rope", "prompt_attention", "prompt_workspace_bytes", "token_logprobs")
 
 
 def __getattr__(name):
-    if name not in _DECODE:
+    if name in _DECODE:
+        from . import decode as module
+        names = _DECODE
+    elif name in _PROMPT:
+        from . import prompt as module
+        names = _PROMPT
+    else:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    from . import decode
-    globals().update((n, getattr(decode, n)) for n in _DECODE)
+    globals().update((n, getattr(module, n)) for n in names)
     return globals()[name]

@@ -29,6 +29,10 @@ SYMBOLS = ("kq_block_bytes", "kq_matrix_bytes", "kq_matvec",
 DECODE_SYMBOLS = ("kq_kv_page_bytes", "kq_rope_table", "kq_rope", "kq_kv_append", "kq_kv_read",
                   "kq_kv_move", "kq_tree_attention", "kq_attn_workspace_bytes", "kq_verify_tree")
 
+# include/kq_prompt.h
+PROMPT_SYMBOLS = ("kq_norm_rope", "kq_prompt_attention", "kq_prompt_workspace_bytes",
+                  "kq_token_logprobs")
+
 
 class KqMat(ctypes.Structure):
     """Mirror of `kq_mat` in include/kq.h."""
@@ -77,6 +81,19 @@ class KqRopeScaling(ctypes.Structure):
         ("fast", ctypes.c_double),
         ("slow", ctypes.c_double),
         ("magnitude", ctypes.c_double),
+    ]
+
+
+class KqNormPart(ctypes.Structure):
+    """Mirror of `kq_norm_part` in include/kq_prompt.h."""
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("stride", ctypes.c_int64),
+        ("weight", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("out_stride", ctypes.c_int64),
+        ("heads", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
     ]
 
 
@@ -153,8 +170,16 @@ def load(path: str | None = None):
                                           vp]
         lib.kq_verify_tree.argtypes = [i32, i64, i32, vp, vp, vp, vp, i64, vp, i64, i32, vp, vp,
                                        vp, vp, vp, vp]
+        lib.kq_norm_rope.argtypes = [ctypes.POINTER(KqNormPart), i32, i32, i32, i64, i32,
+                                     ctypes.c_float, vp, vp, i64, i32, i32, vp]
+        lib.kq_prompt_workspace_bytes.argtypes = [i32, i32, i64, i64, i32, i32, i32]
+        lib.kq_prompt_workspace_bytes.restype = i64
+        lib.kq_prompt_attention.argtypes = [i32, i32, i64, i64, vp, vp, vp, i64, i32, vp, i64, vp,
+                                            i64, i32, i32, ctypes.c_float, vp, vp, i64, vp]
+        lib.kq_token_logprobs.argtypes = [i32, i64, i32, vp, i64, vp, i32, vp, vp, vp, vp, vp]
         for name in ("kq_rope_table", "kq_rope", "kq_kv_append", "kq_kv_read", "kq_kv_move",
-                     "kq_tree_attention", "kq_verify_tree"):
+                     "kq_tree_attention", "kq_verify_tree", "kq_norm_rope", "kq_prompt_attention",
+                     "kq_token_logprobs"):
             getattr(lib, name).restype = i32
         if path is None:
             _lib = lib

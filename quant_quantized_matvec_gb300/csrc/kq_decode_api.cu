@@ -10,44 +10,15 @@
 #include "kq_decode_launch.h"
 #include "kq_host.h"
 
-using kqhost::meet;
-using kqhost::Span;
-using kqhost::span;
+using kqhost::aligned;
+using kqhost::launched;
+using kqhost::Pointers;
 
 namespace {
 
 constexpr int64_t kMaxCount = 1 << 24;      // tokens, pages of a table, positions of a step
 constexpr int64_t kMaxPositions = 1 << 28;  // of a rotary table
 constexpr int64_t kMaxStride = 1LL << 32;
-
-bool aligned(const void *p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
-
-// Pointers of a call, for the alias and memory checks.
-struct Pointers {
-    Span in[12], out[4];
-    const void *p[16];
-    int ni = 0, no = 0, np = 0;
-    void read(const void *q, int64_t bytes) { in[ni++] = span(q, bytes), p[np++] = q; }
-    void write(const void *q, int64_t bytes) { out[no++] = span(q, bytes), p[np++] = q; }
-    kq_status check() const {
-        for (int i = 0; i < no; ++i) {
-            for (int j = 0; j < ni; ++j)
-                if (meet(out[i], in[j])) return KQ_ERR_ALIAS;
-            for (int j = 0; j < i; ++j)
-                if (meet(out[i], out[j])) return KQ_ERR_ALIAS;
-        }
-        int dev = 0;
-        const cudaError_t e = cudaGetDevice(&dev);
-        if (e != cudaSuccess) return kqhost::cuda_failed(e);
-        for (int i = 0; i < np; ++i) {
-            const kq_status s = kqhost::on_device(p[i], dev);
-            if (s != KQ_OK) return s;
-        }
-        return KQ_OK;
-    }
-};
-
-kq_status launched(cudaError_t e) { return e == cudaSuccess ? KQ_OK : kqhost::cuda_failed(e); }
 
 kq_status check_kv(const kq_kv *kv) {
     if (!kv) return KQ_ERR_NULL;

@@ -1,0 +1,837 @@
+// kq_prompt_attn.cuh -- attention of whole prompts (kq_prompt_attention): what
+// its kernels share, and the kernel that takes every type and width.
+//
+//   out_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = 2^(s_ij - m_i),  j <= limit of i
+//
+// Work: an item is up to 128 rows that share a key head, T tokens of a
+// sequence by the query heads of the group (head fastest), so that few tokens
+// fill a tile where heads are shared.  A sequence's last items come first, as
+// they are the longest.  An item goes over its keys from the last to the first
+// in tiles, with the running maximum m and sum of a softmax; where there are
+// fewer items than SMs the keys are cut into parts, whose results are joined by
+// a second kernel.
+//
+// The rows are the 128 lanes of an accumulator, a thread each.  Queries and
+// probabilities are the first operand, in tensor memory, keys and values the
+// second, in shared memory.  A tile's S = Q K is formed ahead in one of two
+// buffers; the softmax warps turn it into P in place; O = P V of the tile
+// starts at zero and is added to the row's f32 sums in registers, by warps of
+// their own, with the correction of the running maximum: the sums are rounded
+// to nearest, whatever the tensor core's additions do over thousands of steps.
+//
+// f32 (two f16 terms hi + lo, after a scaling by a power of two):
+//   S = Qlo Khi + Qhi Klo + Qhi Khi,  O = Plo Vhi + Phi Vlo + Phi Vhi
+// the small products first, as the tensor core cuts its sums off at each step
+// (4097 keys of width 128, off by 4.9e-7 in all; the other order 1.8e-6).
+// Keys and values are split once, by a kernel before, into tiles as the
+// products take them (a sequence's 64 or 32 tokens of a head, zeros past its
+// end), with the tile's powers of two.  The query is multiplied by scale *
+// log2(e) in f32 first, so that what follows only multiplies by powers of two,
+// and the difference to the maximum is one rounding, however large both are.
+//
+// 16-bit types are copied as they are, by tensor copies.  Probabilities that
+// become f16 are held times 2^15, as f16 has few bits below 2^-14.
+//
+// NaN and infinities must not reach rows that do not attend them (0 * inf):
+// values that are not finite are zeros in the tile (f32: all tiles; 16 bits:
+// those that some row sees in part), and rows that attend them add them in the
+// end.
+#pragma once
+
+#include <cuda.h>
+
+#include <atomic>
+#include <type_traits>
+
+#include "kq_decode.cuh"
+#include "kq_host.h"
+#include "kq_prompt_launch.h"
+#include "kq_tc5.cuh"
+#include "kq_types.cuh"
+
+namespace kqp {
+
+using kqd::quiet_nan;
+
+constexpr int kRows = 128;  // rows of an item
+constexpr float kLog2E = 1.44269504088896340736f;
+
+// Powers of two of a tile of an f32 call, and whether its values had some that
+// are not finite.
+struct TileInfo {
+    int ek;    // keys = stored * 2^ek
+    float vf;  // values * 2^-15 = stored * vf
+    int bad, pad;
+};
+
+struct PromptArgs {
+    CUtensorMap qmap, kmap, vmap;  // 16-bit types
+    const int32_t *start, *kstart;
+    const void *q, *v;
+    int64_t q_stride, k_stride, v_stride;
+    const void *k;
+    void *out;
+    uint8_t *tiles;  // f32: [slot][kv_heads][tile]
+    TileInfo *info;  // f32: [slot][kv_heads]
+    float *part;     // splits > 1
+    int32_t nseq, ntok, nkeys, q_heads, kv_heads;
+    int32_t per;      // query heads of a key head
+    int32_t hb;       // of them in an item
+    int32_t hblocks;  // runs of hb heads
+    int32_t tok;      // tokens of an item
+    int32_t splits;
+    int32_t items;    // items in all, at most
+    float scale;      // with its sign
+    unsigned int *err;
+    unsigned long long wait_ns;
+    uint32_t suspend_ns;
+};
+
+// A run of rows and the keys they see, as all threads of a CTA read it.
+struct Item {
+    int seq, first, n, kfirst, m;  // the sequence, its tokens and keys
+    int tok0, nt;                  // the item's tokens, of the sequence's
+    int head, hq, nh;              // key head; first query head, how many
+    int found;
+
+    // Row r: its token (of the sequence) and head (of the item).
+    __device__ __forceinline__ bool row(int hb, int r, int &t, int &h) const {
+        t = r / hb, h = r - t * hb;
+        t += tok0;
+        return t < tok0 + nt && h < nh;
+    }
+    // The last key that token t attends; keys that the item attends.
+    __device__ __forceinline__ int limit(int t) const { return m - n + t; }
+    __device__ __forceinline__ int keys() const { return max(0, min(m, m - n + tok0 + nt)); }
+};
+
+__device__ __forceinline__ int scan_max(int x, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int v = __shfl_up_sync(~0u, x, o);
+        if (lane >= o) x = max(x, v);
+    }
+    return x;
+}
+
+// Walks the sequences, 32 at a time: body(b, first token, end, first key, key
+// end) for each lane's sequence (an empty one past the last), until it returns
+// true.  A start counts as the largest so far, within what there is.  By one
+// warp.
+template <class F>
+__device__ __forceinline__ void walk(const PromptArgs &a, int lane, F &&body) {
+    int s_before = 0, k_before = 0;
+    for (int b0 = 0; b0 < a.nseq; b0 += 32) {
+        const int b = min(b0 + lane, a.nseq), b1 = min(b + 1, a.nseq);
+        auto runs = [&](const int32_t *start, int all, int &before, int &lo, int &hi) {
+            lo = max(scan_max(min(max(__ldg(start + b), 0), all), lane), before);
+            hi = max(lo, min(max(__ldg(start + b1), 0), all));
+            before = __shfl_sync(~0u, hi, 31);
+        };
+        int lo, hi, klo, khi;
+        runs(a.start, a.ntok, s_before, lo, hi);
+        if (a.kstart) runs(a.kstart, a.nkeys, k_before, klo, khi);
+        else klo = lo, khi = hi;
+        if (body(b, lo, hi, klo, khi)) return;
+    }
+}
+
+// Item `i` of the call into shared memory, by warp 0; found = 0 past the last.
+__device__ __forceinline__ void find_item(const PromptArgs &a, int i, Item &it, int lane) {
+    const int across = a.kv_heads * a.hblocks;
+    const int blk = i / across, h = i - blk * across;
+    if (lane == 0) it.found = 0;
+    __syncwarp();
+    int before = 0;
+    walk(a, lane, [&](int b, int lo, int hi, int klo, int khi) {
+        const int blocks = (hi - lo + a.tok - 1) / a.tok;
+        int upto = blocks;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int v = __shfl_up_sync(~0u, upto, o);
+            if (lane >= o) upto += v;
+        }
+        upto += before;
+        const unsigned past = __ballot_sync(~0u, upto > blk);
+        before = __shfl_sync(~0u, upto, 31);
+        if (past == 0) return false;
+        if (lane == __ffs(past) - 1) {
+            const int at = upto - 1 - blk;  // the last block first
+            it.seq = b, it.first = lo, it.n = hi - lo, it.kfirst = klo, it.m = khi - klo;
+            it.tok0 = at * a.tok, it.nt = min(a.tok, it.n - it.tok0);
+            it.head = h / a.hblocks;
+            const int run = h - it.head * a.hblocks;
+            it.hq = it.head * a.per + run * a.hb, it.nh = min(a.hb, a.per - run * a.hb);
+            it.found = 1;
+        }
+        return true;
+    });
+    __syncwarp();
+}
+
+// 32-bit words of two 16-bit values of which one is not finite.
+template <class T>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+    constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7C007C00u : 0x7F807F80u;
+    constexpr uint32_t kOne = std::is_same<T, __half>::value ? 0x04000400u : 0x00800080u;
+    return ((w & kExp) + kOne) & 0x80008000u;  // the exponent's carry
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Two f16 terms of two values, as pairs (what is not finite has no lo).
+__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
+    hi = pack2<__half>(a, b);
+    const float2 f = unpack2<__half>(hi);
+    lo = pack2<__half>(a - f.x, b - f.y);
+}
+
+// ------------------------------------------------------- splitting f32
+// The largest finite magnitude's exponent e: it is below 2^e.
+__device__ __forceinline__ int exponent_of(float top, int least) {
+    return max((int)(__float_as_uint(top) >> 23 & 255) - 126, least);
+}
+
+// Bytes of a tile's keys, or values, of both terms.
+__host__ __device__ constexpr int f32_tile_tokens(int d) { return d == 256 ? 32 : 64; }
+constexpr int kSplitThreads = 256;
+
+// One CTA per slot, head, and keys or values: 64 (32) tokens of a sequence into
+// hi and lo tiles.  A sequence's slots begin at first key / tokens + its number.
+template <int D>
+__global__ void __launch_bounds__(kSplitThreads)
+    kq_prompt_split(const __grid_constant__ PromptArgs a) {
+    constexpr int TK = f32_tile_tokens(D), kPart = TK * D * 4;
+    constexpr int kEach = TK * D / 4 / kSplitThreads;  // float4 of a thread
+    __shared__ int found[4];
+    __shared__ uint32_t tops;
+    __shared__ int bad;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int slot = blockIdx.x, head = blockIdx.y;
+    const bool values = blockIdx.z != 0;
+    kq::allow_dependents();
+    if (tid == 0) found[0] = 0, tops = 0, bad = 0;
+    if (tid < 32) {
+        __syncwarp();
+        walk(a, lane, [&](int b, int lo, int hi, int klo, int khi) {
+            const int base = klo / TK + b, tiles = b < a.nseq ? (khi - klo + TK - 1) / TK : 0;
+            const bool here = slot >= base && slot < base + tiles;
+            if (here) found[1] = klo + (slot - base) * TK, found[2] = min(TK, khi - found[1]), found[0] = 1;
+            return __any_sync(~0u, here) != 0;
+        });
+    }
+    __syncthreads();
+    if (!found[0]) return;
+    const int first = found[1], held = found[2];
+    const float *x = static_cast<const float *>(values ? a.v : a.k);
+    const int64_t stride = values ? a.v_stride : a.k_stride;
+    float4 v[kEach];
+    float top = 0.f;
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int at = tid + i * kSplitThreads, t = at / (D / 4), e = at % (D / 4);
+        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t < held)
+            v[i] = __ldg(reinterpret_cast<const float4 *>(x + (int64_t)(first + t) * stride +
+                                                          (int64_t)head * D) + e);
+        float *f = &v[i].x;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float m = fabsf(f[k]);
+            if (m < INFINITY) {
+                top = fmaxf(top, m);
+            } else {
+                odd = true;
+                if (values) f[k] = 0.f;
+            }
+        }
+    }
+    const uint32_t most = __reduce_max_sync(~0u, __float_as_uint(top));
+    const bool any = __any_sync(~0u, odd);
+    if (lane == 0) {
+        atomicMax(&tops, most);
+        if (any) atomicOr(&bad, 1);
+    }
+    __syncthreads();
+    // (values' least: their factor is 2^-15 smaller)
+    const int ex = exponent_of(__uint_as_float(tops), values ? -96 : -111);
+    const float up = __uint_as_float((uint32_t)(127 + 15 - ex) << 23);
+    uint8_t *to = a.tiles + ((int64_t)slot * a.kv_heads + head) * (2 * kPart) + (values ? kPart : 0);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int at = tid + i * kSplitThreads, t = at / (D / 4), e = at % (D / 4);
+        uint2 hi, lo;
+        split2(v[i].x * up, v[i].y * up, hi.x, lo.x);
+        split2(v[i].z * up, v[i].w * up, hi.y, lo.y);
+        if (odd) {  // (inf - inf)
+            lo.x = lo.x & (not_finite<__half>(hi.x) ? 0u : ~0u);
+            lo.y = lo.y & (not_finite<__half>(hi.y) ? 0u : ~0u);
+        }
+        uint8_t *p = to + (e / 16) * (TK * 128) + tile_at(t, (e % 16) / 2) + (e & 1) * 8;
+        *reinterpret_cast<uint2 *>(p) = hi;
+        *reinterpret_cast<uint2 *>(p + kPart / 2) = lo;
+    }
+    TileInfo *info = a.info + (int64_t)slot * a.kv_heads + head;
+    if (tid == 0) {
+        if (values) info->vf = __uint_as_float((uint32_t)(127 + ex - 30) << 23), info->bad = bad;
+        else info->ek = ex - 15;
+    }
+}
+
+// --------------------------------------------------- any type and width
+template <class T, int D>
+struct Rows {
+    static constexpr bool kTwo = std::is_same<T, float>::value;  // terms
+    using H = typename std::conditional<kTwo, __half, T>::type;  // of the products
+    static constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    static constexpr int TK = kTwo ? f32_tile_tokens(D) : 64;
+    static constexpr int kTerm = TK * D * 2;                 // one term of a tile's keys or values
+    static constexpr int kPart = kTerm * (kTwo ? 2 : 1);
+    // columns of tensor memory: Q (lo in shared memory at width 256), S and P, O
+    static constexpr bool kLoShared = kTwo && D == 256;
+    static constexpr int kQCols = kTwo && !kLoShared ? D : D / 2;
+    static constexpr int kS = kQCols, kO = kS + 2 * TK;
+    static constexpr int OB = kO + 2 * D <= 512 ? 2 : 1;     // buffers of O
+    static constexpr int OW = D == 256 ? 8 : 4;              // warps that sum O
+    static constexpr int OC = D * 4 / OW;                    // columns of each
+    static constexpr int kThreads = 32 * (4 + OW + 4);
+    static constexpr int kFirst = 4 + OW;                    // MMA, copies, two that clean
+    static constexpr int kControl = 4096, kQLo = kLoShared ? kRows * D * 2 : 0;
+    static constexpr int kRing = kControl + kQLo;
+    static constexpr int kRoom = (227 * 1024 - 1024 - kRing) / kPart;
+    static constexpr int kSlots = kRoom < 8 ? kRoom : 8;
+    static constexpr int kBytes = kRing + kSlots * kPart + 1024;
+    static_assert(kO + OB * D <= 512 && kSlots >= 4, "layout");
+};
+
+struct RowsShared {
+    Item item;
+    uint64_t full[8], empty[8], sdone[2], pready[2], odone[2], ofree[2], cready[4], vclean[4], ldone, drain;
+    uint32_t tmem;
+    int dead, bad;
+    float corr[4][kRows];  // of tile i & 3: the factor of what was summed before
+    float m[kRows], l[kRows];
+};
+static_assert(sizeof(RowsShared) <= 4096, "layout");
+
+template <class T, int D>
+__global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
+    kq_prompt_rows(const __grid_constant__ PromptArgs a) {
+    using M = Rows<T, D>;
+    using H = typename M::H;
+    constexpr bool kTwo = M::kTwo;
+    constexpr int TK = M::TK, OB = M::OB;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024 - (kq::smem_addr(smem_raw) & 1023)) & 1023);
+    RowsShared &cm = *reinterpret_cast<RowsShared *>(smem);
+    const uint32_t base = kq::smem_addr(smem);
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    auto bar = [&](const uint64_t &b) { return kq::smem_addr(&b); };
+
+    const int rank = blockIdx.x % a.splits;
+    if (w == 0) {
+        find_item(a, blockIdx.x / a.splits, cm.item, lane);
+    } else if (tid == 32) {
+        for (int i = 0; i < 8; ++i) kq::mbar_init(bar(cm.full[i]), 1), kq::mbar_init(bar(cm.empty[i]), 1);
+        for (int i = 0; i < 2; ++i) {
+            kq::mbar_init(bar(cm.sdone[i]), 1);
+            kq::mbar_init(bar(cm.pready[i]), 4);
+            kq::mbar_init(bar(cm.odone[i]), 1);
+            kq::mbar_init(bar(cm.ofree[i]), M::OW);
+        }
+        for (int i = 0; i < 4; ++i) kq::mbar_init(bar(cm.cready[i]), 4), kq::mbar_init(bar(cm.vclean[i]), 2);
+        kq::mbar_init(bar(cm.ldone), kTwo ? 4 : 6);
+        kq::mbar_init(bar(cm.drain), 1);
+        cm.dead = cm.bad = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    const Item it = cm.item;
+    if (!it.found) return;
+    if (w == M::kFirst) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                         kq::smem_addr(&cm.tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = cm.tmem;
+
+    auto dead = [&]() { return *(volatile int *)&cm.dead != 0; };
+    auto wait = [&](const uint64_t &b, int phase) {  // the completion of the barrier's phase
+        if (kq::mbar_test(bar(b), phase & 1) || dead()) return;
+        if (!kq::mbar_wait_for(bar(b), phase & 1, a.wait_ns, a.suspend_ns)) {
+            *(volatile int *)&cm.dead = 1;
+            atomicOr(a.err, 1u);
+        }
+    };
+
+    // The item's tiles, its last first: tile i of the walk is tile t1 - 1 - i
+    // of the sequence.  The first `edges` of them some row sees in part.
+    const int tiles = (it.keys() + TK - 1) / TK;
+    const int t0 = (int)((int64_t)tiles * rank / a.splits);
+    const int t1 = (int)((int64_t)tiles * (rank + 1) / a.splits);
+    const int count = t1 - t0;
+    const int whole = max(0, it.limit(it.tok0) + 1) / TK;  // tiles that every row sees
+    const int edges = min(max(t1 - max(whole, t0), 0), count);
+    const int64_t slot0 = kTwo ? (int64_t)(it.kfirst / TK + it.seq) * a.kv_heads + it.head : 0;
+
+    if constexpr (kTwo) kq::wait_prerequisites();  // the tiles
+    int copied = 0;  // copies that were begun
+
+    if (w < 4) {
+        // ------------------------------------------------- softmax warps
+        const int r = 32 * w + lane;
+        int tok, hq;
+        const bool on = it.row(a.hb, r, tok, hq);
+        const uint32_t mine = tmem + ((uint32_t)(32 * w) << 16);
+        int ex = 0;
+        {   // ---- the row's query into tensor memory
+            const T *x = static_cast<const T *>(a.q) + (int64_t)(it.first + tok) * a.q_stride +
+                         (int64_t)(it.hq + hq) * D;
+            if constexpr (kTwo) {
+                const float4 *x4 = reinterpret_cast<const float4 *>(x);
+                const float sc = a.scale * kLog2E;
+                float top = 0.f;
+                for (int i = 0; i < D / 4; ++i) {
+                    const float4 v = on ? __ldg(x4 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    top = fmaxf(top, fmaxf(fmaxf(fabsf(v.x * sc), fabsf(v.y * sc)),
+                                           fmaxf(fabsf(v.z * sc), fabsf(v.w * sc))));
+                }
+                ex = exponent_of(top, -111);
+                const float up = __uint_as_float((uint32_t)(127 + 15 - ex) << 23);
+#pragma unroll 1
+                for (int i = 0; i < D / 32; ++i) {
+                    uint32_t hi[16], lo[16];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float4 v = on ? __ldg(x4 + 8 * i + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        split2(v.x * sc * up, v.y * sc * up, hi[2 * k], lo[2 * k]);
+                        split2(v.z * sc * up, v.w * sc * up, hi[2 * k + 1], lo[2 * k + 1]);
+                    }
+                    tc_store16(mine + 16 * i, hi);
+                    if constexpr (M::kLoShared) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            *reinterpret_cast<uint4 *>(smem + M::kControl + (i / 2) * (kRows * 128) +
+                                                       tile_at(r, (i & 1) * 4 + k)) =
+                                make_uint4(lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
+                    } else {
+                        tc_store16(mine + D / 2 + 16 * i, lo);
+                    }
+                }
+                if constexpr (M::kLoShared) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            } else {
+                const uint4 *x8 = reinterpret_cast<const uint4 *>(x);
+                const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;
+#pragma unroll 1
+                for (int i = 0; i < D / 32; ++i) {
+                    uint32_t q[16];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint4 v = on ? __ldg(x8 + 4 * i + k) : make_uint4(0, 0, 0, 0);
+                        q[4 * k] = v.x ^ sign, q[4 * k + 1] = v.y ^ sign;
+                        q[4 * k + 2] = v.z ^ sign, q[4 * k + 3] = v.w ^ sign;
+                    }
+                    tc_store16(mine + 16 * i, q);
+                }
+            }
+            tc_stored();
+            tc_before();
+        }
+        __syncthreads();
+        const int limit = on ? it.limit(tok) : -1;
+        const float factor = fabsf(a.scale) * kLog2E;  // (16-bit types)
+        constexpr float kUp = M::kBf16 ? 0.f : 15.f;
+        const TileInfo *info = nullptr;
+        int ek = 0;
+        if constexpr (kTwo) {
+            info = a.info + slot0;
+            if (count) ek = __ldg(&info[(int64_t)(t1 - 1) * a.kv_heads].ek);
+        }
+        float m = -INFINITY, l = 0.f;
+        for (int i = 0; i < count; ++i) {
+            const int t = t1 - 1 - i;
+            float f = 1.f;
+            if constexpr (kTwo) {
+                f = __uint_as_float((uint32_t)(127 + min(max(ex - 15 + ek, -126), 127)) << 23);
+                if (i + 1 < count) ek = __ldg(&info[(int64_t)(t - 1) * a.kv_heads].ek);
+            }
+            wait(cm.sdone[i & 1], i >> 1);
+            tc_after();
+            uint32_t d[TK];
+            const uint32_t sa = mine + M::kS + TK * (i & 1);
+#pragma unroll
+            for (int k = 0; k < TK / 32; ++k) tc_load32(d + 32 * k, sa + 32 * k);
+            tc_loaded();
+            const int seen = i < edges ? limit + 1 - t * TK : TK;  // columns that the row attends
+            if (i < edges) {
+#pragma unroll
+                for (int k = 0; k < TK; ++k)
+                    if (k >= seen) d[k] = 0xFF800000u;
+            }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int k = 0; k < TK; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(d[k]));
+            mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            // The reference: f32, the maximum less 15, rounded up (it is in
+            // units of log 2); 16 bits, the maximum of the scores themselves.
+            float corr;
+            if constexpr (kTwo) {
+                const float now = fmaxf(m, mx[0] == -INFINITY ? mx[0] : __fsub_ru(mx[0] * f, 15.f));
+                corr = exp2_fast(m - (now == -INFINITY ? 0.f : now));
+                m = now;
+            } else {
+                const float now = fmaxf(m, mx[0]);
+                corr = now == m ? 1.f : m == -INFINITY ? 0.f : exp2_fast((m - now) * factor);
+                m = now;
+            }
+            const float from = m == -INFINITY ? 0.f : m;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < TK; ++k) {
+                const float s = __uint_as_float(d[k]);
+                float p = exp2_fast(kTwo ? fmaf(s, f, -from) : fmaf(s - from, factor, kUp));
+                if (i < edges && k >= seen) p = 0.f;
+                sum[k & 3] += p;
+                d[k] = __float_as_uint(p);
+            }
+            l = fmaf(l, corr, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+            cm.corr[i & 3][r] = corr;
+#pragma unroll
+            for (int k = 0; k < TK / 32; ++k) {
+                uint32_t hi[16], lo[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float p0 = __uint_as_float(d[32 * k + 2 * j]), p1 = __uint_as_float(d[32 * k + 2 * j + 1]);
+                    if constexpr (kTwo) split2(p0, p1, hi[j], lo[j]);
+                    else hi[j] = pack2<H>(p0, p1);
+                }
+                tc_store16(sa + 16 * k, hi);
+                if constexpr (kTwo) tc_store16(sa + TK / 2 + 16 * k, lo);
+            }
+            tc_stored();
+            tc_before();
+            __syncwarp();
+            if (lane == 0) {
+                kq::mbar_arrive(bar(cm.pready[i & 1]));
+                kq::mbar_arrive(bar(cm.cready[i & 3]));
+            }
+        }
+        cm.m[r] = m;
+        cm.l[r] = l;
+        __syncwarp();
+        if (lane == 0) kq::mbar_arrive(bar(cm.ldone));
+    } else if (w < M::kFirst) {
+        // ------------------------------------------- the sums of O, and out
+        if constexpr (D == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+        __syncthreads();
+        const int r = 32 * (w & 3) + lane, c0 = (w - 4) / 4 * M::OC;
+        const uint32_t mine = tmem + ((uint32_t)(32 * (w & 3)) << 16) + M::kO + c0;
+        int tok, hq;
+        const bool on = it.row(a.hb, r, tok, hq);
+        float O[M::OC];
+#pragma unroll
+        for (int k = 0; k < M::OC; ++k) O[k] = 0.f;
+        bool bad = false;
+        const TileInfo *info = kTwo ? a.info + slot0 : nullptr;
+        float vf = 1.f;
+        int vbad = 0;
+        auto look = [&](int i) {
+            if constexpr (kTwo) {
+                const TileInfo *p = info + (int64_t)(t1 - 1 - i) * a.kv_heads;
+                vf = __ldg(&p->vf), vbad = __ldg(&p->bad);
+            }
+        };
+        if (count) look(0);
+        for (int i = 0; i < count; ++i) {
+            const float f = vf;
+            bad |= vbad != 0;
+            if (i + 1 < count) look(i + 1);
+            wait(cm.cready[i & 3], i >> 2);
+            const float corr = cm.corr[i & 3][r];
+            wait(cm.odone[i % OB], i / OB);
+            tc_after();
+            const uint32_t at = mine + (i % OB) * D;
+#pragma unroll
+            for (int k = 0; k < M::OC; k += 32) {
+                uint32_t d[32];
+                tc_load32(d, at + k);
+                tc_loaded();
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    O[k + j] = kTwo ? fmaf(__uint_as_float(d[j]), f, O[k + j] * corr)
+                                    : fmaf(O[k + j], corr, __uint_as_float(d[j]));
+            }
+            tc_before();
+            __syncwarp();
+            if (lane == 0) kq::mbar_arrive(bar(cm.ofree[i % OB]));
+        }
+        wait(cm.ldone, 0);
+        float l = cm.l[r];
+        const float m = cm.m[r];
+        const int limit = on ? it.limit(tok) : -1;
+        if constexpr (!kTwo) bad = *(volatile int *)&cm.bad != 0;
+        if (bad && on) {
+            // values that are not finite, of the tiles that left them out
+            for (int t = kTwo ? t0 : t1 - edges; t < t1; ++t) {
+                if (kTwo && !info[(int64_t)t * a.kv_heads].bad) continue;
+                for (int j = t * TK; j < min((t + 1) * TK, limit + 1); ++j) {
+                    const T *v = static_cast<const T *>(a.v) + (int64_t)(it.kfirst + j) * a.v_stride +
+                                 (int64_t)it.head * D + c0;
+#pragma unroll
+                    for (int k = 0; k < M::OC; ++k) {
+                        const float x = to_f32<T>(v[k]);
+                        if (!(fabsf(x) < INFINITY)) O[k] += x;
+                    }
+                }
+            }
+        }
+        if (dead()) l = quiet_nan();
+        if (a.splits > 1) {
+            float *part = a.part + (int64_t)blockIdx.x * kRows * (D + 2);
+            float4 *to = reinterpret_cast<float4 *>(part + r * D + c0);
+            if (on) {
+#pragma unroll
+                for (int k = 0; k < M::OC / 4; ++k)
+                    to[k] = make_float4(O[4 * k], O[4 * k + 1], O[4 * k + 2], O[4 * k + 3]);
+                if (c0 == 0) part[kRows * D + r] = m, part[kRows * (D + 1) + r] = l;
+            }
+        } else if (on) {
+            // (a row that attends something and has no sum has scores of
+            // -infinity only)
+            float inv = limit < 0 ? 0.f : __fdiv_rn(kTwo ? 32768.f : 1.f, l);
+            if (dead()) inv = quiet_nan();
+            T *to = static_cast<T *>(a.out) +
+                    ((int64_t)(it.first + tok) * a.q_heads + it.hq + hq) * D + c0;
+#pragma unroll
+            for (int k = 0; k < M::OC; k += 4)
+                store4(to + k, make_float4(O[k] * inv, O[k + 1] * inv, O[k + 2] * inv, O[k + 3] * inv));
+        }
+    } else {
+        if constexpr (D == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        __syncthreads();
+        if (w == M::kFirst + 1 && lane == 0) {
+            // --------------------------------------------- copies
+            for (int k = 0; k < 2 * count; ++k) {
+                const int s = k % M::kSlots, t = t1 - 1 - (k >> 1);
+                if (k >= M::kSlots) wait(cm.empty[s], k / M::kSlots - 1);
+                if (dead()) break;
+                const uint32_t to = base + M::kRing + s * M::kPart, done = bar(cm.full[s]);
+                kq::mbar_expect_tx(done, M::kPart);
+                copied = k + 1;
+                if constexpr (kTwo) {
+                    kq::bulk_g2s(to, a.tiles + (slot0 + (int64_t)t * a.kv_heads) * (2 * M::kPart) +
+                                         (k & 1) * M::kPart, M::kPart, done);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c)
+                        tensor2d_g2s(to + c * TK * 128, k & 1 ? &a.vmap : &a.kmap, it.head * D + 64 * c,
+                                     it.kfirst + t * TK, done);
+                }
+            }
+        } else if (w == M::kFirst) {
+            // --------------------------------------------- products
+            tc_after();
+            const uint32_t tm = uniform(tmem);
+            constexpr int kTerms = kTwo ? 3 : 1;
+            auto lo_first = [](int term) { return kTwo && term == 0; };
+            auto lo_second = [](int term) { return kTwo && term == 1; };
+            constexpr uint32_t is = mma_idesc(TK, M::kBf16, false), io = mma_idesc(D, M::kBf16, true);
+            auto scores = [&](int i) {
+                const int k = 2 * i;
+                wait(cm.full[k % M::kSlots], k / M::kSlots);
+                if (__any_sync(~0u, dead())) return;
+                tc_after();
+                const uint32_t s = uniform(k % M::kSlots), b = uniform(i & 1);
+                const uint32_t d = tm + M::kS + TK * b;
+                const uint32_t kt = base + M::kRing + s * M::kPart;
+                if (elected()) {
+#pragma unroll
+                    for (int term = 0; term < kTerms; ++term)
+#pragma unroll
+                        for (int j = 0; j < D / 16; ++j) {
+                            const uint64_t kd = desc_k(kt + (lo_second(term) ? M::kTerm : 0) +
+                                                       (j >> 2) * (TK * 128) + (j & 3) * 32);
+                            if (M::kLoShared && lo_first(term))
+                                tc_mma_ss(d, desc_k(base + M::kControl + (j >> 2) * (kRows * 128) + (j & 3) * 32),
+                                          kd, is, term + j > 0);
+                            else
+                                tc_mma_ts(d, tm + (lo_first(term) ? D / 2 : 0) + 8 * j, kd, is, term + j > 0);
+                        }
+                    tc_commit(bar(cm.empty[0]) + 8 * s);
+                    tc_commit(bar(cm.sdone[0]) + 8 * b);
+                }
+                __syncwarp();
+            };
+            if (count > 0) scores(0);
+            if (count > 1) scores(1);
+            for (int i = 0; i < count; ++i) {
+                const int k = 2 * i + 1;
+                wait(cm.full[k % M::kSlots], k / M::kSlots);
+                if (!kTwo && i < edges) wait(cm.vclean[i & 3], i >> 2);
+                if (i >= OB) wait(cm.ofree[i % OB], i / OB - 1);
+                wait(cm.pready[i & 1], i >> 1);
+                if (__any_sync(~0u, dead())) break;
+                tc_after();
+                const uint32_t s = uniform(k % M::kSlots), b = uniform(i & 1), o = uniform(i % OB);
+                const uint32_t vt = base + M::kRing + s * M::kPart, p = tm + M::kS + TK * b;
+                const uint32_t d = tm + M::kO + D * o;
+                if (elected()) {
+#pragma unroll
+                    for (int term = 0; term < kTerms; ++term)
+#pragma unroll
+                        for (int j = 0; j < TK / 16; ++j)
+                            tc_mma_ts(d, p + (lo_first(term) ? TK / 2 : 0) + 8 * j,
+                                      desc_n(vt + (lo_second(term) ? M::kTerm : 0) + j * 2048, TK * 128),
+                                      io, term + j > 0);
+                    tc_commit(bar(cm.empty[0]) + 8 * s);
+                    tc_commit(bar(cm.odone[0]) + 8 * o);
+                }
+                __syncwarp();
+                if (i + 2 < count) {  // the buffer of P is S's again
+                    wait(cm.odone[i % OB], i / OB);
+                    scores(i + 2);
+                }
+            }
+        } else if (!kTwo && w >= M::kFirst + 2) {
+            // ------------- values that are not finite, of tiles seen in part
+            for (int i = 0; i < edges; ++i) {
+                const int k = 2 * i + 1, s = k % M::kSlots;
+                wait(cm.full[s], k / M::kSlots);
+                uint4 *v = reinterpret_cast<uint4 *>(smem + M::kRing + s * M::kPart);
+                bool found = false;
+                if (!dead())
+                    for (int c = (w - M::kFirst - 2) * 32 + lane; c < M::kPart / 16; c += 64) {
+                        uint4 x = v[c];
+                        if (not_finite<H>(x.x) | not_finite<H>(x.y) | not_finite<H>(x.z) | not_finite<H>(x.w)) {
+                            found = true;
+                            uint32_t *e = &x.x;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t n = not_finite<H>(e[j]);
+                                if (n & 0x8000u) e[j] &= 0xFFFF0000u;
+                                if (n & 0x80000000u) e[j] &= 0x0000FFFFu;
+                            }
+                            v[c] = x;
+                        }
+                    }
+                if (found) *(volatile int *)&cm.bad = 1;
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) kq::mbar_arrive(bar(cm.vclean[i & 3]));
+            }
+            __syncwarp();
+            if (lane == 0) kq::mbar_arrive(bar(cm.ldone));
+        }
+        __syncwarp();
+    }
+    tc_before();
+    __syncthreads();
+    // After an expired wait no copy and no product may run on past this.
+    if (dead()) {
+        if (w == M::kFirst + 1 && lane == 0) {
+            for (int k = max(0, copied - M::kSlots); k < copied; ++k)
+                kq::mbar_wait(bar(cm.full[k % M::kSlots]), (k / M::kSlots) & 1, kq::kWaitLimitNs);
+        }
+        if (w == M::kFirst) {
+            tc_after();
+            if (elected()) tc_commit(bar(cm.drain));
+            __syncwarp();
+            kq::mbar_wait(bar(cm.drain), 0, kq::kWaitLimitNs);
+            __syncwarp();
+        }
+        __syncthreads();
+    }
+    if (w == M::kFirst) {
+        tc_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    }
+}
+
+// ------------------------------------------------------------------ host
+// Slots of an f32 call's tiles.
+inline int64_t f32_slots(const PromptArgs &a, int d) { return a.nkeys / f32_tile_tokens(d) + a.nseq; }
+
+// Workspace: tiles, their powers of two, partial results; in all.
+struct Space {
+    int64_t info, part, bytes;
+};
+inline Space space_of(const PromptArgs &a, bool f32, int d) {
+    Space s{};
+    const int64_t tiles = f32 ? f32_slots(a, d) * a.kv_heads : 0;
+    s.info = tiles * (f32_tile_tokens(d) * d * 8);
+    s.part = (s.info + tiles * (int64_t)sizeof(TileInfo) + 255) / 256 * 256;
+    s.bytes = s.part + (a.splits > 1 ? 4ll * a.items * a.splits * kRows * (d + 2) : 0);
+    s.bytes = (s.bytes + 255) / 256 * 256;
+    return s;
+}
+
+// What a call's sizes say of its work (T tokens of an item at most kRows / hb).
+void divide(PromptArgs &a, int rows, int tile, int sms);
+
+template <auto KERNEL>
+cudaError_t allow_shared(int bytes) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (done.load() >> dev & 1))) return e;
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev);
+    return e;
+}
+
+// A launch that may begin before the one before it ends (it waits itself).
+template <class F, class... A>
+cudaError_t launch_early(F *kernel, dim3 grid, int threads, int smem, cudaStream_t s, const A &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Keys or values as a tensor map of tokens by all heads' values.
+template <class T>
+cudaError_t keys_map(const void *p, int64_t stride, const PromptArgs &a, int d, int tokens, CUtensorMap *m) {
+    const uint64_t dims[2] = {(uint64_t)a.kv_heads * d, (uint64_t)a.nkeys}, strides[1] = {2ull * stride};
+    const uint32_t box[2] = {64, (uint32_t)tokens};
+    return kqhost::values_map(p, std::is_same<T, __nv_bfloat16>::value, 2, dims, strides, box, m);
+}
+
+template <class T, int D>
+cudaError_t launch_rows(PromptArgs &a, cudaStream_t s) {
+    using M = Rows<T, D>;
+    cudaError_t e = allow_shared<kq_prompt_rows<T, D>>(M::kBytes);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)(a.items * a.splits));
+    if constexpr (M::kTwo) {
+        const dim3 tiles((unsigned)f32_slots(a, D), a.kv_heads, 2);
+        kq_prompt_split<D><<<tiles, kSplitThreads, 0, s>>>(a);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        return launch_early(kq_prompt_rows<T, D>, grid, M::kThreads, M::kBytes, s, a);
+    } else {
+        if (a.nkeys > 0) {
+            e = keys_map<T>(a.k, a.k_stride, a, D, M::TK, &a.kmap);
+            if (e == cudaSuccess) e = keys_map<T>(a.v, a.v_stride, a, D, M::TK, &a.vmap);
+            if (e != cudaSuccess) return e;
+        }
+        kq_prompt_rows<T, D><<<grid, M::kThreads, M::kBytes, s>>>(a);
+        return cudaGetLastError();
+    }
+}
+
+}  // namespace kqp
