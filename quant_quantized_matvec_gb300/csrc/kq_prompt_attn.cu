@@ -6,16 +6,16 @@
 
 namespace kqp {
 
-cudaError_t prompt_f32(int d, PromptArgs &a, cudaStream_t s);
-cudaError_t prompt_f16(int d, PromptArgs &a, cudaStream_t s);
-cudaError_t prompt_bf16(int d, PromptArgs &a, cudaStream_t s);
+cudaError_t prompt_f32(int d, PromptArgs &a, int sms, cudaStream_t s);
+cudaError_t prompt_f16(int d, PromptArgs &a, int sms, cudaStream_t s);
+cudaError_t prompt_bf16(int d, PromptArgs &a, int sms, cudaStream_t s);
 
 constexpr int kJoinThreads = 256;
 
 // One CTA per item: its rows' parts in their order.
 template <class T>
 __global__ void __launch_bounds__(kJoinThreads)
-    kq_prompt_join(const __grid_constant__ PromptArgs a, int d, int rows) {
+    kq_prompt_join(const __grid_constant__ PromptArgs a, int d, int blocks) {
     __shared__ Item item;
     if (threadIdx.x < 32) find_item(a, blockIdx.x, item, threadIdx.x);
     kq::wait_prerequisites();
@@ -24,12 +24,14 @@ __global__ void __launch_bounds__(kJoinThreads)
     if (!it.found) return;
     const float factor = std::is_same<T, float>::value ? 1.f : fabsf(a.scale) * kLog2E;
     const float up = std::is_same<T, float>::value ? 32768.f : 1.f;
+    const int rows = blocks * kRows, half = a.tok / blocks;
     const int64_t each = (int64_t)rows * (d + 2);
     const float *part = a.part + (int64_t)blockIdx.x * a.splits * each;
     for (int i = threadIdx.x; i < rows * (d / 4); i += kJoinThreads) {
         const int r = i / (d / 4), e = 4 * (i % (d / 4));
-        int tok, h;
-        if (!it.row(a.hb, r, tok, h)) continue;
+        const int t = r % kRows / a.hb, h = r % kRows - t * a.hb, at = r / kRows * half + t;
+        if (t >= half || at >= it.nt || h >= it.nh) continue;
+        const int tok = it.tok0 + at;
         const float *m = part + rows * d + r, *l = m + rows;
         float top = -INFINITY;
         for (int k = 0; k < a.splits; ++k) top = fmaxf(top, m[k * each]);
@@ -50,24 +52,39 @@ __global__ void __launch_bounds__(kJoinThreads)
     }
 }
 
-// Tokens of an item, items at most, and parts of the keys where items are few.
-void divide(PromptArgs &a, int rows, int tile, int sms) {
+// Tokens of an item of `blocks` blocks, items at most, and the parts into which
+// their keys are cut.
+void divide(PromptArgs &a, int blocks, int tile, int sms) {
     a.per = a.q_heads / a.kv_heads;
-    a.hb = std::min(a.per, rows);
+    a.hb = std::min(a.per, kRows);
     a.hblocks = (a.per + a.hb - 1) / a.hb;
-    a.tok = rows / a.hb;
-    const int64_t blocks =
+    a.tok = kRows / a.hb * blocks;
+    const int64_t runs =
         std::min<int64_t>(a.ntok, (int64_t)a.ntok / a.tok + std::min(a.nseq, a.ntok));
-    const int64_t items = blocks * a.kv_heads * a.hblocks;
+    const int64_t items = runs * a.kv_heads * a.hblocks;
     a.items = (int32_t)std::min<int64_t>(items, 0x7FFFFFFF);
-    // each part has four tiles or more (of a sequence of mean length)
-    const int64_t tiles = (int64_t)a.nkeys / a.nseq / tile;
-    a.splits = (int32_t)std::max<int64_t>(1, std::min<int64_t>(sms / std::max(a.items, 1), tiles / 4));
+    // The cut that ends first, in tiles: of the longest item, or of rounds of
+    // mean ones, each with what a part costs beside its tiles (about 400 keys'
+    // time to begin and to end, and as much again to write partial results and
+    // join them).
+    a.splits = 1;
+    if (items >= 2 * (int64_t)sms) return;
+    const double keys = (double)a.nkeys / a.nseq, mine = (double)a.ntok / a.nseq;
+    const double most = keys / tile, mean = std::max(keys - mine / 2, 1.0) / tile;
+    double best = 1e30;
+    for (int n = 1; n <= 32 && (n == 1 || n * 2 <= most); ++n) {
+        const double extra = (n > 1 ? 800.0 : 400.0) / tile;
+        const double rounds = (double)((items * n + sms - 1) / sms);
+        const double cost = std::max(most / n + extra, rounds * (mean / n + extra));
+        if (cost < 0.97 * best) best = cost, a.splits = n;
+    }
 }
 
 namespace {
-int rows_of(int type, int d) { return kRows; }
-int tile_of(int type, int d) { return type == KQ_F32 ? f32_tile_tokens(d) : 64; }
+// Whether the kernel of two blocks takes a call, keys of a tile, blocks.
+bool pairs(int type, int d) { return type != KQ_F32 && d <= 128; }
+int tile_of(int type, int d) { return pairs(type, d) ? 128 : type == KQ_F32 ? f32_tile_tokens(d) : 64; }
+int blocks_of(int type, int d) { return pairs(type, d) ? 2 : 1; }
 
 PromptArgs args_of(const PromptCall &c, int sms) {
     PromptArgs a{};
@@ -76,36 +93,36 @@ PromptArgs args_of(const PromptCall &c, int sms) {
     a.q_stride = c.q_stride, a.k_stride = c.k_stride, a.v_stride = c.v_stride;
     a.nseq = c.nseq, a.ntok = c.ntok, a.nkeys = c.nkeys;
     a.q_heads = c.q_heads, a.kv_heads = c.kv_heads, a.scale = c.scale;
-    divide(a, rows_of(c.type, c.dim), tile_of(c.type, c.dim), sms);
+    divide(a, blocks_of(c.type, c.dim), tile_of(c.type, c.dim), sms);
     return a;
 }
 }  // namespace
 
 int64_t prompt_workspace(const PromptCall &c, int sms) {
     const PromptArgs a = args_of(c, sms);
-    if ((int64_t)a.items * a.splits >= 0x7FFFFFFF) return -1;
-    return space_of(a, c.type == KQ_F32, c.dim).bytes;
+    if ((int64_t)a.items * a.splits >= 0x7FFF0000) return -1;  // (numbers go a round past)
+    return space_of(a, blocks_of(c.type, c.dim), c.type == KQ_F32, c.dim).bytes;
 }
 
 cudaError_t prompt_attention(const PromptCall &c, void *ws, int sms, unsigned int *err,
                              unsigned long long wait_ns, cudaStream_t s) {
     PromptArgs a = args_of(c, sms);
-    const Space at = space_of(a, c.type == KQ_F32, c.dim);
+    const int blocks = blocks_of(c.type, c.dim);
+    const Space at = space_of(a, blocks, c.type == KQ_F32, c.dim);
     a.tiles = static_cast<uint8_t *>(ws);
     a.info = reinterpret_cast<TileInfo *>(a.tiles + at.info);
     a.part = reinterpret_cast<float *>(a.tiles + at.part);
     a.err = err, a.wait_ns = wait_ns;
     a.suspend_ns = wait_ns < kq::kSuspendNs ? (uint32_t)wait_ns : kq::kSuspendNs;
-    cudaError_t e = c.type == KQ_F32   ? prompt_f32(c.dim, a, s)
-                    : c.type == KQ_F16 ? prompt_f16(c.dim, a, s)
-                                       : prompt_bf16(c.dim, a, s);
+    cudaError_t e = c.type == KQ_F32   ? prompt_f32(c.dim, a, sms, s)
+                    : c.type == KQ_F16 ? prompt_f16(c.dim, a, sms, s)
+                                       : prompt_bf16(c.dim, a, sms, s);
     if (e != cudaSuccess || a.splits == 1) return e;
     const dim3 grid((unsigned)a.items);
-    const int rows = rows_of(c.type, c.dim);
-    return c.type == KQ_F32 ? launch_early(kq_prompt_join<float>, grid, kJoinThreads, 0, s, a, c.dim, rows)
+    return c.type == KQ_F32 ? launch_early(kq_prompt_join<float>, grid, kJoinThreads, 0, s, a, c.dim, blocks)
            : c.type == KQ_F16
-               ? launch_early(kq_prompt_join<__half>, grid, kJoinThreads, 0, s, a, c.dim, rows)
-               : launch_early(kq_prompt_join<__nv_bfloat16>, grid, kJoinThreads, 0, s, a, c.dim, rows);
+               ? launch_early(kq_prompt_join<__half>, grid, kJoinThreads, 0, s, a, c.dim, blocks)
+               : launch_early(kq_prompt_join<__nv_bfloat16>, grid, kJoinThreads, 0, s, a, c.dim, blocks);
 }
 
 }  // namespace kqp

@@ -40,6 +40,7 @@
 
 #include <cuda.h>
 
+#include <algorithm>
 #include <atomic>
 #include <type_traits>
 
@@ -78,7 +79,7 @@ struct PromptArgs {
     int32_t per;      // query heads of a key head
     int32_t hb;       // of them in an item
     int32_t hblocks;  // runs of hb heads
-    int32_t tok;      // tokens of an item
+    int32_t tok;      // tokens of an item (equally many in each of its blocks of 128 rows)
     int32_t splits;
     int32_t items;    // items in all, at most
     float scale;      // with its sign
@@ -310,7 +311,7 @@ struct Rows {
 
 struct RowsShared {
     Item item;
-    uint64_t full[8], empty[8], sdone[2], pready[2], odone[2], ofree[2], cready[4], vclean[4], ldone, drain;
+    uint64_t full[8], empty[8], sdone[2], pready[2], odone[2], ofree[2], cready[4], vraw[4], vclean[4], ldone, drain;
     uint32_t tmem;
     int dead, bad;
     float corr[4][kRows];  // of tile i & 3: the factor of what was summed before
@@ -343,7 +344,10 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
             kq::mbar_init(bar(cm.odone[i]), 1);
             kq::mbar_init(bar(cm.ofree[i]), M::OW);
         }
-        for (int i = 0; i < 4; ++i) kq::mbar_init(bar(cm.cready[i]), 4), kq::mbar_init(bar(cm.vclean[i]), 2);
+        for (int i = 0; i < 4; ++i) {
+            kq::mbar_init(bar(cm.cready[i]), 4);
+            kq::mbar_init(bar(cm.vraw[i]), 1), kq::mbar_init(bar(cm.vclean[i]), 2);
+        }
         kq::mbar_init(bar(cm.ldone), kTwo ? 4 : 6);
         kq::mbar_init(bar(cm.drain), 1);
         cm.dead = cm.bad = 0;
@@ -623,7 +627,14 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
                 const int s = k % M::kSlots, t = t1 - 1 - (k >> 1);
                 if (k >= M::kSlots) wait(cm.empty[s], k / M::kSlots - 1);
                 if (dead()) break;
-                const uint32_t to = base + M::kRing + s * M::kPart, done = bar(cm.full[s]);
+                const uint32_t to = base + M::kRing + s * M::kPart;
+                uint32_t done = bar(cm.full[s]);
+                // Values that are cleaned have barriers of their own: who waits
+                // for some tiles only could be two phases ahead of a slot's.
+                if (!kTwo && (k & 1) && (k >> 1) < edges) {
+                    kq::mbar_arrive(done);
+                    done = bar(cm.vraw[(k >> 1) & 3]);
+                }
                 kq::mbar_expect_tx(done, M::kPart);
                 copied = k + 1;
                 if constexpr (kTwo) {
@@ -704,7 +715,7 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
             // ------------- values that are not finite, of tiles seen in part
             for (int i = 0; i < edges; ++i) {
                 const int k = 2 * i + 1, s = k % M::kSlots;
-                wait(cm.full[s], k / M::kSlots);
+                wait(cm.vraw[i & 3], i >> 2);
                 uint4 *v = reinterpret_cast<uint4 *>(smem + M::kRing + s * M::kPart);
                 bool found = false;
                 if (!dead())
@@ -739,6 +750,9 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
         if (w == M::kFirst + 1 && lane == 0) {
             for (int k = max(0, copied - M::kSlots); k < copied; ++k)
                 kq::mbar_wait(bar(cm.full[k % M::kSlots]), (k / M::kSlots) & 1, kq::kWaitLimitNs);
+            const int raw = kTwo ? 0 : min(copied / 2, edges);  // (copies of values are the odd ones)
+            for (int i = max(0, raw - 4); i < raw; ++i)
+                kq::mbar_wait(bar(cm.vraw[i & 3]), (i >> 2) & 1, kq::kWaitLimitNs);
         }
         if (w == M::kFirst) {
             tc_after();
@@ -763,18 +777,15 @@ inline int64_t f32_slots(const PromptArgs &a, int d) { return a.nkeys / f32_tile
 struct Space {
     int64_t info, part, bytes;
 };
-inline Space space_of(const PromptArgs &a, bool f32, int d) {
+inline Space space_of(const PromptArgs &a, int blocks, bool f32, int d) {
     Space s{};
     const int64_t tiles = f32 ? f32_slots(a, d) * a.kv_heads : 0;
     s.info = tiles * (f32_tile_tokens(d) * d * 8);
     s.part = (s.info + tiles * (int64_t)sizeof(TileInfo) + 255) / 256 * 256;
-    s.bytes = s.part + (a.splits > 1 ? 4ll * a.items * a.splits * kRows * (d + 2) : 0);
+    s.bytes = s.part + (a.splits > 1 ? 4ll * a.items * a.splits * blocks * kRows * (d + 2) : 0);
     s.bytes = (s.bytes + 255) / 256 * 256;
     return s;
 }
-
-// What a call's sizes say of its work (T tokens of an item at most kRows / hb).
-void divide(PromptArgs &a, int rows, int tile, int sms);
 
 template <auto KERNEL>
 cudaError_t allow_shared(int bytes) {

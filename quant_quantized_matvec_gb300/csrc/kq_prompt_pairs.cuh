@@ -1,0 +1,582 @@
+// kq_prompt_pairs.cuh -- attention of whole prompts in 16 bits, widths 64 and
+// 128.  Formula, items and what is not finite are those of kq_prompt_attn.cuh;
+// an item has 256 rows here, two blocks of 128 over the same keys, a CTA goes
+// through several items, and a tile is 128 keys.
+//
+// Both blocks' queries stay in shared memory, their S and O in tensor memory: a
+// block's S = Q K is turned into P where it stands, and O += P V adds up there.
+// While the softmax warps of one block (a row a thread) are at a tile, the
+// tensor core forms the other block's O and its next S.  O is only corrected
+// when a row's maximum has grown by 2^8 or more over its reference: until then
+// probabilities are held up to 2^8 times as large, in the sum too, and the
+// quotient is the same.  The warps that hold the row do it themselves, as it is
+// rare after the first tiles.
+//
+// Products that one thread issues run in their order: a block's next S is
+// issued behind the O that reads P in its place.
+#pragma once
+
+#include "kq_prompt_attn.cuh"
+
+namespace kqp {
+
+template <class T, int D>
+struct Pairs {
+    static constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    static constexpr int TK = 128;
+    static constexpr int kQTile = kRows * D * 2, kTile = TK * D * 2;
+    static constexpr int kControl = 2048;
+    static constexpr int kRing = kControl + 2 * kQTile;
+    static constexpr int kRoom = (227 * 1024 - 1024 - kRing) / kTile;
+    static constexpr int kSlots = kRoom < 8 ? kRoom : 8;
+    static constexpr int kBytes = kRing + kSlots * kTile + 1024;
+    // columns of tensor memory: S (and P) of both blocks, O of both
+    static constexpr int kS = 0, kO = 2 * TK;
+    // P of f16 times 2^7: with the 2^8 below the correction it stays below 2^16
+    static constexpr float kUp = kBf16 ? 0.f : 7.f;
+    static_assert(kO + 2 * D <= 512 && kSlots >= 5, "layout");
+};
+constexpr int kPairThreads = 512, kPairOther = 8;  // first warp that is not softmax
+// Registers after the split: 256 * 200 + 256 * 56 = the 512 * 128 at launch.
+constexpr int kPairSoftRegs = 200, kPairOtherRegs = 56;
+constexpr float kPairLazy = 8.f;  // log2 of the growth that is not corrected
+
+// A unit: a part of an item's keys, with what each block sees of it.
+struct Unit {
+    Item item;      // of both blocks: up to 2 * tok tokens
+    int32_t t0, t1; // tiles, last first
+    int32_t edges;  // of them, from the last, that some row sees in part
+    int32_t n[2];   // tiles of each block, the last n of the walk
+    int32_t u;      // its number
+};
+
+struct PairShared {
+    Unit unit[2];
+    uint64_t ufull[2], ufree[2], qfull[2], qfree, full[8], empty[8], sdone[2], pready[2], odone[2],
+        vraw[4], vclean[4], drain;
+    uint32_t tmem;
+    int dead, bad[2];
+};
+static_assert(sizeof(PairShared) <= 2048, "layout");
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+        " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}\n"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
+        " add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+
+// Unit `u` into shared memory, by one warp; false past the last.
+__device__ __forceinline__ bool find_unit(const PromptArgs &a, int u, int tile, Unit &g, int lane) {
+    find_item(a, u / a.splits, g.item, lane);
+    const Item &it = g.item;
+    const bool found = it.found != 0;
+    if (found && lane == 0) {
+        const int rank = u % a.splits, half = a.tok / 2;
+        const int tiles = (it.keys() + tile - 1) / tile;
+        g.t0 = (int)((int64_t)tiles * rank / a.splits);
+        g.t1 = (int)((int64_t)tiles * (rank + 1) / a.splits);
+        const int whole = max(0, it.limit(it.tok0) + 1) / tile;
+        g.edges = min(max(g.t1 - max(whole, g.t0), 0), g.t1 - g.t0);
+        // the first block's tokens end earlier (it may have all of them)
+        const int first = min(half, it.nt);
+        const int keys = max(0, min(it.m, it.limit(it.tok0 + first - 1) + 1));
+        g.n[1] = it.nt > half ? g.t1 - g.t0 : 0;
+        g.n[0] = max(0, min(g.t1, (keys + tile - 1) / tile) - g.t0);
+        g.u = u;
+    }
+    __syncwarp();
+    return found;
+}
+
+template <class T, int D>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    kq_prompt_pairs(const __grid_constant__ PromptArgs a) {
+    using M = Pairs<T, D>;
+    constexpr int TK = M::TK;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024 - (kq::smem_addr(smem_raw) & 1023)) & 1023);
+    PairShared &cm = *reinterpret_cast<PairShared *>(smem);
+    const uint32_t base = kq::smem_addr(smem);
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    auto bar = [&](const uint64_t &b) { return kq::smem_addr(&b); };
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            kq::mbar_init(bar(cm.ufull[i]), 1);
+            kq::mbar_init(bar(cm.ufree[i]), 8 + 2 + 4);
+            kq::mbar_init(bar(cm.qfull[i]), 1);
+            kq::mbar_init(bar(cm.sdone[i]), 1);
+            kq::mbar_init(bar(cm.pready[i]), 4);
+            kq::mbar_init(bar(cm.odone[i]), 1);
+        }
+        for (int i = 0; i < 8; ++i) kq::mbar_init(bar(cm.full[i]), 1), kq::mbar_init(bar(cm.empty[i]), 1);
+        for (int i = 0; i < 4; ++i) kq::mbar_init(bar(cm.vraw[i]), 1), kq::mbar_init(bar(cm.vclean[i]), 4);
+        kq::mbar_init(bar(cm.qfree), 1);
+        kq::mbar_init(bar(cm.drain), 1);
+        cm.dead = cm.bad[0] = cm.bad[1] = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (w == kPairOther) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                         kq::smem_addr(&cm.tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = cm.tmem;
+
+    auto dead = [&]() { return *(volatile int *)&cm.dead != 0; };
+    auto wait = [&](const uint64_t &b, int phase) {  // the completion of the barrier's phase
+        if (kq::mbar_test(bar(b), phase & 1) || dead()) return;
+        if (!kq::mbar_wait_for(bar(b), phase & 1, a.wait_ns, a.suspend_ns)) {
+            *(volatile int *)&cm.dead = 1;
+            atomicOr(a.err, 1u);
+        }
+    };
+    // The CTA's k-th unit: rounds over all CTAs, there and back, as the units
+    // of a sequence get shorter.
+    const int units = a.items * a.splits;
+    auto unit_of = [&](int k) {
+        const int at = k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+        return k * (int)gridDim.x + at;
+    };
+    // The next unit as a role reads it; false at the end.  (After an expired
+    // wait there is none.)  Its place is handed back once all have read it, and
+    // the softmax warps are done with it.
+    auto next = [&](int k, Unit &g) {
+        wait(cm.ufull[k & 1], k >> 1);
+        if (__any_sync(~0u, dead())) return false;
+        g = cm.unit[k & 1];
+        __syncwarp();
+        if (w >= kPairOther && lane == 0) kq::mbar_arrive(bar(cm.ufree[k & 1]));
+        return g.u >= 0;
+    };
+    // Copies of tiles, of values that are cleaned, and of blocks' queries, that
+    // were begun.  (Values that are cleaned have barriers of their own: who
+    // waits for some tiles only could be two phases ahead of a slot's, and take
+    // the phase before for it.)
+    int copied = 0, raw = 0, queries = 0;
+
+    if (w < kPairOther) {
+        // ------------------------------------------------- softmax warps
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairSoftRegs));
+        const int block = w >> 2, r = 32 * (w & 3) + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * (w & 3)) << 16);
+        const uint32_t sa = lanes + M::kS + TK * block, oa = lanes + M::kO + D * block;
+        const float sc = fmaxf(fabsf(a.scale) * kLog2E, 1.2e-38f);  // (not 0: -infinity * 0)
+        int seen_tiles = 0, outs = 0;  // tiles and results of all units
+        Unit g;
+        for (int k = 0; next(k, g); ++k) {
+            const Item &it = g.item;
+            const int half = a.tok / 2;
+            const int t = r / a.hb, hq = r - t * a.hb, tok = it.tok0 + block * half + t;
+            const bool on = t < half && tok < it.tok0 + it.nt && hq < it.nh;
+            const int limit = on ? it.limit(tok) : -1;
+            const int count = g.n[block], top = g.t0 + count;  // tiles t0..top-1, last first
+            const int whole = g.t1 - g.edges;                  // tiles below are seen by all rows
+            float m = -INFINITY, l = 0.f;
+            for (int i = 0; i < count; ++i) {
+                const int at = top - 1 - i;
+                wait(cm.sdone[block], seen_tiles + i);
+                if (__any_sync(~0u, dead())) break;
+                tc_after();
+                uint32_t d[TK];
+#pragma unroll
+                for (int j = 0; j < TK; j += 32) tc_load32(d + j, sa + j);
+                tc_loaded();
+                if (at >= whole) {
+                    const int seen = limit + 1 - at * TK;
+#pragma unroll
+                    for (int j = 0; j < TK; ++j)
+                        if (j >= seen) d[j] = 0xFF800000u;
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int j = 0; j < TK; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(d[j]));
+                const float now = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), m);
+                // (-infinity before the first key that the row attends)
+                const bool grown = now > m && !((now - m) * sc <= kPairLazy);
+                if (__any_sync(~0u, grown)) {
+                    const float f = !grown ? 1.f : m == -INFINITY ? 0.f : exp2_fast((m - now) * sc);
+                    if (grown) m = now;
+                    l *= f;
+                    if (i > 0) {  // S came after the O before it
+#pragma unroll
+                        for (int j = 0; j < D; j += 16) {
+                            uint32_t o[16];
+                            tc_load16(o, oa + j);
+                            tc_loaded();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tc_store16(oa + j, o);
+                        }
+                    }
+                }
+                // p = 2^(s sc - m sc + up).  With a product m sc past 2^10 its
+                // rounding would show: the difference is taken first.  (Lanes
+                // without a row hold anything, and have no say in it.)
+                float c = m == -INFINITY ? M::kUp : M::kUp - m * sc;
+                if (__any_sync(~0u, on && !(fabsf(c) < 1024.f))) {
+                    const float from = m == -INFINITY ? 0.f : m;
+#pragma unroll
+                    for (int j = 0; j < TK; ++j) d[j] = __float_as_uint(__uint_as_float(d[j]) - from);
+                    c = M::kUp;
+                }
+                float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+                for (int j = 0; j < TK; j += 32) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 x =
+                            fma2(make_float2(__uint_as_float(d[j + 2 * e]), __uint_as_float(d[j + 2 * e + 1])),
+                                 make_float2(sc, sc), make_float2(c, c));
+                        const float2 y = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+                        if (e & 1) sum1 = add2(sum1, y);
+                        else sum0 = add2(sum0, y);
+                        p[e] = pack2<T>(y.x, y.y);
+                    }
+                    tc_store16(sa + j / 2, p);
+                }
+                tc_stored();
+                tc_before();
+                __syncwarp();
+                if (lane == 0) kq::mbar_arrive(bar(cm.pready[block]));
+                sum0 = add2(sum0, sum1);
+                l += sum0.x + sum0.y;
+            }
+            seen_tiles += count;
+            if (__any_sync(~0u, dead())) break;
+            // ---- the rows' results
+            if (count) wait(cm.odone[block], outs++);
+            if (__any_sync(~0u, dead())) break;
+            tc_after();
+            const float inv = limit < 0 ? 0.f : __fdiv_rn(1.f, l);
+            const bool bad = *(volatile int *)&cm.bad[k & 1] != 0;
+            T *to = static_cast<T *>(a.out) + ((int64_t)(it.first + tok) * a.q_heads + it.hq + hq) * D;
+            float *part = a.part + (int64_t)g.u * (2 * kRows) * (D + 2);
+            const int row = block * kRows + r;
+#pragma unroll 1
+            for (int j = 0; j < D; j += 32) {
+                uint32_t o[32];
+                if (count) {
+                    tc_load32(o, oa + j);
+                    tc_loaded();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0;
+                }
+                if (bad && on) {
+                    // values that are not finite, of the tiles that left them out
+                    for (int y = whole * TK; y < min(g.t1 * TK, limit + 1); ++y) {
+                        const T *v = static_cast<const T *>(a.v) + (int64_t)(it.kfirst + y) * a.v_stride +
+                                     (int64_t)it.head * D + j;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const float x = to_f32<T>(v[e]);
+                            if (!(fabsf(x) < INFINITY)) o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
+                        }
+                    }
+                }
+                if (on && a.splits > 1) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<uint4 *>(part + row * D + j + e) =
+                            make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                } else if (on) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t q[4];
+#pragma unroll
+                        for (int z = 0; z < 4; ++z)
+                            q[z] = pack2<T>(__uint_as_float(o[e + 2 * z]) * inv,
+                                            __uint_as_float(o[e + 2 * z + 1]) * inv);
+                        *reinterpret_cast<uint4 *>(to + j + e) = make_uint4(q[0], q[1], q[2], q[3]);
+                    }
+                }
+                __syncwarp();
+            }
+            if (a.splits > 1 && on) part[2 * kRows * D + row] = m, part[2 * kRows * (D + 1) + row] = l;
+            tc_before();
+            __syncwarp();
+            if (lane == 0) kq::mbar_arrive(bar(cm.ufree[k & 1]));
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairOtherRegs));
+        if (w == kPairOther + 2) {
+            // ----------------------------------------- the units, one ahead
+            for (int k = 0;; ++k) {
+                if (k >= 2) wait(cm.ufree[k & 1], (k >> 1) - 1);
+                if (__any_sync(~0u, dead())) break;
+                const int u = unit_of(k);
+                Unit &g = cm.unit[k & 1];
+                const bool found = u < units && find_unit(a, u, TK, g, lane);
+                if (lane == 0) {
+                    if (!found) g.u = -1;
+                    *(volatile int *)&cm.bad[k & 1] = 0;
+                    __threadfence_block();
+                    kq::mbar_arrive(bar(cm.ufull[k & 1]));
+                }
+                __syncwarp();
+                if (!found) break;
+            }
+        } else if (w == kPairOther + 1) {
+            // --------------------------------------------- copies
+            Unit g;
+            for (int k = 0; next(k, g); ++k) {
+                const Item &it = g.item;
+                const int count = g.t1 - g.t0;
+                if (count == 0) continue;
+                if (lane == 0) {
+                    const uint32_t bytes = (uint32_t)(a.tok / 2) * a.hb * 128;
+                    for (int n = 0; n < 2 * count; ++n) {
+                        // first keys, then the queries, then the rest by turns
+                        if (n == 1) {
+                            if (queries) wait(cm.qfree, queries - 1);
+                            if (dead()) break;
+                            for (int b = 0; b < 2; ++b) {
+                                kq::mbar_expect_tx(bar(cm.qfull[b]), bytes * (D / 64));
+                                for (int c = 0; c < D / 64; ++c)
+                                    tensor3d_g2s(base + M::kControl + b * M::kQTile + c * (kRows * 128), &a.qmap,
+                                                 64 * c, it.hq, it.first + it.tok0 + b * (a.tok / 2),
+                                                 bar(cm.qfull[b]));
+                            }
+                            ++queries;
+                        }
+                        const int s = copied % M::kSlots;
+                        if (copied >= M::kSlots) wait(cm.empty[s], copied / M::kSlots - 1);
+                        if (dead()) break;
+                        uint32_t done = bar(cm.full[s]);
+                        if ((n & 1) && (n >> 1) < g.edges) {
+                            kq::mbar_arrive(done);
+                            done = bar(cm.vraw[raw++ & 3]);
+                        }
+                        kq::mbar_expect_tx(done, M::kTile);
+                        ++copied;
+#pragma unroll
+                        for (int c = 0; c < D / 64; ++c)
+                            tensor2d_g2s(base + M::kRing + s * M::kTile + c * (TK * 128), n & 1 ? &a.vmap : &a.kmap,
+                                         it.head * D + 64 * c, it.kfirst + (g.t1 - 1 - (n >> 1)) * TK,
+                                         done);
+                    }
+                }
+                __syncwarp();
+            }
+        } else if (w == kPairOther) {
+            // --------------------------------------------- products
+            const uint32_t tm = uniform(tmem);
+            const uint32_t is = mma_idesc(TK, M::kBf16, false) | (a.scale < 0.f ? 1u << 13 : 0u);
+            constexpr uint32_t io = mma_idesc(D, M::kBf16, true);
+            int tile = 0, cleaned = 0, have = 0;  // tiles of both rings so far; units with queries
+            int turns[2] = {0, 0};                // tiles of each block so far
+            Unit g;
+            for (int k = 0; next(k, g); ++k) {
+                const int count = g.t1 - g.t0;
+                if (count == 0) continue;
+                const int from[2] = {count - g.n[0], count - g.n[1]};  // first tile of each block
+                auto scores = [&](int b, int i) {
+                    const int n = 2 * (tile + i);
+                    const uint32_t s = uniform(n % M::kSlots);
+                    const uint32_t kt = base + M::kRing + s * M::kTile;
+                    const uint32_t qt = base + M::kControl + b * M::kQTile;
+                    if (elected()) {
+#pragma unroll
+                        for (int j = 0; j < D / 16; ++j)
+                            tc_mma_ss(tm + M::kS + TK * b, desc_k(qt + (j >> 2) * (kRows * 128) + (j & 3) * 32),
+                                      desc_k(kt + (j >> 2) * (TK * 128) + (j & 3) * 32), is, j > 0);
+                        tc_commit(bar(cm.sdone[b]));
+                    }
+                    __syncwarp();
+                };
+                auto keys = [&](int i) {  // tile i's keys are there
+                    const int n = 2 * (tile + i);
+                    wait(cm.full[n % M::kSlots], n / M::kSlots);
+                };
+                auto free_slot = [&](int n) {
+                    const uint32_t s = uniform(n % M::kSlots);
+                    if (elected()) tc_commit(bar(cm.empty[0]) + 8 * s);
+                    __syncwarp();
+                };
+                keys(0);
+                wait(cm.qfull[0], have);
+                wait(cm.qfull[1], have);
+                ++have;
+                if (__any_sync(~0u, dead())) break;
+                tc_after();
+                for (int b = 0; b < 2; ++b)
+                    if (from[b] == 0 && g.n[b] > 0) scores(b, 0);
+                free_slot(2 * tile);
+                bool stop = false;
+                for (int i = 0; i < count && !stop; ++i) {
+                    const int n = 2 * (tile + i) + 1;
+                    wait(cm.full[n % M::kSlots], n / M::kSlots);
+                    if (i < g.edges) wait(cm.vclean[(cleaned + i) & 3], (cleaned + i) >> 2);
+                    bool there = false;
+                    const uint32_t s = uniform(n % M::kSlots);
+                    const uint32_t vt = base + M::kRing + s * M::kTile;
+                    for (int b = 0; b < 2; ++b) {
+                        if (i >= from[b]) {
+                            wait(cm.pready[b], turns[b] + i - from[b]);
+                            if (__any_sync(~0u, dead())) {
+                                stop = true;
+                                break;
+                            }
+                            tc_after();
+                            if (elected()) {
+#pragma unroll
+                                for (int j = 0; j < TK / 16; ++j)
+                                    tc_mma_ts(tm + M::kO + D * b, tm + M::kS + TK * b + 8 * j,
+                                              desc_n(vt + j * 2048, TK * 128), io, i > from[b] || j > 0);
+                                if (i == count - 1) tc_commit(bar(cm.odone[b]));
+                            }
+                            __syncwarp();
+                        }
+                        if (i + 1 < count && i + 1 >= from[b]) {
+                            if (!there) keys(i + 1);
+                            there = true;
+                            if (__any_sync(~0u, dead())) {
+                                stop = true;
+                                break;
+                            }
+                            tc_after();
+                            scores(b, i + 1);
+                        }
+                    }
+                    if (stop) break;
+                    free_slot(n);
+                    if (i + 1 < count) free_slot(n + 1);
+                    if (i + 2 == count || count == 1) {  // (the last S was issued)
+                        if (elected()) tc_commit(bar(cm.qfree));
+                        __syncwarp();
+                    }
+                }
+                if (stop) break;
+                tile += count;
+                cleaned += g.edges;
+                for (int b = 0; b < 2; ++b) turns[b] += g.n[b];
+            }
+        } else if (w >= kPairOther + 4) {
+            // ------------- values that are not finite, of tiles seen in part
+            int tile = 0, cleaned = 0;
+            Unit g;
+            for (int k = 0; next(k, g); ++k) {
+                for (int i = 0; i < g.edges; ++i, ++cleaned) {
+                    const int n = 2 * (tile + i) + 1, s = n % M::kSlots;
+                    wait(cm.vraw[cleaned & 3], cleaned >> 2);
+                    if (__any_sync(~0u, dead())) break;
+                    uint4 *v = reinterpret_cast<uint4 *>(smem + M::kRing + s * M::kTile) +
+                               (w - kPairOther - 4) * (M::kTile / 64) + lane;
+                    bool found = false;
+#pragma unroll 4
+                    for (int c = 0; c < M::kTile / 64; c += 32) {
+                        uint4 x = v[c];
+                        if (not_finite<T>(x.x) | not_finite<T>(x.y) | not_finite<T>(x.z) | not_finite<T>(x.w)) {
+                            found = true;
+                            uint32_t *e = &x.x;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t f = not_finite<T>(e[j]);
+                                if (f & 0x8000u) e[j] &= 0xFFFF0000u;
+                                if (f & 0x80000000u) e[j] &= 0x0000FFFFu;
+                            }
+                            v[c] = x;
+                        }
+                    }
+                    if (found) *(volatile int *)&cm.bad[k & 1] = 1;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) kq::mbar_arrive(bar(cm.vclean[cleaned & 3]));
+                }
+                tile += g.t1 - g.t0;
+            }
+        }
+        __syncwarp();
+    }
+    __syncwarp();
+    tc_before();
+    __syncthreads();
+    // After an expired wait no copy and no product may run on past this; what
+    // the CTA had to write is NaN.
+    if (dead()) {
+        if (w == kPairOther + 1 && lane == 0) {
+            for (int n = max(0, copied - M::kSlots); n < copied; ++n)
+                kq::mbar_wait(bar(cm.full[n % M::kSlots]), (n / M::kSlots) & 1, kq::kWaitLimitNs);
+            for (int n = max(0, raw - 4); n < raw; ++n)
+                kq::mbar_wait(bar(cm.vraw[n & 3]), (n >> 2) & 1, kq::kWaitLimitNs);
+            if (queries)
+                for (int b = 0; b < 2; ++b)
+                    kq::mbar_wait(bar(cm.qfull[b]), (queries - 1) & 1, kq::kWaitLimitNs);
+        }
+        if (w == kPairOther) {
+            tc_after();
+            if (elected()) tc_commit(bar(cm.drain));
+            __syncwarp();
+            kq::mbar_wait(bar(cm.drain), 0, kq::kWaitLimitNs);
+            __syncwarp();
+        }
+        for (int k = 0; unit_of(k) < units; ++k) {
+            __syncthreads();
+            bool found = true;
+            if (w == 0) found = find_unit(a, unit_of(k), TK, cm.unit[0], lane);
+            if (tid == 0 && !found) cm.unit[0].u = -1;
+            __syncthreads();
+            const Unit &g = cm.unit[0];
+            if (g.u < 0) break;
+            const Item &it = g.item;
+            if (a.splits > 1) {
+                float *part = a.part + (int64_t)g.u * (2 * kRows) * (D + 2);
+                for (int i = tid; i < 2 * kRows; i += kPairThreads)
+                    part[2 * kRows * D + i] = -INFINITY, part[2 * kRows * (D + 1) + i] = quiet_nan();
+                continue;
+            }
+            const int across = it.nh * (D / 8);
+            for (int i = tid; i < it.nt * across; i += kPairThreads) {
+                const int tok = it.tok0 + i / across, e = i % across;
+                const uint32_t n = pack2<T>(quiet_nan(), quiet_nan());
+                *reinterpret_cast<uint4 *>(static_cast<T *>(a.out) +
+                                           ((int64_t)(it.first + tok) * a.q_heads + it.hq) * D + 8 * e) =
+                    make_uint4(n, n, n, n);
+            }
+        }
+        __syncthreads();
+    }
+    if (w == kPairOther) {
+        tc_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    }
+}
+
+template <class T, int D>
+cudaError_t launch_pairs(PromptArgs &a, int sms, cudaStream_t s) {
+    using M = Pairs<T, D>;
+    cudaError_t e = allow_shared<kq_prompt_pairs<T, D>>(M::kBytes);
+    if (e == cudaSuccess && a.nkeys > 0) {
+        e = keys_map<T>(a.k, a.k_stride, a, D, M::TK, &a.kmap);
+        if (e == cudaSuccess) e = keys_map<T>(a.v, a.v_stride, a, D, M::TK, &a.vmap);
+    }
+    if (e != cudaSuccess) return e;
+    // queries as (value, head, token): a block's box is hb heads of tok / 2 tokens
+    const uint64_t dims[3] = {(uint64_t)D, (uint64_t)a.q_heads, (uint64_t)a.ntok};
+    const uint64_t strides[2] = {2ull * D, 2ull * a.q_stride};
+    const uint32_t box[3] = {64, (uint32_t)a.hb, (uint32_t)(a.tok / 2)};
+    e = kqhost::values_map(a.q, M::kBf16, 3, dims, strides, box, &a.qmap);
+    if (e != cudaSuccess) return e;
+    const int grid = (int)std::min<int64_t>(sms, (int64_t)a.items * a.splits);
+    kq_prompt_pairs<T, D><<<grid, kPairThreads, M::kBytes, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace kqp
