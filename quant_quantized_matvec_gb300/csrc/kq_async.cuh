@@ -94,6 +94,25 @@ __device__ __forceinline__ bool mbar_wait_for(uint32_t bar, uint32_t parity,
     }
     return true;
 }
+// The same without sleeping between tries, for waits that the work goes by.
+__device__ __forceinline__ bool mbar_wait_awake(uint32_t bar, uint32_t parity,
+                                                unsigned long long limit_ns, uint32_t suspend_ns) {
+    unsigned long long t0 = 0;
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n"
+            " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(suspend_ns)
+            : "memory");
+        if (ok) return true;
+        const unsigned long long now = global_ns();
+        if (t0 == 0) t0 = now;
+        else if (now - t0 > limit_ns) return false;
+    }
+}
 __device__ __forceinline__ void bulk_g2s(uint32_t dst, const void *src,
                                          uint32_t bytes, uint32_t bar) {
     asm volatile(

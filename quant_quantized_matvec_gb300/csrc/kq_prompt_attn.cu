@@ -1,6 +1,6 @@
 // kq_prompt_attn.cu -- kq_prompt_attention's launches: what chooses the kernel
 // and divides its work, and the kernel that joins the parts of cut keys.
-#include "kq_prompt_attn.cuh"
+#include "kq_prompt_pairs.cuh"
 
 #include <algorithm>
 
@@ -83,7 +83,7 @@ void divide(PromptArgs &a, int blocks, int tile, int sms) {
 namespace {
 // Whether the kernel of two blocks takes a call, keys of a tile, blocks.
 bool pairs(int type, int d) { return type != KQ_F32 && d <= 128; }
-int tile_of(int type, int d) { return pairs(type, d) ? 128 : type == KQ_F32 ? f32_tile_tokens(d) : 64; }
+int tile_of(int type, int d) { return pairs(type, d) ? pair_tile(d) : type == KQ_F32 ? f32_tile_tokens(d) : 64; }
 int blocks_of(int type, int d) { return pairs(type, d) ? 2 : 1; }
 
 PromptArgs args_of(const PromptCall &c, int sms) {

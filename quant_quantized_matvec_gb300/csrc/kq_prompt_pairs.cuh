@@ -1,40 +1,41 @@
 // kq_prompt_pairs.cuh -- attention of whole prompts in 16 bits, widths 64 and
 // 128.  Formula, items and what is not finite are those of kq_prompt_attn.cuh;
-// an item has 256 rows here, two blocks of 128 over the same keys, a CTA goes
-// through several items, and a tile is 128 keys.
+// an item has 256 rows here, two blocks of 128 over the same keys, and a CTA goes
+// through several items.
 //
-// Both blocks' queries stay in shared memory, their S and O in tensor memory: a
-// block's S = Q K is turned into P where it stands, and O += P V adds up there.
-// While the softmax warps of one block (a row a thread) are at a tile, the
-// tensor core forms the other block's O and its next S.  O is only corrected
-// when a row's maximum has grown by 2^8 or more over its reference: until then
+// Both blocks' queries stay in shared memory; S, P and O are in tensor memory,
+// each by itself: a tile's S is formed while the softmax warps (a row a thread)
+// are at the tile before it, as soon as they have taken that one into registers,
+// and O += P V adds up behind them.  Each block has a warp that issues its
+// products, so neither block waits for the other.  O is only corrected when a
+// row's maximum has grown by 2^8 or more over its reference: until then
 // probabilities are held up to 2^8 times as large, in the sum too, and the
 // quotient is the same.  The warps that hold the row do it themselves, as it is
 // rare after the first tiles.
-//
-// Products that one thread issues run in their order: a block's next S is
-// issued behind the O that reads P in its place.
 #pragma once
 
 #include "kq_prompt_attn.cuh"
 
 namespace kqp {
 
+constexpr int pair_tile(int d) { return d == 64 ? 128 : 80; }
+
 template <class T, int D>
 struct Pairs {
     static constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-    static constexpr int TK = 128;
+    // Keys of a tile: what tensor memory holds of S, P and O for two blocks.
+    static constexpr int TK = pair_tile(D);
     static constexpr int kQTile = kRows * D * 2, kTile = TK * D * 2;
     static constexpr int kControl = 2048;
     static constexpr int kRing = kControl + 2 * kQTile;
     static constexpr int kRoom = (227 * 1024 - 1024 - kRing) / kTile;
     static constexpr int kSlots = kRoom < 8 ? kRoom : 8;
     static constexpr int kBytes = kRing + kSlots * kTile + 1024;
-    // columns of tensor memory: S (and P) of both blocks, O of both
-    static constexpr int kS = 0, kO = 2 * TK;
+    // columns of tensor memory of a block: O, S, P
+    static constexpr int kO = 0, kS = D, kP = D + TK, kBlock = 256;
     // P of f16 times 2^7: with the 2^8 below the correction it stays below 2^16
     static constexpr float kUp = kBf16 ? 0.f : 7.f;
-    static_assert(kO + 2 * D <= 512 && kSlots >= 5, "layout");
+    static_assert(kP + TK / 2 <= kBlock && kSlots >= 5 && TK % 16 == 0, "layout");
 };
 constexpr int kPairThreads = 512, kPairOther = 8;  // first warp that is not softmax
 // Registers after the split: 256 * 200 + 256 * 56 = the 512 * 128 at launch.
@@ -52,8 +53,8 @@ struct Unit {
 
 struct PairShared {
     Unit unit[2];
-    uint64_t ufull[2], ufree[2], qfull[2], qfree, full[8], empty[8], sdone[2], pready[2], odone[2],
-        vraw[4], vclean[4], drain;
+    uint64_t ufull[2], ufree[2], qfull[2], qfree[2], full[8], empty[8], sdone[2], sfree[2], pready[2],
+        odone[2], vraw[4], vclean[4], drain[2];
     uint32_t tmem;
     int dead, bad[2];
 };
@@ -114,16 +115,17 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             kq::mbar_init(bar(cm.ufull[i]), 1);
-            kq::mbar_init(bar(cm.ufree[i]), 8 + 2 + 4);
+            kq::mbar_init(bar(cm.ufree[i]), 8 + 3 + 4);
             kq::mbar_init(bar(cm.qfull[i]), 1);
+            kq::mbar_init(bar(cm.qfree[i]), 1);
             kq::mbar_init(bar(cm.sdone[i]), 1);
+            kq::mbar_init(bar(cm.sfree[i]), 4);
             kq::mbar_init(bar(cm.pready[i]), 4);
             kq::mbar_init(bar(cm.odone[i]), 1);
+            kq::mbar_init(bar(cm.drain[i]), 1);
         }
-        for (int i = 0; i < 8; ++i) kq::mbar_init(bar(cm.full[i]), 1), kq::mbar_init(bar(cm.empty[i]), 1);
+        for (int i = 0; i < 8; ++i) kq::mbar_init(bar(cm.full[i]), 1), kq::mbar_init(bar(cm.empty[i]), 2);
         for (int i = 0; i < 4; ++i) kq::mbar_init(bar(cm.vraw[i]), 1), kq::mbar_init(bar(cm.vclean[i]), 4);
-        kq::mbar_init(bar(cm.qfree), 1);
-        kq::mbar_init(bar(cm.drain), 1);
         cm.dead = cm.bad[0] = cm.bad[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -141,7 +143,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     auto dead = [&]() { return *(volatile int *)&cm.dead != 0; };
     auto wait = [&](const uint64_t &b, int phase) {  // the completion of the barrier's phase
         if (kq::mbar_test(bar(b), phase & 1) || dead()) return;
-        if (!kq::mbar_wait_for(bar(b), phase & 1, a.wait_ns, a.suspend_ns)) {
+        if (!kq::mbar_wait_awake(bar(b), phase & 1, a.wait_ns, a.suspend_ns)) {
             *(volatile int *)&cm.dead = 1;
             atomicOr(a.err, 1u);
         }
@@ -168,35 +170,42 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     // were begun.  (Values that are cleaned have barriers of their own: who
     // waits for some tiles only could be two phases ahead of a slot's, and take
     // the phase before for it.)
-    int copied = 0, raw = 0, queries = 0;
+    int copied = 0, raw = 0, queries[2] = {0, 0};
 
     if (w < kPairOther) {
         // ------------------------------------------------- softmax warps
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairSoftRegs));
         const int block = w >> 2, r = 32 * (w & 3) + lane;
-        const uint32_t lanes = tmem + ((uint32_t)(32 * (w & 3)) << 16);
-        const uint32_t sa = lanes + M::kS + TK * block, oa = lanes + M::kO + D * block;
+        const uint32_t mine = tmem + M::kBlock * block + ((uint32_t)(32 * (w & 3)) << 16);
+        const uint32_t sa = mine + M::kS, pa = mine + M::kP, oa = mine + M::kO;
         const float sc = fmaxf(fabsf(a.scale) * kLog2E, 1.2e-38f);  // (not 0: -infinity * 0)
-        int seen_tiles = 0, outs = 0;  // tiles and results of all units
-        Unit g;
-        for (int k = 0; next(k, g); ++k) {
+        const int half = a.tok / 2, t = r / a.hb, hq = r - t * a.hb;
+        int turn = 0;  // tiles of all units
+        for (int k = 0;; ++k) {
+            wait(cm.ufull[k & 1], k >> 1);
+            if (__any_sync(~0u, dead())) break;
+            const Unit &g = cm.unit[k & 1];  // (ours until it is handed back)
+            if (g.u < 0) break;
             const Item &it = g.item;
-            const int half = a.tok / 2;
-            const int t = r / a.hb, hq = r - t * a.hb, tok = it.tok0 + block * half + t;
+            const int tok = it.tok0 + block * half + t;
             const bool on = t < half && tok < it.tok0 + it.nt && hq < it.nh;
             const int limit = on ? it.limit(tok) : -1;
             const int count = g.n[block], top = g.t0 + count;  // tiles t0..top-1, last first
             const int whole = g.t1 - g.edges;                  // tiles below are seen by all rows
             float m = -INFINITY, l = 0.f;
             for (int i = 0; i < count; ++i) {
-                const int at = top - 1 - i;
-                wait(cm.sdone[block], seen_tiles + i);
+                wait(cm.sdone[block], turn + i);
                 if (__any_sync(~0u, dead())) break;
                 tc_after();
                 uint32_t d[TK];
 #pragma unroll
-                for (int j = 0; j < TK; j += 32) tc_load32(d + j, sa + j);
+                for (int j = 0; j + 32 <= TK; j += 32) tc_load32(d + j, sa + j);
+                if constexpr (TK % 32 != 0) tc_load16(d + TK - 16, sa + TK - 16);
                 tc_loaded();
+                tc_before();
+                __syncwarp();
+                if (lane == 0) kq::mbar_arrive(bar(cm.sfree[block]));
+                const int at = top - 1 - i;
                 if (at >= whole) {
                     const int seen = limit + 1 - at * TK;
 #pragma unroll
@@ -213,7 +222,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     const float f = !grown ? 1.f : m == -INFINITY ? 0.f : exp2_fast((m - now) * sc);
                     if (grown) m = now;
                     l *= f;
-                    if (i > 0) {  // S came after the O before it
+                    if (i > 0) {
+                        wait(cm.odone[block], turn + i - 1);
+                        if (__any_sync(~0u, dead())) break;
+                        tc_after();
 #pragma unroll
                         for (int j = 0; j < D; j += 16) {
                             uint32_t o[16];
@@ -236,32 +248,36 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     c = M::kUp;
                 }
                 float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+                uint32_t p[TK / 2];
 #pragma unroll
-                for (int j = 0; j < TK; j += 32) {
-                    uint32_t p[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float2 x =
-                            fma2(make_float2(__uint_as_float(d[j + 2 * e]), __uint_as_float(d[j + 2 * e + 1])),
-                                 make_float2(sc, sc), make_float2(c, c));
-                        const float2 y = make_float2(exp2_fast(x.x), exp2_fast(x.y));
-                        if (e & 1) sum1 = add2(sum1, y);
-                        else sum0 = add2(sum0, y);
-                        p[e] = pack2<T>(y.x, y.y);
-                    }
-                    tc_store16(sa + j / 2, p);
+                for (int j = 0; j < TK / 2; ++j) {
+                    const float2 x = fma2(make_float2(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1])),
+                                          make_float2(sc, sc), make_float2(c, c));
+                    const float2 y = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+                    if (j & 1) sum1 = add2(sum1, y);
+                    else sum0 = add2(sum0, y);
+                    p[j] = pack2<T>(y.x, y.y);
                 }
+                sum0 = add2(sum0, sum1);
+                l += sum0.x + sum0.y;
+                // ---- P, once the O before it has read its place
+                if (i > 0) {
+                    wait(cm.odone[block], turn + i - 1);
+                    if (__any_sync(~0u, dead())) break;
+                    tc_after();
+                }
+#pragma unroll
+                for (int j = 0; j + 32 <= TK / 2; j += 32) tc_store32(pa + j, p + j);
+                if constexpr (TK / 2 % 32 != 0) tc_store8(pa + TK / 2 - 8, p + TK / 2 - 8);
                 tc_stored();
                 tc_before();
                 __syncwarp();
                 if (lane == 0) kq::mbar_arrive(bar(cm.pready[block]));
-                sum0 = add2(sum0, sum1);
-                l += sum0.x + sum0.y;
             }
-            seen_tiles += count;
+            turn += count;
             if (__any_sync(~0u, dead())) break;
             // ---- the rows' results
-            if (count) wait(cm.odone[block], outs++);
+            if (count) wait(cm.odone[block], turn - 1);
             if (__any_sync(~0u, dead())) break;
             tc_after();
             const float inv = limit < 0 ? 0.f : __fdiv_rn(1.f, l);
@@ -316,7 +332,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairOtherRegs));
-        if (w == kPairOther + 2) {
+        if (w == kPairOther + 3) {
             // ----------------------------------------- the units, one ahead
             for (int k = 0;; ++k) {
                 if (k >= 2) wait(cm.ufree[k & 1], (k >> 1) - 1);
@@ -333,7 +349,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 __syncwarp();
                 if (!found) break;
             }
-        } else if (w == kPairOther + 1) {
+        } else if (w == kPairOther + 2) {
             // --------------------------------------------- copies
             Unit g;
             for (int k = 0; next(k, g); ++k) {
@@ -345,17 +361,19 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     for (int n = 0; n < 2 * count; ++n) {
                         // first keys, then the queries, then the rest by turns
                         if (n == 1) {
-                            if (queries) wait(cm.qfree, queries - 1);
-                            if (dead()) break;
                             for (int b = 0; b < 2; ++b) {
+                                if (g.n[b] == 0) continue;
+                                if (queries[b]) wait(cm.qfree[b], queries[b] - 1);
+                                if (dead()) break;
                                 kq::mbar_expect_tx(bar(cm.qfull[b]), bytes * (D / 64));
                                 for (int c = 0; c < D / 64; ++c)
                                     tensor3d_g2s(base + M::kControl + b * M::kQTile + c * (kRows * 128), &a.qmap,
                                                  64 * c, it.hq, it.first + it.tok0 + b * (a.tok / 2),
                                                  bar(cm.qfull[b]));
+                                ++queries[b];
                             }
-                            ++queries;
                         }
+                        if (dead()) break;
                         const int s = copied % M::kSlots;
                         if (copied >= M::kSlots) wait(cm.empty[s], copied / M::kSlots - 1);
                         if (dead()) break;
@@ -375,98 +393,90 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 }
                 __syncwarp();
             }
-        } else if (w == kPairOther) {
-            // --------------------------------------------- products
-            const uint32_t tm = uniform(tmem);
+        } else if (w < kPairOther + 2) {
+            // ------------------------------------- products of a block
+            const int b = w - kPairOther;
+            const uint32_t tm = uniform(tmem + M::kBlock * b), qt = uniform(base + M::kControl + b * M::kQTile);
             const uint32_t is = mma_idesc(TK, M::kBf16, false) | (a.scale < 0.f ? 1u << 13 : 0u);
             constexpr uint32_t io = mma_idesc(D, M::kBf16, true);
-            int tile = 0, cleaned = 0, have = 0;  // tiles of both rings so far; units with queries
-            int turns[2] = {0, 0};                // tiles of each block so far
+            int tile = 0, cleaned = 0;  // tiles of both blocks so far, and those that were cleaned
+            int turn = 0, have = 0;     // tiles of this block; units with queries
             Unit g;
             for (int k = 0; next(k, g); ++k) {
-                const int count = g.t1 - g.t0;
-                if (count == 0) continue;
-                const int from[2] = {count - g.n[0], count - g.n[1]};  // first tile of each block
-                auto scores = [&](int b, int i) {
-                    const int n = 2 * (tile + i);
-                    const uint32_t s = uniform(n % M::kSlots);
+                const int count = g.t1 - g.t0, n = g.n[b], from = count - n;
+                // Copy x of the walk (keys, values by turns) is there; and is
+                // given back: once the products so far are done, or at once.
+                auto there = [&](int x) {
+                    wait(cm.full[x % M::kSlots], x / M::kSlots);
+                };
+                auto clean = [&](int i) {
+                    if (i < g.edges) wait(cm.vclean[(cleaned + i) & 3], (cleaned + i) >> 2);
+                };
+                bool stop = false;
+                for (int i = 0; i < from; ++i) {  // tiles that only the other block sees
+                    for (int x = 2 * (tile + i); x < 2 * (tile + i) + 2; ++x) {
+                        there(x);
+                        if (x & 1) clean(i);
+                        if (__any_sync(~0u, dead())) stop = true;
+                        if (stop) break;
+                        if (lane == 0) kq::mbar_arrive(bar(cm.empty[x % M::kSlots]));
+                        __syncwarp();
+                    }
+                    if (stop) break;
+                }
+                if (stop) break;
+                if (n > 0) wait(cm.qfull[b], have++);
+                auto scores = [&](int i) {
+                    const int x = 2 * (tile + i);
+                    there(x);
+                    if (i > from) wait(cm.sfree[b], turn + i - from - 1);
+                    if (__any_sync(~0u, dead())) return false;
+                    tc_after();
+                    const uint32_t s = uniform(x % M::kSlots);
                     const uint32_t kt = base + M::kRing + s * M::kTile;
-                    const uint32_t qt = base + M::kControl + b * M::kQTile;
                     if (elected()) {
 #pragma unroll
                         for (int j = 0; j < D / 16; ++j)
-                            tc_mma_ss(tm + M::kS + TK * b, desc_k(qt + (j >> 2) * (kRows * 128) + (j & 3) * 32),
+                            tc_mma_ss(tm + M::kS, desc_k(qt + (j >> 2) * (kRows * 128) + (j & 3) * 32),
                                       desc_k(kt + (j >> 2) * (TK * 128) + (j & 3) * 32), is, j > 0);
                         tc_commit(bar(cm.sdone[b]));
+                        tc_commit(bar(cm.empty[0]) + 8 * s);
+                        if (i == count - 1) tc_commit(bar(cm.qfree[b]));
                     }
                     __syncwarp();
+                    return true;
                 };
-                auto keys = [&](int i) {  // tile i's keys are there
-                    const int n = 2 * (tile + i);
-                    wait(cm.full[n % M::kSlots], n / M::kSlots);
-                };
-                auto free_slot = [&](int n) {
-                    const uint32_t s = uniform(n % M::kSlots);
-                    if (elected()) tc_commit(bar(cm.empty[0]) + 8 * s);
-                    __syncwarp();
-                };
-                keys(0);
-                wait(cm.qfull[0], have);
-                wait(cm.qfull[1], have);
-                ++have;
-                if (__any_sync(~0u, dead())) break;
-                tc_after();
-                for (int b = 0; b < 2; ++b)
-                    if (from[b] == 0 && g.n[b] > 0) scores(b, 0);
-                free_slot(2 * tile);
-                bool stop = false;
-                for (int i = 0; i < count && !stop; ++i) {
-                    const int n = 2 * (tile + i) + 1;
-                    wait(cm.full[n % M::kSlots], n / M::kSlots);
-                    if (i < g.edges) wait(cm.vclean[(cleaned + i) & 3], (cleaned + i) >> 2);
-                    bool there = false;
-                    const uint32_t s = uniform(n % M::kSlots);
+                if (n > 0 && !scores(from)) break;
+                for (int i = from; i < count; ++i) {
+                    if (i + 1 < count && !scores(i + 1)) {
+                        stop = true;
+                        break;
+                    }
+                    const int x = 2 * (tile + i) + 1;
+                    there(x);
+                    clean(i);
+                    wait(cm.pready[b], turn + i - from);
+                    if (__any_sync(~0u, dead())) {
+                        stop = true;
+                        break;
+                    }
+                    tc_after();
+                    const uint32_t s = uniform(x % M::kSlots);
                     const uint32_t vt = base + M::kRing + s * M::kTile;
-                    for (int b = 0; b < 2; ++b) {
-                        if (i >= from[b]) {
-                            wait(cm.pready[b], turns[b] + i - from[b]);
-                            if (__any_sync(~0u, dead())) {
-                                stop = true;
-                                break;
-                            }
-                            tc_after();
-                            if (elected()) {
+                    if (elected()) {
 #pragma unroll
-                                for (int j = 0; j < TK / 16; ++j)
-                                    tc_mma_ts(tm + M::kO + D * b, tm + M::kS + TK * b + 8 * j,
-                                              desc_n(vt + j * 2048, TK * 128), io, i > from[b] || j > 0);
-                                if (i == count - 1) tc_commit(bar(cm.odone[b]));
-                            }
-                            __syncwarp();
-                        }
-                        if (i + 1 < count && i + 1 >= from[b]) {
-                            if (!there) keys(i + 1);
-                            there = true;
-                            if (__any_sync(~0u, dead())) {
-                                stop = true;
-                                break;
-                            }
-                            tc_after();
-                            scores(b, i + 1);
-                        }
+                        for (int j = 0; j < TK / 16; ++j)
+                            tc_mma_ts(tm + M::kO, tm + M::kP + 8 * j, desc_n(vt + j * 2048, TK * 128), io,
+                                      i > from || j > 0);
+                        tc_commit(bar(cm.odone[b]));
+                        tc_commit(bar(cm.empty[0]) + 8 * s);
                     }
-                    if (stop) break;
-                    free_slot(n);
-                    if (i + 1 < count) free_slot(n + 1);
-                    if (i + 2 == count || count == 1) {  // (the last S was issued)
-                        if (elected()) tc_commit(bar(cm.qfree));
-                        __syncwarp();
-                    }
+                    __syncwarp();
                 }
                 if (stop) break;
                 tile += count;
                 cleaned += g.edges;
-                for (int b = 0; b < 2; ++b) turns[b] += g.n[b];
+                turn += n;
             }
         } else if (w >= kPairOther + 4) {
             // ------------- values that are not finite, of tiles seen in part
@@ -511,20 +521,20 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     // After an expired wait no copy and no product may run on past this; what
     // the CTA had to write is NaN.
     if (dead()) {
-        if (w == kPairOther + 1 && lane == 0) {
+        if (w == kPairOther + 2 && lane == 0) {
             for (int n = max(0, copied - M::kSlots); n < copied; ++n)
                 kq::mbar_wait(bar(cm.full[n % M::kSlots]), (n / M::kSlots) & 1, kq::kWaitLimitNs);
             for (int n = max(0, raw - 4); n < raw; ++n)
                 kq::mbar_wait(bar(cm.vraw[n & 3]), (n >> 2) & 1, kq::kWaitLimitNs);
-            if (queries)
-                for (int b = 0; b < 2; ++b)
-                    kq::mbar_wait(bar(cm.qfull[b]), (queries - 1) & 1, kq::kWaitLimitNs);
+            for (int b = 0; b < 2; ++b)
+                if (queries[b]) kq::mbar_wait(bar(cm.qfull[b]), (queries[b] - 1) & 1, kq::kWaitLimitNs);
         }
-        if (w == kPairOther) {
+        if (w == kPairOther || w == kPairOther + 1) {
+            const uint64_t &drain = cm.drain[w - kPairOther];
             tc_after();
-            if (elected()) tc_commit(bar(cm.drain));
+            if (elected()) tc_commit(bar(drain));
             __syncwarp();
-            kq::mbar_wait(bar(cm.drain), 0, kq::kWaitLimitNs);
+            kq::mbar_wait(bar(drain), 0, kq::kWaitLimitNs);
             __syncwarp();
         }
         for (int k = 0; unit_of(k) < units; ++k) {

@@ -321,12 +321,13 @@ def test_offsets_past_32_bits(kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("dim,new,ctx", [(128, [300, 200], [0, 9]), (64, [16], [4000]), (256, [300], [0])])
+@pytest.mark.parametrize("dim,new,ctx", [(128, [300, 200], [0, 9]), (64, [16], [4000]), (256, [300], [0]),
+                                         (64, [9000], [0]), (128, [9000], [0]), (256, [5000], [0])])
 def test_expired_waits(dim, new, ctx, kind):
     """A limit below the time that copies and products take: the call ends in
     time, the error word is set where a wait ran out, rows are NaN or right, and
-    the next calls are right.  (The clock's steps are about a microsecond, so
-    that short waits may end before; a cold cache makes some of them longer.)"""
+    the next calls are right.  (Waits of a microsecond or two may end before
+    the clock is looked at; with several items a CTA some are longer.)"""
     from quant_quantized_matvec_gb300 import _binding
     lib = _binding.load()
     q, k, v, s, ks = inputs(new, ctx, 8, 2, dim, kind, 17)
@@ -355,7 +356,7 @@ def test_expired_waits(dim, new, ctx, kind):
         assert torch.isnan(got).any() == expired
         for _ in range(2):
             assert torch.equal(kq.prompt_attention(q, k, v, sd, kd), want)
-    assert times or dim == 64  # (its few keys may come before the clock's next step)
+    assert times or sum(new) < 5000
 
 
 def test_agrees_with_the_cache():
