@@ -2,7 +2,7 @@
 #include "kq_prompt_attn.cuh"
 
 namespace kqp {
-cudaError_t prompt_f32(int d, PromptArgs &a, int sms, cudaStream_t s) {
+cudaError_t prompt_f32(int d, PromptArgs &a, cudaStream_t s) {
     return d == 64    ? launch_rows<float, 64>(a, s)
            : d == 128 ? launch_rows<float, 128>(a, s)
                       : launch_rows<float, 256>(a, s);

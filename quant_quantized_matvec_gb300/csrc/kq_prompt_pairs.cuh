@@ -52,11 +52,13 @@ struct Unit {
 };
 
 struct PairShared {
+    uint4 answer;  // of ask_for_cta
     Unit unit[2];
     uint64_t ufull[2], ufree[2], qfull[2], qfree[2], full[8], empty[8], sdone[2], sfree[2], pready[2],
-        odone[2], vraw[4], vclean[4], drain[2];
+        odone[2], vraw[4], vclean[4], given, drain[2];
     uint32_t tmem;
     int dead, bad[2];
+    int asked, claimed;  // after an expired wait: an answer to come; a unit that no role has seen
 };
 static_assert(sizeof(PairShared) <= 2048, "layout");
 
@@ -75,6 +77,31 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         : "=f"(r.x), "=f"(r.y)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
+}
+
+// Another CTA of the grid that has not begun, whose work this one takes over
+// instead: asked for, its number 16 bytes later at `to`.
+__device__ __forceinline__ void ask_for_cta(uint32_t to, uint32_t bar) {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(to),
+        "r"(bar)
+        : "memory");
+}
+// The answer: the CTA's number, or -1 where there is none (then none is asked
+// for again).
+__device__ __forceinline__ int cta_given(uint32_t at) {
+    int x;
+    asm volatile(
+        "{\n .reg .b128 h;\n .reg .pred p;\n .reg .b32 a, b, c, d;\n"
+        " ld.shared.b128 h, [%1];\n"
+        " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n"
+        " mov.b32 a, -1;\n"
+        " @p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {a, b, c, d}, h;\n"
+        " mov.b32 %0, a;\n}\n"
+        : "=r"(x)
+        : "r"(at)
+        : "memory");
+    return x;
 }
 
 // Unit `u` into shared memory, by one warp; false past the last.
@@ -98,6 +125,27 @@ __device__ __forceinline__ bool find_unit(const PromptArgs &a, int u, int tile, 
     }
     __syncwarp();
     return found;
+}
+
+// Four lanes of a row each hold four 16-byte chunks of their own row: turned, so
+// that chunk j of the rows of lanes 4 q .. 4 q + 3 is in lane 4 q + j, and four
+// lanes write 64 bytes of one row.  v: chunk c in words 4 c .. 4 c + 3.
+__device__ __forceinline__ void turn_chunks(uint32_t *v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 4; o *= 2) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            if (c & o) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                uint32_t &x = v[4 * c + e], &y = v[4 * (c + o) + e];
+                const uint32_t got = __shfl_xor_sync(~0u, up ? x : y, o);
+                if (up) x = got;
+                else y = got;
+            }
+        }
+    }
 }
 
 template <class T, int D>
@@ -126,7 +174,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         for (int i = 0; i < 8; ++i) kq::mbar_init(bar(cm.full[i]), 1), kq::mbar_init(bar(cm.empty[i]), 2);
         for (int i = 0; i < 4; ++i) kq::mbar_init(bar(cm.vraw[i]), 1), kq::mbar_init(bar(cm.vclean[i]), 4);
+        kq::mbar_init(bar(cm.given), 1);
         cm.dead = cm.bad[0] = cm.bad[1] = 0;
+        cm.unit[0].u = cm.unit[1].u = -1;
+        cm.asked = 0, cm.claimed = -1;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (w == kPairOther) {
@@ -147,13 +198,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             *(volatile int *)&cm.dead = 1;
             atomicOr(a.err, 1u);
         }
-    };
-    // The CTA's k-th unit: rounds over all CTAs, there and back, as the units
-    // of a sequence get shorter.
-    const int units = a.items * a.splits;
-    auto unit_of = [&](int k) {
-        const int at = k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
-        return k * (int)gridDim.x + at;
     };
     // The next unit as a role reads it; false at the end.  (After an expired
     // wait there is none.)  Its place is handed back once all have read it, and
@@ -282,7 +326,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             tc_after();
             const float inv = limit < 0 ? 0.f : __fdiv_rn(1.f, l);
             const bool bad = *(volatile int *)&cm.bad[k & 1] != 0;
-            T *to = static_cast<T *>(a.out) + ((int64_t)(it.first + tok) * a.q_heads + it.hq + hq) * D;
+            T *to = static_cast<T *>(a.out) +
+                    ((int64_t)(it.first + it.tok0 + block * half) * a.q_heads + it.hq) * D;
+            const uint32_t place = t * a.q_heads + hq;  // the row's, from there
+            const uint32_t rows = __ballot_sync(~0u, on);
             float *part = a.part + (int64_t)g.u * (2 * kRows) * (D + 2);
             const int row = block * kRows + r;
 #pragma unroll 1
@@ -307,20 +354,30 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         }
                     }
                 }
-                if (on && a.splits > 1) {
+                __syncwarp();
+                // chunk `lane & 3` of the rows of four lanes
+                const int four = lane & ~3, mine4 = 4 * (lane & 3);
+                if (a.splits > 1) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<uint4 *>(part + row * D + j + e) =
-                            make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                } else if (on) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint32_t q[4];
+                    for (int e = 0; e < 32; e += 16) {
+                        turn_chunks(o + e, lane);
 #pragma unroll
                         for (int z = 0; z < 4; ++z)
-                            q[z] = pack2<T>(__uint_as_float(o[e + 2 * z]) * inv,
-                                            __uint_as_float(o[e + 2 * z + 1]) * inv);
-                        *reinterpret_cast<uint4 *>(to + j + e) = make_uint4(q[0], q[1], q[2], q[3]);
+                            if (rows >> (four + z) & 1)
+                                *reinterpret_cast<uint4 *>(part + (row - lane + four + z) * D + j + e + mine4) =
+                                    make_uint4(o[e + 4 * z], o[e + 4 * z + 1], o[e + 4 * z + 2], o[e + 4 * z + 3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        o[e] = pack2<T>(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                    turn_chunks(o, lane);
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        const uint32_t at = __shfl_sync(~0u, place, four + z);
+                        if (rows >> (four + z) & 1)
+                            *reinterpret_cast<uint4 *>(to + (int64_t)at * D + j + 2 * mine4) =
+                                make_uint4(o[4 * z], o[4 * z + 1], o[4 * z + 2], o[4 * z + 3]);
                     }
                 }
                 __syncwarp();
@@ -334,12 +391,19 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairOtherRegs));
         if (w == kPairOther + 3) {
             // ----------------------------------------- the units, one ahead
+            // A CTA begins with the unit of its number, and then takes over those
+            // of CTAs that have not begun, in their order: a sequence's longest
+            // first.  (Dealt out evenly beforehand, in rounds there and back:
+            // 234 against 2xx us for nine prompts of up to 2049 tokens.)
+            int u = blockIdx.x;
             for (int k = 0;; ++k) {
                 if (k >= 2) wait(cm.ufree[k & 1], (k >> 1) - 1);
-                if (__any_sync(~0u, dead())) break;
-                const int u = unit_of(k);
+                if (__any_sync(~0u, dead())) {
+                    if (lane == 0) cm.claimed = u;
+                    break;
+                }
                 Unit &g = cm.unit[k & 1];
-                const bool found = u < units && find_unit(a, u, TK, g, lane);
+                const bool found = u >= 0 && find_unit(a, u, TK, g, lane);
                 if (lane == 0) {
                     if (!found) g.u = -1;
                     *(volatile int *)&cm.bad[k & 1] = 0;
@@ -348,6 +412,19 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 }
                 __syncwarp();
                 if (!found) break;
+                if (lane == 0) {
+                    kq::mbar_expect_tx(bar(cm.given), 16);
+                    ask_for_cta(kq::smem_addr(&cm.answer), bar(cm.given));
+                }
+                __syncwarp();
+                wait(cm.given, k);
+                if (__any_sync(~0u, dead())) {
+                    if (lane == 0) cm.asked = k + 1;
+                    break;
+                }
+                u = cta_given(kq::smem_addr(&cm.answer));
+                __syncwarp();
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             }
         } else if (w == kPairOther + 2) {
             // --------------------------------------------- copies
@@ -537,14 +614,20 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             kq::mbar_wait(bar(drain), 0, kq::kWaitLimitNs);
             __syncwarp();
         }
-        for (int k = 0; unit_of(k) < units; ++k) {
+        if (w == kPairOther + 3 && lane == 0 && cm.asked) {
+            if (kq::mbar_wait(bar(cm.given), (cm.asked - 1) & 1, kq::kWaitLimitNs))
+                cm.claimed = cta_given(kq::smem_addr(&cm.answer));
+        }
+        for (int k = 0; k < 3; ++k) {  // the units that roles were at, and one that none has seen
             __syncthreads();
-            bool found = true;
-            if (w == 0) found = find_unit(a, unit_of(k), TK, cm.unit[0], lane);
-            if (tid == 0 && !found) cm.unit[0].u = -1;
-            __syncthreads();
-            const Unit &g = cm.unit[0];
-            if (g.u < 0) break;
+            if (k == 2) {
+                const int u = cm.claimed;
+                __syncthreads();
+                if (w == 0 && (u < 0 || !find_unit(a, u, TK, cm.unit[0], lane)) && lane == 0) cm.unit[0].u = -1;
+                __syncthreads();
+            }
+            const Unit &g = cm.unit[k & 1];
+            if (g.u < 0) continue;
             const Item &it = g.item;
             if (a.splits > 1) {
                 float *part = a.part + (int64_t)g.u * (2 * kRows) * (D + 2);
@@ -570,7 +653,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 }
 
 template <class T, int D>
-cudaError_t launch_pairs(PromptArgs &a, int sms, cudaStream_t s) {
+cudaError_t launch_pairs(PromptArgs &a, cudaStream_t s) {
     using M = Pairs<T, D>;
     cudaError_t e = allow_shared<kq_prompt_pairs<T, D>>(M::kBytes);
     if (e == cudaSuccess && a.nkeys > 0) {
@@ -584,8 +667,7 @@ cudaError_t launch_pairs(PromptArgs &a, int sms, cudaStream_t s) {
     const uint32_t box[3] = {64, (uint32_t)a.hb, (uint32_t)(a.tok / 2)};
     e = kqhost::values_map(a.q, M::kBf16, 3, dims, strides, box, &a.qmap);
     if (e != cudaSuccess) return e;
-    const int grid = (int)std::min<int64_t>(sms, (int64_t)a.items * a.splits);
-    kq_prompt_pairs<T, D><<<grid, kPairThreads, M::kBytes, s>>>(a);
+    kq_prompt_pairs<T, D><<<(unsigned)(a.items * a.splits), kPairThreads, M::kBytes, s>>>(a);
     return cudaGetLastError();
 }
 
