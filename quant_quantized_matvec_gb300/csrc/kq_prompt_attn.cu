@@ -10,15 +10,19 @@ cudaError_t prompt_f32(int d, PromptArgs &a, cudaStream_t s);
 cudaError_t prompt_f16(int d, PromptArgs &a, cudaStream_t s);
 cudaError_t prompt_bf16(int d, PromptArgs &a, cudaStream_t s);
 
-constexpr int kJoinThreads = 256, kJoinRows = 16;
+constexpr int kJoinThreads = 256, kJoinRows = 32;
 
-// 16 rows of an item a CTA, four values a thread: their parts in their order.
-// (A CTA an item: 130 us against 8, 40 items of 256 rows of width 128 in 7 parts.)
-template <class T>
+// 32 rows of an item a CTA, a lane each; a warp has some of their values and
+// joins the parts in their order.  Rows go out through shared memory.  (A CTA
+// an item: 130 us against 8, 40 items of 256 rows of width 128 in 7 parts.)
+template <class T, int D>
 __global__ void __launch_bounds__(kJoinThreads)
-    kq_prompt_join(const __grid_constant__ PromptArgs a, int d, int blocks) {
+    kq_prompt_join(const __grid_constant__ PromptArgs a, int blocks) {
+    constexpr int V = D / (kJoinThreads / 32);  // values of a thread
     __shared__ Item item;
-    if (threadIdx.x < 32) find_item(a, blockIdx.x, item, threadIdx.x);
+    __shared__ float tile[kJoinRows][D + 1];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    if (w == 0) find_item(a, blockIdx.x, item, lane);
     kq::wait_prerequisites();
     __syncthreads();
     const Item it = item;
@@ -26,34 +30,56 @@ __global__ void __launch_bounds__(kJoinThreads)
     const float factor = std::is_same<T, float>::value ? 1.f : fabsf(a.scale) * kLog2E;
     const float up = std::is_same<T, float>::value ? 32768.f : 1.f;
     const int rows = blocks * kRows, half = a.tok / blocks;
-    const int64_t each = (int64_t)rows * (d + 2);
+    // row r's place among the item's tokens and heads; -1: none
+    auto place = [&](int r, int &at, int &h) {
+        const int t = r % kRows / a.hb;
+        h = r % kRows - t * a.hb, at = r / kRows * half + t;
+        return t < half && at < it.nt && h < it.nh;
+    };
+    const int64_t each = (int64_t)rows * (D + 2);
     const float *part = a.part + (int64_t)blockIdx.x * a.splits * each;
-    for (int i = threadIdx.x; i < kJoinRows * (d / 4); i += kJoinThreads) {
-        const int r = blockIdx.y * kJoinRows + i / (d / 4), e = 4 * (i % (d / 4));
-        const int t = r % kRows / a.hb, h = r % kRows - t * a.hb, at = r / kRows * half + t;
-        if (t >= half || at >= it.nt || h >= it.nh) continue;
-        const int tok = it.tok0 + at;
-        const float *m = part + rows * d + r, *l = m + rows, *o = part + r * d + e;
-        // (the reference moves as the parts come, by 2^0 most of the time)
-        float top = -INFINITY, sum = 0.f;
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int k = 0; k < a.splits; ++k) {
-            const float mk = m[k * each], lk = l[k * each];
-            const float4 v = *reinterpret_cast<const float4 *>(o + k * each);
-            const float now = fmaxf(top, mk);
-            const float g = top == now ? 1.f : top == -INFINITY ? 0.f : exp2_fast((top - now) * factor);
-            const float f = mk == now ? 1.f : mk == -INFINITY ? 0.f : exp2_fast((mk - now) * factor);
-            top = now;
-            sum = fmaf(f, lk, sum * g);
-            y.x = fmaf(f, v.x, y.x * g), y.y = fmaf(f, v.y, y.y * g);
-            y.z = fmaf(f, v.z, y.z * g), y.w = fmaf(f, v.w, y.w * g);
-        }
-        // (an expired wait left a sum of NaN, also in rows that attend nothing)
-        const float inv = it.limit(tok) < 0 && sum == 0.f ? 0.f : __fdiv_rn(up, sum);
-        store4(static_cast<T *>(a.out) + ((int64_t)(it.first + tok) * a.q_heads + it.hq + h) * d + e,
-               make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+    const int r0 = blockIdx.y * kJoinRows;
+    const float *m = part + rows * D + r0 + lane, *l = m + rows;
+    const float *o = part + (r0 * D + w * V * 32) + lane;
+    // (the reference moves as the parts come, by 2^0 most of the time)
+    float top = -INFINITY, sum = 0.f, y[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) y[e] = 0.f;
+    for (int k = 0; k < a.splits; ++k) {
+        const float mk = m[k * each], lk = l[k * each];
+        float v[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = o[k * each + 32 * e];
+        const float now = fmaxf(top, mk);
+        const float g = top == now ? 1.f : top == -INFINITY ? 0.f : exp2_fast((top - now) * factor);
+        const float f = mk == now ? 1.f : mk == -INFINITY ? 0.f : exp2_fast((mk - now) * factor);
+        top = now;
+        sum = fmaf(f, lk, sum * g);
+#pragma unroll
+        for (int e = 0; e < V; ++e) y[e] = fmaf(f, v[e], y[e] * g);
     }
+    int at, h;
+    const bool on = place(r0 + lane, at, h);
+    // (an expired wait left a sum of NaN, also in rows that attend nothing)
+    const float inv = on && it.limit(it.tok0 + at) < 0 && sum == 0.f ? 0.f : __fdiv_rn(up, sum);
+#pragma unroll
+    for (int e = 0; e < V; ++e) tile[lane][w * V + e] = y[e] * inv;
+    __syncthreads();
+    for (int i = threadIdx.x; i < kJoinRows * (D / 4); i += kJoinThreads) {
+        const int r = i / (D / 4), e = 4 * (i % (D / 4));
+        if (!place(r0 + r, at, h)) continue;
+        store4(static_cast<T *>(a.out) +
+                   ((int64_t)(it.first + it.tok0 + at) * a.q_heads + it.hq + h) * D + e,
+               make_float4(tile[r][e], tile[r][e + 1], tile[r][e + 2], tile[r][e + 3]));
+    }
+}
+
+template <class T>
+cudaError_t launch_join(const PromptArgs &a, int d, int blocks, cudaStream_t s) {
+    const dim3 grid((unsigned)a.items, blocks * kRows / kJoinRows);
+    return d == 64    ? launch_early(kq_prompt_join<T, 64>, grid, kJoinThreads, 0, s, a, blocks)
+           : d == 128 ? launch_early(kq_prompt_join<T, 128>, grid, kJoinThreads, 0, s, a, blocks)
+                      : launch_early(kq_prompt_join<T, 256>, grid, kJoinThreads, 0, s, a, blocks);
 }
 
 // Tokens of an item of `blocks` blocks, items at most, and the parts into which
@@ -122,11 +148,9 @@ cudaError_t prompt_attention(const PromptCall &c, void *ws, int sms, unsigned in
                     : c.type == KQ_F16 ? prompt_f16(c.dim, a, s)
                                        : prompt_bf16(c.dim, a, s);
     if (e != cudaSuccess || a.splits == 1) return e;
-    const dim3 grid((unsigned)a.items, blocks * kRows / kJoinRows);
-    return c.type == KQ_F32 ? launch_early(kq_prompt_join<float>, grid, kJoinThreads, 0, s, a, c.dim, blocks)
-           : c.type == KQ_F16
-               ? launch_early(kq_prompt_join<__half>, grid, kJoinThreads, 0, s, a, c.dim, blocks)
-               : launch_early(kq_prompt_join<__nv_bfloat16>, grid, kJoinThreads, 0, s, a, c.dim, blocks);
+    return c.type == KQ_F32   ? launch_join<float>(a, c.dim, blocks, s)
+           : c.type == KQ_F16 ? launch_join<__half>(a, c.dim, blocks, s)
+                              : launch_join<__nv_bfloat16>(a, c.dim, blocks, s);
 }
 
 }  // namespace kqp

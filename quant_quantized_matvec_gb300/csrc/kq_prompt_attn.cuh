@@ -115,36 +115,45 @@ __device__ __forceinline__ int scan_max(int x, int lane) {
     return x;
 }
 
-// Walks the sequences, 32 at a time: body(b, first token, end, first key, key
-// end) for each lane's sequence (an empty one past the last), until it returns
-// true.  A start counts as the largest so far, within what there is.  By one
-// warp.
+// Where a walk over the sequences is: at number b0, with the largest starts
+// before it, and the blocks of rows before it.
+struct Place {
+    int b0 = 0, s = 0, k = 0, blocks = 0;
+};
+
+// Walks the sequences from `p` on, 32 at a time: body(b, first token, end, first
+// key, key end) for each lane's sequence (an empty one past the last), until it
+// returns true; p is then where it was.  A start counts as the largest so far,
+// within what there is.  By one warp.
 template <class F>
-__device__ __forceinline__ void walk(const PromptArgs &a, int lane, F &&body) {
-    int s_before = 0, k_before = 0;
-    for (int b0 = 0; b0 < a.nseq; b0 += 32) {
-        const int b = min(b0 + lane, a.nseq), b1 = min(b + 1, a.nseq);
-        auto runs = [&](const int32_t *start, int all, int &before, int &lo, int &hi) {
-            lo = max(scan_max(min(max(__ldg(start + b), 0), all), lane), before);
-            hi = max(lo, min(max(__ldg(start + b1), 0), all));
-            before = __shfl_sync(~0u, hi, 31);
+__device__ __forceinline__ void walk(const PromptArgs &a, int lane, Place &p, F &&body) {
+    while (p.b0 < a.nseq) {
+        const int b = min(p.b0 + lane, a.nseq), b1 = min(b + 1, a.nseq);
+        // (all loads at once)
+        const int x0 = __ldg(a.start + b), x1 = __ldg(a.start + b1);
+        const int y0 = a.kstart ? __ldg(a.kstart + b) : 0, y1 = a.kstart ? __ldg(a.kstart + b1) : 0;
+        auto run = [&](int x, int y, int all, int before, int &lo, int &hi) {
+            lo = max(scan_max(min(max(x, 0), all), lane), before);
+            hi = max(lo, min(max(y, 0), all));
         };
         int lo, hi, klo, khi;
-        runs(a.start, a.ntok, s_before, lo, hi);
-        if (a.kstart) runs(a.kstart, a.nkeys, k_before, klo, khi);
+        run(x0, x1, a.ntok, p.s, lo, hi);
+        if (a.kstart) run(y0, y1, a.nkeys, p.k, klo, khi);
         else klo = lo, khi = hi;
         if (body(b, lo, hi, klo, khi)) return;
+        p.b0 += 32;
+        p.s = __shfl_sync(~0u, hi, 31), p.k = __shfl_sync(~0u, khi, 31);
     }
 }
 
-// Item `i` of the call into shared memory, by warp 0; found = 0 past the last.
-__device__ __forceinline__ void find_item(const PromptArgs &a, int i, Item &it, int lane) {
+// Item `i` of the call into shared memory, by a warp; found = 0 past the last.
+// p: where the walk for a lower item ended, or the beginning.
+__device__ __forceinline__ void find_item(const PromptArgs &a, int i, Item &it, int lane, Place &p) {
     const int across = a.kv_heads * a.hblocks;
     const int blk = i / across, h = i - blk * across;
     if (lane == 0) it.found = 0;
     __syncwarp();
-    int before = 0;
-    walk(a, lane, [&](int b, int lo, int hi, int klo, int khi) {
+    walk(a, lane, p, [&](int b, int lo, int hi, int klo, int khi) {
         const int blocks = (hi - lo + a.tok - 1) / a.tok;
         int upto = blocks;
 #pragma unroll
@@ -152,10 +161,12 @@ __device__ __forceinline__ void find_item(const PromptArgs &a, int i, Item &it, 
             const int v = __shfl_up_sync(~0u, upto, o);
             if (lane >= o) upto += v;
         }
-        upto += before;
+        upto += p.blocks;
         const unsigned past = __ballot_sync(~0u, upto > blk);
-        before = __shfl_sync(~0u, upto, 31);
-        if (past == 0) return false;
+        if (past == 0) {
+            p.blocks = __shfl_sync(~0u, upto, 31);
+            return false;
+        }
         if (lane == __ffs(past) - 1) {
             const int at = upto - 1 - blk;  // the last block first
             it.seq = b, it.first = lo, it.n = hi - lo, it.kfirst = klo, it.m = khi - klo;
@@ -168,6 +179,10 @@ __device__ __forceinline__ void find_item(const PromptArgs &a, int i, Item &it, 
         return true;
     });
     __syncwarp();
+}
+__device__ __forceinline__ void find_item(const PromptArgs &a, int i, Item &it, int lane) {
+    Place p;
+    find_item(a, i, it, lane, p);
 }
 
 // 32-bit words of two 16-bit values of which one is not finite.
@@ -217,7 +232,8 @@ __global__ void __launch_bounds__(kSplitThreads)
     if (tid == 0) found[0] = 0, tops = 0, bad = 0;
     if (tid < 32) {
         __syncwarp();
-        walk(a, lane, [&](int b, int lo, int hi, int klo, int khi) {
+        Place p;
+        walk(a, lane, p, [&](int b, int lo, int hi, int klo, int khi) {
             const int base = klo / TK + b, tiles = b < a.nseq ? (khi - klo + TK - 1) / TK : 0;
             const bool here = slot >= base && slot < base + tiles;
             if (here) found[1] = klo + (slot - base) * TK, found[2] = min(TK, khi - found[1]), found[0] = 1;
@@ -600,13 +616,11 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
         if (dead()) l = quiet_nan();
         if (a.splits > 1) {
             float *part = a.part + (int64_t)blockIdx.x * kRows * (D + 2);
-            float4 *to = reinterpret_cast<float4 *>(part + r * D + c0);
-            if (on) {
+            // by values, of 32 rows each: part[32 rows][D][32]
+            float *to = part + (r - lane) * D + c0 * 32 + lane;
 #pragma unroll
-                for (int k = 0; k < M::OC / 4; ++k)
-                    to[k] = make_float4(O[4 * k], O[4 * k + 1], O[4 * k + 2], O[4 * k + 3]);
-                if (c0 == 0) part[kRows * D + r] = m, part[kRows * (D + 1) + r] = l;
-            }
+            for (int k = 0; k < M::OC; ++k) to[32 * k] = O[k];
+            if (c0 == 0) part[kRows * D + r] = m, part[kRows * (D + 1) + r] = l;
         } else if (on) {
             // (a row that attends something and has no sum has scores of
             // -infinity only)

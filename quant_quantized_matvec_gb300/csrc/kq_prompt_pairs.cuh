@@ -37,9 +37,15 @@ struct Pairs {
     static constexpr float kUp = kBf16 ? 0.f : 7.f;
     static_assert(kP + TK / 2 <= kBlock && kSlots >= 5 && TK % 16 == 0, "layout");
 };
-constexpr int kPairThreads = 512, kPairOther = 8;  // first warp that is not softmax
-// Registers after the split: 256 * 200 + 256 * 56 = the 512 * 128 at launch.
+// Warps: 8 of softmax; two that issue products, one for copies, one that finds
+// units; four that clean values.
+constexpr int kPairThreads = 512, kPairOther = 8, kPairClean = 12;
+// Registers after the split: 256 * 200 + 256 * 56, the 512 * 128 at launch.
 constexpr int kPairSoftRegs = 200, kPairOtherRegs = 56;
+constexpr int kPairLaunchRegs = 65536 / kPairThreads;
+static_assert(256 * kPairSoftRegs + 256 * kPairOtherRegs <= kPairThreads * kPairLaunchRegs &&
+                  kPairSoftRegs > kPairLaunchRegs && kPairOtherRegs < kPairLaunchRegs,
+              "setmaxnreg: the shares, and the way each goes");
 constexpr float kPairLazy = 8.f;  // log2 of the growth that is not corrected
 
 // A unit: a part of an item's keys, with what each block sees of it.
@@ -51,13 +57,15 @@ struct Unit {
     int32_t u;      // its number
 };
 
+constexpr int kUnits = 3;  // that are being worked on: a third is found while two are
+
 struct PairShared {
     uint4 answer;  // of ask_for_cta
-    Unit unit[2];
-    uint64_t ufull[2], ufree[2], qfull[2], qfree[2], full[8], empty[8], sdone[2], sfree[2], pready[2],
-        odone[2], vraw[4], vclean[4], given, drain[2];
+    Unit unit[kUnits];
+    uint64_t ufull[kUnits], ufree[kUnits], qfull[2], qfree[2], full[8], empty[8], sdone[2], sfree[2], pready[2],
+        odone[2], vraw[4], vclean[4], given, begun, drain[2];
     uint32_t tmem;
-    int dead, bad[2];
+    int dead, bad[kUnits];
     int asked, claimed;  // after an expired wait: an answer to come; a unit that no role has seen
 };
 static_assert(sizeof(PairShared) <= 2048, "layout");
@@ -105,8 +113,8 @@ __device__ __forceinline__ int cta_given(uint32_t at) {
 }
 
 // Unit `u` into shared memory, by one warp; false past the last.
-__device__ __forceinline__ bool find_unit(const PromptArgs &a, int u, int tile, Unit &g, int lane) {
-    find_item(a, u / a.splits, g.item, lane);
+__device__ __forceinline__ bool find_unit(const PromptArgs &a, int u, int tile, Unit &g, int lane, Place &p) {
+    find_item(a, u / a.splits, g.item, lane, p);
     const Item &it = g.item;
     const bool found = it.found != 0;
     if (found && lane == 0) {
@@ -127,24 +135,15 @@ __device__ __forceinline__ bool find_unit(const PromptArgs &a, int u, int tile, 
     return found;
 }
 
-// Four lanes of a row each hold four 16-byte chunks of their own row: turned, so
-// that chunk j of the rows of lanes 4 q .. 4 q + 3 is in lane 4 q + j, and four
-// lanes write 64 bytes of one row.  v: chunk c in words 4 c .. 4 c + 3.
-__device__ __forceinline__ void turn_chunks(uint32_t *v, int lane) {
-#pragma unroll
-    for (int o = 1; o < 4; o *= 2) {
-        const bool up = lane & o;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            if (c & o) continue;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                uint32_t &x = v[4 * c + e], &y = v[4 * (c + o) + e];
-                const uint32_t got = __shfl_xor_sync(~0u, up ? x : y, o);
-                if (up) x = got;
-                else y = got;
-            }
-        }
+// 32 bytes of a row.
+__device__ __forceinline__ void store32(void *p, const uint32_t *v, bool aligned) {
+    if (aligned) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
+                     "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<uint4 *>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
     }
 }
 
@@ -160,10 +159,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     auto bar = [&](const uint64_t &b) { return kq::smem_addr(&b); };
 
-    if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
-            kq::mbar_init(bar(cm.ufull[i]), 1);
-            kq::mbar_init(bar(cm.ufree[i]), 8 + 3 + 4);
+    if (w == 0) {  // a lane a barrier, or a few
+        const int i = lane;
+        if (i < 2) {
             kq::mbar_init(bar(cm.qfull[i]), 1);
             kq::mbar_init(bar(cm.qfree[i]), 1);
             kq::mbar_init(bar(cm.sdone[i]), 1);
@@ -171,20 +169,34 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             kq::mbar_init(bar(cm.pready[i]), 4);
             kq::mbar_init(bar(cm.odone[i]), 1);
             kq::mbar_init(bar(cm.drain[i]), 1);
+        } else if (i < 10) {
+            kq::mbar_init(bar(cm.full[i - 2]), 1), kq::mbar_init(bar(cm.empty[i - 2]), 2);
+        } else if (i < 14) {
+            kq::mbar_init(bar(cm.vraw[i - 10]), 1), kq::mbar_init(bar(cm.vclean[i - 10]), 4);
+        } else if (i < 14 + kUnits) {
+            kq::mbar_init(bar(cm.ufree[i - 14]), 8 + 3 + 4);
+        } else if (i == 31) {
+            kq::mbar_init(bar(cm.given), 1), kq::mbar_init(bar(cm.begun), 1);
+            for (int j = 0; j < kUnits; ++j) kq::mbar_init(bar(cm.ufull[j]), 1);
+            cm.dead = 0, cm.asked = 0, cm.claimed = -1;
         }
-        for (int i = 0; i < 8; ++i) kq::mbar_init(bar(cm.full[i]), 1), kq::mbar_init(bar(cm.empty[i]), 2);
-        for (int i = 0; i < 4; ++i) kq::mbar_init(bar(cm.vraw[i]), 1), kq::mbar_init(bar(cm.vclean[i]), 4);
-        kq::mbar_init(bar(cm.given), 1);
-        cm.dead = cm.bad[0] = cm.bad[1] = 0;
-        cm.unit[0].u = cm.unit[1].u = -1;
-        cm.asked = 0, cm.claimed = -1;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    if (w == kPairOther) {
+    } else if (w == kPairOther) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                          kq::smem_addr(&cm.tmem))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    } else if (w == kPairOther + 2 && lane < 3) {
+        const CUtensorMap *map = lane == 0 ? &a.qmap : lane == 1 ? &a.kmap : &a.vmap;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+    }
+    // the first unit: the CTA's number
+    Place place;
+    if (w == kPairOther + 3) {
+        if (lane < kUnits) cm.bad[lane] = 0, cm.unit[lane].u = -1;
+        __syncwarp();
+        const bool found = find_unit(a, blockIdx.x, TK, cm.unit[0], lane, place);
+        if (!found && lane == 0) cm.unit[0].u = -1;
     }
     tc_before();
     __syncthreads();
@@ -203,11 +215,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     // wait there is none.)  Its place is handed back once all have read it, and
     // the softmax warps are done with it.
     auto next = [&](int k, Unit &g) {
-        wait(cm.ufull[k & 1], k >> 1);
+        const int at = k % kUnits;
+        wait(cm.ufull[at], k / kUnits);
         if (__any_sync(~0u, dead())) return false;
-        g = cm.unit[k & 1];
+        g = cm.unit[at];
         __syncwarp();
-        if (w >= kPairOther && lane == 0) kq::mbar_arrive(bar(cm.ufree[k & 1]));
+        if (lane == 0) kq::mbar_arrive(bar(cm.ufree[at]));
         return g.u >= 0;
     };
     // Copies of tiles, of values that are cleaned, and of blocks' queries, that
@@ -224,11 +237,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const uint32_t sa = mine + M::kS, pa = mine + M::kP, oa = mine + M::kO;
         const float sc = fmaxf(fabsf(a.scale) * kLog2E, 1.2e-38f);  // (not 0: -infinity * 0)
         const int half = a.tok / 2, t = r / a.hb, hq = r - t * a.hb;
+        const bool wide = ((uintptr_t)a.out & 31) == 0;
         int turn = 0;  // tiles of all units
         for (int k = 0;; ++k) {
-            wait(cm.ufull[k & 1], k >> 1);
+            const int slot = k % kUnits;
+            wait(cm.ufull[slot], k / kUnits);
             if (__any_sync(~0u, dead())) break;
-            const Unit &g = cm.unit[k & 1];  // (ours until it is handed back)
+            const Unit &g = cm.unit[slot];  // (ours until it is handed back)
             if (g.u < 0) break;
             const Item &it = g.item;
             const int tok = it.tok0 + block * half + t;
@@ -324,68 +339,68 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             if (count) wait(cm.odone[block], turn - 1);
             if (__any_sync(~0u, dead())) break;
             tc_after();
-            const float inv = limit < 0 ? 0.f : __fdiv_rn(1.f, l);
-            const bool bad = *(volatile int *)&cm.bad[k & 1] != 0;
-            T *to = static_cast<T *>(a.out) +
-                    ((int64_t)(it.first + it.tok0 + block * half) * a.q_heads + it.hq) * D;
-            const uint32_t place = t * a.q_heads + hq;  // the row's, from there
-            const uint32_t rows = __ballot_sync(~0u, on);
-            float *part = a.part + (int64_t)g.u * (2 * kRows) * (D + 2);
             const int row = block * kRows + r;
-#pragma unroll 1
-            for (int j = 0; j < D; j += 32) {
-                uint32_t o[32];
+            const float inv = limit < 0 ? 0.f : __fdiv_rn(1.f, l);
+            const bool bad = *(volatile int *)&cm.bad[slot] != 0;
+            T *to = static_cast<T *>(a.out) + ((int64_t)(it.first + tok) * a.q_heads + it.hq + hq) * D;
+            float *part = a.part + (int64_t)g.u * (2 * kRows) * (D + 2);
+            // half of O's columns, with what the tiles left out: values that
+            // are not finite
+            auto half_of = [&](uint32_t (&o)[D / 2], int c0) {
                 if (count) {
-                    tc_load32(o, oa + j);
+#pragma unroll
+                    for (int j = 0; j < D / 2; j += 32) tc_load32(o + j, oa + c0 + j);
                     tc_loaded();
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = 0;
+                    for (int e = 0; e < D / 2; ++e) o[e] = 0;
                 }
                 if (bad && on) {
-                    // values that are not finite, of the tiles that left them out
                     for (int y = whole * TK; y < min(g.t1 * TK, limit + 1); ++y) {
                         const T *v = static_cast<const T *>(a.v) + (int64_t)(it.kfirst + y) * a.v_stride +
-                                     (int64_t)it.head * D + j;
+                                     (int64_t)it.head * D + c0;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
+                        for (int e = 0; e < D / 2; ++e) {
                             const float x = to_f32<T>(v[e]);
                             if (!(fabsf(x) < INFINITY)) o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
                         }
                     }
                 }
                 __syncwarp();
-                // chunk `lane & 3` of the rows of four lanes
-                const int four = lane & ~3, mine4 = 4 * (lane & 3);
-                if (a.splits > 1) {
+            };
+            uint32_t o[D / 2];
+            half_of(o, 0);
+            if (a.splits > 1) {
+                // by values, of 32 rows each: part[32 rows][D][32]
+                uint32_t *to = reinterpret_cast<uint32_t *>(part) + (row - lane) * D + lane;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 16) {
-                        turn_chunks(o + e, lane);
+                for (int e = 0; e < D / 2; ++e) to[32 * e] = o[e];
+                half_of(o, D / 2);
 #pragma unroll
-                        for (int z = 0; z < 4; ++z)
-                            if (rows >> (four + z) & 1)
-                                *reinterpret_cast<uint4 *>(part + (row - lane + four + z) * D + j + e + mine4) =
-                                    make_uint4(o[e + 4 * z], o[e + 4 * z + 1], o[e + 4 * z + 2], o[e + 4 * z + 3]);
+                for (int e = 0; e < D / 2; ++e) to[32 * (D / 2 + e)] = o[e];
+                part[2 * kRows * D + row] = m, part[2 * kRows * (D + 1) + row] = l;
+            } else {
+                uint32_t q[D / 4];
+                auto round = [&]() {
+#pragma unroll
+                    for (int e = 0; e < D / 4; ++e)
+                        q[e] = pack2<T>(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                };
+                auto write = [&](int c0) {
+                    if (on) {
+#pragma unroll
+                        for (int j = 0; j < D / 4; j += 8) store32(to + c0 + 2 * j, q + j, wide);
                     }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        o[e] = pack2<T>(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-                    turn_chunks(o, lane);
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        const uint32_t at = __shfl_sync(~0u, place, four + z);
-                        if (rows >> (four + z) & 1)
-                            *reinterpret_cast<uint4 *>(to + (int64_t)at * D + j + 2 * mine4) =
-                                make_uint4(o[4 * z], o[4 * z + 1], o[4 * z + 2], o[4 * z + 3]);
-                    }
-                }
-                __syncwarp();
+                };
+                round();
+                half_of(o, D / 2);
+                write(0);
+                round();
+                write(D / 2);
             }
-            if (a.splits > 1 && on) part[2 * kRows * D + row] = m, part[2 * kRows * (D + 1) + row] = l;
             tc_before();
             __syncwarp();
-            if (lane == 0) kq::mbar_arrive(bar(cm.ufree[k & 1]));
+            if (lane == 0) kq::mbar_arrive(bar(cm.ufree[slot]));
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairOtherRegs));
@@ -394,29 +409,51 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             // A CTA begins with the unit of its number, and then takes over those
             // of CTAs that have not begun, in their order: a sequence's longest
             // first.  (Dealt out evenly beforehand, in rounds there and back:
-            // 234 against 2xx us for nine prompts of up to 2049 tokens.)
+            // 234 against 224 us for nine prompts of up to 2049 tokens.)
             int u = blockIdx.x;
-            for (int k = 0;; ++k) {
-                if (k >= 2) wait(cm.ufree[k & 1], (k >> 1) - 1);
-                if (__any_sync(~0u, dead())) {
-                    if (lane == 0) cm.claimed = u;
-                    break;
-                }
-                Unit &g = cm.unit[k & 1];
-                const bool found = u >= 0 && find_unit(a, u, TK, g, lane);
-                if (lane == 0) {
-                    if (!found) g.u = -1;
-                    *(volatile int *)&cm.bad[k & 1] = 0;
-                    __threadfence_block();
-                    kq::mbar_arrive(bar(cm.ufull[k & 1]));
-                }
-                __syncwarp();
-                if (!found) break;
+            auto ask = [&]() {
                 if (lane == 0) {
                     kq::mbar_expect_tx(bar(cm.given), 16);
                     ask_for_cta(kq::smem_addr(&cm.answer), bar(cm.given));
                 }
                 __syncwarp();
+            };
+            for (int k = 0;; ++k) {
+                const int slot = k % kUnits;
+                if (k >= kUnits) wait(cm.ufree[slot], k / kUnits - 1);
+                if (__any_sync(~0u, dead())) {
+                    if (lane == 0) cm.claimed = u;
+                    break;
+                }
+                Unit &g = cm.unit[slot];
+                const bool found = k == 0 ? g.u >= 0 : u >= 0 && find_unit(a, u, TK, g, lane, place);
+                if (lane == 0) {
+                    if (!found) g.u = -1;
+                    *(volatile int *)&cm.bad[slot] = 0;
+                    __threadfence_block();
+                    kq::mbar_arrive(bar(cm.ufull[slot]));
+                }
+                __syncwarp();
+                if (!found) {
+                    // Units past the last (there are at most so many): their
+                    // CTAs need not begin.
+                    for (int n = k; u >= 0; ++n) {
+                        ask();
+                        wait(cm.given, n);
+                        if (__any_sync(~0u, dead())) {
+                            if (lane == 0) cm.asked = n + 1;
+                            break;
+                        }
+                        u = cta_given(kq::smem_addr(&cm.answer));
+                        __syncwarp();
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    }
+                    break;
+                }
+                // The next one is taken when the last few copies for this one are
+                // made: not before, as others may be free earlier.
+                wait(cm.begun, k);
+                ask();
                 wait(cm.given, k);
                 if (__any_sync(~0u, dead())) {
                     if (lane == 0) cm.asked = k + 1;
@@ -432,25 +469,25 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             for (int k = 0; next(k, g); ++k) {
                 const Item &it = g.item;
                 const int count = g.t1 - g.t0;
-                if (count == 0) continue;
                 if (lane == 0) {
                     const uint32_t bytes = (uint32_t)(a.tok / 2) * a.hb * 128;
+                    // The queries' place is free when the last S of the unit before
+                    // has been formed: a few tiles are copied before that.
+                    const int when = k == 0 ? 0 : min(3, 2 * count - 1);
+                    if (count == 0) kq::mbar_arrive(bar(cm.begun));
                     for (int n = 0; n < 2 * count; ++n) {
-                        // first keys, then the queries, then the rest by turns
-                        if (n == 1) {
-                            for (int b = 0; b < 2; ++b) {
-                                if (g.n[b] == 0) continue;
-                                if (queries[b]) wait(cm.qfree[b], queries[b] - 1);
-                                if (dead()) break;
-                                kq::mbar_expect_tx(bar(cm.qfull[b]), bytes * (D / 64));
-                                for (int c = 0; c < D / 64; ++c)
-                                    tensor3d_g2s(base + M::kControl + b * M::kQTile + c * (kRows * 128), &a.qmap,
-                                                 64 * c, it.hq, it.first + it.tok0 + b * (a.tok / 2),
-                                                 bar(cm.qfull[b]));
-                                ++queries[b];
-                            }
+                        // (asking and finding take two microseconds, about two tiles)
+                        if (n == max(0, 2 * count - 8)) kq::mbar_arrive(bar(cm.begun));
+                        for (int b = 0; b < 2 && n == when; ++b) {
+                            if (g.n[b] == 0) continue;
+                            if (queries[b]) wait(cm.qfree[b], queries[b] - 1);
+                            if (dead()) break;
+                            kq::mbar_expect_tx(bar(cm.qfull[b]), bytes * (D / 64));
+                            for (int c = 0; c < D / 64; ++c)
+                                tensor3d_g2s(base + M::kControl + b * M::kQTile + c * (kRows * 128), &a.qmap, 64 * c,
+                                             it.hq, it.first + it.tok0 + b * (a.tok / 2), bar(cm.qfull[b]));
+                            ++queries[b];
                         }
-                        if (dead()) break;
                         const int s = copied % M::kSlots;
                         if (copied >= M::kSlots) wait(cm.empty[s], copied / M::kSlots - 1);
                         if (dead()) break;
@@ -477,7 +514,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const uint32_t is = mma_idesc(TK, M::kBf16, false) | (a.scale < 0.f ? 1u << 13 : 0u);
             constexpr uint32_t io = mma_idesc(D, M::kBf16, true);
             int tile = 0, cleaned = 0;  // tiles of both blocks so far, and those that were cleaned
-            int turn = 0, have = 0;     // tiles of this block; units with queries
+            int turn = 0, have = 0;     // tiles of this block; units with some
             Unit g;
             for (int k = 0; next(k, g); ++k) {
                 const int count = g.t1 - g.t0, n = g.n[b], from = count - n;
@@ -492,8 +529,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 bool stop = false;
                 for (int i = 0; i < from; ++i) {  // tiles that only the other block sees
                     for (int x = 2 * (tile + i); x < 2 * (tile + i) + 2; ++x) {
+                        // (not for values to be cleaned: a slot is only copied to
+                        // again when its values four tiles ago are done with)
                         there(x);
-                        if (x & 1) clean(i);
                         if (__any_sync(~0u, dead())) stop = true;
                         if (stop) break;
                         if (lane == 0) kq::mbar_arrive(bar(cm.empty[x % M::kSlots]));
@@ -555,23 +593,23 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 cleaned += g.edges;
                 turn += n;
             }
-        } else if (w >= kPairOther + 4) {
+        } else if (w >= kPairClean) {
             // ------------- values that are not finite, of tiles seen in part
             int tile = 0, cleaned = 0;
             Unit g;
             for (int k = 0; next(k, g); ++k) {
                 for (int i = 0; i < g.edges; ++i, ++cleaned) {
-                    const int n = 2 * (tile + i) + 1, s = n % M::kSlots;
+                    const int s = (2 * (tile + i) + 1) % M::kSlots;  // (values are the odd copies)
                     wait(cm.vraw[cleaned & 3], cleaned >> 2);
                     if (__any_sync(~0u, dead())) break;
                     uint4 *v = reinterpret_cast<uint4 *>(smem + M::kRing + s * M::kTile) +
-                               (w - kPairOther - 4) * (M::kTile / 64) + lane;
-                    bool found = false;
-#pragma unroll 4
+                               (w - kPairClean) * (M::kTile / 64) + lane;
+                    bool odd = false;
+#pragma unroll 5
                     for (int c = 0; c < M::kTile / 64; c += 32) {
                         uint4 x = v[c];
                         if (not_finite<T>(x.x) | not_finite<T>(x.y) | not_finite<T>(x.z) | not_finite<T>(x.w)) {
-                            found = true;
+                            odd = true;
                             uint32_t *e = &x.x;
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
@@ -582,7 +620,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                             v[c] = x;
                         }
                     }
-                    if (found) *(volatile int *)&cm.bad[k & 1] = 1;
+                    if (odd) *(volatile int *)&cm.bad[k % kUnits] = 1;
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                     if (lane == 0) kq::mbar_arrive(bar(cm.vclean[cleaned & 3]));
@@ -618,15 +656,17 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             if (kq::mbar_wait(bar(cm.given), (cm.asked - 1) & 1, kq::kWaitLimitNs))
                 cm.claimed = cta_given(kq::smem_addr(&cm.answer));
         }
-        for (int k = 0; k < 3; ++k) {  // the units that roles were at, and one that none has seen
+        for (int k = 0; k <= kUnits; ++k) {  // the units that roles were at, and one that none has seen
             __syncthreads();
-            if (k == 2) {
+            if (k == kUnits) {
                 const int u = cm.claimed;
                 __syncthreads();
-                if (w == 0 && (u < 0 || !find_unit(a, u, TK, cm.unit[0], lane)) && lane == 0) cm.unit[0].u = -1;
+                Place p;
+                if (w == 0 && (u < 0 || !find_unit(a, u, TK, cm.unit[0], lane, p)) && lane == 0)
+                    cm.unit[0].u = -1;
                 __syncthreads();
             }
-            const Unit &g = cm.unit[k & 1];
+            const Unit &g = cm.unit[k % kUnits];
             if (g.u < 0) continue;
             const Item &it = g.item;
             if (a.splits > 1) {
