@@ -170,7 +170,7 @@ def load(path: str | None = None):
                                           vp]
         lib.kq_verify_tree.argtypes = [i32, i64, i32, vp, vp, vp, vp, i64, vp, i64, i32, vp, vp,
                                        vp, vp, vp, vp]
-        lib.kq_norm_rope.argtypes = [ctypes.POINTER(KqNormPart), i32, i32, i32, i64, i32,
+        lib.kq_norm_rope.argtypes = [vp, i32, i32, i32, i64, i32,
                                      ctypes.c_float, vp, vp, i64, i32, i32, vp]
         lib.kq_prompt_workspace_bytes.argtypes = [i32, i32, i64, i64, i32, i32, i32]
         lib.kq_prompt_workspace_bytes.restype = i64

@@ -6,9 +6,10 @@
 // logits, a sorted list with one entry a lane.  An entry is a 64-bit number,
 // the logit's bits turned to order like it above the token's complement, so
 // all differ and any order of merging gives the same list.  A batch is looked
-// at only where a value passes the list's last entry: few are merged in one by
-// one, many by a sorting network of the lanes' largest and a merge.  Lists and
-// sums are joined by warps, then over a cluster of CTAs that share a row.
+// at only where its largest reaches what some warp of the CTA holds `top` values
+// of already: few are merged in one by one, many by a sorting network of the
+// lanes' largest and a merge.  Lists and sums are joined by warps, then over a
+// cluster of CTAs that share a row.
 //
 // Bound by memory for many rows, by latency for few.
 #include <cooperative_groups.h>
@@ -90,7 +91,17 @@ __device__ __forceinline__ Sums joined(Sums a, Sums b) {
     return {m, a.s + b.s, a.t + b.t};
 }
 
+// A value that orders as it does, for atomics; never a NaN.
+__device__ __forceinline__ uint32_t order_of(float x) {
+    const uint32_t b = __float_as_uint(x + 0.f);
+    return b ^ (b >> 31 ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ __forceinline__ float ordered(uint32_t k) {
+    return __uint_as_float(k >> 31 ? k ^ 0x80000000u : ~k);
+}
+
 struct ScoreShared {
+    uint32_t bar;  // order_of a value that `top` values of some warp reach
     Key list[kScoreWarps][32];
     Sums sums[kScoreWarps];
     // of the cluster's CTAs, gathered in the first
@@ -128,9 +139,10 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
     Sums mine = {-INFINITY, 0.f, 0.f};
     Key list = 0;  // (below every key)
     Key last = 0;  // the list's entry that a candidate has to pass
-    float bar = -INFINITY;
-    for (int j0 = lo; j0 < hi; j0 += kScoreThreads * kBatchValues) {
-        float v[kBatchValues];
+    if (tid == 0) sh.bar = order_of(-INFINITY);
+    __syncthreads();
+    // A batch's values; the next one's are on their way while it is looked at.
+    auto load = [&](int j0, float (&v)[kBatchValues]) {
         const int first = j0 + tid * V;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -153,62 +165,99 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
                     v[V * r + i] = j + i >= skew && j + i < hi ? to_f32<T>(line[j + i]) : -INFINITY;
             }
         }
-        float top = mine.m;
-        bool found = false;
+    };
+    constexpr int kStep = kScoreThreads * kBatchValues;
+    float ahead[kBatchValues];
+    load(lo, ahead);
+    for (int j0 = lo; j0 < hi; j0 += kStep) {
+        float v[kBatchValues];
 #pragma unroll
-        for (int i = 0; i < kBatchValues; ++i) top = fmaxf(top, v[i]);
+        for (int i = 0; i < kBatchValues; ++i) v[i] = ahead[i];
+        const int first = j0 + tid * V;
+        if (j0 + kStep < hi) load(j0 + kStep, ahead);
+        float most = v[0];
+#pragma unroll
+        for (int i = 1; i < kBatchValues; ++i) most = fmaxf(most, v[i]);
+        const float top = fmaxf(mine.m, most);
         mine = about(mine, top);
         const float from = top == -INFINITY ? 0.f : top;
-        float s0 = 0.f, s1 = 0.f, t0 = 0.f, t1 = 0.f;
+        float2 s2 = make_float2(0.f, 0.f), t2 = s2;
 #pragma unroll
         for (int i = 0; i < kBatchValues; i += 2) {
-            const float d0 = (v[i] - from) * kLog2e, d1 = (v[i + 1] - from) * kLog2e;
-            const float e0 = exp2_of(d0), e1 = exp2_of(d1);
-            s0 += e0, s1 += e1;
-            t0 = fmaf(e0, fmaxf(d0, kFar), t0), t1 = fmaf(e1, fmaxf(d1, kFar), t1);
-            // (not below: a NaN is a candidate too)
-            found |= !(v[i] < bar) || !(v[i + 1] < bar);
+            const float2 d = mul2(add2(make_float2(v[i], v[i + 1]), make_float2(-from, -from)),
+                                  make_float2(kLog2e, kLog2e));
+            const float2 e = make_float2(exp2_of(d.x), exp2_of(d.y));
+            s2 = add2(s2, e);
+            t2 = fma2(e, make_float2(fmaxf(d.x, kFar), fmaxf(d.y, kFar)), t2);
         }
-        mine.s += s0 + s1, mine.t += t0 + t1;
-        if (a.top == 0 || !__any_sync(~0u, found)) continue;
-        // ---- candidates: by turns each lane's largest that is not in yet
+        const float sum = s2.x + s2.y;
+        mine.s += sum, mine.t += t2.x + t2.y;
+        if (a.top == 0) continue;
+        if (j0 == lo) {
+            // The first batch: `top` lanes' largest are a bound at once.
+            float x = most != most ? -INFINITY : most;
+#pragma unroll
+            for (int n = 2; n <= 32; n *= 2)
+#pragma unroll
+                for (int o = n / 2; o; o /= 2) {
+                    const float other = __shfl_xor_sync(~0u, x, o);
+                    x = ((lane & o) == 0) == ((lane & n) == 0) ? fmaxf(x, other) : fminf(x, other);
+                }
+            if (lane == a.top - 1) atomicMax(&sh.bar, order_of(x));
+        }
+        // (a NaN is a candidate too, and shows in the sum)
+        const float bar = ordered(*(volatile uint32_t *)&sh.bar);
+        if (!__any_sync(~0u, !(most < bar) || sum != sum)) continue;
+        // ---- candidates
         uint32_t left = 0;
 #pragma unroll
         for (int i = 0; i < kBatchValues; ++i) {
             const int j = first + (i / V) * kScoreThreads * V + i % V;
-            if (j >= skew && j < hi && key_of(v[i], j - skew) > last) left |= 1u << i;
+            if (!(v[i] < bar) && j >= skew && j < hi) left |= 1u << i;
         }
-        while (true) {
-            Key best = 0;
-            int at = 0;
+        const int many = __reduce_add_sync(~0u, __popc(left));
+        if (many <= 12) {
+            // one by one
 #pragma unroll
             for (int i = 0; i < kBatchValues; ++i) {
                 const int j = first + (i / V) * kScoreThreads * V + i % V;
-                const Key k = key_of(v[i], j - skew);
-                if (left >> i & 1) {
-                    if (k <= last) left &= ~(1u << i);
-                    else if (k > best) best = k, at = i;
-                }
-            }
-            unsigned who = __ballot_sync(~0u, best != 0);
-            if (who == 0) break;
-            if (best) left &= ~(1u << at);
-            if (__popc(who) > 6) {
-                list = merged(list, sorted(best, lane), lane);
-            } else {
+                unsigned who = __ballot_sync(~0u, left >> i & 1);
                 while (who) {
-                    const Key k = __shfl_sync(~0u, best, __ffs(who) - 1);
+                    const int at = __ffs(who) - 1;
                     who &= who - 1;
+                    const Key k = key_of(__shfl_sync(~0u, v[i], at), __shfl_sync(~0u, j, at) - skew);
                     const Key up = __shfl_up_sync(~0u, list, 1);
                     const int place = __popc(__ballot_sync(~0u, list > k));
                     list = lane < place ? list : lane == place ? k : up;
                 }
             }
-            last = __shfl_sync(~0u, list, a.top - 1);
+        } else {
+            // by turns each lane's largest that is not in yet
+            while (true) {
+                Key best = 0;
+                int at = 0;
+#pragma unroll
+                for (int i = 0; i < kBatchValues; ++i) {
+                    const int j = first + (i / V) * kScoreThreads * V + i % V;
+                    const Key k = key_of(v[i], j - skew);
+                    if (left >> i & 1) {
+                        if (k <= last) left &= ~(1u << i);
+                        else if (k > best) best = k, at = i;
+                    }
+                }
+                if (!__any_sync(~0u, best != 0)) break;
+                if (best) left &= ~(1u << at);
+                list = merged(list, sorted(best, lane), lane);
+                last = __shfl_sync(~0u, list, a.top - 1);
+            }
         }
-        // (a NaN at the list's end lets no number pass, only another NaN)
-        bar = last == 0 ? -INFINITY : value_of(last);
-        if (bar != bar) bar = INFINITY;
+        const Key now = __shfl_sync(~0u, list, a.top - 1);
+        if (now != last || many > 12) {
+            last = now;
+            // (where the list ends with a NaN, no number passes)
+            const float x = value_of(last);
+            if (lane == 0 && last) atomicMax(&sh.bar, order_of(x != x ? INFINITY : x));
+        }
     }
     // ---- joined over the warp, the CTA, the cluster
 #pragma unroll

@@ -80,8 +80,6 @@ kq_status kq_norm_rope(const kq_norm_part *parts, int n, int type, int out_type,
         if (bad_stride(p.stride, row, size) || bad_stride(p.out_stride, row, out_size))
             return KQ_ERR_SHAPE;
         a.part[i] = p;
-        a.heads += p.heads;
-        a.upto[i] = a.heads;
     }
     if (ntok < 0 || ntok > kMaxCount) return KQ_ERR_NTOK;
     if (ntok == 0) return KQ_OK;
@@ -118,7 +116,7 @@ kq_status kq_norm_rope(const kq_norm_part *parts, int n, int type, int out_type,
     if (st != KQ_OK) return st;
     a.ntok = ntok, a.positions = positions, a.pos = pos, a.table = table, a.eps = eps;
     a.dim = dim, a.rot = table ? rot : 0, a.inter = interleaved != 0;
-    return launched(kqp::norm_rope(a, type, out_type, (cudaStream_t)stream));
+    return launched(kqp::norm_rope(a, n, type, out_type, (cudaStream_t)stream));
 }
 
 int64_t kq_prompt_workspace_bytes(int type, int nseq, int64_t ntok, int64_t nkeys, int q_heads,

@@ -11,14 +11,15 @@ namespace kqp {
 
 struct NormArgs {
     kq_norm_part part[KQ_MAX_NORM_PARTS];
-    int32_t upto[KQ_MAX_NORM_PARTS];  // heads of a token up to and with each part
+    int32_t upto[KQ_MAX_NORM_PARTS];  // runs of a token's heads up to and with each part
     int64_t ntok, positions;
     const int32_t *pos;
     const float *table;  // (NULL: no rotation, rot 0)
     float eps;
-    int32_t heads, dim, rot, inter;
+    int32_t runs, dim, rot, inter;
 };
-cudaError_t norm_rope(const NormArgs &a, int type, int out_type, cudaStream_t s);
+// (sets the runs: upto and runs)
+cudaError_t norm_rope(NormArgs &a, int parts, int type, int out_type, cudaStream_t s);
 
 struct ScoreArgs {
     const void *x;

@@ -16,7 +16,7 @@ values, read back in order (kv_read with ctx 0), with their own starts:
 """
 from __future__ import annotations
 
-import ctypes
+import struct
 
 import torch
 
@@ -34,17 +34,41 @@ def _type(dtype, name):
     return code
 
 
+# The wrappers run between kernels of a few microseconds: each looks at a
+# tensor's shape and strides once.
 def _strided(t, name, dtype, shape):
-    """Address and token stride of [ntok, heads, dim] whose tokens may lie
-    apart (a slice of a fused projection's output)."""
-    p = _tensor(t, name, dtype, shape, dense=False)
+    """Address and token stride of [ntok, heads, dim] (of this shape) whose
+    tokens may lie apart (a slice of a fused projection's output)."""
+    if not (t.is_cuda and t.dtype is dtype):
+        _tensor(t, name, dtype, dense=False)  # (says what is wrong)
     n, h, d = shape
     s0, s1, s2 = t.stride()
     if (d > 1 and s2 != 1) or (h > 1 and s1 != d):
         if n == 0:
-            return p, h * d
+            return t.data_ptr(), h * d
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    return p, s0 if n > 1 else h * d
+    return t.data_ptr(), s0 if n > 1 else h * d
+
+
+def _part(x, weight, out, name, n, d, kind, dtype, on):
+    """One tensor of norm_rope: its descriptor and its output."""
+    shape = x.shape
+    if len(shape) != 3 or shape[0] != n or shape[2] != d:
+        raise ValueError(f"{name} must be [{n}, heads, {d}], got {tuple(shape)}")
+    xp, xs = _strided(x, name, kind, shape)
+    wp = 0 if weight is None else _tensor(weight, name + "_weight", torch.float32, (d,))
+    h = shape[1]
+    if out is None:
+        out = _empty(shape, dtype, x.device, on)
+        op, os_ = out.data_ptr(), h * d
+    else:
+        if out.shape != shape:
+            raise ValueError(f"{name}_out must have shape {tuple(shape)}, got {tuple(out.shape)}")
+        op, os_ = _strided(out, name + "_out", dtype, shape)
+    return _pack_part(xp, xs, wp, op, os_, h, 0), out
+
+
+_pack_part = struct.Struct("@PqPPqii").pack  # kq_norm_part, without padding
 
 
 def norm_rope(q, k=None, q_weight=None, k_weight=None, positions=None, table=None, eps=1e-6,
@@ -55,15 +79,15 @@ def norm_rope(q, k=None, q_weight=None, k_weight=None, positions=None, table=Non
     may be None.  dtype: of the outputs, which may be float16 or bfloat16 where
     the inputs are float32 (it is the inputs' unless given).  q_out and k_out may
     be q and k.  Returns (q, k)."""
-    xs = [(q, q_weight, q_out, "q")]
-    if k is not None:
-        xs.append((k, k_weight, k_out, "k"))
-    if q.dim() != 3:
+    shape, kind = q.shape, q.dtype
+    if len(shape) != 3:
         raise ValueError("q must be [ntok, heads, dim]")
-    n, _, d = q.shape
-    kind = _type(q.dtype, "q")
-    dtype = q.dtype if dtype is None else dtype
-    out_kind = _type(dtype, "dtype")
+    n, _, d = shape
+    code = _type(kind, "q")
+    if dtype is None:
+        dtype, out_code = kind, code
+    else:
+        out_code = _type(dtype, "dtype")
     pp = tp = None
     npos = rot = 0
     if table is not None:
@@ -72,34 +96,38 @@ def norm_rope(q, k=None, q_weight=None, k_weight=None, positions=None, table=Non
             raise ValueError("a table needs positions")
         pp = _tensor(positions, "positions", torch.int32, (n,))
     st, on = _on(stream)
-    parts = (_binding.KqNormPart * len(xs))()
-    outs = []
-    for part, (x, weight, out, name) in zip(parts, xs):
-        if x.dim() != 3 or x.shape[0] != n or x.shape[2] != d:
-            raise ValueError(f"{name} must be [{n}, heads, {d}], got {tuple(x.shape)}")
-        part.x, part.stride = _strided(x, name, q.dtype, x.shape)
-        part.weight = None if weight is None else _tensor(weight, name + "_weight", torch.float32, (d,))
-        if out is None:
-            out = _empty(x.shape, dtype, x.device, on)
-            part.out, part.out_stride = out.data_ptr(), x.shape[1] * d
-        else:
-            part.out, part.out_stride = _strided(out, name + "_out", dtype, x.shape)
-        part.heads = x.shape[1]
-        outs.append(out)
-    _call("kq_norm_rope", parts, len(xs), kind, out_kind, n, d, float(eps), pp, tp, npos, rot,
-          bool(interleaved), st)
-    return outs[0], outs[1] if k is not None else None
+    first, q_out = _part(q, q_weight, q_out, "q", n, d, kind, dtype, on)
+    if k is None:
+        parts, count, k_out = first, 1, None
+    else:
+        second, k_out = _part(k, k_weight, k_out, "k", n, d, kind, dtype, on)
+        parts, count = first + second, 2
+    _call("kq_norm_rope", parts, count, code, out_code, n, d, eps, pp, tp, npos, rot, interleaved, st)
+    return q_out, k_out
+
+
+_space = {}  # workspace bytes by device and sizes, which they depend on alone
+
+
+def _workspace(code, nseq, n, m, h, g, d):
+    key = (torch._C._cuda_getDevice(), code, nseq, n, m, h, g, d)
+    got = _space.get(key)
+    if got is None:
+        got = int(_binding.load().kq_prompt_workspace_bytes(code, nseq, n, m, h, g, d))
+        if got < 0:
+            raise KQError(-got, "kq_prompt_workspace_bytes")
+        if len(_space) >= 4096:
+            _space.clear()
+        _space[key] = got
+    return got
 
 
 def prompt_workspace_bytes(q, k, nseq):
     """Bytes of prompt_attention's workspace for q [ntok, q_heads, dim] and k
     [nkeys, kv_heads, dim] of nseq sequences (it depends on sizes and type
     alone)."""
-    n = int(_binding.load().kq_prompt_workspace_bytes(
-        _type(q.dtype, "q"), int(nseq), q.shape[0], k.shape[0], q.shape[1], k.shape[1], q.shape[2]))
-    if n < 0:
-        raise KQError(-n, "kq_prompt_workspace_bytes")
-    return n
+    return _workspace(_type(q.dtype, "q"), int(nseq), q.shape[0], k.shape[0], q.shape[1], k.shape[1],
+                      q.shape[2])
 
 
 def prompt_attention(q, k, v, start, key_start=None, scale=None, out=None, workspace=None,
@@ -111,28 +139,30 @@ def prompt_attention(q, k, v, start, key_start=None, scale=None, out=None, works
     scale: 1 / sqrt(dim) unless given.  workspace: a CUDA uint8 tensor of
     prompt_workspace_bytes(...) or more; otherwise torch's allocator gives one
     for the call.  Returns [ntok, q_heads, dim] of q's type."""
-    if q.dim() != 3 or k.dim() != 3:
+    shape, held, kind = q.shape, k.shape, q.dtype
+    if len(shape) != 3 or len(held) != 3:
         raise ValueError("q and k must be [tokens, heads, dim]")
-    kind = _type(q.dtype, "q")
-    (n, h, d), (m, g, _) = q.shape, k.shape
-    qp, qs = _strided(q, "q", q.dtype, (n, h, d))
-    kp, ks = _strided(k, "k", q.dtype, (m, g, d))
-    vp, vs = _strided(v, "v", q.dtype, (m, g, d))
+    code = _type(kind, "q")
+    (n, h, d), (m, g, kd) = shape, held
+    if kd != d or v.shape != held:
+        raise ValueError(f"k and v must be [nkeys, kv_heads, {d}], got {tuple(held)} and {tuple(v.shape)}")
+    qp, qs = _strided(q, "q", kind, shape)
+    kp, ks = _strided(k, "k", kind, held)
+    vp, vs = _strided(v, "v", kind, held)
     nseq = start.numel() - 1
     sp = _tensor(start, "start", torch.int32, (nseq + 1,))
     cp = None if key_start is None else _tensor(key_start, "key_start", torch.int32, (nseq + 1,))
     st, on = _on(stream)
-    out, op = _out(out, "out", q.dtype, (n, h, d), q.device, on)
-    wp, wn = None, 0
+    out, op = _out(out, "out", kind, shape, q.device, on)
     if workspace is not None:
         wp, wn = _tensor(workspace, "workspace", torch.uint8), workspace.numel()
     else:
-        wn = prompt_workspace_bytes(q, k, nseq)
+        wp, wn = None, _workspace(code, nseq, n, m, h, g, d)
         if wn:
             workspace = _empty(wn, torch.uint8, q.device, on)
             wp = workspace.data_ptr()
-    _call("kq_prompt_attention", kind, nseq, n, m, sp, cp, qp, qs, h, kp, ks, vp, vs, g, d,
-          d ** -0.5 if scale is None else float(scale), op, wp, wn, st)
+    _call("kq_prompt_attention", code, nseq, n, m, sp, cp, qp, qs, h, kp, ks, vp, vs, g, d,
+          d ** -0.5 if scale is None else scale, op, wp, wn, st)
     return out
 
 
@@ -143,27 +173,30 @@ def token_logprobs(logits, tokens=None, top=0, entropy=True, stream=None):
     best first, of equal ones the lower token first.  Returns (logp [n], entropy
     [n], top_logp [n, top], top_tokens int32 [n, top]), None for what was left
     out."""
-    if logits.dim() != 2:
+    shape, kind = logits.shape, logits.dtype
+    if len(shape) != 2:
         raise ValueError("logits must be [n, vocab]")
-    n, vocab = logits.shape
-    kind = _type(logits.dtype, "logits")
-    xp = _tensor(logits, "logits", logits.dtype, dense=False)
-    if n and vocab > 1 and logits.stride(1) != 1:
+    n, vocab = shape
+    code = _type(kind, "logits")
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor")
+    s0, s1 = logits.stride()
+    if n and vocab > 1 and s1 != 1:
         raise ValueError("logits: a row must be contiguous")
-    stride = logits.stride(0) if n > 1 else vocab
-    tp = None if tokens is None else _tensor(tokens, "tokens", torch.int32, (n,))
     st, on = _on(stream)
     dev = logits.device
-
-    def new(want, dtype, *shape):
-        if not want:
-            return None, None
-        t = _empty(shape, dtype, dev, on)
-        return t, t.data_ptr()
-
-    logp, lp = new(tokens is not None, torch.float32, n)
-    ent, ep = new(entropy, torch.float32, n)
-    top_logp, tlp = new(top > 0, torch.float32, n, max(top, 0))
-    top_token, ttp = new(top > 0, torch.int32, n, max(top, 0))
-    _call("kq_token_logprobs", kind, n, vocab, xp, stride, tp, int(top), lp, ep, tlp, ttp, st)
+    logp = ent = top_logp = top_token = tp = lp = ep = tlp = ttp = None
+    if tokens is not None:
+        tp = _tensor(tokens, "tokens", torch.int32, (n,))
+        logp = _empty((n,), torch.float32, dev, on)
+        lp = logp.data_ptr()
+    if entropy:
+        ent = _empty((n,), torch.float32, dev, on)
+        ep = ent.data_ptr()
+    if top > 0:
+        top_logp = _empty((n, top), torch.float32, dev, on)
+        top_token = _empty((n, top), torch.int32, dev, on)
+        tlp, ttp = top_logp.data_ptr(), top_token.data_ptr()
+    _call("kq_token_logprobs", code, n, vocab, logits.data_ptr(), s0 if n > 1 else vocab, tp, top, lp,
+          ep, tlp, ttp, st)
     return logp, ent, top_logp, top_token

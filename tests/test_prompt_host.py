@@ -120,6 +120,10 @@ def test_logprob_refusals(lib):
 
 def test_struct_matches_the_header():
     assert ctypes.sizeof(_binding.KqNormPart) == 48
+    torch = pytest.importorskip("torch")  # noqa: F841 (the wrapper's packing needs it)
+    from quant_quantized_matvec_gb300 import prompt
+    packed = prompt._pack_part(1, 2, 3, 4, 5, 6, 0)
+    assert packed == bytes(_binding.KqNormPart(1, 2, 3, 4, 5, 6, 0))
 
 
 def test_python_checks():
