@@ -668,6 +668,7 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
             constexpr int kTerms = kTwo ? 3 : 1;
             auto lo_first = [](int term) { return kTwo && term == 0; };
             auto lo_second = [](int term) { return kTwo && term == 1; };
+            const uint64_t qd = desc_k(uniform(base + M::kControl));  // (the queries' lo terms)
             constexpr uint32_t is = mma_idesc(TK, M::kBf16, false), io = mma_idesc(D, M::kBf16, true);
             auto scores = [&](int i) {
                 const int k = 2 * i;
@@ -676,19 +677,23 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
                 tc_after();
                 const uint32_t s = uniform(k % M::kSlots), b = uniform(i & 1);
                 const uint32_t d = tm + M::kS + TK * b;
-                const uint32_t kt = base + M::kRing + s * M::kPart;
+                const uint64_t kd = desc_k(uniform(base + M::kRing) + s * M::kPart);
                 if (elected()) {
 #pragma unroll
                     for (int term = 0; term < kTerms; ++term)
 #pragma unroll
                         for (int j = 0; j < D / 16; ++j) {
-                            const uint64_t kd = desc_k(kt + (lo_second(term) ? M::kTerm : 0) +
-                                                       (j >> 2) * (TK * 128) + (j & 3) * 32);
-                            if (M::kLoShared && lo_first(term))
-                                tc_mma_ss(d, desc_k(base + M::kControl + (j >> 2) * (kRows * 128) + (j & 3) * 32),
-                                          kd, is, term + j > 0);
-                            else
-                                tc_mma_ts(d, tm + (lo_first(term) ? D / 2 : 0) + 8 * j, kd, is, term + j > 0);
+                            const uint64_t kj = kd + (((lo_second(term) ? M::kTerm : 0) +
+                                                       (j >> 2) * (TK * 128) + (j & 3) * 32) >> 4);
+                            const uint64_t qj = qd + (((j >> 2) * (kRows * 128) + (j & 3) * 32) >> 4);
+                            const uint32_t qt = tm + (lo_first(term) ? D / 2 : 0) + 8 * j;
+                            if (M::kLoShared && lo_first(term)) {
+                                if (term + j) tc_add_ss(d, qj, kj, is);
+                                else tc_mma_ss(d, qj, kj, is, false);
+                            } else {
+                                if (term + j) tc_add_ts(d, qt, kj, is);
+                                else tc_mma_ts(d, qt, kj, is, false);
+                            }
                         }
                     tc_commit(bar(cm.empty[0]) + 8 * s);
                     tc_commit(bar(cm.sdone[0]) + 8 * b);
@@ -706,16 +711,18 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
                 if (__any_sync(~0u, dead())) break;
                 tc_after();
                 const uint32_t s = uniform(k % M::kSlots), b = uniform(i & 1), o = uniform(i % OB);
-                const uint32_t vt = base + M::kRing + s * M::kPart, p = tm + M::kS + TK * b;
-                const uint32_t d = tm + M::kO + D * o;
+                const uint64_t vd = desc_n(uniform(base + M::kRing) + s * M::kPart, TK * 128);
+                const uint32_t d = tm + M::kO + D * o, p = tm + M::kS + TK * b;
                 if (elected()) {
 #pragma unroll
                     for (int term = 0; term < kTerms; ++term)
 #pragma unroll
-                        for (int j = 0; j < TK / 16; ++j)
-                            tc_mma_ts(d, p + (lo_first(term) ? TK / 2 : 0) + 8 * j,
-                                      desc_n(vt + (lo_second(term) ? M::kTerm : 0) + j * 2048, TK * 128),
-                                      io, term + j > 0);
+                        for (int j = 0; j < TK / 16; ++j) {
+                            const uint32_t pj = p + (lo_first(term) ? TK / 2 : 0) + 8 * j;
+                            const uint64_t vj = vd + (((lo_second(term) ? M::kTerm : 0) + j * 2048) >> 4);
+                            if (term + j) tc_add_ts(d, pj, vj, io);
+                            else tc_mma_ts(d, pj, vj, io, false);
+                        }
                     tc_commit(bar(cm.empty[0]) + 8 * s);
                     tc_commit(bar(cm.odone[0]) + 8 * o);
                 }

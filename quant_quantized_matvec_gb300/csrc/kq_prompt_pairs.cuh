@@ -493,7 +493,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         } else if (w < kPairOther + 2) {
             // ------------------------------------- products of a block
             const int b = w - kPairOther;
-            const uint32_t tm = uniform(tmem + M::kBlock * b), qt = uniform(base + M::kControl + b * M::kQTile);
+            const uint32_t tm = uniform(tmem + M::kBlock * b);
+            const uint64_t qd = desc_k(uniform(base + M::kControl + b * M::kQTile));
             const uint32_t is = mma_idesc(TK, M::kBf16, false) | (a.scale < 0.f ? 1u << 13 : 0u);
             constexpr uint32_t io = mma_idesc(D, M::kBf16, true);
             int tile = 0, cleaned = 0;  // tiles of both blocks so far, and those that were cleaned
@@ -531,12 +532,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     if (__any_sync(~0u, dead())) return false;
                     tc_after();
                     const uint32_t s = uniform(x % M::kSlots);
-                    const uint32_t kt = base + M::kRing + s * M::kTile;
+                    const uint64_t kd = desc_k(uniform(base + M::kRing) + s * M::kTile);
                     if (elected()) {
 #pragma unroll
-                        for (int j = 0; j < D / 16; ++j)
-                            tc_mma_ss(tm + M::kS, desc_k(qt + (j >> 2) * (kRows * 128) + (j & 3) * 32),
-                                      desc_k(kt + (j >> 2) * (TK * 128) + (j & 3) * 32), is, j > 0);
+                        for (int j = 0; j < D / 16; ++j) {
+                            const uint64_t qj = qd + (((j >> 2) * (kRows * 128) + (j & 3) * 32) >> 4);
+                            const uint64_t kj = kd + (((j >> 2) * (TK * 128) + (j & 3) * 32) >> 4);
+                            if (j) tc_add_ss(tm + M::kS, qj, kj, is);
+                            else tc_mma_ss(tm + M::kS, qj, kj, is, false);
+                        }
                         tc_commit(bar(cm.sdone[b]));
                         tc_commit(bar(cm.empty[0]) + 8 * s);
                         if (i == count - 1) tc_commit(bar(cm.qfree[b]));
@@ -559,13 +563,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         break;
                     }
                     tc_after();
-                    const uint32_t s = uniform(x % M::kSlots);
-                    const uint32_t vt = base + M::kRing + s * M::kTile;
+                    const uint32_t s = uniform(x % M::kSlots), more = uniform(i > from);
+                    const uint64_t vd = desc_n(uniform(base + M::kRing) + s * M::kTile, TK * 128);
                     if (elected()) {
+                        tc_mma_ts(tm + M::kO, tm + M::kP, vd, io, more);
 #pragma unroll
-                        for (int j = 0; j < TK / 16; ++j)
-                            tc_mma_ts(tm + M::kO, tm + M::kP + 8 * j, desc_n(vt + j * 2048, TK * 128), io,
-                                      i > from || j > 0);
+                        for (int j = 1; j < TK / 16; ++j)
+                            tc_add_ts(tm + M::kO, tm + M::kP + 8 * j, vd + j * (2048 >> 4), io);
                         tc_commit(bar(cm.odone[b]));
                         tc_commit(bar(cm.empty[0]) + 8 * s);
                     }
