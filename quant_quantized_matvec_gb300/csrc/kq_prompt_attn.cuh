@@ -13,10 +13,10 @@
 //
 // The rows are the 128 lanes of an accumulator, a thread each.  Queries and
 // probabilities are the first operand, in tensor memory, keys and values the
-// second, in shared memory.  A tile's S = Q K is formed ahead in one of two
-// buffers; the softmax warps turn it into P in place; O = P V of the tile
-// starts at zero and is added to the row's f32 sums in registers, by warps of
-// their own, with the correction of the running maximum: the sums are rounded
+// second, in shared memory.  A warp issues S = Q K of each tile as soon as the
+// softmax warps have taken an earlier one into registers, another O = P V.  O of
+// a tile starts at zero and is added to the row's f32 sums in registers, by warps
+// of their own, with the correction of the running maximum: the sums are rounded
 // to nearest, whatever the tensor core's additions do over thousands of steps.
 //
 // f32 (two f16 terms hi + lo, after a scaling by a power of two):
@@ -308,15 +308,18 @@ struct Rows {
     static constexpr int TK = kTwo ? f32_tile_tokens(D) : 64;
     static constexpr int kTerm = TK * D * 2;                 // one term of a tile's keys or values
     static constexpr int kPart = kTerm * (kTwo ? 2 : 1);
-    // columns of tensor memory: Q (lo in shared memory at width 256), S and P, O
+    // columns of tensor memory: Q (lo in shared memory at width 256), S, P, O,
+    // and how many of each it holds
     static constexpr bool kLoShared = kTwo && D == 256;
     static constexpr int kQCols = kTwo && !kLoShared ? D : D / 2;
-    static constexpr int kS = kQCols, kO = kS + 2 * TK;
-    static constexpr int OB = kO + 2 * D <= 512 ? 2 : 1;     // buffers of O
+    static constexpr int kPCols = kTwo ? TK : TK / 2;
+    static constexpr int PB = 2, OB = D == 64 ? 2 : 1;
+    static constexpr int SB = kQCols + 2 * TK + PB * kPCols + OB * D <= 512 ? 2 : 1;
+    static constexpr int kS = kQCols, kP = kS + SB * TK, kO = kP + PB * kPCols;
     static constexpr int OW = D == 256 ? 8 : 4;              // warps that sum O
     static constexpr int OC = D * 4 / OW;                    // columns of each
     static constexpr int kThreads = 32 * (4 + OW + 4);
-    static constexpr int kFirst = 4 + OW;                    // MMA, copies, two that clean
+    static constexpr int kFirst = 4 + OW;                    // S, copies, O, one that cleans
     static constexpr int kControl = 4096, kQLo = kLoShared ? kRows * D * 2 : 0;
     static constexpr int kRing = kControl + kQLo;
     static constexpr int kRoom = (227 * 1024 - 1024 - kRing) / kPart;
@@ -327,7 +330,8 @@ struct Rows {
 
 struct RowsShared {
     Item item;
-    uint64_t full[8], empty[8], sdone[2], pready[2], odone[2], ofree[2], cready[4], vraw[4], vclean[4], ldone, drain;
+    uint64_t full[8], empty[8], sdone[2], sfree[2], pready[2], pfree[2], odone[2], ofree[2], cready[4],
+        vraw[4], vclean[4], ldone, drain[2];
     uint32_t tmem;
     int dead, bad;
     float corr[4][kRows];  // of tile i & 3: the factor of what was summed before
@@ -341,7 +345,7 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
     using M = Rows<T, D>;
     using H = typename M::H;
     constexpr bool kTwo = M::kTwo;
-    constexpr int TK = M::TK, OB = M::OB;
+    constexpr int TK = M::TK, SB = M::SB, PB = M::PB, OB = M::OB;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (kq::smem_addr(smem_raw) & 1023)) & 1023);
     RowsShared &cm = *reinterpret_cast<RowsShared *>(smem);
@@ -355,17 +359,16 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
     } else if (tid == 32) {
         for (int i = 0; i < 8; ++i) kq::mbar_init(bar(cm.full[i]), 1), kq::mbar_init(bar(cm.empty[i]), 1);
         for (int i = 0; i < 2; ++i) {
-            kq::mbar_init(bar(cm.sdone[i]), 1);
-            kq::mbar_init(bar(cm.pready[i]), 4);
-            kq::mbar_init(bar(cm.odone[i]), 1);
-            kq::mbar_init(bar(cm.ofree[i]), M::OW);
+            kq::mbar_init(bar(cm.sdone[i]), 1), kq::mbar_init(bar(cm.sfree[i]), 4);
+            kq::mbar_init(bar(cm.pready[i]), 4), kq::mbar_init(bar(cm.pfree[i]), 1);
+            kq::mbar_init(bar(cm.odone[i]), 1), kq::mbar_init(bar(cm.ofree[i]), M::OW);
+            kq::mbar_init(bar(cm.drain[i]), 1);
         }
         for (int i = 0; i < 4; ++i) {
             kq::mbar_init(bar(cm.cready[i]), 4);
-            kq::mbar_init(bar(cm.vraw[i]), 1), kq::mbar_init(bar(cm.vclean[i]), 2);
+            kq::mbar_init(bar(cm.vraw[i]), 1), kq::mbar_init(bar(cm.vclean[i]), 1);
         }
-        kq::mbar_init(bar(cm.ldone), kTwo ? 4 : 6);
-        kq::mbar_init(bar(cm.drain), 1);
+        kq::mbar_init(bar(cm.ldone), kTwo ? 4 : 5);
         cm.dead = cm.bad = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -483,13 +486,16 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
                 f = __uint_as_float((uint32_t)(127 + min(max(ex - 15 + ek, -126), 127)) << 23);
                 if (i + 1 < count) ek = __ldg(&info[(int64_t)(t - 1) * a.kv_heads].ek);
             }
-            wait(cm.sdone[i & 1], i >> 1);
+            wait(cm.sdone[i % SB], i / SB);
             tc_after();
             uint32_t d[TK];
-            const uint32_t sa = mine + M::kS + TK * (i & 1);
+            const uint32_t sa = mine + M::kS + TK * (i % SB), pa = mine + M::kP + M::kPCols * (i % PB);
 #pragma unroll
             for (int k = 0; k < TK / 32; ++k) tc_load32(d + 32 * k, sa + 32 * k);
             tc_loaded();
+            tc_before();
+            __syncwarp();
+            if (lane == 0) kq::mbar_arrive(bar(cm.sfree[i % SB]));
             const int seen = i < edges ? limit + 1 - t * TK : TK;  // columns that the row attends
             if (i < edges) {
 #pragma unroll
@@ -523,6 +529,10 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
                 d[k] = __float_as_uint(p);
             }
             l = fmaf(l, corr, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+            if (i >= PB) {  // the O before has read P's place
+                wait(cm.pfree[i % PB], i / PB - 1);
+                tc_after();
+            }
             cm.corr[i & 3][r] = corr;
 #pragma unroll
             for (int k = 0; k < TK / 32; ++k) {
@@ -533,14 +543,14 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
                     if constexpr (kTwo) split2(p0, p1, hi[j], lo[j]);
                     else hi[j] = pack2<H>(p0, p1);
                 }
-                tc_store16(sa + 16 * k, hi);
-                if constexpr (kTwo) tc_store16(sa + TK / 2 + 16 * k, lo);
+                tc_store16(pa + 16 * k, hi);
+                if constexpr (kTwo) tc_store16(pa + TK / 2 + 16 * k, lo);
             }
             tc_stored();
             tc_before();
             __syncwarp();
             if (lane == 0) {
-                kq::mbar_arrive(bar(cm.pready[i & 1]));
+                kq::mbar_arrive(bar(cm.pready[i % PB]));
                 kq::mbar_arrive(bar(cm.cready[i & 3]));
             }
         }
@@ -635,6 +645,10 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
     } else {
         if constexpr (D == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         __syncthreads();
+        // terms' products, the small ones first
+        constexpr int kTerms = kTwo ? 3 : 1;
+        auto lo_first = [](int term) { return kTwo && term == 0; };
+        auto lo_second = [](int term) { return kTwo && term == 1; };
         if (w == M::kFirst + 1 && lane == 0) {
             // --------------------------------------------- copies
             for (int k = 0; k < 2 * count; ++k) {
@@ -662,20 +676,18 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
                 }
             }
         } else if (w == M::kFirst) {
-            // --------------------------------------------- products
+            // --------------------------------------------- S of each tile
             tc_after();
             const uint32_t tm = uniform(tmem);
-            constexpr int kTerms = kTwo ? 3 : 1;
-            auto lo_first = [](int term) { return kTwo && term == 0; };
-            auto lo_second = [](int term) { return kTwo && term == 1; };
             const uint64_t qd = desc_k(uniform(base + M::kControl));  // (the queries' lo terms)
-            constexpr uint32_t is = mma_idesc(TK, M::kBf16, false), io = mma_idesc(D, M::kBf16, true);
-            auto scores = [&](int i) {
+            constexpr uint32_t is = mma_idesc(TK, M::kBf16, false);
+            for (int i = 0; i < count; ++i) {
                 const int k = 2 * i;
                 wait(cm.full[k % M::kSlots], k / M::kSlots);
-                if (__any_sync(~0u, dead())) return;
+                if (i >= SB) wait(cm.sfree[i % SB], i / SB - 1);
+                if (__any_sync(~0u, dead())) break;
                 tc_after();
-                const uint32_t s = uniform(k % M::kSlots), b = uniform(i & 1);
+                const uint32_t s = uniform(k % M::kSlots), b = uniform(i % SB);
                 const uint32_t d = tm + M::kS + TK * b;
                 const uint64_t kd = desc_k(uniform(base + M::kRing) + s * M::kPart);
                 if (elected()) {
@@ -695,24 +707,27 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
                                 else tc_mma_ts(d, qt, kj, is, false);
                             }
                         }
-                    tc_commit(bar(cm.empty[0]) + 8 * s);
                     tc_commit(bar(cm.sdone[0]) + 8 * b);
+                    tc_commit(bar(cm.empty[0]) + 8 * s);
                 }
                 __syncwarp();
-            };
-            if (count > 0) scores(0);
-            if (count > 1) scores(1);
+            }
+        } else if (w == M::kFirst + 2) {
+            // --------------------------------------------- O of each tile
+            tc_after();
+            const uint32_t tm = uniform(tmem);
+            constexpr uint32_t io = mma_idesc(D, M::kBf16, true);
             for (int i = 0; i < count; ++i) {
                 const int k = 2 * i + 1;
                 wait(cm.full[k % M::kSlots], k / M::kSlots);
                 if (!kTwo && i < edges) wait(cm.vclean[i & 3], i >> 2);
                 if (i >= OB) wait(cm.ofree[i % OB], i / OB - 1);
-                wait(cm.pready[i & 1], i >> 1);
+                wait(cm.pready[i % PB], i / PB);
                 if (__any_sync(~0u, dead())) break;
                 tc_after();
-                const uint32_t s = uniform(k % M::kSlots), b = uniform(i & 1), o = uniform(i % OB);
+                const uint32_t s = uniform(k % M::kSlots), b = uniform(i % PB), o = uniform(i % OB);
                 const uint64_t vd = desc_n(uniform(base + M::kRing) + s * M::kPart, TK * 128);
-                const uint32_t d = tm + M::kO + D * o, p = tm + M::kS + TK * b;
+                const uint32_t d = tm + M::kO + D * o, p = tm + M::kP + M::kPCols * b;
                 if (elected()) {
 #pragma unroll
                     for (int term = 0; term < kTerms; ++term)
@@ -723,16 +738,13 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
                             if (term + j) tc_add_ts(d, pj, vj, io);
                             else tc_mma_ts(d, pj, vj, io, false);
                         }
-                    tc_commit(bar(cm.empty[0]) + 8 * s);
                     tc_commit(bar(cm.odone[0]) + 8 * o);
+                    tc_commit(bar(cm.pfree[0]) + 8 * b);
+                    tc_commit(bar(cm.empty[0]) + 8 * s);
                 }
                 __syncwarp();
-                if (i + 2 < count) {  // the buffer of P is S's again
-                    wait(cm.odone[i % OB], i / OB);
-                    scores(i + 2);
-                }
             }
-        } else if (!kTwo && w >= M::kFirst + 2) {
+        } else if (!kTwo && w == M::kFirst + 3) {
             // ------------- values that are not finite, of tiles seen in part
             for (int i = 0; i < edges; ++i) {
                 const int k = 2 * i + 1, s = k % M::kSlots;
@@ -740,7 +752,7 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
                 uint4 *v = reinterpret_cast<uint4 *>(smem + M::kRing + s * M::kPart);
                 bool found = false;
                 if (!dead())
-                    for (int c = (w - M::kFirst - 2) * 32 + lane; c < M::kPart / 16; c += 64) {
+                    for (int c = lane; c < M::kPart / 16; c += 32) {
                         uint4 x = v[c];
                         if (not_finite<H>(x.x) | not_finite<H>(x.y) | not_finite<H>(x.z) | not_finite<H>(x.w)) {
                             found = true;
@@ -775,11 +787,12 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
             for (int i = max(0, raw - 4); i < raw; ++i)
                 kq::mbar_wait(bar(cm.vraw[i & 3]), (i >> 2) & 1, kq::kWaitLimitNs);
         }
-        if (w == M::kFirst) {
+        if (w == M::kFirst || w == M::kFirst + 2) {
+            const uint64_t &drain = cm.drain[w == M::kFirst ? 0 : 1];
             tc_after();
-            if (elected()) tc_commit(bar(cm.drain));
+            if (elected()) tc_commit(bar(drain));
             __syncwarp();
-            kq::mbar_wait(bar(cm.drain), 0, kq::kWaitLimitNs);
+            kq::mbar_wait(bar(drain), 0, kq::kWaitLimitNs);
             __syncwarp();
         }
         __syncthreads();
