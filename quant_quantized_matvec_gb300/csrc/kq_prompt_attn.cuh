@@ -205,6 +205,18 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t 
     lo = pack2<__half>(a - f.x, b - f.y);
 }
 
+// 32 bytes of a row.
+__device__ __forceinline__ void store32(void *p, const uint32_t *v, bool aligned) {
+    if (aligned) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
+                     "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<uint4 *>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+}
+
 // ------------------------------------------------------- splitting f32
 // The largest finite magnitude's exponent e: it is below 2^e.
 __device__ __forceinline__ int exponent_of(float top, int least) {
@@ -419,50 +431,72 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
             const T *x = static_cast<const T *>(a.q) + (int64_t)(it.first + tok) * a.q_stride +
                          (int64_t)(it.hq + hq) * D;
             if constexpr (kTwo) {
+                // (up to width 128 the row is read once, all loads on their way)
+                constexpr int kHeld = D <= 128 ? D / 4 : 16;
                 const float4 *x4 = reinterpret_cast<const float4 *>(x);
                 const float sc = a.scale * kLog2E;
+                float4 v[kHeld];
+                auto load = [&](int i0) {
+#pragma unroll
+                    for (int i = 0; i < kHeld; ++i)
+                        v[i] = on ? __ldg(x4 + i0 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+                };
                 float top = 0.f;
-                for (int i = 0; i < D / 4; ++i) {
-                    const float4 v = on ? __ldg(x4 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    top = fmaxf(top, fmaxf(fmaxf(fabsf(v.x * sc), fabsf(v.y * sc)),
-                                           fmaxf(fabsf(v.z * sc), fabsf(v.w * sc))));
+#pragma unroll 1
+                for (int i0 = 0; i0 < D / 4; i0 += kHeld) {
+                    load(i0);
+#pragma unroll
+                    for (int i = 0; i < kHeld; ++i)
+                        top = fmaxf(top, fmaxf(fmaxf(fabsf(v[i].x * sc), fabsf(v[i].y * sc)),
+                                               fmaxf(fabsf(v[i].z * sc), fabsf(v[i].w * sc))));
                 }
                 ex = exponent_of(top, -111);
                 const float up = __uint_as_float((uint32_t)(127 + 15 - ex) << 23);
 #pragma unroll 1
-                for (int i = 0; i < D / 32; ++i) {
-                    uint32_t hi[16], lo[16];
+                for (int i0 = 0; i0 < D / 4; i0 += kHeld) {
+                    if (kHeld < D / 4) load(i0);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float4 v = on ? __ldg(x4 + 8 * i + k) : make_float4(0.f, 0.f, 0.f, 0.f);
-                        split2(v.x * sc * up, v.y * sc * up, hi[2 * k], lo[2 * k]);
-                        split2(v.z * sc * up, v.w * sc * up, hi[2 * k + 1], lo[2 * k + 1]);
-                    }
-                    tc_store16(mine + 16 * i, hi);
-                    if constexpr (M::kLoShared) {
+                    for (int i = 0; i < kHeld / 8; ++i) {
+                        uint32_t hi[16], lo[16];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            *reinterpret_cast<uint4 *>(smem + M::kControl + (i / 2) * (kRows * 128) +
-                                                       tile_at(r, (i & 1) * 4 + k)) =
-                                make_uint4(lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
-                    } else {
-                        tc_store16(mine + D / 2 + 16 * i, lo);
+                        for (int k = 0; k < 8; ++k) {
+                            const float4 e = v[8 * i + k];
+                            split2(e.x * sc * up, e.y * sc * up, hi[2 * k], lo[2 * k]);
+                            split2(e.z * sc * up, e.w * sc * up, hi[2 * k + 1], lo[2 * k + 1]);
+                        }
+                        const int at = i0 / 8 + i;  // 32 values of the row
+                        tc_store16(mine + 16 * at, hi);
+                        if constexpr (M::kLoShared) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                *reinterpret_cast<uint4 *>(smem + M::kControl + (at / 2) * (kRows * 128) +
+                                                           tile_at(r, (at & 1) * 4 + k)) =
+                                    make_uint4(lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
+                        } else {
+                            tc_store16(mine + D / 2 + 16 * at, lo);
+                        }
                     }
                 }
                 if constexpr (M::kLoShared) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             } else {
                 const uint4 *x8 = reinterpret_cast<const uint4 *>(x);
                 const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;
+                // (half a row's loads on their way)
 #pragma unroll 1
-                for (int i = 0; i < D / 32; ++i) {
-                    uint32_t q[16];
+                for (int i = 0; i < D / 32; i += 4) {
+                    uint4 v[16];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint4 v = on ? __ldg(x8 + 4 * i + k) : make_uint4(0, 0, 0, 0);
-                        q[4 * k] = v.x ^ sign, q[4 * k + 1] = v.y ^ sign;
-                        q[4 * k + 2] = v.z ^ sign, q[4 * k + 3] = v.w ^ sign;
+                    for (int k = 0; k < 16; ++k) v[k] = on ? __ldg(x8 + 4 * i + k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t q[16];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            q[4 * k] = v[4 * c + k].x ^ sign, q[4 * k + 1] = v[4 * c + k].y ^ sign;
+                            q[4 * k + 2] = v[4 * c + k].z ^ sign, q[4 * k + 3] = v[4 * c + k].w ^ sign;
+                        }
+                        tc_store16(mine + 16 * (i + c), q);
                     }
-                    tc_store16(mine + 16 * i, q);
                 }
             }
             tc_stored();
@@ -638,20 +672,24 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
             if (dead()) inv = quiet_nan();
             T *to = static_cast<T *>(a.out) +
                     ((int64_t)(it.first + tok) * a.q_heads + it.hq + hq) * D + c0;
+            const bool wide = ((uintptr_t)a.out & 31) == 0;
+            constexpr int kEach = 32 / sizeof(T);
 #pragma unroll
-            for (int k = 0; k < M::OC; k += 4)
-                store4(to + k, make_float4(O[k] * inv, O[k + 1] * inv, O[k + 2] * inv, O[k + 3] * inv));
+            for (int k = 0; k < M::OC; k += kEach) {
+                uint32_t q[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if constexpr (kTwo) q[e] = __float_as_uint(O[k + e] * inv);
+                    else q[e] = pack2<H>(O[k + 2 * e] * inv, O[k + 2 * e + 1] * inv);
+                }
+                store32(to + k, q, wide);
+            }
         }
     } else {
         if constexpr (D == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-        __syncthreads();
-        // terms' products, the small ones first
-        constexpr int kTerms = kTwo ? 3 : 1;
-        auto lo_first = [](int term) { return kTwo && term == 0; };
-        auto lo_second = [](int term) { return kTwo && term == 1; };
-        if (w == M::kFirst + 1 && lane == 0) {
-            // --------------------------------------------- copies
-            for (int k = 0; k < 2 * count; ++k) {
+        // ------------------------------------------------- copies
+        auto copy = [&](int until) {
+            for (int k = copied; k < until; ++k) {
                 const int s = k % M::kSlots, t = t1 - 1 - (k >> 1);
                 if (k >= M::kSlots) wait(cm.empty[s], k / M::kSlots - 1);
                 if (dead()) break;
@@ -675,6 +713,16 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
                                      it.kfirst + t * TK, done);
                 }
             }
+        };
+        const bool producer = w == M::kFirst + 1 && lane == 0;
+        if (producer) copy(min(2 * count, M::kSlots));  // (while the queries are fetched)
+        __syncthreads();
+        // terms' products, the small ones first
+        constexpr int kTerms = kTwo ? 3 : 1;
+        auto lo_first = [](int term) { return kTwo && term == 0; };
+        auto lo_second = [](int term) { return kTwo && term == 1; };
+        if (producer) {
+            copy(2 * count);
         } else if (w == M::kFirst) {
             // --------------------------------------------- S of each tile
             tc_after();

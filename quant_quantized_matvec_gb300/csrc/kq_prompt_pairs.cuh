@@ -118,18 +118,6 @@ __device__ __forceinline__ bool find_unit(const PromptArgs &a, int u, int tile, 
     return found;
 }
 
-// 32 bytes of a row.
-__device__ __forceinline__ void store32(void *p, const uint32_t *v, bool aligned) {
-    if (aligned) {
-        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
-                     "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                     : "memory");
-    } else {
-        reinterpret_cast<uint4 *>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<uint4 *>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
-    }
-}
-
 template <class T, int D>
 __global__ void __launch_bounds__(kPairThreads, 1)
     kq_prompt_pairs(const __grid_constant__ PromptArgs a) {
