@@ -14,10 +14,11 @@
 // The rows are the 128 lanes of an accumulator, a thread each.  Queries and
 // probabilities are the first operand, in tensor memory, keys and values the
 // second, in shared memory.  A warp issues S = Q K of each tile as soon as the
-// softmax warps have taken an earlier one into registers, another O = P V.  O of
-// a tile starts at zero and is added to the row's f32 sums in registers, by warps
-// of their own, with the correction of the running maximum: the sums are rounded
-// to nearest, whatever the tensor core's additions do over thousands of steps.
+// softmax warps have taken an earlier one into registers, another O = P V.  In
+// f32 O of a tile starts at zero and is added to the row's f32 sums in registers,
+// by warps of their own, with the correction of the running maximum: the sums are
+// rounded to nearest, whatever the tensor core's additions do over thousands of
+// steps.
 //
 // f32 (two f16 terms hi + lo, after a scaling by a power of two):
 //   S = Qlo Khi + Qhi Klo + Qhi Khi,  O = Plo Vhi + Phi Vlo + Phi Vhi
@@ -29,8 +30,10 @@
 // log2(e) in f32 first, so that what follows only multiplies by powers of two,
 // and the difference to the maximum is one rounding, however large both are.
 //
-// 16-bit types are copied as they are, by tensor copies.  Probabilities that
-// become f16 are held times 2^15, as f16 has few bits below 2^-14.
+// 16-bit types are copied as they are, by tensor copies, and O adds up in tensor
+// memory, corrected when a maximum has grown by 2^8 or more; until then
+// probabilities are held up to 2^8 times as large, in the sum too.  Those that
+// become f16 are held times 2^7 besides, as f16 has few bits below 2^-14.
 //
 // NaN and infinities must not reach rows that do not attend them (0 * inf):
 // values that are not finite are zeros in the tile (f32: all tiles; 16 bits:
@@ -55,6 +58,7 @@ namespace kqp {
 using kqd::quiet_nan;
 
 constexpr int kRows = 128;  // rows of an item
+constexpr float kLazy = 8.f;  // 16 bits: log2 of the growth of a maximum that is not corrected
 constexpr float kLog2E = 1.44269504088896340736f;
 
 // Powers of two of a tile of an f32 call, and whether its values had some that
@@ -325,7 +329,10 @@ struct Rows {
     static constexpr bool kLoShared = kTwo && D == 256;
     static constexpr int kQCols = kTwo && !kLoShared ? D : D / 2;
     static constexpr int kPCols = kTwo ? TK : TK / 2;
-    static constexpr int PB = 2, OB = D == 64 ? 2 : 1;
+    // (f32 at width 128: two of O and one of S and P; one of O, which is read
+    // before it is formed again, and two of S and P: 326 against 2xx us)
+    static constexpr int OB = kTwo && D <= 128 ? 2 : 1;
+    static constexpr int PB = kTwo && D == 128 ? 1 : 2;
     static constexpr int SB = kQCols + 2 * TK + PB * kPCols + OB * D <= 512 ? 2 : 1;
     static constexpr int kS = kQCols, kP = kS + SB * TK, kO = kP + PB * kPCols;
     static constexpr int OW = D == 256 ? 8 : 4;              // warps that sum O
@@ -505,7 +512,7 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
         __syncthreads();
         const int limit = on ? it.limit(tok) : -1;
         const float factor = fabsf(a.scale) * kLog2E;  // (16-bit types)
-        constexpr float kUp = M::kBf16 ? 0.f : 15.f;
+        constexpr float kUp = M::kBf16 ? 0.f : 7.f;
         const TileInfo *info = nullptr;
         int ek = 0;
         if constexpr (kTwo) {
@@ -541,16 +548,38 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
             for (int k = 0; k < TK; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(d[k]));
             mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             // The reference: f32, the maximum less 15, rounded up (it is in
-            // units of log 2); 16 bits, the maximum of the scores themselves.
-            float corr;
+            // units of log 2).  16 bits: a maximum of the scores themselves,
+            // which is only moved when it has grown by 2^8 or more, as O has to
+            // be corrected then.
+            float corr = 1.f;
             if constexpr (kTwo) {
                 const float now = fmaxf(m, mx[0] == -INFINITY ? mx[0] : __fsub_ru(mx[0] * f, 15.f));
                 corr = exp2_fast(m - (now == -INFINITY ? 0.f : now));
                 m = now;
             } else {
                 const float now = fmaxf(m, mx[0]);
-                corr = now == m ? 1.f : m == -INFINITY ? 0.f : exp2_fast((m - now) * factor);
-                m = now;
+                const bool grown = now > m && !((now - m) * factor <= kLazy);
+                if (__any_sync(~0u, grown)) {
+                    corr = !grown ? 1.f : m == -INFINITY ? 0.f : exp2_fast((m - now) * factor);
+                    if (grown) m = now;
+                    if (i > 0) {
+                        wait(cm.pfree[(i - 1) % PB], (i - 1) / PB);
+                        tc_after();
+                        const uint32_t oa = mine + M::kO;
+                        if (!__any_sync(~0u, dead())) {
+#pragma unroll 4
+                            for (int k = 0; k < D; k += 16) {
+                                uint32_t o[16];
+                                tc_load16(o, oa + k);
+                                tc_loaded();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+                                tc_store16(oa + k, o);
+                            }
+                        }
+                    }
+                }
             }
             const float from = m == -INFINITY ? 0.f : m;
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
@@ -567,7 +596,7 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
                 wait(cm.pfree[i % PB], i / PB - 1);
                 tc_after();
             }
-            cm.corr[i & 3][r] = corr;
+            if constexpr (kTwo) cm.corr[i & 3][r] = corr;
 #pragma unroll
             for (int k = 0; k < TK / 32; ++k) {
                 uint32_t hi[16], lo[16];
@@ -585,7 +614,7 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
             __syncwarp();
             if (lane == 0) {
                 kq::mbar_arrive(bar(cm.pready[i % PB]));
-                kq::mbar_arrive(bar(cm.cready[i & 3]));
+                if constexpr (kTwo) kq::mbar_arrive(bar(cm.cready[i & 3]));
             }
         }
         cm.m[r] = m;
@@ -614,30 +643,41 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
             }
         };
         if (count) look(0);
-        for (int i = 0; i < count; ++i) {
-            const float f = vf;
-            bad |= vbad != 0;
-            if (i + 1 < count) look(i + 1);
-            wait(cm.cready[i & 3], i >> 2);
-            const float corr = cm.corr[i & 3][r];
-            wait(cm.odone[i % OB], i / OB);
-            tc_after();
-            const uint32_t at = mine + (i % OB) * D;
+        if constexpr (kTwo) {
+            for (int i = 0; i < count; ++i) {
+                const float f = vf;
+                bad |= vbad != 0;
+                if (i + 1 < count) look(i + 1);
+                wait(cm.cready[i & 3], i >> 2);
+                const float corr = cm.corr[i & 3][r];
+                wait(cm.odone[i % OB], i / OB);
+                tc_after();
+                const uint32_t at = mine + (i % OB) * D;
 #pragma unroll
-            for (int k = 0; k < M::OC; k += 32) {
-                uint32_t d[32];
-                tc_load32(d, at + k);
-                tc_loaded();
+                for (int k = 0; k < M::OC; k += 32) {
+                    uint32_t d[32];
+                    tc_load32(d, at + k);
+                    tc_loaded();
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    O[k + j] = kTwo ? fmaf(__uint_as_float(d[j]), f, O[k + j] * corr)
-                                    : fmaf(O[k + j], corr, __uint_as_float(d[j]));
+                    for (int j = 0; j < 32; ++j)
+                        O[k + j] = fmaf(__uint_as_float(d[j]), f, O[k + j] * corr);
+                }
+                tc_before();
+                __syncwarp();
+                if (lane == 0) kq::mbar_arrive(bar(cm.ofree[i % OB]));
             }
-            tc_before();
-            __syncwarp();
-            if (lane == 0) kq::mbar_arrive(bar(cm.ofree[i % OB]));
         }
         wait(cm.ldone, 0);
+        if (!kTwo && count) {  // the sums are in tensor memory
+            wait(cm.odone[0], 0);
+            tc_after();
+            if (!__any_sync(~0u, dead())) {
+#pragma unroll
+                for (int k = 0; k < M::OC; k += 32) tc_load32(reinterpret_cast<uint32_t *>(O) + k, mine + k);
+                tc_loaded();
+                tc_before();
+            }
+        }
         float l = cm.l[r];
         const float m = cm.m[r];
         const int limit = on ? it.limit(tok) : -1;
@@ -769,11 +809,12 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
                 const int k = 2 * i + 1;
                 wait(cm.full[k % M::kSlots], k / M::kSlots);
                 if (!kTwo && i < edges) wait(cm.vclean[i & 3], i >> 2);
-                if (i >= OB) wait(cm.ofree[i % OB], i / OB - 1);
+                if (kTwo && i >= OB) wait(cm.ofree[i % OB], i / OB - 1);
                 wait(cm.pready[i % PB], i / PB);
                 if (__any_sync(~0u, dead())) break;
                 tc_after();
-                const uint32_t s = uniform(k % M::kSlots), b = uniform(i % PB), o = uniform(i % OB);
+                const uint32_t s = uniform(k % M::kSlots), b = uniform(i % PB);
+                const uint32_t o = kTwo ? uniform(i % OB) : 0, more = uniform(!kTwo && i > 0);
                 const uint64_t vd = desc_n(uniform(base + M::kRing) + s * M::kPart, TK * 128);
                 const uint32_t d = tm + M::kO + D * o, p = tm + M::kP + M::kPCols * b;
                 if (elected()) {
@@ -784,9 +825,9 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
                             const uint32_t pj = p + (lo_first(term) ? TK / 2 : 0) + 8 * j;
                             const uint64_t vj = vd + (((lo_second(term) ? M::kTerm : 0) + j * 2048) >> 4);
                             if (term + j) tc_add_ts(d, pj, vj, io);
-                            else tc_mma_ts(d, pj, vj, io, false);
+                            else tc_mma_ts(d, pj, vj, io, more);
                         }
-                    tc_commit(bar(cm.odone[0]) + 8 * o);
+                    if (kTwo || i == count - 1) tc_commit(bar(cm.odone[0]) + 8 * o);
                     tc_commit(bar(cm.pfree[0]) + 8 * b);
                     tc_commit(bar(cm.empty[0]) + 8 * s);
                 }

@@ -46,7 +46,6 @@ constexpr int kPairLaunchRegs = 65536 / kPairThreads;
 static_assert(256 * kPairSoftRegs + 256 * kPairOtherRegs <= kPairThreads * kPairLaunchRegs &&
                   kPairSoftRegs > kPairLaunchRegs && kPairOtherRegs < kPairLaunchRegs,
               "setmaxnreg: the shares, and the way each goes");
-constexpr float kPairLazy = 8.f;  // log2 of the growth that is not corrected
 
 // A unit: a part of an item's keys, with what each block sees of it.
 struct Unit {
@@ -247,7 +246,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 for (int j = 0; j < TK; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(d[j]));
                 const float now = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), m);
                 // (-infinity before the first key that the row attends)
-                const bool grown = now > m && !((now - m) * sc <= kPairLazy);
+                const bool grown = now > m && !((now - m) * sc <= kLazy);
                 if (__any_sync(~0u, grown)) {
                     const float f = !grown ? 1.f : m == -INFINITY ? 0.f : exp2_fast((m - now) * sc);
                     if (grown) m = now;
