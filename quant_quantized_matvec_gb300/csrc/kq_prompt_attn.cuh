@@ -330,7 +330,7 @@ struct Rows {
     static constexpr int kQCols = kTwo && !kLoShared ? D : D / 2;
     static constexpr int kPCols = kTwo ? TK : TK / 2;
     // (f32 at width 128: two of O and one of S and P; one of O, which is read
-    // before it is formed again, and two of S and P: 326 against 2xx us)
+    // before it is formed again, and two of S and P measured the same)
     static constexpr int OB = kTwo && D <= 128 ? 2 : 1;
     static constexpr int PB = kTwo && D == 128 ? 1 : 2;
     static constexpr int SB = kQCols + 2 * TK + PB * kPCols + OB * D <= 512 ? 2 : 1;
@@ -765,6 +765,8 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
             copy(2 * count);
         } else if (w == M::kFirst) {
             // --------------------------------------------- S of each tile
+            // (One warp for both, O first: f32 370 against 328 us, as it issues
+            // a product in about the time that the tensor core takes for one.)
             tc_after();
             const uint32_t tm = uniform(tmem);
             const uint64_t qd = desc_k(uniform(base + M::kControl));  // (the queries' lo terms)
