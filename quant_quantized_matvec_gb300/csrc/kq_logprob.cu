@@ -112,17 +112,19 @@ struct ScoreShared {
     Sums parts[kScoreCluster];
 };
 
-// The `top` largest of n sorted lists (of up to 16), in sh.best: entries below
-// the largest of the lists' last ones are left out, the others go to the place
-// that the number of larger ones gives.  (A tree of merges: 1.7 us against 0.5.)
+// The `top` largest of n sorted lists (of up to 16), in sh.best.  Entries that
+// cannot be of them are left out: what the `top`-th of some list, or the r-th of
+// every one (n r >= top), passes.  The others go to the place that the number of
+// larger ones gives.  (A tree of merges: 1.7 us against 0.5.)
 __device__ __forceinline__ void join_lists(ScoreShared &sh, const Key (*list)[32], int n, int top, int w,
                                            int lane) {
     __syncthreads();
     if (threadIdx.x == 0) sh.count = 0;
     if (threadIdx.x < 32) sh.best[lane] = 0;
     __syncthreads();
-    const uint32_t least =
-        __reduce_max_sync(~0u, lane < n ? (uint32_t)(list[lane][top - 1] >> 32) : 0u);
+    const uint32_t last = lane < n ? (uint32_t)(list[lane][top - 1] >> 32) : 0u;
+    const uint32_t each = lane < n ? (uint32_t)(list[lane][(top + n - 1) / n - 1] >> 32) : ~0u;
+    const uint32_t least = max(__reduce_max_sync(~0u, last), __reduce_min_sync(~0u, each));
     const Key mine = w < n ? list[w][lane] : 0;
     const bool in = mine != 0 && lane < top && (uint32_t)(mine >> 32) >= least;
     const uint32_t who = __ballot_sync(~0u, in);
@@ -132,12 +134,19 @@ __device__ __forceinline__ void join_lists(ScoreShared &sh, const Key (*list)[32
     if (in) sh.pool[at + __popc(who & ((1u << lane) - 1))] = mine;
     __syncthreads();
     const int all = sh.count;
-    if ((int)threadIdx.x < all) {
-        const Key k = sh.pool[threadIdx.x];
+    // up to 128 keys: four threads count for each
+    const int by = all <= kScoreThreads / 4 ? 4 : 1;
+    const int i = threadIdx.x / by, part = threadIdx.x & (by - 1);
+    if (w * 32 < all * by) {
+        const Key k = i < all ? sh.pool[i] : ~0ull;
         int before = 0;
-#pragma unroll 8
-        for (int i = 0; i < all; ++i) before += sh.pool[i] > k;
-        if (before < top) sh.best[before] = k;
+#pragma unroll 4
+        for (int j = part; j < all; j += by) before += sh.pool[j] > k;
+        if (by == 4) {
+            before += __shfl_xor_sync(~0u, before, 1);
+            before += __shfl_xor_sync(~0u, before, 2);
+        }
+        if (i < all && part == 0 && before < top) sh.best[before] = k;
     }
     __syncthreads();
 }

@@ -267,14 +267,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     }
                 }
                 // p = 2^(s sc - m sc + up).  With a product m sc past 2^10 its
-                // rounding would show: the difference is taken first.  (Lanes
-                // without a row hold anything, and have no say in it.)
+                // rounding would show: that row's difference is taken first.
+                // (Lanes without a row hold anything, and have no say in it.)
                 float c = m == -INFINITY ? M::kUp : M::kUp - m * sc;
-                if (__any_sync(~0u, on && !(fabsf(c) < 1024.f))) {
-                    const float from = m == -INFINITY ? 0.f : m;
+                const bool far = on && !(fabsf(c) < 1024.f);
+                if (__any_sync(~0u, far)) {
+                    const float from = far ? m : 0.f;
 #pragma unroll
                     for (int j = 0; j < TK; ++j) d[j] = __float_as_uint(__uint_as_float(d[j]) - from);
-                    c = M::kUp;
+                    if (far) c = M::kUp;
                 }
                 float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
                 uint32_t p[TK / 2];
