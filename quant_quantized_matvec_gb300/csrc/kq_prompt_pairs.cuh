@@ -181,6 +181,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             atomicOr(a.err, 1u);
         }
     };
+    // The same by a whole warp: false after an expired wait of any (which is only
+    // looked for where the barrier is not there yet).
+    auto arrived = [&](const uint64_t &b, int phase) {
+        if (__all_sync(~0u, kq::mbar_test(bar(b), phase & 1))) return true;
+        wait(b, phase);
+        return !__any_sync(~0u, dead());
+    };
     // The next unit as a role reads it; false at the end.  (After an expired
     // wait there is none.)  Its place is handed back once all have read it, and
     // the softmax warps are done with it.
@@ -223,8 +230,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const int whole = g.t1 - g.edges;                  // tiles below are seen by all rows
             float m = -INFINITY, l = 0.f;
             for (int i = 0; i < count; ++i) {
-                wait(cm.sdone[block], turn + i);
-                if (__any_sync(~0u, dead())) break;
+                if (!arrived(cm.sdone[block], turn + i)) break;
                 tc_after();
                 uint32_t d[TK];
 #pragma unroll
@@ -252,8 +258,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     if (grown) m = now;
                     l *= f;
                     if (i > 0) {
-                        wait(cm.odone[block], turn + i - 1);
-                        if (__any_sync(~0u, dead())) break;
+                        if (!arrived(cm.odone[block], turn + i - 1)) break;
                         tc_after();
 #pragma unroll
                         for (int j = 0; j < D; j += 16) {
@@ -292,8 +297,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 l += sum0.x + sum0.y;
                 // ---- P, once the O before it has read its place
                 if (i > 0) {
-                    wait(cm.odone[block], turn + i - 1);
-                    if (__any_sync(~0u, dead())) break;
+                    if (!arrived(cm.odone[block], turn + i - 1)) break;
                     tc_after();
                 }
 #pragma unroll
@@ -492,19 +496,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 const int count = g.t1 - g.t0, n = g.n[b], from = count - n;
                 // Copy x of the walk (keys, values by turns) is there; and is
                 // given back: once the products so far are done, or at once.
-                auto there = [&](int x) {
-                    wait(cm.full[x % M::kSlots], x / M::kSlots);
-                };
-                auto clean = [&](int i) {
-                    if (i < g.edges) wait(cm.vclean[(cleaned + i) & 3], (cleaned + i) >> 2);
-                };
+                auto there = [&](int x) { return arrived(cm.full[x % M::kSlots], x / M::kSlots); };
                 bool stop = false;
                 for (int i = 0; i < from; ++i) {  // tiles that only the other block sees
                     for (int x = 2 * (tile + i); x < 2 * (tile + i) + 2; ++x) {
                         // (not for values to be cleaned: a slot is only copied to
                         // again when its values four tiles ago are done with)
-                        there(x);
-                        if (__any_sync(~0u, dead())) stop = true;
+                        stop = !there(x);
                         if (stop) break;
                         if (lane == 0) kq::mbar_arrive(bar(cm.empty[x % M::kSlots]));
                         __syncwarp();
@@ -512,12 +510,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     if (stop) break;
                 }
                 if (stop) break;
-                if (n > 0) wait(cm.qfull[b], have++);
+                if (n > 0 && !arrived(cm.qfull[b], have++)) break;
                 auto scores = [&](int i) {
                     const int x = 2 * (tile + i);
-                    there(x);
-                    if (i > from) wait(cm.sfree[b], turn + i - from - 1);
-                    if (__any_sync(~0u, dead())) return false;
+                    if (!there(x)) return false;
+                    if (i > from && !arrived(cm.sfree[b], turn + i - from - 1)) return false;
                     tc_after();
                     const uint32_t s = uniform(x % M::kSlots);
                     const uint64_t kd = desc_k(uniform(base + M::kRing) + s * M::kTile);
@@ -543,13 +540,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         break;
                     }
                     const int x = 2 * (tile + i) + 1;
-                    there(x);
-                    clean(i);
-                    wait(cm.pready[b], turn + i - from);
-                    if (__any_sync(~0u, dead())) {
-                        stop = true;
-                        break;
-                    }
+                    const int e = cleaned + i;
+                    stop = !there(x) || (i < g.edges && !arrived(cm.vclean[e & 3], e >> 2)) ||
+                           !arrived(cm.pready[b], turn + i - from);
+                    if (stop) break;
                     tc_after();
                     const uint32_t s = uniform(x % M::kSlots), more = uniform(i > from);
                     const uint64_t vd = desc_n(uniform(base + M::kRing) + s * M::kTile, TK * 128);
