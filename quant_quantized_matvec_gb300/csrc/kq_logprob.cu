@@ -11,7 +11,12 @@
 // lanes' largest and a merge.  Lists and sums are joined by warps, then over a
 // cluster of CTAs that share a row.
 //
-// Bound by memory for many rows, by latency for few.
+// Bound by memory for many rows: 1999 rows of 202048 f32 logits, 5 alternatives,
+// 275 us, 87% of the copy rate (486 us with a bound of each warp's own, where two
+// batches of three had to be looked at).  By latency for few: one row 12.4 us with
+// 20 alternatives, 4.7 without; the load takes 1.2 us, and what the first batch
+// holds, candidates and two joins, the rest.  (The first batch's candidates into
+// one pool, sorted by counting: 14.8 us.)
 #include <cooperative_groups.h>
 
 #include <mutex>
