@@ -130,42 +130,68 @@ __device__ __forceinline__ int scan_max(int x, int lane) {
 struct Place {
     int b0 = 0, s = 0, k = 0, blocks = 0;
 };
+// N sequences: first token and end, first key and end.
+template <int N>
+struct Some {
+    int b, lo[N], hi[N], klo[N], khi[N];
+};
 
-// Walks the sequences from `p` on, 32 at a time: body(b, first token, end, first
-// key, key end) for each lane's sequence (an empty one past the last), until it
-// returns true; p is then where it was.  A start counts as the largest so far,
-// within what there is.  By one warp.
-template <class F>
+// Walks the sequences from `p` on, N a lane and 32 N at a time (empty ones past
+// the last), until body(Some) returns true; p is then where it was.  A start
+// counts as the largest so far, within what there is.  By one warp.
+template <int N, class F>
 __device__ __forceinline__ void walk(const PromptArgs &a, int lane, Place &p, F &&body) {
     while (p.b0 < a.nseq) {
-        const int b = min(p.b0 + lane, a.nseq), b1 = min(b + 1, a.nseq);
-        // (all loads at once)
-        const int x0 = __ldg(a.start + b), x1 = __ldg(a.start + b1);
-        const int y0 = a.kstart ? __ldg(a.kstart + b) : 0, y1 = a.kstart ? __ldg(a.kstart + b1) : 0;
-        auto run = [&](int x, int y, int all, int before, int &lo, int &hi) {
-            lo = max(scan_max(min(max(x, 0), all), lane), before);
-            hi = max(lo, min(max(y, 0), all));
+        Some<N> q;
+        q.b = p.b0 + N * lane;
+        int x[N + 1], y[N + 1];
+#pragma unroll
+        for (int e = 0; e <= N; ++e) {  // (all loads at once)
+            const int b = min(q.b + e, a.nseq);
+            x[e] = __ldg(a.start + b), y[e] = a.kstart ? __ldg(a.kstart + b) : 0;
+        }
+        auto run = [&](int (&v)[N + 1], int all, int before, int (&lo)[N], int (&hi)[N]) {
+            int most = 0;
+#pragma unroll
+            for (int e = 0; e <= N; ++e) {
+                v[e] = min(max(v[e], 0), all);
+                if (e < N) most = max(most, v[e]);
+            }
+            const int upto = scan_max(most, lane);
+            const int prev = __shfl_up_sync(~0u, upto, 1);
+            lo[0] = max(v[0], lane ? max(prev, before) : before);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                hi[e] = max(lo[e], v[e + 1]);
+                if (e + 1 < N) lo[e + 1] = hi[e];
+            }
         };
-        int lo, hi, klo, khi;
-        run(x0, x1, a.ntok, p.s, lo, hi);
-        if (a.kstart) run(y0, y1, a.nkeys, p.k, klo, khi);
-        else klo = lo, khi = hi;
-        if (body(b, lo, hi, klo, khi)) return;
-        p.b0 += 32;
-        p.s = __shfl_sync(~0u, hi, 31), p.k = __shfl_sync(~0u, khi, 31);
+        run(x, a.ntok, p.s, q.lo, q.hi);
+        if (a.kstart) {
+            run(y, a.nkeys, p.k, q.klo, q.khi);
+        } else {
+#pragma unroll
+            for (int e = 0; e < N; ++e) q.klo[e] = q.lo[e], q.khi[e] = q.hi[e];
+        }
+        if (body(q)) return;
+        p.b0 += 32 * N;
+        p.s = __shfl_sync(~0u, q.hi[N - 1], 31), p.k = __shfl_sync(~0u, q.khi[N - 1], 31);
     }
 }
 
 // Item `i` of the call into shared memory, by a warp; found = 0 past the last.
 // p: where the walk for a lower item ended, or the beginning.
+template <int N>
 __device__ __forceinline__ void find_item(const PromptArgs &a, int i, Item &it, int lane, Place &p) {
     const int across = a.kv_heads * a.hblocks;
     const int blk = i / across, h = i - blk * across;
     if (lane == 0) it.found = 0;
     __syncwarp();
-    walk(a, lane, p, [&](int b, int lo, int hi, int klo, int khi) {
-        const int blocks = (hi - lo + a.tok - 1) / a.tok;
-        int upto = blocks;
+    walk<N>(a, lane, p, [&](const Some<N> &q) {
+        int blocks[N], upto = 0;
+#pragma unroll
+        for (int e = 0; e < N; ++e) blocks[e] = (q.hi[e] - q.lo[e] + a.tok - 1) / a.tok, upto += blocks[e];
+        const int mine = upto;
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
             const int v = __shfl_up_sync(~0u, upto, o);
@@ -178,21 +204,33 @@ __device__ __forceinline__ void find_item(const PromptArgs &a, int i, Item &it, 
             return false;
         }
         if (lane == __ffs(past) - 1) {
-            const int at = upto - 1 - blk;  // the last block first
-            it.seq = b, it.first = lo, it.n = hi - lo, it.kfirst = klo, it.m = khi - klo;
-            it.tok0 = at * a.tok, it.nt = min(a.tok, it.n - it.tok0);
-            it.head = h / a.hblocks;
-            const int run = h - it.head * a.hblocks;
-            it.hq = it.head * a.per + run * a.hb, it.nh = min(a.hb, a.per - run * a.hb);
-            it.found = 1;
+            int end = upto - mine;
+            bool there = false;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                end += blocks[e];
+                if (there || end <= blk) continue;
+                there = true;
+                const int at = end - 1 - blk;  // the last block first
+                it.seq = q.b + e, it.first = q.lo[e], it.n = q.hi[e] - q.lo[e];
+                it.kfirst = q.klo[e], it.m = q.khi[e] - q.klo[e];
+                it.tok0 = at * a.tok, it.nt = min(a.tok, it.n - it.tok0);
+                it.head = h / a.hblocks;
+                const int run = h - it.head * a.hblocks;
+                it.hq = it.head * a.per + run * a.hb, it.nh = min(a.hb, a.per - run * a.hb);
+                it.found = 1;
+            }
         }
         return true;
     });
     __syncwarp();
 }
 __device__ __forceinline__ void find_item(const PromptArgs &a, int i, Item &it, int lane) {
+    // (From the beginning, four sequences a lane where there are many: 4096
+    // prompts of 8 tokens, 16 / 4 heads of 256, 5.6 ms with one, 2.6 with four.)
     Place p;
-    find_item(a, i, it, lane, p);
+    if (a.nseq > 32) find_item<4>(a, i, it, lane, p);
+    else find_item<1>(a, i, it, lane, p);
 }
 
 // 32-bit words of two 16-bit values of which one is not finite.
@@ -213,6 +251,31 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t 
     hi = pack2<__half>(a, b);
     const float2 f = unpack2<__half>(hi);
     lo = pack2<__half>(a - f.x, b - f.y);
+}
+
+// Another CTA of the grid that has not begun, whose work this one takes over
+// instead: asked for, its number 16 bytes later at `to`.
+__device__ __forceinline__ void ask_for_cta(uint32_t to, uint32_t bar) {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(to),
+        "r"(bar)
+        : "memory");
+}
+// The answer: the CTA's number, or -1 where there is none (then none is asked
+// for again).
+__device__ __forceinline__ int cta_given(uint32_t at) {
+    int x;
+    asm volatile(
+        "{\n .reg .b128 h;\n .reg .pred p;\n .reg .b32 a, b, c, d;\n"
+        " ld.shared.b128 h, [%1];\n"
+        " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n"
+        " mov.b32 a, -1;\n"
+        " @p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {a, b, c, d}, h;\n"
+        " mov.b32 %0, a;\n}\n"
+        : "=r"(x)
+        : "r"(at)
+        : "memory");
+    return x;
 }
 
 // 32 bytes of a row.
@@ -257,10 +320,17 @@ __global__ void __launch_bounds__(kSplitThreads)
     if (tid < 32) {
         __syncwarp();
         Place p;
-        walk(a, lane, p, [&](int b, int lo, int hi, int klo, int khi) {
-            const int base = klo / TK + b, tiles = b < a.nseq ? (khi - klo + TK - 1) / TK : 0;
-            const bool here = slot >= base && slot < base + tiles;
-            if (here) found[1] = klo + (slot - base) * TK, found[2] = min(TK, khi - found[1]), found[0] = 1;
+        walk<4>(a, lane, p, [&](const Some<4> &q) {
+            bool here = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int base = q.klo[e] / TK + q.b + e, tiles = (q.khi[e] - q.klo[e] + TK - 1) / TK;
+                if (q.b + e < a.nseq && slot >= base && slot < base + tiles) {
+                    here = true;
+                    found[1] = q.klo[e] + (slot - base) * TK, found[2] = min(TK, q.khi[e] - found[1]);
+                    found[0] = 1;
+                }
+            }
             return __any_sync(~0u, here) != 0;
         });
     }
@@ -356,9 +426,10 @@ struct Rows {
 };
 
 struct RowsShared {
+    uint4 answer;  // of ask_for_cta
     Item item;
     uint64_t full[8], empty[8], sdone[2], sfree[2], pready[2], pfree[2], odone[2], ofree[2], cready[4],
-        vraw[4], vclean[4], ldone, drain[2];
+        vraw[4], vclean[4], ldone, given, drain[2];
     uint32_t tmem;
     int dead, bad;
     float corr[4][kRows];  // of tile i & 3: the factor of what was summed before
@@ -396,12 +467,27 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
             kq::mbar_init(bar(cm.vraw[i]), 1), kq::mbar_init(bar(cm.vclean[i]), 1);
         }
         kq::mbar_init(bar(cm.ldone), kTwo ? 4 : 5);
+        kq::mbar_init(bar(cm.given), 1);
         cm.dead = cm.bad = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
     const Item it = cm.item;
-    if (!it.found) return;
+    if (!it.found) {
+        // Past the last item (grids go by the most that there may be): the CTAs
+        // after this one, which have none either, need not begin.  (4096 prompts
+        // of 8 tokens, f32: 2.4 ms if they do.)
+        for (int n = 0; tid == 0; ++n) {
+            kq::mbar_expect_tx(bar(cm.given), 16);
+            ask_for_cta(kq::smem_addr(&cm.answer), bar(cm.given));
+            if (!kq::mbar_wait(bar(cm.given), n & 1, kq::kWaitLimitNs) ||
+                cta_given(kq::smem_addr(&cm.answer)) < 0)
+                break;
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        if constexpr (kTwo) kq::wait_prerequisites();
+        return;
+    }
     if (w == M::kFirst) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                          kq::smem_addr(&cm.tmem))

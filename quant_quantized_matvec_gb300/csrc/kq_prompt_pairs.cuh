@@ -83,34 +83,9 @@ struct PairShared {
 };
 static_assert(sizeof(PairShared) <= 2048, "layout");
 
-// Another CTA of the grid that has not begun, whose work this one takes over
-// instead: asked for, its number 16 bytes later at `to`.
-__device__ __forceinline__ void ask_for_cta(uint32_t to, uint32_t bar) {
-    asm volatile(
-        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(to),
-        "r"(bar)
-        : "memory");
-}
-// The answer: the CTA's number, or -1 where there is none (then none is asked
-// for again).
-__device__ __forceinline__ int cta_given(uint32_t at) {
-    int x;
-    asm volatile(
-        "{\n .reg .b128 h;\n .reg .pred p;\n .reg .b32 a, b, c, d;\n"
-        " ld.shared.b128 h, [%1];\n"
-        " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n"
-        " mov.b32 a, -1;\n"
-        " @p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {a, b, c, d}, h;\n"
-        " mov.b32 %0, a;\n}\n"
-        : "=r"(x)
-        : "r"(at)
-        : "memory");
-    return x;
-}
-
 // Unit `u` into shared memory, by one warp; false past the last.
 __device__ __forceinline__ bool find_unit(const PromptArgs &a, int u, int tile, Unit &g, int lane, Place &p) {
-    find_item(a, u / a.splits, g.item, lane, p);
+    find_item<1>(a, u / a.splits, g.item, lane, p);
     const Item &it = g.item;
     const bool found = it.found != 0;
     if (found && lane == 0) {
