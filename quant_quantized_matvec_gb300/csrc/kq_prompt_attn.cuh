@@ -454,24 +454,36 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
     const int rank = blockIdx.x % a.splits;
     if (w == 0) {
         find_item(a, blockIdx.x / a.splits, cm.item, lane);
-    } else if (tid == 32) {
-        for (int i = 0; i < 8; ++i) kq::mbar_init(bar(cm.full[i]), 1), kq::mbar_init(bar(cm.empty[i]), 1);
-        for (int i = 0; i < 2; ++i) {
+    } else if (w == 1) {  // a lane a barrier, or a few
+        if (lane < 8) {
+            kq::mbar_init(bar(cm.full[lane]), 1), kq::mbar_init(bar(cm.empty[lane]), 1);
+        } else if (lane < 10) {
+            const int i = lane - 8;
             kq::mbar_init(bar(cm.sdone[i]), 1), kq::mbar_init(bar(cm.sfree[i]), 4);
             kq::mbar_init(bar(cm.pready[i]), 4), kq::mbar_init(bar(cm.pfree[i]), 1);
             kq::mbar_init(bar(cm.odone[i]), 1), kq::mbar_init(bar(cm.ofree[i]), M::OW);
             kq::mbar_init(bar(cm.drain[i]), 1);
-        }
-        for (int i = 0; i < 4; ++i) {
+        } else if (lane < 14) {
+            const int i = lane - 10;
             kq::mbar_init(bar(cm.cready[i]), 4);
             kq::mbar_init(bar(cm.vraw[i]), 1), kq::mbar_init(bar(cm.vclean[i]), 1);
+        } else if (lane == 14) {
+            kq::mbar_init(bar(cm.ldone), kTwo ? 4 : 5);
+            kq::mbar_init(bar(cm.given), 1);
+            cm.dead = cm.bad = 0;
         }
-        kq::mbar_init(bar(cm.ldone), kTwo ? 4 : 5);
-        kq::mbar_init(bar(cm.given), 1);
-        cm.dead = cm.bad = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    } else if (w == M::kFirst) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                         kq::smem_addr(&cm.tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    } else if (!kTwo && w == M::kFirst + 1 && lane < 2) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(lane ? &a.vmap : &a.kmap) : "memory");
     }
+    tc_before();
     __syncthreads();
+    tc_after();
     const Item it = cm.item;
     if (!it.found) {
         // Past the last item (grids go by the most that there may be): the CTAs
@@ -485,18 +497,11 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
                 break;
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
+        if (w == M::kFirst)
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(cm.tmem));
         if constexpr (kTwo) kq::wait_prerequisites();
         return;
     }
-    if (w == M::kFirst) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
-                         kq::smem_addr(&cm.tmem))
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
-    tc_before();
-    __syncthreads();
-    tc_after();
     const uint32_t tmem = cm.tmem;
 
     auto dead = [&]() { return *(volatile int *)&cm.dead != 0; };
