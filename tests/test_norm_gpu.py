@@ -40,6 +40,26 @@ def test_against_64_bits(n, hq, hk, dim, rot, inter, kind, dtype):
     check(yk, k, w[1], pos, table, inter, 1e-6, dtype)
 
 
+@pytest.mark.parametrize("kind,dtype", [(F32, F32), (F32, BF16), (F16, F16)])
+@pytest.mark.parametrize("n,hq,hk,dim,rot,inter", [(9001, 9, 2, 128, 64, False), (5003, 6, 5, 256, 256, True),
+                                                   (16001, 7, 3, 96, 40, False), (20011, 5, 4, 64, 64, True)])
+def test_many_tokens(n, hq, hk, dim, rot, inter, kind, dtype):
+    """Sizes at which a group of lanes goes through four heads, or what is left
+    of them."""
+    q, k, w, pos, table = inputs(n, hq, hk, dim, rot, kind, n, extra=1)
+    pos[n // 2] = 50
+    q[5, 1, 3], k[7, 0] = float("inf"), 0
+    yq, yk = kq.norm_rope(q, k, *w, pos, table, interleaved=inter, dtype=dtype)
+    assert yq[n // 2].isnan().all() and yk[n // 2].isnan().all() and yq[5, 1].isnan().any()
+    assert (yk[7, 0] == 0).all()
+    keep = torch.ones(n, dtype=torch.bool, device="cuda")
+    keep[[5, n // 2]] = False
+    for y, x, weight in ((yq, q, w[0]), (yk, k, w[1])):
+        check(y[keep], x[keep], weight, pos[keep], table, inter, 1e-6, dtype)
+    assert torch.equal(kq.norm_rope(q[5:6], None, w[0], None, pos[5:6], table, interleaved=inter,
+                                    dtype=dtype)[0][0, 2:], yq[5, 2:])
+
+
 def test_without_weights_table_or_keys():
     q, k, w, pos, table = inputs(11, 4, 2, 128, 128, F32, 3)
     yq, none = kq.norm_rope(q)

@@ -246,6 +246,56 @@ def test_many_sequences(kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dim", [64, 256])
+def test_the_most_sequences(dim, kind):
+    """4096 sequences, most of them empty or of one token: far fewer items than
+    the grid has CTAs for."""
+    new = [1 + i % 2 if i % 3 == 0 else 0 for i in range(4095)] + [70]
+    q, k, v, s, ks = inputs(new, [i % 5 if n else 0 for i, n in enumerate(new)], 2, 1, dim, kind, 18)
+    check(kq.prompt_attention(q, k, v, dev(s), dev(ks)), q, k, v, s, ks)
+    # and none at all
+    out = torch.full_like(q, 3.0)
+    kq.prompt_attention(q, k, v, torch.zeros_like(dev(s)), torch.zeros_like(dev(s)), out=out)
+    assert (out == 3).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("hq,hkv", [(1024, 1), (1024, 1024), (130, 1)])
+def test_many_heads(hq, hkv, kind):
+    q, k, v, s, ks = inputs([3, 2], [5, 0], hq, hkv, 64, kind, 19)
+    check(kq.prompt_attention(q, k, v, dev(s), dev(ks)), q, k, v, s, ks)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dim,new,ctx", [(128, [50], [20]), (64, [9], [4000]), (256, [9], [4000])])
+def test_without_a_workspace(dim, new, ctx, kind):
+    """The C call takes a stream-ordered temporary; also in a captured graph."""
+    from quant_quantized_matvec_gb300 import _binding
+    lib = _binding.load()
+    q, k, v, s, ks = inputs(new, ctx, 4, 2, dim, kind, 21)
+    sd, kd = dev(s), dev(ks)
+    want = kq.prompt_attention(q, k, v, sd, kd)
+    got = torch.empty_like(q)
+
+    def call():
+        return lib.kq_prompt_attention(
+            {F32: 0, F16: 1, BF16: 30}[kind], 1, q.shape[0], k.shape[0], sd.data_ptr(), kd.data_ptr(),
+            q.data_ptr(), 4 * dim, 4, k.data_ptr(), 2 * dim, v.data_ptr(), 2 * dim, 2, dim, dim ** -0.5,
+            got.data_ptr(), None, 0, torch.cuda.current_stream().cuda_stream)
+
+    assert call() == 0
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        assert call() == 0
+    got.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("dim,new,ctx", [(128, [700, 300], [0, 0]), (128, [16], [4000]), (256, [90], [800]),
                                          (64, [333, 5], [9, 400])])
 def test_streams_graphs_and_workspaces(dim, new, ctx, kind):
@@ -357,6 +407,28 @@ def test_expired_waits(dim, new, ctx, kind):
         for _ in range(2):
             assert torch.equal(kq.prompt_attention(q, k, v, sd, kd), want)
     assert times or sum(new) < 5000
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_wrong_arguments(kind):
+    q, k, v, s, ks = inputs([30], [10], 4, 2, 64, kind, 22)
+    sd, kd = dev(s), dev(ks)
+    with pytest.raises(kq.KQError, match="ALIAS"):
+        kq.prompt_attention(q, k, v, sd, kd, out=q)
+    with pytest.raises(kq.KQError, match="NTOK"):
+        kq.prompt_attention(q, k, v, sd)  # more keys than queries, and no starts of theirs
+    with pytest.raises(kq.KQError, match="SHAPE"):
+        kq.prompt_attention(q[:, :3], k, v, sd, kd)
+    with pytest.raises(kq.KQError, match="COUNT"):
+        kq.prompt_attention(q, k, v, sd[:1], kd[:1])
+    for bad in (dict(q=q.double()), dict(k=k.double()), dict(v=v[:5]), dict(start=sd.long()), dict(v=v.cpu()),
+                dict(q=q[..., ::2]), dict(out=torch.empty_like(q)[:5]), dict(start=sd.cpu())):
+        args = dict(q=q, k=k, v=v, start=sd, key_start=kd)
+        args.update(bad)
+        with pytest.raises(ValueError):
+            kq.prompt_attention(**args)
+    got = kq.prompt_attention(q[:0], k, v, torch.zeros_like(sd), kd)
+    assert got.shape == (0, 4, 64)
 
 
 def test_agrees_with_the_cache():
