@@ -278,18 +278,6 @@ __device__ __forceinline__ int cta_given(uint32_t at) {
     return x;
 }
 
-// 32 bytes of a row.
-__device__ __forceinline__ void store32(void *p, const uint32_t *v, bool aligned) {
-    if (aligned) {
-        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
-                     "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                     : "memory");
-    } else {
-        reinterpret_cast<uint4 *>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<uint4 *>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
-    }
-}
-
 // ------------------------------------------------------- splitting f32
 // The largest finite magnitude's exponent e: it is below 2^e.
 __device__ __forceinline__ int exponent_of(float top, int least) {
@@ -796,7 +784,8 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
                 }
             }
         }
-        if (dead()) l = quiet_nan();
+        const bool lost = __any_sync(~0u, dead());
+        if (lost) l = quiet_nan();
         if (a.splits > 1) {
             float *part = a.part + (int64_t)blockIdx.x * kRows * (D + 2);
             // by values, of 32 rows each: part[32 rows][D][32]
@@ -804,24 +793,41 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
 #pragma unroll
             for (int k = 0; k < M::OC; ++k) to[32 * k] = O[k];
             if (c0 == 0) part[kRows * D + r] = m, part[kRows * (D + 1) + r] = l;
-        } else if (on) {
+        } else {
             // (a row that attends something and has no sum has scores of
             // -infinity only)
             float inv = limit < 0 ? 0.f : __fdiv_rn(kTwo ? 32768.f : 1.f, l);
-            if (dead()) inv = quiet_nan();
-            T *to = static_cast<T *>(a.out) +
-                    ((int64_t)(it.first + tok) * a.q_heads + it.hq + hq) * D + c0;
-            const bool wide = ((uintptr_t)a.out & 31) == 0;
-            constexpr int kEach = 32 / sizeof(T);
+            if (lost) inv = quiet_nan();
+            T *to = static_cast<T *>(a.out) + ((int64_t)(it.first + it.tok0) * a.q_heads + it.hq) * D + c0;
+            const uint32_t place = (tok - it.tok0) * a.q_heads + hq, rows = __ballot_sync(~0u, on);
+            // Rows go out whole, through shared memory (every copy there was used
+            // up by the last O): a lane's own row in pieces of 32 bytes took 3 us.
+            constexpr int kRow = M::OC * sizeof(T), kLanes = kRow / 16;  // bytes; lanes of a row
+            uint8_t *stage = smem + M::kRing + (w - 4) * 32 * kRow;
+            static_assert(M::OW * 32 * kRow <= M::kSlots * M::kPart && 32 % kLanes == 0, "layout");
+            if (lost) {  // (copies may still come)
+                for (int k = 0; k < M::OC && on; ++k) to[(int64_t)place * D + k] = from_f32<T>(inv);
+            } else {
 #pragma unroll
-            for (int k = 0; k < M::OC; k += kEach) {
-                uint32_t q[8];
+                for (int k = 0; k < kLanes; ++k) {
+                    uint4 x;
+                    uint32_t *q = &x.x;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if constexpr (kTwo) q[e] = __float_as_uint(O[k + e] * inv);
-                    else q[e] = pack2<H>(O[k + 2 * e] * inv, O[k + 2 * e + 1] * inv);
+                    for (int e = 0; e < 4; ++e) {
+                        if constexpr (kTwo) q[e] = __float_as_uint(O[4 * k + e] * inv);
+                        else q[e] = pack2<H>(O[8 * k + 2 * e] * inv, O[8 * k + 2 * e + 1] * inv);
+                    }
+                    *reinterpret_cast<uint4 *>(stage + lane * kRow + ((k ^ (lane & 7)) << 4)) = x;
                 }
-                store32(to + k, q, wide);
+                __syncwarp();
+#pragma unroll 8
+                for (int k = 0; k < kLanes; ++k) {
+                    const int at = k * (32 / kLanes) + lane / kLanes, c = lane % kLanes;
+                    const uint4 x = *reinterpret_cast<const uint4 *>(stage + at * kRow + ((c ^ (at & 7)) << 4));
+                    const uint32_t far = __shfl_sync(~0u, place, at);
+                    if (rows >> at & 1)
+                        *reinterpret_cast<uint4 *>(to + (int64_t)far * D + c * (16 / sizeof(T))) = x;
+                }
             }
         }
     } else {

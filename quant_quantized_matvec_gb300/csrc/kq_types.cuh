@@ -23,6 +23,15 @@ __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
 template <>
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 
+template <class T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32(float x) { return x; }
+template <>
+__device__ __forceinline__ __half from_f32(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32(float x) { return __float2bfloat16_rn(x); }
+
 // Two values as a word of 16-bit ones, the first low.
 template <class T>
 __device__ __forceinline__ uint32_t pack2(float a, float b);
