@@ -14,6 +14,7 @@
 
 #include "kq.h"
 #include "kq_host.h"
+#include "kq_prompt.h"
 #include "kq_internal.h"
 #include "kq_launch.cuh"
 #include "kq_plan.h"
@@ -1264,7 +1265,7 @@ cudaError_t rows_map(const void *data, int rows, int64_t blocks, int box, CUtens
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
-cudaError_t values_map(const void *data, bool bf16, int rank, const uint64_t *dims,
+cudaError_t values_map(const void *data, int type, int rank, const uint64_t *dims,
                        const uint64_t *strides, const uint32_t *box, CUtensorMap *out) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return cudaErrorNotSupported;
@@ -1273,7 +1274,11 @@ cudaError_t values_map(const void *data, bool bf16, int rank, const uint64_t *di
     for (int i = 0; i < rank; ++i) d[i] = dims[i], b[i] = box[i], each[i] = 1;
     for (int i = 0; i + 1 < rank; ++i) st[i] = strides[i];
     const CUresult r =
-        enc(out, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+        enc(out,
+            type == KQ_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+            : type == KQ_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                              : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+            rank,
             const_cast<void *>(data), d, st, b, each, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);

@@ -29,10 +29,10 @@ cudaError_t device(Device &d);
 // `box` rows, swizzled over 64 bytes.
 cudaError_t rows_map(const void *data, int rows, int64_t blocks, int box, CUtensorMap *out);
 
-// A tensor map of 16-bit values, `rank` dimensions (strides in bytes, of the
-// second and on), boxes of 64 values by the others, swizzled over 128 bytes,
-// with zeros outside.
-cudaError_t values_map(const void *data, bool bf16, int rank, const uint64_t *dims,
+// A tensor map of values of a type of kq_prompt.h, `rank` dimensions (strides in
+// bytes, of the second and on), boxes of 128 bytes by the others, swizzled over
+// 128 bytes, with zeros outside.
+cudaError_t values_map(const void *data, int type, int rank, const uint64_t *dims,
                        const uint64_t *strides, const uint32_t *box, CUtensorMap *out);
 
 struct Span {

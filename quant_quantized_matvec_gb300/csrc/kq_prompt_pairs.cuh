@@ -661,11 +661,7 @@ cudaError_t launch_pairs(PromptArgs &a, cudaStream_t s) {
         if (e == cudaSuccess) e = keys_map<T>(a.v, a.v_stride, a, D, M::TK, &a.vmap);
     }
     if (e != cudaSuccess) return e;
-    // queries as (value, head, token): a block's box is hb heads of tok / 2 tokens
-    const uint64_t dims[3] = {(uint64_t)D, (uint64_t)a.q_heads, (uint64_t)a.ntok};
-    const uint64_t strides[2] = {2ull * D, 2ull * a.q_stride};
-    const uint32_t box[3] = {64, (uint32_t)a.hb, (uint32_t)(a.tok / 2)};
-    e = kqhost::values_map(a.q, M::kBf16, 3, dims, strides, box, &a.qmap);
+    e = queries_map<T>(a, D, a.tok / 2, &a.qmap);  // (a block's)
     if (e != cudaSuccess) return e;
     kq_prompt_pairs<T, D><<<(unsigned)(a.items * a.splits), kPairThreads, M::kBytes, s>>>(a);
     return cudaGetLastError();

@@ -7,12 +7,19 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <type_traits>
+
 #include "kq_prompt.h"
 
 namespace kqp {
 
 inline int type_size(int type) { return type == KQ_F32 ? 4 : 2; }
 inline bool is_type(int type) { return type == KQ_F32 || type == KQ_F16 || type == KQ_BF16; }
+
+template <class T>
+constexpr int type_of() {
+    return sizeof(T) == 4 ? KQ_F32 : std::is_same<T, __half>::value ? KQ_F16 : KQ_BF16;
+}
 
 template <class T>
 __device__ __forceinline__ float to_f32(T x);
