@@ -36,10 +36,10 @@
 // become f16 are held times 2^7 besides, as f16 has few bits below 2^-14.
 //
 // Bound by the products and what stands between two of them.  f32, 4097 tokens,
-// 32 / 2 heads of 128: 328 us, 419 TFLOP/s of the formula and three times that of
-// products; the tensor core is at work 57% of the time, a tile takes 2500 clocks
-// for 1536 of products.  bf16 at width 256, three prompts of up to 3001 tokens
-// behind 500, 16 / 4 heads: 269 us, 901 TFLOP/s.
+// 32 / 2 heads of 128: 317 us, 434 TFLOP/s of the formula and three times that of
+// products; the tensor core is at work 62% of the time, a tile takes 1950 to 2000
+// clocks for 1536 of products.  bf16 at width 256, three prompts of up to 3001
+// tokens behind 500, 16 / 4 heads: 257 us, 943 TFLOP/s.
 //
 // NaN and infinities must not reach rows that do not attend them (0 * inf):
 // values that are not finite are zeros in the tile (f32: all tiles; 16 bits:
