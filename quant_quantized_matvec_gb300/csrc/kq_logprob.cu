@@ -12,11 +12,12 @@
 // cluster of CTAs that share a row.
 //
 // Bound by memory for many rows: 1999 rows of 202048 f32 logits, 5 alternatives,
-// 275 us, 87% of the copy rate (486 us with a bound of each warp's own, where two
-// batches of three had to be looked at).  By latency for few: one row 12.4 us with
-// 20 alternatives, 4.7 without; the load takes 1.2 us, and what the first batch
-// holds, candidates and two joins, the rest.  (The first batch's candidates into
-// one pool, sorted by counting: 14.8 us.)
+// 252 us, 95% of the copy rate (486 us with a bound of each warp's own, where two
+// batches of three had to be looked at).  By latency for few: one row 8.7 us with
+// 20 alternatives, 4.6 without; the load takes 1.1 us, and what the first batch
+// holds, candidates and two joins, the rest.  Code that runs once is fetched as it
+// is reached, so it is kept short: candidates in a loop and one copy of the join
+// instead of all of it written out, 12.3 and 276 to 11.9 and 261 us.
 #include <cooperative_groups.h>
 
 #include <mutex>
@@ -35,6 +36,9 @@ constexpr int kScoreWarps = kScoreThreads / 32;
 constexpr int kScoreCluster = 16;  // most CTAs of a row
 constexpr int kScoreCtas = 304;    // two an SM of this chip
 constexpr int kBatchValues = 16;   // of a thread, loads in flight
+// Candidates of a warp's batch that are merged in one by one (64 rows of 32000,
+// 20 alternatives: 8 10.5 us, 12 to 32 9.4).
+constexpr int kFew = 16;
 
 using Key = unsigned long long;
 
@@ -110,6 +114,7 @@ struct ScoreShared {
     uint32_t bar;  // order_of a value that `top` values of some warp reach
     Key list[kScoreWarps][32];  // (0: no entry)
     Key pool[kScoreThreads];    // those that may be of the best
+    uint32_t nth[kScoreWarps];  // of a warp's lanes, in the first batch
     Key best[32];
     Sums sums[kScoreWarps];
     // of the cluster's CTAs, gathered in the first
@@ -117,12 +122,35 @@ struct ScoreShared {
     Sums parts[kScoreCluster];
 };
 
+// What `top` values of the CTA's first batch reach: in n warps, r lanes or more
+// have a largest value at or above the n-th largest of all warps' r-th such, so
+// that n r >= top values do.  r: of random logits, where the fewest pass.  (The
+// least of the warps' second largest: one row 11.9 us against 8.7.)
+__device__ __forceinline__ uint32_t first_bound(uint32_t *nth, float most, int top, int w, int lane) {
+    static_assert(kScoreWarps == 16 && KQ_MAX_TOP <= 3 * kScoreWarps, "the first bound");
+    const int r = top <= 12 ? 1 : top <= 24 ? 2 : 3, n = (top + r - 1) / r;
+    uint32_t x = order_of(most != most ? -INFINITY : most), its = __reduce_max_sync(~0u, x);
+#pragma unroll 1
+    for (int i = 1; i < r; ++i) {
+        if (lane == __ffs(__ballot_sync(~0u, x == its)) - 1) x = 0;
+        its = __reduce_max_sync(~0u, x);
+    }
+    if (lane == 0) nth[w] = its;
+    __syncthreads();
+    its = nth[lane & 15];
+    int before = 0;
+#pragma unroll
+    for (int o = 1; o < kScoreWarps; ++o) before += __shfl_xor_sync(~0u, its, o) > its;
+    return __reduce_min_sync(~0u, before < n ? its : ~0u);
+}
+
 // The `top` largest of n sorted lists (of up to 16), in sh.best.  Entries that
 // cannot be of them are left out: what the `top`-th of some list, or the r-th of
 // every one (n r >= top), passes.  The others go to the place that the number of
-// larger ones gives.  (A tree of merges: 1.7 us against 0.5.)
-__device__ __forceinline__ void join_lists(ScoreShared &sh, const Key (*list)[32], int n, int top, int w,
-                                           int lane) {
+// larger ones gives.  (A tree of merges: 1.7 us against 0.5.)  A function of its
+// own, as both calls then run the same code.
+__device__ __noinline__ void join_lists(ScoreShared &sh, const Key (*list)[32], int n, int top, int w,
+                                        int lane) {
     __syncthreads();
     if (threadIdx.x == 0) sh.count = 0;
     if (threadIdx.x < 32) sh.best[lane] = 0;
@@ -177,8 +205,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
     Sums mine = {-INFINITY, 0.f, 0.f};
     Key list = 0;  // (below every key)
     Key last = 0;  // the list's entry that a candidate has to pass
-    static_assert(KQ_MAX_TOP <= 2 * kScoreWarps, "the first bound");
-    if (tid == 0) sh.bar = 0xFFFFFFFFu;
+    if (tid == 0) sh.bar = 0;
     __syncthreads();
     // A batch's values; the next one's are on their way while it is looked at.
     auto load = [&](int j0, float (&v)[kBatchValues]) {
@@ -233,15 +260,9 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
         mine.s += sum, mine.t += t2.x + t2.y;
         if (a.top == 0) continue;
         if (j0 == lo) {
-            // The first batch: of each warp's lanes two have a largest value at
-            // or above the least of the warps' second largest such, so that `top`
-            // values do (top <= 2 * 16).
-            const uint32_t x = order_of(most != most ? -INFINITY : most);
-            const uint32_t first_max = __reduce_max_sync(~0u, x);
-            const int holder = __ffs(__ballot_sync(~0u, x == first_max)) - 1;
-            const uint32_t second = __reduce_max_sync(~0u, lane == holder ? 0u : x);
-            if (lane == 0) atomicMin(&sh.bar, a.top > kScoreWarps ? second : first_max);
-            __syncthreads();
+            const uint32_t least = first_bound(sh.nth, most, a.top, w, lane);
+            if (lane == 0) atomicMax(&sh.bar, least);
+            __syncwarp();
         }
         // (a NaN is a candidate too, and shows in the sum)
         const float bar = ordered(*(volatile uint32_t *)&sh.bar);
@@ -254,16 +275,18 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
             if (!(v[i] < bar) && j >= skew && j < hi) left |= 1u << i;
         }
         const int many = __reduce_add_sync(~0u, __popc(left));
-        if (many <= 12) {
-            // one by one
+        if (many <= kFew) {
+            // one by one, of the lanes' next
+            while (unsigned who = __ballot_sync(~0u, left != 0)) {
+                const int i = __ffs(left) - 1;
+                float next = v[0];
 #pragma unroll
-            for (int i = 0; i < kBatchValues; ++i) {
-                const int j = first + (i / V) * kScoreThreads * V + i % V;
-                unsigned who = __ballot_sync(~0u, left >> i & 1);
-                while (who) {
-                    const int at = __ffs(who) - 1;
-                    who &= who - 1;
-                    const Key k = key_of(__shfl_sync(~0u, v[i], at), __shfl_sync(~0u, j, at) - skew);
+                for (int n = 1; n < kBatchValues; ++n) next = n == i ? v[n] : next;
+                const Key key = key_of(next, first + (i / V) * kScoreThreads * V + i % V - skew);
+                left &= left - 1;
+#pragma unroll 1
+                for (; who; who &= who - 1) {
+                    const Key k = __shfl_sync(~0u, key, __ffs(who) - 1);
                     const Key up = __shfl_up_sync(~0u, list, 1);
                     const int place = __popc(__ballot_sync(~0u, list > k));
                     list = lane < place ? list : lane == place ? k : up;
@@ -290,7 +313,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
             }
         }
         const Key now = __shfl_sync(~0u, list, a.top - 1);
-        if (now != last || many > 12) {
+        if (now != last || many > kFew) {
             last = now;
             // (where the list ends with a NaN, no number passes)
             const float x = value_of(last);
