@@ -401,22 +401,33 @@ struct Rows {
     static constexpr int PB = kTwo && D == 128 ? 1 : 2;
     static constexpr int SB = kQCols + 2 * TK + PB * kPCols + OB * D <= 512 ? 2 : 1;
     static constexpr int kS = kQCols, kP = kS + SB * TK, kO = kP + PB * kPCols;
-    static constexpr int OW = D == 256 ? 8 : 4;              // warps that sum O
+    // Softmax warps: four, or four for each second tile, which hand each other
+    // the rows' references.
+    static constexpr int SG = kTwo ? 1 : 2, kSoft = 4 * SG;
+    static constexpr int OW = D == 256 ? 8 : 4;              // warps that write rows: f32 those that sum O
     static constexpr int OC = D * 4 / OW;                    // columns of each
-    static constexpr int kThreads = 32 * (4 + OW + 4);
-    static constexpr int kFirst = 4 + OW;                    // S, copies, O, one that cleans
-    static constexpr int kControl = 4096, kQLo = kLoShared ? kRows * D * 2 : 0;
+    static constexpr int kFirst = kTwo ? 4 + OW : kSoft;     // S, copies, O, one that cleans
+    static constexpr int kThreads = 32 * (kFirst + 4);
+    static constexpr int kControl = 5120, kQLo = kLoShared ? kRows * D * 2 : 0;
     static constexpr int kRing = kControl + kQLo;
     static constexpr int kRoom = (227 * 1024 - 1024 - kRing) / kPart;
     static constexpr int kSlots = kRoom < 8 ? kRoom : 8;
     static constexpr int kBytes = kRing + kSlots * kPart + 1024;
+    // Copies: tile i's keys are copy 2 i, its values 2 i + 1.  f32: slots by turns.
+    // 16 bits: a half of the slots for each, as keys are used up to two tiles ahead
+    // of the values (by turns: 255 us against 239 for three prompts).
+    static constexpr int kEach = kSlots / 2;
+    static __device__ __forceinline__ int slot(int k) {
+        return kTwo ? k % kSlots : (k & 1) * kEach + (k >> 1) % kEach;
+    }
+    static __device__ __forceinline__ int turn(int k) { return kTwo ? k / kSlots : (k >> 1) / kEach; }
     // f32 up to width 128: an item's queries are copied to the ring's last two
     // slots first.  (Each thread its own row from memory: 318 against 314 us for
     // 4097 tokens.)
     static constexpr bool kQStaged = kTwo && D <= 128;
     static constexpr int kFree = kQStaged ? kSlots - 2 : kSlots;  // slots that are free meanwhile
     static constexpr int kQStage = kRing + (kSlots - 2) * kPart;
-    static_assert(kO + OB * D <= 512 && kSlots >= 4, "layout");
+    static_assert(kO + OB * D <= 512 && kSlots >= 4 && (kTwo || (SB == 1 && PB == SG && OW == kSoft)), "layout");
     static_assert(!kQStaged || kRows * D * 4 <= 2 * kPart, "layout");
 };
 
@@ -424,13 +435,15 @@ struct RowsShared {
     uint4 answer;  // of ask_for_cta
     Item item;
     uint64_t full[8], empty[8], sdone[2], sfree[2], pready[2], pfree[2], odone[2], ofree[2], cready[4],
-        vraw[4], vclean[4], ldone, given, qfull, drain[2];
+        vraw[4], vclean[4], handed[8], ldone, given, qfull, drain[2];
     uint32_t tmem;
     int dead, bad;
-    float corr[4][kRows];  // of tile i & 3: the factor of what was summed before
-    float m[kRows], l[kRows];
+    // f32, of tile i & 3: the factor of what was summed before; 16 bits, of tile
+    // i & 1: the rows' references after it
+    float corr[4][kRows];
+    float m[2][kRows], l[2][kRows];  // of each softmax warps' tiles
 };
-static_assert(sizeof(RowsShared) <= 4096, "layout");
+static_assert(sizeof(RowsShared) <= 5120, "layout");
 
 template <class T, int D>
 __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
@@ -463,9 +476,11 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
             kq::mbar_init(bar(cm.cready[i]), 4);
             kq::mbar_init(bar(cm.vraw[i]), 1), kq::mbar_init(bar(cm.vclean[i]), 1);
         } else if (lane == 14) {
-            kq::mbar_init(bar(cm.ldone), kTwo ? 4 : 5);
+            kq::mbar_init(bar(cm.ldone), kTwo ? 4 : M::kSoft + 1);
             kq::mbar_init(bar(cm.given), 1), kq::mbar_init(bar(cm.qfull), 1);
             cm.dead = cm.bad = 0;
+        } else if (lane >= 16 && lane < 24) {
+            kq::mbar_init(bar(cm.handed[lane - 16]), 1);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     } else if (w == M::kFirst) {
@@ -519,14 +534,96 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
     const int64_t slot0 = kTwo ? (int64_t)(it.kfirst / TK + it.seq) * a.kv_heads + it.head : 0;
 
     if constexpr (kTwo) kq::wait_prerequisites();  // the tiles
-    int copied = 0;  // copies that were begun
+    int copied = 0;  // copies that this warp has begun (16 bits: of keys, or of values)
 
-    if (w < 4) {
-        // ------------------------------------------------- softmax warps
-        const int r = 32 * w + lane;
+    // The rows' results, by warp n of those that write: its columns of O.
+    auto write_rows = [&](float (&O)[M::OC], bool bad, int n) {
+        const int r = 32 * (n & 3) + lane, c0 = n / 4 * M::OC;
         int tok, hq;
         const bool on = it.row(a.hb, r, tok, hq);
-        const uint32_t mine = tmem + ((uint32_t)(32 * w) << 16);
+        wait(cm.ldone, 0);
+        float l, m;
+        if constexpr (kTwo) {
+            l = cm.l[0][r], m = cm.m[0][r];
+        } else {  // both halves' sums, of the last tile's reference
+            const int last = count > 0 ? (count - 1) & 1 : 0;
+            m = cm.m[last][r];
+            const float other = cm.m[last ^ 1][r];
+            const float f = other == m ? 1.f : other == -INFINITY ? 0.f
+                                             : exp2_fast((other - m) * (fabsf(a.scale) * kLog2E));
+            l = fmaf(cm.l[last ^ 1][r], f, cm.l[last][r]);
+        }
+        const int limit = on ? it.limit(tok) : -1;
+        if constexpr (!kTwo) bad = *(volatile int *)&cm.bad != 0;
+        if (bad && on) {
+            // values that are not finite, of the tiles that left them out
+            for (int t = kTwo ? t0 : t1 - edges; t < t1; ++t) {
+                if (kTwo && !a.info[slot0 + (int64_t)t * a.kv_heads].bad) continue;
+                for (int j = t * TK; j < min((t + 1) * TK, limit + 1); ++j) {
+                    const T *v = static_cast<const T *>(a.v) + (int64_t)(it.kfirst + j) * a.v_stride +
+                                 (int64_t)it.head * D + c0;
+#pragma unroll
+                    for (int k = 0; k < M::OC; ++k) {
+                        const float x = to_f32<T>(v[k]);
+                        if (!(fabsf(x) < INFINITY)) O[k] += x;
+                    }
+                }
+            }
+        }
+        const bool lost = __any_sync(~0u, dead());
+        if (lost) l = quiet_nan();
+        if (a.splits > 1) {
+            float *part = a.part + (int64_t)blockIdx.x * kRows * (D + 2);
+            // by values, of 32 rows each: part[32 rows][D][32]
+            float *to = part + (r - lane) * D + c0 * 32 + lane;
+#pragma unroll
+            for (int k = 0; k < M::OC; ++k) to[32 * k] = O[k];
+            if (c0 == 0) part[kRows * D + r] = m, part[kRows * (D + 1) + r] = l;
+        } else {
+            // (a row that attends something and has no sum has scores of
+            // -infinity only)
+            float inv = limit < 0 ? 0.f : __fdiv_rn(kTwo ? 32768.f : 1.f, l);
+            if (lost) inv = quiet_nan();
+            T *to = static_cast<T *>(a.out) + ((int64_t)(it.first + it.tok0) * a.q_heads + it.hq) * D + c0;
+            const uint32_t place = (tok - it.tok0) * a.q_heads + hq, rows = __ballot_sync(~0u, on);
+            // Rows go out whole, through shared memory (every copy there was used
+            // up by the last O): a lane's own row in pieces of 32 bytes took 3 us.
+            constexpr int kRow = M::OC * sizeof(T), kLanes = kRow / 16;  // bytes; lanes of a row
+            uint8_t *stage = smem + M::kRing + n * 32 * kRow;
+            static_assert(M::OW * 32 * kRow <= M::kSlots * M::kPart && 32 % kLanes == 0, "layout");
+            if (lost) {  // (copies may still come)
+                for (int k = 0; k < M::OC && on; ++k) to[(int64_t)place * D + k] = from_f32<T>(inv);
+            } else {
+#pragma unroll
+                for (int k = 0; k < kLanes; ++k) {
+                    uint4 x;
+                    uint32_t *q = &x.x;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if constexpr (kTwo) q[e] = __float_as_uint(O[4 * k + e] * inv);
+                        else q[e] = pack2<H>(O[8 * k + 2 * e] * inv, O[8 * k + 2 * e + 1] * inv);
+                    }
+                    *reinterpret_cast<uint4 *>(stage + lane * kRow + ((k ^ (lane & 7)) << 4)) = x;
+                }
+                __syncwarp();
+#pragma unroll 8
+                for (int k = 0; k < kLanes; ++k) {
+                    const int at = k * (32 / kLanes) + lane / kLanes, c = lane % kLanes;
+                    const uint4 x = *reinterpret_cast<const uint4 *>(stage + at * kRow + ((c ^ (at & 7)) << 4));
+                    const uint32_t far = __shfl_sync(~0u, place, at);
+                    if (rows >> at & 1)
+                        *reinterpret_cast<uint4 *>(to + (int64_t)far * D + c * (16 / sizeof(T))) = x;
+                }
+            }
+        }
+    };
+
+    if (w < M::kSoft) {
+        // ------------------------------------------------- softmax warps
+        const int g = w >> 2, r = 32 * (w & 3) + lane;  // (g: of which tiles)
+        int tok, hq;
+        const bool on = it.row(a.hb, r, tok, hq);
+        const uint32_t mine = tmem + ((uint32_t)(32 * (w & 3)) << 16);
         int ex = 0;
         {   // ---- the row's query into tensor memory
             const T *x = static_cast<const T *>(a.q) + (int64_t)(it.first + tok) * a.q_stride +
@@ -592,9 +689,10 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
             } else {
                 const uint4 *x8 = reinterpret_cast<const uint4 *>(x);
                 const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;
-                // (half a row's loads on their way)
-#pragma unroll 1
-                for (int i = 0; i < D / 32; i += 4) {
+                // (half a row each)
+                static_assert(D == 256, "halves of a row");
+                {
+                    const int i = 4 * g;
                     uint4 v[16];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) v[k] = on ? __ldg(x8 + 4 * i + k) : make_uint4(0, 0, 0, 0);
@@ -624,12 +722,21 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
             if (count) ek = __ldg(&info[(int64_t)(t1 - 1) * a.kv_heads].ek);
         }
         float m = -INFINITY, l = 0.f;
-        for (int i = 0; i < count; ++i) {
+        for (int i = g; i < count; i += M::SG) {
             const int t = t1 - 1 - i;
             float f = 1.f;
             if constexpr (kTwo) {
                 f = __uint_as_float((uint32_t)(127 + min(max(ex - 15 + ek, -126), 127)) << 23);
                 if (i + 1 < count) ek = __ldg(&info[(int64_t)(t - 1) * a.kv_heads].ek);
+            }
+            float before = -INFINITY;  // the reference after the tile before
+            if constexpr (!kTwo) {
+                // (Who has handed it on has also seen the S before, and the O of
+                // two tiles before that: no barrier is ever two phases behind.)
+                if (i > 0) {
+                    wait(cm.handed[4 * (g ^ 1) + (w & 3)], (i - 1) >> 1);
+                    before = cm.corr[(i - 1) & 1][r];
+                }
             }
             wait(cm.sdone[i % SB], i / SB);
             tc_after();
@@ -661,26 +768,33 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
                 corr = exp2_fast(m - (now == -INFINITY ? 0.f : now));
                 m = now;
             } else {
-                const float now = fmaxf(m, mx[0]);
-                const bool grown = now > m && !((now - m) * factor <= kLazy);
-                if (__any_sync(~0u, grown)) {
-                    corr = !grown ? 1.f : m == -INFINITY ? 0.f : exp2_fast((m - now) * factor);
-                    if (grown) m = now;
-                    if (i > 0) {
-                        wait(cm.pfree[(i - 1) % PB], (i - 1) / PB);
-                        tc_after();
-                        const uint32_t oa = mine + M::kO;
-                        if (!__any_sync(~0u, dead())) {
+                if (i >= PB) {  // the O before has read P's place
+                    wait(cm.pfree[i % PB], i / PB - 1);
+                    tc_after();
+                }
+                const float now = fmaxf(before, mx[0]);
+                const bool grown = now > before && !((now - before) * factor <= kLazy);
+                const float ref = grown ? now : before;
+                cm.corr[i & 1][r] = ref;
+                __syncwarp();
+                if (lane == 0) kq::mbar_arrive(bar(cm.handed[4 * g + (w & 3)]));
+                if (__any_sync(~0u, ref != m))
+                    corr = ref == m ? 1.f : m == -INFINITY ? 0.f : exp2_fast((m - ref) * factor);
+                m = ref;
+                if (__any_sync(~0u, grown) && i > 0) {
+                    const float by = !grown ? 1.f : before == -INFINITY ? 0.f : exp2_fast((before - ref) * factor);
+                    wait(cm.pfree[(i - 1) % PB], (i - 1) / PB);
+                    tc_after();
+                    const uint32_t oa = mine + M::kO;
+                    if (!__any_sync(~0u, dead())) {
 #pragma unroll 4
-                            for (int k = 0; k < D; k += 16) {
-                                uint32_t o[16];
-                                tc_load16(o, oa + k);
-                                tc_loaded();
+                        for (int k = 0; k < D; k += 16) {
+                            uint32_t o[16];
+                            tc_load16(o, oa + k);
+                            tc_loaded();
 #pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-                                tc_store16(oa + k, o);
-                            }
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * by);
+                            tc_store16(oa + k, o);
                         }
                     }
                 }
@@ -696,7 +810,7 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
                 d[k] = __float_as_uint(p);
             }
             l = fmaf(l, corr, (sum[0] + sum[1]) + (sum[2] + sum[3]));
-            if (i >= PB) {  // the O before has read P's place
+            if (kTwo && i >= PB) {  // the O before has read P's place
                 wait(cm.pfree[i % PB], i / PB - 1);
                 tc_after();
             }
@@ -721,13 +835,30 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
                 if constexpr (kTwo) kq::mbar_arrive(bar(cm.cready[i & 3]));
             }
         }
-        cm.m[r] = m;
-        cm.l[r] = l;
+        cm.m[g][r] = m;
+        cm.l[g][r] = l;
         __syncwarp();
         if (lane == 0) kq::mbar_arrive(bar(cm.ldone));
-    } else if (w < M::kFirst) {
+        if constexpr (!kTwo) {
+            float O[M::OC];
+#pragma unroll
+            for (int k = 0; k < M::OC; ++k) O[k] = 0.f;
+            if (count) {  // the sums are in tensor memory
+                wait(cm.odone[0], 0);
+                tc_after();
+                if (!__any_sync(~0u, dead())) {
+#pragma unroll
+                    for (int k = 0; k < M::OC; k += 32)
+                        tc_load32(reinterpret_cast<uint32_t *>(O) + k, mine + M::kO + g * M::OC + k);
+                    tc_loaded();
+                    tc_before();
+                }
+            }
+            write_rows(O, false, w);
+        }
+    } else if (kTwo && w < M::kFirst) {
         // ------------------------------------------- the sums of O, and out
-        if constexpr (D == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+        if constexpr (kTwo && D == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
         __syncthreads();
         const int r = 32 * (w & 3) + lane, c0 = (w - 4) / 4 * M::OC;
         const uint32_t mine = tmem + ((uint32_t)(32 * (w & 3)) << 16) + M::kO + c0;
@@ -771,109 +902,39 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
                 if (lane == 0) kq::mbar_arrive(bar(cm.ofree[i % OB]));
             }
         }
-        wait(cm.ldone, 0);
-        if (!kTwo && count) {  // the sums are in tensor memory
-            wait(cm.odone[0], 0);
-            tc_after();
-            if (!__any_sync(~0u, dead())) {
-#pragma unroll
-                for (int k = 0; k < M::OC; k += 32) tc_load32(reinterpret_cast<uint32_t *>(O) + k, mine + k);
-                tc_loaded();
-                tc_before();
+        write_rows(O, bad, w - 4);
+    } else {
+        if constexpr (kTwo && D == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        // ------------------------------------------------- copies
+        auto copy = [&](int k) {
+            const int s = M::slot(k), t = t1 - 1 - (k >> 1);
+            const uint32_t to = base + M::kRing + s * M::kPart;
+            uint32_t done = bar(cm.full[s]);
+            // Values that are cleaned have barriers of their own: who waits
+            // for some tiles only could be two phases ahead of a slot's.
+            if (!kTwo && (k & 1) && (k >> 1) < edges) {
+                kq::mbar_arrive(done);
+                done = bar(cm.vraw[(k >> 1) & 3]);
             }
-        }
-        float l = cm.l[r];
-        const float m = cm.m[r];
-        const int limit = on ? it.limit(tok) : -1;
-        if constexpr (!kTwo) bad = *(volatile int *)&cm.bad != 0;
-        if (bad && on) {
-            // values that are not finite, of the tiles that left them out
-            for (int t = kTwo ? t0 : t1 - edges; t < t1; ++t) {
-                if (kTwo && !info[(int64_t)t * a.kv_heads].bad) continue;
-                for (int j = t * TK; j < min((t + 1) * TK, limit + 1); ++j) {
-                    const T *v = static_cast<const T *>(a.v) + (int64_t)(it.kfirst + j) * a.v_stride +
-                                 (int64_t)it.head * D + c0;
-#pragma unroll
-                    for (int k = 0; k < M::OC; ++k) {
-                        const float x = to_f32<T>(v[k]);
-                        if (!(fabsf(x) < INFINITY)) O[k] += x;
-                    }
-                }
-            }
-        }
-        const bool lost = __any_sync(~0u, dead());
-        if (lost) l = quiet_nan();
-        if (a.splits > 1) {
-            float *part = a.part + (int64_t)blockIdx.x * kRows * (D + 2);
-            // by values, of 32 rows each: part[32 rows][D][32]
-            float *to = part + (r - lane) * D + c0 * 32 + lane;
-#pragma unroll
-            for (int k = 0; k < M::OC; ++k) to[32 * k] = O[k];
-            if (c0 == 0) part[kRows * D + r] = m, part[kRows * (D + 1) + r] = l;
-        } else {
-            // (a row that attends something and has no sum has scores of
-            // -infinity only)
-            float inv = limit < 0 ? 0.f : __fdiv_rn(kTwo ? 32768.f : 1.f, l);
-            if (lost) inv = quiet_nan();
-            T *to = static_cast<T *>(a.out) + ((int64_t)(it.first + it.tok0) * a.q_heads + it.hq) * D + c0;
-            const uint32_t place = (tok - it.tok0) * a.q_heads + hq, rows = __ballot_sync(~0u, on);
-            // Rows go out whole, through shared memory (every copy there was used
-            // up by the last O): a lane's own row in pieces of 32 bytes took 3 us.
-            constexpr int kRow = M::OC * sizeof(T), kLanes = kRow / 16;  // bytes; lanes of a row
-            uint8_t *stage = smem + M::kRing + (w - 4) * 32 * kRow;
-            static_assert(M::OW * 32 * kRow <= M::kSlots * M::kPart && 32 % kLanes == 0, "layout");
-            if (lost) {  // (copies may still come)
-                for (int k = 0; k < M::OC && on; ++k) to[(int64_t)place * D + k] = from_f32<T>(inv);
+            kq::mbar_expect_tx(done, M::kPart);
+            if constexpr (kTwo) {
+                kq::bulk_g2s(to, a.tiles + (slot0 + (int64_t)t * a.kv_heads) * (2 * M::kPart) +
+                                     (k & 1) * M::kPart, M::kPart, done);
             } else {
 #pragma unroll
-                for (int k = 0; k < kLanes; ++k) {
-                    uint4 x;
-                    uint32_t *q = &x.x;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if constexpr (kTwo) q[e] = __float_as_uint(O[4 * k + e] * inv);
-                        else q[e] = pack2<H>(O[8 * k + 2 * e] * inv, O[8 * k + 2 * e + 1] * inv);
-                    }
-                    *reinterpret_cast<uint4 *>(stage + lane * kRow + ((k ^ (lane & 7)) << 4)) = x;
-                }
-                __syncwarp();
-#pragma unroll 8
-                for (int k = 0; k < kLanes; ++k) {
-                    const int at = k * (32 / kLanes) + lane / kLanes, c = lane % kLanes;
-                    const uint4 x = *reinterpret_cast<const uint4 *>(stage + at * kRow + ((c ^ (at & 7)) << 4));
-                    const uint32_t far = __shfl_sync(~0u, place, at);
-                    if (rows >> at & 1)
-                        *reinterpret_cast<uint4 *>(to + (int64_t)far * D + c * (16 / sizeof(T))) = x;
-                }
+                for (int c = 0; c < D / 64; ++c)
+                    tensor2d_g2s(to + c * TK * 128, k & 1 ? &a.vmap : &a.kmap, it.head * D + 64 * c,
+                                 it.kfirst + t * TK, done);
             }
-        }
-    } else {
-        if constexpr (D == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-        // ------------------------------------------------- copies
-        auto copy = [&](int until) {
-            for (int k = copied; k < until; ++k) {
-                const int s = k % M::kSlots, t = t1 - 1 - (k >> 1);
-                if (k >= M::kSlots) wait(cm.empty[s], k / M::kSlots - 1);
+        };
+        // by the producer: all copies, or the values'
+        constexpr int kStep = kTwo ? 1 : 2;
+        auto copy_until = [&](int until) {
+            for (; copied < until; ++copied) {
+                const int k = kStep * copied + (kStep - 1);
+                if (M::turn(k) > 0) wait(cm.empty[M::slot(k)], M::turn(k) - 1);
                 if (dead()) break;
-                const uint32_t to = base + M::kRing + s * M::kPart;
-                uint32_t done = bar(cm.full[s]);
-                // Values that are cleaned have barriers of their own: who waits
-                // for some tiles only could be two phases ahead of a slot's.
-                if (!kTwo && (k & 1) && (k >> 1) < edges) {
-                    kq::mbar_arrive(done);
-                    done = bar(cm.vraw[(k >> 1) & 3]);
-                }
-                kq::mbar_expect_tx(done, M::kPart);
-                copied = k + 1;
-                if constexpr (kTwo) {
-                    kq::bulk_g2s(to, a.tiles + (slot0 + (int64_t)t * a.kv_heads) * (2 * M::kPart) +
-                                         (k & 1) * M::kPart, M::kPart, done);
-                } else {
-#pragma unroll
-                    for (int c = 0; c < D / 64; ++c)
-                        tensor2d_g2s(to + c * TK * 128, k & 1 ? &a.vmap : &a.kmap, it.head * D + 64 * c,
-                                     it.kfirst + t * TK, done);
-                }
+                copy(k);
             }
         };
         const bool producer = w == M::kFirst + 1 && lane == 0;
@@ -883,14 +944,19 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
                 tensor3d_g2s(base + M::kQStage + c * (kRows * 128), &a.qmap, 32 * c, it.hq, it.first + it.tok0,
                              bar(cm.qfull));
         }
-        if (producer) copy(min(2 * count, M::kFree));  // (while the queries are fetched)
+        // (while the queries are fetched)
+        if (producer) copy_until(kTwo ? min(2 * count, M::kFree) : min(count, M::kEach));
+        if (!kTwo && w == M::kFirst) {
+            for (; copied < min(count, M::kEach); ++copied)
+                if (lane == 0) copy(2 * copied);
+        }
         __syncthreads();
         // terms' products, the small ones first
         constexpr int kTerms = kTwo ? 3 : 1;
         auto lo_first = [](int term) { return kTwo && term == 0; };
         auto lo_second = [](int term) { return kTwo && term == 1; };
         if (producer) {
-            copy(2 * count);
+            copy_until(kTwo ? 2 * count : count);
         } else if (w == M::kFirst) {
             // --------------------------------------------- S of each tile
             // (One warp for both, O first: f32 370 against 328 us, as it issues
@@ -901,11 +967,11 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
             constexpr uint32_t is = mma_idesc(TK, M::kBf16, false);
             for (int i = 0; i < count; ++i) {
                 const int k = 2 * i;
-                wait(cm.full[k % M::kSlots], k / M::kSlots);
+                wait(cm.full[M::slot(k)], M::turn(k));
                 if (i >= SB) wait(cm.sfree[i % SB], i / SB - 1);
                 if (__any_sync(~0u, dead())) break;
                 tc_after();
-                const uint32_t s = uniform(k % M::kSlots), b = uniform(i % SB);
+                const uint32_t s = uniform(M::slot(k)), b = uniform(i % SB);
                 const uint32_t d = tm + M::kS + TK * b;
                 const uint64_t kd = desc_k(uniform(base + M::kRing) + s * M::kPart);
                 if (elected()) {
@@ -926,7 +992,12 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
                             }
                         }
                     tc_commit(bar(cm.sdone[0]) + 8 * b);
-                    tc_commit(bar(cm.empty[0]) + 8 * s);
+                    if (kTwo) tc_commit(bar(cm.empty[0]) + 8 * s);
+                }
+                // 16 bits: the S before has been read, so its keys' slot is free
+                if (!kTwo && i > 0 && copied < count) {
+                    if (lane == 0) copy(2 * copied);
+                    ++copied;
                 }
                 __syncwarp();
             }
@@ -937,13 +1008,13 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
             constexpr uint32_t io = mma_idesc(D, M::kBf16, true);
             for (int i = 0; i < count; ++i) {
                 const int k = 2 * i + 1;
-                wait(cm.full[k % M::kSlots], k / M::kSlots);
+                wait(cm.full[M::slot(k)], M::turn(k));
                 if (!kTwo && i < edges) wait(cm.vclean[i & 3], i >> 2);
                 if (kTwo && i >= OB) wait(cm.ofree[i % OB], i / OB - 1);
                 wait(cm.pready[i % PB], i / PB);
                 if (__any_sync(~0u, dead())) break;
                 tc_after();
-                const uint32_t s = uniform(k % M::kSlots), b = uniform(i % PB);
+                const uint32_t s = uniform(M::slot(k)), b = uniform(i % PB);
                 const uint32_t o = kTwo ? uniform(i % OB) : 0, more = uniform(!kTwo && i > 0);
                 const uint64_t vd = desc_n(uniform(base + M::kRing) + s * M::kPart, TK * 128);
                 const uint32_t d = tm + M::kO + D * o, p = tm + M::kP + M::kPCols * b;
@@ -966,7 +1037,7 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
         } else if (!kTwo && w == M::kFirst + 3) {
             // ------------- values that are not finite, of tiles seen in part
             for (int i = 0; i < edges; ++i) {
-                const int k = 2 * i + 1, s = k % M::kSlots;
+                const int k = 2 * i + 1, s = M::slot(k);
                 wait(cm.vraw[i & 3], i >> 2);
                 uint4 *v = reinterpret_cast<uint4 *>(smem + M::kRing + s * M::kPart);
                 bool found = false;
@@ -999,13 +1070,14 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
     __syncthreads();
     // After an expired wait no copy and no product may run on past this.
     if (dead()) {
-        if (w == M::kFirst + 1 && lane == 0) {
-            for (int k = max(0, copied - M::kSlots); k < copied; ++k)
-                kq::mbar_wait(bar(cm.full[k % M::kSlots]), (k / M::kSlots) & 1, kq::kWaitLimitNs);
+        if ((w == M::kFirst + 1 || (!kTwo && w == M::kFirst)) && lane == 0) {
+            const bool values = !kTwo && w == M::kFirst + 1;
+            for (int n = max(0, copied - (kTwo ? M::kSlots : M::kEach)); n < copied; ++n) {
+                const int k = kTwo ? n : 2 * n + values;
+                kq::mbar_wait(bar(cm.full[M::slot(k)]), M::turn(k) & 1, kq::kWaitLimitNs);
+                if (values && n < edges) kq::mbar_wait(bar(cm.vraw[n & 3]), (n >> 2) & 1, kq::kWaitLimitNs);
+            }
             if (M::kQStaged) kq::mbar_wait(bar(cm.qfull), 0, kq::kWaitLimitNs);
-            const int raw = kTwo ? 0 : min(copied / 2, edges);  // (copies of values are the odd ones)
-            for (int i = max(0, raw - 4); i < raw; ++i)
-                kq::mbar_wait(bar(cm.vraw[i & 3]), (i >> 2) & 1, kq::kWaitLimitNs);
         }
         if (w == M::kFirst || w == M::kFirst + 2) {
             const uint64_t &drain = cm.drain[w == M::kFirst ? 0 : 1];
