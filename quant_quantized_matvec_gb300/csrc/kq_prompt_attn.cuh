@@ -39,7 +39,11 @@
 // 32 / 2 heads of 128: 317 us, 434 TFLOP/s of the formula and three times that of
 // products; the tensor core is at work 62% of the time, a tile takes 1950 to 2000
 // clocks for 1536 of products.  bf16 at width 256, three prompts of up to 3001
-// tokens behind 500, 16 / 4 heads: 257 us, 943 TFLOP/s.
+// tokens behind 500, 16 / 4 heads: 239 us, 1014 TFLOP/s; a tile takes 1600 clocks
+// for 1024 of products, which with the copies of its keys and values also take
+// 1024 of shared memory (128 bytes a clock).  (S and, two tiles later, O by one
+// warp: 266 us.  Clusters of two CTAs, each copying a half of a tile to both: 279,
+// as a slot waits for both.)
 //
 // NaN and infinities must not reach rows that do not attend them (0 * inf):
 // values that are not finite are zeros in the tile (f32: all tiles; 16 bits:
@@ -402,7 +406,7 @@ struct Rows {
     static constexpr int SB = kQCols + 2 * TK + PB * kPCols + OB * D <= 512 ? 2 : 1;
     static constexpr int kS = kQCols, kP = kS + SB * TK, kO = kP + PB * kPCols;
     // Softmax warps: four, or four for each second tile, which hand each other
-    // the rows' references.
+    // the rows' references (so that one tile's softmax is not what S waits for).
     static constexpr int SG = kTwo ? 1 : 2, kSoft = 4 * SG;
     static constexpr int OW = D == 256 ? 8 : 4;              // warps that write rows: f32 those that sum O
     static constexpr int OC = D * 4 / OW;                    // columns of each
