@@ -40,10 +40,10 @@
 // products; the tensor core is at work 62% of the time, a tile takes 1950 to 2000
 // clocks for 1536 of products.  bf16 at width 256, three prompts of up to 3001
 // tokens behind 500, 16 / 4 heads: 239 us, 1014 TFLOP/s; a tile takes 1600 clocks
-// for 1024 of products, which with the copies of its keys and values also take
-// 1024 of shared memory (128 bytes a clock).  (S and, two tiles later, O by one
-// warp: 266 us.  Clusters of two CTAs, each copying a half of a tile to both: 279,
-// as a slot waits for both.)
+// for 1024 of products: S waits 340 for the one before to be taken, and then runs
+// beside O.  (S and, two tiles later, O by one warp: 266 us; O not before the S of
+// one or two tiles on is done: 247.  Clusters of two CTAs, each copying a half of
+// a tile to both: 279, as a slot waits for both.)
 //
 // NaN and infinities must not reach rows that do not attend them (0 * inf):
 // values that are not finite are zeros in the tile (f32: all tiles; 16 bits:
