@@ -135,3 +135,25 @@ def test_streams_and_graphs():
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, kq.token_logprobs(x, t, top=6)))
+
+
+@pytest.mark.parametrize("top", [1, 12, 13, 24, 25, 32])
+@pytest.mark.parametrize("n,v", [(1, 9001), (2, 150001), (400, 20011)])
+def test_alternatives_of_few_values(n, v, top):
+    """Many equal logits, in rows as they come, rising and falling, and rows of
+    one value: the lower token first, whatever the order of the merging."""
+    g = torch.Generator(device="cuda").manual_seed(v + top)
+    x = torch.randint(-40, 9, (n, v), generator=g, device="cuda").float()
+    x[0, :] = torch.arange(v, device="cuda") // 7 % 1000 if n == 1 else 3.0
+    if n > 2:
+        x[1] = x[1].sort().values
+        x[2] = x[2].sort(descending=True).values
+        x[3, 5:] = -float("inf")
+    logp, ent, tl, tt = kq.token_logprobs(x, None, top=top)
+    want = x.sort(dim=1, descending=True, stable=True)
+    assert torch.equal(tt.long(), want.indices[:, :top])
+    ref = want.values[:, :top].double() - torch.logsumexp(x.double(), 1, keepdim=True)
+    at = torch.isfinite(ref)
+    # (2^-21: the sum, its logarithm below 16, and a difference below 1100)
+    assert ((tl.double() - ref)[at].abs() <= 2.0 ** -21 * (16 + ref[at].abs())).all()
+    assert (tl[~at] == -float("inf")).all()

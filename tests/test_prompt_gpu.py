@@ -214,6 +214,21 @@ def test_large_logits(dim, kind, size):
     assert (err <= want.abs()[clear] * 2.0 ** -20).all()
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("levels", ["all", "every second", "falling", "up and down"])
+def test_maxima_that_grow_from_tile_to_tile(levels, dim, kind):
+    """Scores whose level changes by more than 2^8 every 64 keys, from the last
+    to the first: what was summed before is corrected each time, or never."""
+    q, k, v, s, ks = inputs([150, 70], [800, 100], 4, 2, dim, kind, 21, size=0.25)
+    n = torch.cat([torch.arange(m - 1, -1, -1, device="cuda") // 64 for m in (950, 170)])
+    level = {"all": 9 * n, "every second": 18 * (n // 2), "falling": -9 * n,
+             "up and down": 3 * n + 9 * (n % 2)}[levels]
+    q[..., 0] = 4.0
+    k[..., 0] = (level[:, None] * dim ** 0.5 / 4.0).to(kind)
+    check(kq.prompt_attention(q, k, v, dev(s), dev(ks)), q, k, v, s, ks)
+
+
 def test_sizes_of_f32_far_apart():
     """Keys and values of tokens and queries of rows whose sizes differ."""
     q, k, v, s, ks = inputs([200], [100], 4, 2, 128, F32, 12)
