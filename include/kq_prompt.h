@@ -104,8 +104,12 @@ kq_status kq_norm_rope(const kq_norm_part *parts, int n, int type, int out_type,
  * products are exact, probabilities are rounded to the type.  KQ_F32: queries,
  * keys, values and probabilities are held as two f16 terms (22 bits, after a
  * scaling by a power of two: of a query's row, and of a sequence's 64 or 32
- * keys or values; what is below 2^-39 of the largest there is dropped), so
- * logits may be as large as f32 holds, as long as scale * q is finite too.  A
+ * keys or values, or of each of these where their largest values lie further
+ * apart than 2^12; what is below 2^-27 of the largest value of its key, value
+ * or query, or 2^-39 of a row's largest probability times value, is dropped),
+ * so logits may be as large as f32 holds, as long as scale * q is finite too.
+ * However large a key or value is, rows that do not attend it, or whose
+ * probability for it is small enough, keep the bits of what they attend.  A
  * row that attends a key with an infinity may be NaN where the formula has a
  * weight of zero, and so may one that attends an infinite value of a 16-bit
  * type where its probability is too small for the type.

@@ -141,6 +141,7 @@ cudaError_t prompt_attention(const PromptCall &c, void *ws, int sms, unsigned in
     const Space at = space_of(a, blocks, c.type == KQ_F32, c.dim);
     a.tiles = static_cast<uint8_t *>(ws);
     a.info = reinterpret_cast<TileInfo *>(a.tiles + at.info);
+    a.powers = reinterpret_cast<TilePowers *>(a.tiles + at.powers);
     a.part = reinterpret_cast<float *>(a.tiles + at.part);
     a.err = err, a.wait_ns = wait_ns;
     a.suspend_ns = wait_ns < kq::kSuspendNs ? (uint32_t)wait_ns : kq::kSuspendNs;

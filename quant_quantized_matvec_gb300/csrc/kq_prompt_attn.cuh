@@ -26,7 +26,11 @@
 // (4097 keys of width 128, off by 4.9e-7 in all; the other order 1.8e-6).
 // Keys and values are split once, by a kernel before, into tiles as the
 // products take them (a sequence's 64 or 32 tokens of a head, zeros past its
-// end), with the tile's powers of two.  The query is multiplied by scale *
+// end), with the tile's powers of two.  Where a tile's tokens lie further apart
+// than 2^kApart, each has a power of its own, as rows before the larger ones do
+// not attend them: a column of S is scaled by its token's, and of a row's P each
+// by its token's, so that the largest product with a value's largest comes to
+// 2^14; O of the tile then has the row's factor.  The query is multiplied by scale *
 // log2(e) in f32 first, so that what follows only multiplies by powers of two,
 // and the difference to the maximum is one rounding, however large both are.
 //
@@ -71,12 +75,22 @@ constexpr int kRows = 128;  // rows of an item
 constexpr float kLazy = 8.f;  // 16 bits: log2 of the growth of a maximum that is not corrected
 constexpr float kLog2E = 1.44269504088896340736f;
 
-// Powers of two of a tile of an f32 call, and whether its values had some that
-// are not finite.
+// f32: how far apart (log2 of their largest values) a tile's tokens may lie that
+// have one power of two.  A token's values are held to 2^-39 of the tile's
+// largest then, to 2^-27 of the token's.
+constexpr int kApart = 12;
+
+// Powers of two of a tile of an f32 call.
 struct TileInfo {
-    int ek;    // keys = stored * 2^ek
-    float vf;  // values * 2^-15 = stored * vf
-    int bad, pad;
+    int ek;      // keys = stored * 2^ek
+    int kstate;  // kKeysApart
+    int vstate;  // kValuesApart; kSomeNotFinite: zeros in the tile
+    float vf;    // values * 2^-15 = stored * vf
+};
+constexpr int kKeysApart = 1, kValuesApart = 2, kSomeNotFinite = 4;
+// Each token's, where they are apart: keys = stored * 2^k, values * 2^15 = stored * 2^v.
+struct TilePowers {
+    int16_t k[64], v[64];
 };
 
 struct PromptArgs {
@@ -88,6 +102,7 @@ struct PromptArgs {
     void *out;
     uint8_t *tiles;  // f32: [slot][kv_heads][tile]
     TileInfo *info;  // f32: [slot][kv_heads]
+    TilePowers *powers;  // the same
     float *part;     // splits > 1
     int32_t nseq, ntok, nkeys, q_heads, kv_heads;
     int32_t per;      // query heads of a key head
@@ -301,14 +316,16 @@ __global__ void __launch_bounds__(kSplitThreads)
     kq_prompt_split(const __grid_constant__ PromptArgs a) {
     constexpr int TK = f32_tile_tokens(D), kPart = TK * D * 4;
     constexpr int kEach = TK * D / 4 / kSplitThreads;  // float4 of a thread
+    constexpr int kLanes = D / 4 < 32 ? D / 4 : 32;  // of a warp, that share a token
     __shared__ int found[4];
-    __shared__ uint32_t tops;
+    __shared__ uint32_t tops[TK];  // each token's largest finite magnitude
     __shared__ int bad;
     const int tid = threadIdx.x, lane = tid & 31;
     const int slot = blockIdx.x, head = blockIdx.y;
     const bool values = blockIdx.z != 0;
     kq::allow_dependents();
-    if (tid == 0) found[0] = 0, tops = 0, bad = 0;
+    if (tid == 0) found[0] = 0, bad = 0;
+    if (tid < TK) tops[tid] = 0;
     if (tid < 32) {
         __syncwarp();
         Place p;
@@ -332,7 +349,6 @@ __global__ void __launch_bounds__(kSplitThreads)
     const float *x = static_cast<const float *>(values ? a.v : a.k);
     const int64_t stride = values ? a.v_stride : a.k_stride;
     float4 v[kEach];
-    float top = 0.f;
     bool odd = false;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
@@ -341,7 +357,7 @@ __global__ void __launch_bounds__(kSplitThreads)
         if (t < held)
             v[i] = __ldg(reinterpret_cast<const float4 *>(x + (int64_t)(first + t) * stride +
                                                           (int64_t)head * D) + e);
-        float *f = &v[i].x;
+        float *f = &v[i].x, top = 0.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const float m = fabsf(f[k]);
@@ -352,21 +368,32 @@ __global__ void __launch_bounds__(kSplitThreads)
                 if (values) f[k] = 0.f;
             }
         }
+        uint32_t its = __float_as_uint(top);
+        if constexpr (kLanes == 32) {
+            its = __reduce_max_sync(~0u, its);
+        } else {
+#pragma unroll
+            for (int o = kLanes / 2; o; o /= 2) its = max(its, __shfl_xor_sync(~0u, its, o));
+        }
+        if (lane % kLanes == 0) atomicMax(&tops[t], its);
     }
-    const uint32_t most = __reduce_max_sync(~0u, __float_as_uint(top));
     const bool any = __any_sync(~0u, odd);
-    if (lane == 0) {
-        atomicMax(&tops, most);
-        if (any) atomicOr(&bad, 1);
-    }
+    if (lane == 0 && any) atomicOr(&bad, 1);
     __syncthreads();
+    // The tile's largest and its tokens' least (tokens of zeros have no say).
+    const uint32_t one = tops[lane], two = TK > 32 ? tops[lane + TK - 32] : one;
+    const uint32_t most = __reduce_max_sync(~0u, max(one, two));
+    const uint32_t least = __reduce_min_sync(~0u, min(one ? one : ~0u, two ? two : ~0u));
+    const bool apart = most && (int)(most >> 23) - (int)(least >> 23) > kApart;
     // (values' least: their factor is 2^-15 smaller)
-    const int ex = exponent_of(__uint_as_float(tops), values ? -96 : -111);
-    const float up = __uint_as_float((uint32_t)(127 + 15 - ex) << 23);
+    const int from = values ? -96 : -111;
+    const int ex = exponent_of(__uint_as_float(most), from);
     uint8_t *to = a.tiles + ((int64_t)slot * a.kv_heads + head) * (2 * kPart) + (values ? kPart : 0);
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
         const int at = tid + i * kSplitThreads, t = at / (D / 4), e = at % (D / 4);
+        const int its = apart ? exponent_of(__uint_as_float(tops[t]), from) : ex;
+        const float up = __uint_as_float((uint32_t)(127 + 15 - its) << 23);
         uint2 hi, lo;
         split2(v[i].x * up, v[i].y * up, hi.x, lo.x);
         split2(v[i].z * up, v[i].w * up, hi.y, lo.y);
@@ -380,8 +407,18 @@ __global__ void __launch_bounds__(kSplitThreads)
     }
     TileInfo *info = a.info + (int64_t)slot * a.kv_heads + head;
     if (tid == 0) {
-        if (values) info->vf = __uint_as_float((uint32_t)(127 + ex - 30) << 23), info->bad = bad;
-        else info->ek = ex - 15;
+        if (values) {
+            info->vf = __uint_as_float((uint32_t)(127 + ex - 30) << 23);
+            info->vstate = (bad ? kSomeNotFinite : 0) | (apart ? kValuesApart : 0);
+        } else {
+            info->ek = ex - 15, info->kstate = apart ? kKeysApart : 0;
+        }
+    }
+    if (apart && tid < TK) {
+        const int its = exponent_of(__uint_as_float(tops[tid]), from);
+        TilePowers *powers = a.powers + (int64_t)slot * a.kv_heads + head;
+        if (values) powers->v[tid] = (int16_t)its;
+        else powers->k[tid] = (int16_t)(its - 15);
     }
 }
 
@@ -412,7 +449,7 @@ struct Rows {
     static constexpr int OC = D * 4 / OW;                    // columns of each
     static constexpr int kFirst = kTwo ? 4 + OW : kSoft;     // S, copies, O, one that cleans
     static constexpr int kThreads = 32 * (kFirst + 4);
-    static constexpr int kControl = 5120, kQLo = kLoShared ? kRows * D * 2 : 0;
+    static constexpr int kControl = 7168, kQLo = kLoShared ? kRows * D * 2 : 0;
     static constexpr int kRing = kControl + kQLo;
     static constexpr int kRoom = (227 * 1024 - 1024 - kRing) / kPart;
     static constexpr int kSlots = kRoom < 8 ? kRoom : 8;
@@ -445,9 +482,10 @@ struct RowsShared {
     // f32, of tile i & 3: the factor of what was summed before; 16 bits, of tile
     // i & 1: the rows' references after it
     float corr[4][kRows];
+    float vf[4][kRows];  // f32: the row's factor of O of that tile, where its values are apart
     float m[2][kRows], l[2][kRows];  // of each softmax warps' tiles
 };
-static_assert(sizeof(RowsShared) <= 5120, "layout");
+static_assert(sizeof(RowsShared) <= 7168, "layout");
 
 template <class T, int D>
 __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
@@ -540,6 +578,20 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
     if constexpr (kTwo) kq::wait_prerequisites();  // the tiles
     int copied = 0;  // copies that this warp has begun (16 bits: of keys, or of values)
 
+    // f32: tile t's state, and whether some tile of the CTA's has tokens apart.
+    // (The loops over tiles are there twice: with what such tiles take in the
+    // only one, 4097 tokens of 32 / 2 heads of 128 took 326 us on the GPU against
+    // 294 without and 300 now.)
+    auto state_of = [&](int t) {
+        const TileInfo *p = &a.info[slot0 + (int64_t)t * a.kv_heads];
+        return __ldg(&p->kstate) | __ldg(&p->vstate);
+    };
+    auto some_apart = [&]() {
+        int all = 0;
+        for (int t = t0 + lane; t < t1; t += 32) all |= state_of(t);
+        return __any_sync(~0u, all & (kKeysApart | kValuesApart)) != 0;
+    };
+
     // The rows' results, by warp n of those that write: its columns of O.
     auto write_rows = [&](float (&O)[M::OC], bool bad, int n) {
         const int r = 32 * (n & 3) + lane, c0 = n / 4 * M::OC;
@@ -562,7 +614,7 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
         if (bad && on) {
             // values that are not finite, of the tiles that left them out
             for (int t = kTwo ? t0 : t1 - edges; t < t1; ++t) {
-                if (kTwo && !a.info[slot0 + (int64_t)t * a.kv_heads].bad) continue;
+                if (kTwo && !(a.info[slot0 + (int64_t)t * a.kv_heads].vstate & kSomeNotFinite)) continue;
                 for (int j = t * TK; j < min((t + 1) * TK, limit + 1); ++j) {
                     const T *v = static_cast<const T *>(a.v) + (int64_t)(it.kfirst + j) * a.v_stride +
                                  (int64_t)it.head * D + c0;
@@ -628,6 +680,7 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
         int tok, hq;
         const bool on = it.row(a.hb, r, tok, hq);
         const uint32_t mine = tmem + ((uint32_t)(32 * (w & 3)) << 16);
+        const bool apart = kTwo && some_apart();  // (while the queries come)
         int ex = 0;
         {   // ---- the row's query into tensor memory
             const T *x = static_cast<const T *>(a.q) + (int64_t)(it.first + tok) * a.q_stride +
@@ -726,12 +779,15 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
             if (count) ek = __ldg(&info[(int64_t)(t1 - 1) * a.kv_heads].ek);
         }
         float m = -INFINITY, l = 0.f;
-        for (int i = g; i < count; i += M::SG) {
+        auto step = [&](int i, auto far) {
+            constexpr bool kFar = decltype(far)::value;
             const int t = t1 - 1 - i;
             float f = 1.f;
+            int state = 0;
             if constexpr (kTwo) {
                 f = __uint_as_float((uint32_t)(127 + min(max(ex - 15 + ek, -126), 127)) << 23);
                 if (i + 1 < count) ek = __ldg(&info[(int64_t)(t - 1) * a.kv_heads].ek);
+                if (kFar) state = state_of(t);
             }
             float before = -INFINITY;  // the reference after the tile before
             if constexpr (!kTwo) {
@@ -752,6 +808,14 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
             tc_before();
             __syncwarp();
             if (lane == 0) kq::mbar_arrive(bar(cm.sfree[i % SB]));
+            if (kFar && (state & kKeysApart)) {  // each key's own power of two
+                const int16_t *its = a.powers[slot0 + (int64_t)t * a.kv_heads].k;
+#pragma unroll
+                for (int k = 0; k < TK; ++k)
+                    d[k] = __float_as_uint(__uint_as_float(d[k]) *
+                                           __uint_as_float((uint32_t)(127 + min(max(ex - 15 + its[k], -126), 127)) << 23));
+                f = 1.f;
+            }
             const int seen = i < edges ? limit + 1 - t * TK : TK;  // columns that the row attends
             if (i < edges) {
 #pragma unroll
@@ -814,11 +878,29 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
                 d[k] = __float_as_uint(p);
             }
             l = fmaf(l, corr, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+            if (kFar && (state & kValuesApart)) {
+                // each value's own power of two, by the exponents' bits (what is
+                // not a number stays one)
+                const int16_t *its = a.powers[slot0 + (int64_t)t * a.kv_heads].v;
+                auto field = [](uint32_t x) { return (int)(x >> 23); };
+                int most = -1000;
+#pragma unroll
+                for (int k = 0; k < TK; ++k)
+                    if (d[k] != 0 && field(d[k]) < 255) most = max(most, field(d[k]) + its[k]);
+                const int ev = max(most - (127 + 14), -96);
+                f = __uint_as_float((uint32_t)(127 + ev - 30) << 23);
+#pragma unroll
+                for (int k = 0; k < TK; ++k) {
+                    const int by = its[k] - ev;
+                    if (field(d[k]) < 255) d[k] = d[k] != 0 && field(d[k]) + by > 0 ? d[k] + ((uint32_t)by << 23) : 0u;
+                }
+            }
             if (kTwo && i >= PB) {  // the O before has read P's place
                 wait(cm.pfree[i % PB], i / PB - 1);
                 tc_after();
             }
             if constexpr (kTwo) cm.corr[i & 3][r] = corr;
+            if (kFar && (state & kValuesApart)) cm.vf[i & 3][r] = f;
 #pragma unroll
             for (int k = 0; k < TK / 32; ++k) {
                 uint32_t hi[16], lo[16];
@@ -838,6 +920,11 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
                 kq::mbar_arrive(bar(cm.pready[i % PB]));
                 if constexpr (kTwo) kq::mbar_arrive(bar(cm.cready[i & 3]));
             }
+        };
+        if (apart) {
+            for (int i = g; i < count; i += M::SG) step(i, std::bool_constant<kTwo>());
+        } else {
+            for (int i = g; i < count; i += M::SG) step(i, std::false_type());
         }
         cm.m[g][r] = m;
         cm.l[g][r] = l;
@@ -863,6 +950,7 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
     } else if (kTwo && w < M::kFirst) {
         // ------------------------------------------- the sums of O, and out
         if constexpr (kTwo && D == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+        const bool apart = kTwo && some_apart();
         __syncthreads();
         const int r = 32 * (w & 3) + lane, c0 = (w - 4) / 4 * M::OC;
         const uint32_t mine = tmem + ((uint32_t)(32 * (w & 3)) << 16) + M::kO + c0;
@@ -872,23 +960,24 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
 #pragma unroll
         for (int k = 0; k < M::OC; ++k) O[k] = 0.f;
         bool bad = false;
-        const TileInfo *info = kTwo ? a.info + slot0 : nullptr;
-        float vf = 1.f;
-        int vbad = 0;
-        auto look = [&](int i) {
-            if constexpr (kTwo) {
+        auto sums = [&](auto far) {
+            constexpr bool kFar = decltype(far)::value;
+            const TileInfo *info = a.info + slot0;
+            float vf = 1.f;
+            int state = 0;
+            auto look = [&](int i) {
                 const TileInfo *p = info + (int64_t)(t1 - 1 - i) * a.kv_heads;
-                vf = __ldg(&p->vf), vbad = __ldg(&p->bad);
-            }
-        };
-        if (count) look(0);
-        if constexpr (kTwo) {
+                vf = __ldg(&p->vf), state = __ldg(&p->vstate);
+            };
+            if (count) look(0);
             for (int i = 0; i < count; ++i) {
-                const float f = vf;
-                bad |= vbad != 0;
+                float f = vf;
+                const bool own = kFar && (state & kValuesApart);
+                bad |= (state & kSomeNotFinite) != 0;
                 if (i + 1 < count) look(i + 1);
                 wait(cm.cready[i & 3], i >> 2);
                 const float corr = cm.corr[i & 3][r];
+                if (own) f = cm.vf[i & 3][r];
                 wait(cm.odone[i % OB], i / OB);
                 tc_after();
                 const uint32_t at = mine + (i % OB) * D;
@@ -905,6 +994,10 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
                 __syncwarp();
                 if (lane == 0) kq::mbar_arrive(bar(cm.ofree[i % OB]));
             }
+        };
+        if constexpr (kTwo) {
+            if (apart) sums(std::true_type());
+            else sums(std::false_type());
         }
         write_rows(O, bad, w - 4);
     } else {
@@ -1103,15 +1196,16 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
 // Slots of an f32 call's tiles.
 inline int64_t f32_slots(const PromptArgs &a, int d) { return a.nkeys / f32_tile_tokens(d) + a.nseq; }
 
-// Workspace: tiles, their powers of two, partial results; in all.
+// Workspace: tiles, their powers of two, their tokens', partial results; in all.
 struct Space {
-    int64_t info, part, bytes;
+    int64_t info, powers, part, bytes;
 };
 inline Space space_of(const PromptArgs &a, int blocks, bool f32, int d) {
     Space s{};
     const int64_t tiles = f32 ? f32_slots(a, d) * a.kv_heads : 0;
     s.info = tiles * (f32_tile_tokens(d) * d * 8);
-    s.part = (s.info + tiles * (int64_t)sizeof(TileInfo) + 255) / 256 * 256;
+    s.powers = s.info + tiles * (int64_t)sizeof(TileInfo);
+    s.part = (s.powers + tiles * (int64_t)sizeof(TilePowers) + 255) / 256 * 256;
     s.bytes = s.part + (a.splits > 1 ? 4ll * a.items * a.splits * blocks * kRows * (d + 2) : 0);
     s.bytes = (s.bytes + 255) / 256 * 256;
     return s;
