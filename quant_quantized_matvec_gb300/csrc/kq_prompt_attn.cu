@@ -22,7 +22,8 @@ __global__ void __launch_bounds__(kJoinThreads)
     __shared__ Item item;
     __shared__ float tile[kJoinRows][D + 1];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    if (w == 0) find_item(a, blockIdx.x, item, lane);
+    Place from;
+    if (w == 0) find_item(a, blockIdx.x, item, lane, from);
     kq::wait_prerequisites();
     __syncthreads();
     const Item it = item;

@@ -198,12 +198,13 @@ __device__ __forceinline__ void walk(const PromptArgs &a, int lane, Place &p, F 
     }
 }
 
-// Item `i` of the call into shared memory, by a warp; found = 0 past the last.
-// p: where the walk for a lower item ended, or the beginning.
+// Item `i` of the call into shared memory, by a warp; false (and found = 0) past
+// the last.  p: where the walk for any other item ended, or the beginning.
 template <int N>
-__device__ __forceinline__ void find_item(const PromptArgs &a, int i, Item &it, int lane, Place &p) {
+__device__ __forceinline__ bool find_item(const PromptArgs &a, int i, Item &it, int lane, Place &p) {
     const int across = a.kv_heads * a.hblocks;
     const int blk = i / across, h = i - blk * across;
+    if (blk < p.blocks) p = Place();  // (the walk is past it)
     if (lane == 0) it.found = 0;
     __syncwarp();
     walk<N>(a, lane, p, [&](const Some<N> &q) {
@@ -243,13 +244,22 @@ __device__ __forceinline__ void find_item(const PromptArgs &a, int i, Item &it, 
         return true;
     });
     __syncwarp();
+    return it.found != 0;
 }
-__device__ __forceinline__ void find_item(const PromptArgs &a, int i, Item &it, int lane) {
+__device__ __forceinline__ bool find_item(const PromptArgs &a, int i, Item &it, int lane, Place &p) {
     // (From the beginning, four sequences a lane where there are many: 4096
     // prompts of 8 tokens, 16 / 4 heads of 256, 5.6 ms with one, 2.6 with four.)
-    Place p;
-    if (a.nseq > 32) find_item<4>(a, i, it, lane, p);
-    else find_item<1>(a, i, it, lane, p);
+    return a.nseq > 32 ? find_item<4>(a, i, it, lane, p) : find_item<1>(a, i, it, lane, p);
+}
+// The first number of `given` (a CTA's; -1: no more) that find(number) finds
+// something for; -1 if there is none.  Grids go by the most items that there may
+// be, and numbers past the last need no CTA.  But no order of the numbers is
+// promised: one after those may have an item.
+template <class G, class F>
+__device__ __forceinline__ int first_found(G &&given, F &&find) {
+    int u = given();
+    while (u >= 0 && !find(u)) u = given();
+    return u;
 }
 
 // 32-bit words of two 16-bit values of which one is not finite.
@@ -479,6 +489,7 @@ struct RowsShared {
         vraw[4], vclean[4], handed[8], ldone, given, qfull, drain[2];
     uint32_t tmem;
     int dead, bad;
+    int unit;  // the number of the CTA whose work this is, where it is not its own
     // f32, of tile i & 3: the factor of what was summed before; 16 bits, of tile
     // i & 1: the rows' references after it
     float corr[4][kRows];
@@ -501,9 +512,10 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     auto bar = [&](const uint64_t &b) { return kq::smem_addr(&b); };
 
-    const int rank = blockIdx.x % a.splits;
+    int unit = blockIdx.x;
+    Place place;
     if (w == 0) {
-        find_item(a, blockIdx.x / a.splits, cm.item, lane);
+        find_item(a, unit / a.splits, cm.item, lane, place);
     } else if (w == 1) {  // a lane a barrier, or a few
         if (lane < 8) {
             kq::mbar_init(bar(cm.full[lane]), 1), kq::mbar_init(bar(cm.empty[lane]), 1);
@@ -536,24 +548,43 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
     tc_before();
     __syncthreads();
     tc_after();
-    const Item it = cm.item;
-    if (!it.found) {
-        // Past the last item (grids go by the most that there may be): the CTAs
-        // after this one, which have none either, need not begin.  (4096 prompts
-        // of 8 tokens, f32: 2.4 ms if they do.)
-        for (int n = 0; tid == 0; ++n) {
-            kq::mbar_expect_tx(bar(cm.given), 16);
-            ask_for_cta(kq::smem_addr(&cm.answer), bar(cm.given));
-            if (!kq::mbar_wait(bar(cm.given), n & 1, kq::kWaitLimitNs) ||
-                cta_given(kq::smem_addr(&cm.answer)) < 0)
-                break;
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    if (!cm.item.found) {
+        // Past the last item: CTAs that have not begun and have none either need
+        // not begin.  (4096 prompts of 8 tokens, f32: 2.4 ms if they do.)
+        __syncthreads();  // (all have looked)
+        if (w == 0) {
+            int n = 0;
+            unit = first_found(
+                [&]() {
+                    int u = -1;
+                    if (lane == 0) {
+                        kq::mbar_expect_tx(bar(cm.given), 16);
+                        ask_for_cta(kq::smem_addr(&cm.answer), bar(cm.given));
+                        bool there = kq::mbar_wait(bar(cm.given), n & 1, kq::kWaitLimitNs);
+                        if (!there) {
+                            atomicOr(a.err, 1u);
+                            there = kq::mbar_wait(bar(cm.given), n & 1, kq::kWaitLimitNs);
+                        }
+                        if (there) u = cta_given(kq::smem_addr(&cm.answer));
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    }
+                    ++n;
+                    return __shfl_sync(~0u, u, 0);
+                },
+                [&](int u) { return find_item(a, u / a.splits, cm.item, lane, place); });
+            if (lane == 0) cm.unit = unit;
         }
-        if (w == M::kFirst)
-            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(cm.tmem));
-        if constexpr (kTwo) kq::wait_prerequisites();
-        return;
+        __syncthreads();
+        unit = cm.unit;
+        if (unit < 0) {
+            if (w == M::kFirst)
+                asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(cm.tmem));
+            if constexpr (kTwo) kq::wait_prerequisites();
+            return;
+        }
     }
+    const Item it = cm.item;
+    const int rank = unit % a.splits;
     const uint32_t tmem = cm.tmem;
 
     auto dead = [&]() { return *(volatile int *)&cm.dead != 0; };
@@ -629,7 +660,7 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
         const bool lost = __any_sync(~0u, dead());
         if (lost) l = quiet_nan();
         if (a.splits > 1) {
-            float *part = a.part + (int64_t)blockIdx.x * kRows * (D + 2);
+            float *part = a.part + (int64_t)unit * kRows * (D + 2);
             // by values, of 32 rows each: part[32 rows][D][32]
             float *to = part + (r - lane) * D + c0 * 32 + lane;
 #pragma unroll

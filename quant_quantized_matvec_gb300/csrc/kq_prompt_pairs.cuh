@@ -85,9 +85,8 @@ static_assert(sizeof(PairShared) <= 2048, "layout");
 
 // Unit `u` into shared memory, by one warp; false past the last.
 __device__ __forceinline__ bool find_unit(const PromptArgs &a, int u, int tile, Unit &g, int lane, Place &p) {
-    find_item<1>(a, u / a.splits, g.item, lane, p);
+    const bool found = find_item<1>(a, u / a.splits, g.item, lane, p);
     const Item &it = g.item;
-    const bool found = it.found != 0;
     if (found && lane == 0) {
         const int rank = u % a.splits, half = a.tok / 2;
         const int tiles = (it.keys() + tile - 1) / tile;
@@ -373,16 +372,27 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         if (w == kPairOther + 3) {
             // ----------------------------------------- the units, one ahead
             // A CTA begins with the unit of its number, and then takes over those
-            // of CTAs that have not begun, in their order: a sequence's longest
-            // first.  (Dealt out evenly beforehand, in rounds there and back:
+            // of CTAs that have not begun, as a rule in their order (which no
+            // result goes by): a sequence's longest first.  (Dealt out evenly beforehand, in rounds there and back:
             // 234 against 224 us for nine prompts of up to 2049 tokens.)
-            int u = blockIdx.x;
-            auto ask = [&]() {
+            int u = blockIdx.x, asks = 0;
+            bool lost = false;
+            auto given = [&]() {  // another CTA's number; -1: none, or (lost) not in time
                 if (lane == 0) {
                     kq::mbar_expect_tx(bar(cm.given), 16);
                     ask_for_cta(kq::smem_addr(&cm.answer), bar(cm.given));
                 }
                 __syncwarp();
+                wait(cm.given, asks++);
+                if (__any_sync(~0u, dead())) {
+                    if (lane == 0) cm.asked = asks;
+                    lost = true;
+                    return -1;
+                }
+                const int x = cta_given(kq::smem_addr(&cm.answer));
+                __syncwarp();
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                return x;
             };
             for (int k = 0;; ++k) {
                 const int slot = k % kUnits;
@@ -392,42 +402,25 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     break;
                 }
                 Unit &g = cm.unit[slot];
-                const bool found = k == 0 ? g.u >= 0 : u >= 0 && find_unit(a, u, TK, g, lane, place);
+                auto find = [&](int x) { return find_unit(a, x, TK, g, lane, place); };
+                if (u >= 0 && !(k == 0 ? g.u >= 0 : find(u))) {
+                    if (lane == 0) g.u = -1;
+                    u = first_found(given, find);
+                    if (lost) break;
+                }
                 if (lane == 0) {
-                    if (!found) g.u = -1;
+                    if (u < 0) g.u = -1;
                     *(volatile int *)&cm.bad[slot] = 0;
                     __threadfence_block();
                     kq::mbar_arrive(bar(cm.ufull[slot]));
                 }
                 __syncwarp();
-                if (!found) {
-                    // Units past the last (there are at most so many): their
-                    // CTAs need not begin.
-                    for (int n = k; u >= 0; ++n) {
-                        ask();
-                        wait(cm.given, n);
-                        if (__any_sync(~0u, dead())) {
-                            if (lane == 0) cm.asked = n + 1;
-                            break;
-                        }
-                        u = cta_given(kq::smem_addr(&cm.answer));
-                        __syncwarp();
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    }
-                    break;
-                }
+                if (u < 0) break;
                 // The next one is taken when the last few copies for this one are
                 // made: not before, as others may be free earlier.
                 wait(cm.begun, k);
-                ask();
-                wait(cm.given, k);
-                if (__any_sync(~0u, dead())) {
-                    if (lane == 0) cm.asked = k + 1;
-                    break;
-                }
-                u = cta_given(kq::smem_addr(&cm.answer));
-                __syncwarp();
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                u = given();
+                if (lost) break;
             }
         } else if (w == kPairOther + 2) {
             // --------------------------------------------- copies
