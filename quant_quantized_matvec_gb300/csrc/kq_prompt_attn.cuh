@@ -606,7 +606,9 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
     const int edges = min(max(t1 - max(whole, t0), 0), count);
     const int64_t slot0 = kTwo ? (int64_t)(it.kfirst / TK + it.seq) * a.kv_heads + it.head : 0;
 
-    if constexpr (kTwo) kq::wait_prerequisites();  // the tiles
+    // The tiles and their powers of two, which a kernel beside the beginning of this
+    // one writes: plain loads, not those of memory that nobody writes meanwhile.
+    if constexpr (kTwo) kq::wait_prerequisites();
     int copied = 0;  // copies that this warp has begun (16 bits: of keys, or of values)
 
     // f32: tile t's state, and whether some tile of the CTA's has tokens apart.
@@ -615,7 +617,7 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
     // 294 without and 300 now.)
     auto state_of = [&](int t) {
         const TileInfo *p = &a.info[slot0 + (int64_t)t * a.kv_heads];
-        return __ldg(&p->kstate) | __ldg(&p->vstate);
+        return p->kstate | p->vstate;
     };
     auto some_apart = [&]() {
         int all = 0;
@@ -807,7 +809,7 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
         int ek = 0;
         if constexpr (kTwo) {
             info = a.info + slot0;
-            if (count) ek = __ldg(&info[(int64_t)(t1 - 1) * a.kv_heads].ek);
+            if (count) ek = info[(int64_t)(t1 - 1) * a.kv_heads].ek;
         }
         float m = -INFINITY, l = 0.f;
         auto step = [&](int i, auto far) {
@@ -817,7 +819,7 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
             int state = 0;
             if constexpr (kTwo) {
                 f = __uint_as_float((uint32_t)(127 + min(max(ex - 15 + ek, -126), 127)) << 23);
-                if (i + 1 < count) ek = __ldg(&info[(int64_t)(t - 1) * a.kv_heads].ek);
+                if (i + 1 < count) ek = info[(int64_t)(t - 1) * a.kv_heads].ek;
                 if (kFar) state = state_of(t);
             }
             float before = -INFINITY;  // the reference after the tile before
@@ -998,7 +1000,7 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
             int state = 0;
             auto look = [&](int i) {
                 const TileInfo *p = info + (int64_t)(t1 - 1 - i) * a.kv_heads;
-                vf = __ldg(&p->vf), state = __ldg(&p->vstate);
+                vf = p->vf, state = p->vstate;
             };
             if (count) look(0);
             for (int i = 0; i < count; ++i) {
