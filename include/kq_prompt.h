@@ -100,14 +100,15 @@ kq_status kq_norm_rope(const kq_norm_part *parts, int n, int type, int out_type,
  *         small is KQ_ERR_LIMIT.
  *
  * q, k, v and out are 16-byte aligned, strides multiples of 16 bytes.  scale is
- * finite, of either sign.  Sums, maxima and corrections are f32.  16-bit types:
+ * finite, of either sign (16-bit types: below 2.35e38, so that its product with
+ * log2(e) is finite too; KQ_ERR_SHAPE).  Sums, maxima and corrections are f32.  16-bit types:
  * products are exact, probabilities are rounded to the type.  KQ_F32: queries,
  * keys, values and probabilities are held as two f16 terms (22 bits, after a
  * scaling by a power of two: of a query's row, and of a sequence's 64 or 32
  * keys or values, or of each of these where their largest values lie further
  * apart than 2^12; what is below 2^-27 of the largest value of its key, value
  * or query, or 2^-39 of a row's largest probability times value, is dropped),
- * so logits may be as large as f32 holds, as long as scale * q is finite too.
+ * so logits may be as large as 2e38, as long as scale * q is below that too.
  * However large a key or value is, rows that do not attend it, or whose
  * probability for it is small enough, keep the bits of what they attend.  A
  * row that attends a key with an infinity may be NaN where the formula has a

@@ -150,6 +150,8 @@ kq_status kq_prompt_attention(int type, int nseq, int64_t ntok, int64_t nkeys,
     if (bad_stride(q_stride, row, size) || bad_stride(k_stride, kv_row, size) ||
         bad_stride(v_stride, kv_row, size) || !std::isfinite(scale))
         return KQ_ERR_SHAPE;
+    // (16 bits: the scale's product with log2(e) is one number)
+    if (type != KQ_F32 && !std::isfinite(scale * 1.44269504f)) return KQ_ERR_SHAPE;
     if (ntok == 0) return KQ_OK;
     if (!start || !q || !out || (nkeys > 0 && (!k || !v))) return KQ_ERR_NULL;
     if (!aligned(start, 4) || !aligned(key_start, 4) || !aligned(q, 16) || !aligned(k, 16) ||

@@ -3,6 +3,7 @@
 #include "kq_prompt_pairs.cuh"
 
 #include <algorithm>
+#include <cmath>
 
 namespace kqp {
 
@@ -124,6 +125,9 @@ PromptArgs args_of(const PromptCall &c, int sms) {
     a.q_stride = c.q_stride, a.k_stride = c.k_stride, a.v_stride = c.v_stride;
     a.nseq = c.nseq, a.ntok = c.ntok, a.nkeys = c.nkeys;
     a.q_heads = c.q_heads, a.kv_heads = c.kv_heads, a.scale = c.scale;
+    int e = 0;
+    a.scale_m = (float)std::frexp(c.scale * 1.44269504088896340736, &e);
+    a.scale_e = e;
     divide(a, blocks_of(c.type, c.dim), tile_of(c.type, c.dim), sms);
     return a;
 }

@@ -112,6 +112,8 @@ struct PromptArgs {
     int32_t splits;
     int32_t items;    // items in all, at most
     float scale;      // with its sign
+    float scale_m;    // f32: scale times log2(e) = scale_m * 2^scale_e, |scale_m| in 0.5..1,
+    int32_t scale_e;  // or 0
     unsigned int *err;
     unsigned long long wait_ns;
     uint32_t suspend_ns;
@@ -722,7 +724,7 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
                 // (up to width 128 the row is read once)
                 constexpr int kHeld = D <= 128 ? D / 4 : 16;
                 const float4 *x4 = reinterpret_cast<const float4 *>(x);
-                const float sc = a.scale * kLog2E;
+                const float sc = a.scale_m;
                 float4 v[kHeld];
                 if constexpr (M::kQStaged) wait(cm.qfull, 0);
                 auto load = [&](int i0) {
@@ -749,6 +751,7 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
                 }
                 ex = exponent_of(top, -111);
                 const float up = __uint_as_float((uint32_t)(127 + 15 - ex) << 23);
+                ex += a.scale_e;
 #pragma unroll 1
                 for (int i0 = 0; i0 < D / 4; i0 += kHeld) {
                     if (kHeld < D / 4) load(i0);

@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const int block = w >> 2, r = 32 * (w & 3) + lane;
         const uint32_t mine = tmem + M::kBlock * block + ((uint32_t)(32 * (w & 3)) << 16);
         const uint32_t sa = mine + M::kS, pa = mine + M::kP, oa = mine + M::kO;
-        const float sc = fmaxf(fabsf(a.scale) * kLog2E, 1.2e-38f);  // (not 0: -infinity * 0)
+        const float sc = fmaxf(fabsf(a.scale) * kLog2E, 1.4e-45f);  // (not 0: -infinity * 0)
         const int half = a.tok / 2, t = r / a.hb, hq = r - t * a.hb;
         int turn = 0;  // tiles of all units
         for (int k = 0;; ++k) {
