@@ -83,10 +83,9 @@ kq_status kq_norm_rope(const kq_norm_part *parts, int n, int type, int out_type,
  * < n the first queries attend nothing, and their rows are zero.  key_start
  * NULL: start (no tokens before the prompt; nkeys must be ntok).
  *
- * Starts that are not within 0..ntok (0..nkeys) in rising order are cut to
- * what is.  (Starts that fall and rise again can give a token to two
- * sequences; what the call writes for it is then either's.)  Rows of no
- * sequence are left as they were.  NaN and infinities in keys and values that a
+ * A start counts as the largest so far, within 0..ntok (0..nkeys), so that
+ * sequences never overlap, whatever the starts are.  Rows of no sequence are
+ * left as they were.  NaN and infinities in keys and values that a
  * row does not attend do not reach it.
  *
  *   type  of q, k, v and out: KQ_F32, KQ_F16 or KQ_BF16
@@ -102,7 +101,8 @@ kq_status kq_norm_rope(const kq_norm_part *parts, int n, int type, int out_type,
  * q, k, v and out are 16-byte aligned, strides multiples of 16 bytes.  scale is
  * finite, of either sign (16-bit types: below 2.35e38, so that its product with
  * log2(e) is finite too; KQ_ERR_SHAPE).  Sums, maxima and corrections are f32.  16-bit types:
- * products are exact, probabilities are rounded to the type.  KQ_F32: queries,
+ * products are exact, probabilities are rounded to the type (the error is
+ * then 1.25 to 1.4 times that of the output's own rounding).  KQ_F32: queries,
  * keys, values and probabilities are held as two f16 terms (22 bits, after a
  * scaling by a power of two: of a query's row, and of a sequence's 64 or 32
  * keys or values, or of each of these where their largest values lie further

@@ -382,8 +382,10 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
 namespace {
 template <class T>
 cudaError_t launch(const ScoreArgs &a, cudaStream_t s) {
-    // CTAs of a row: up to 16, each with 4096 words or more, and about two an SM
-    // in all.
+    // CTAs of a row: up to 16, each with 4096 words or more, and two an SM in all.
+    // 1, 9, 38, 100, 200 rows of 202048 f32 logits, 5 alternatives: 8.5, 10.8, 20.4,
+    // 27.9, 40.2 us; one CTA a row 22.1, 23.4, 25.9, 27.2, 40.1; one an SM in all 8.6,
+    // 10.8, 18.6, 26.9, 40.3; four an SM 8.4, 10.8, 26.0, 28.1, 40.8.
     int ctas = 1;
     while (ctas < kScoreCluster && ctas * 4096 < a.vocab && 2 * ctas * a.n <= kScoreCtas) ctas *= 2;
     constexpr int V = 16 / sizeof(T);

@@ -98,7 +98,13 @@ void divide(PromptArgs &a, int blocks, int tile, int sms) {
     // The cut that ends first, in tiles: of the longest item, or of rounds of
     // mean ones, each with what a part costs beside its tiles (about 400 keys'
     // time to begin and to end, and as much again to write partial results and
-    // join them).
+    // join them: figures of 16 bits at width 128).  This number of parts, half and
+    // twice as many, on the GPU: 300 tokens behind 32001, 32 / 8 heads, f16 134, 141
+    // and 152 us, f32 481, 666 and 513; 16 / 4 heads of 256, bf16 142, 147 and 174,
+    // f32 591, 648 and 632; 64 tokens behind 4000, f16 23, 26 and 24.  One token
+    // behind 8000 would rather have half as many (bf16 of 256: 30 and 26).  Lengths
+    // count by their means: a long one among short ones is cut too little (300
+    // behind 32001 beside seven prompts of 16: 380 us).
     a.splits = 1;
     if (items >= 2 * (int64_t)sms) return;
     const double keys = (double)a.nkeys / a.nseq, mine = (double)a.ntok / a.nseq;

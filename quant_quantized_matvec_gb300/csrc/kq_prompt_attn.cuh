@@ -1,5 +1,6 @@
 // kq_prompt_attn.cuh -- attention of whole prompts (kq_prompt_attention): what
-// its kernels share, and the kernel that takes every type and width.
+// its kernels share, and the kernel of one block a CTA: f32 at every width, 16 bits
+// at width 256 (kq_prompt_pairs.cuh has the others).
 //
 //   out_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = 2^(s_ij - m_i),  j <= limit of i
 //
@@ -40,8 +41,8 @@
 // become f16 are held times 2^7 besides, as f16 has few bits below 2^-14.
 //
 // Bound by the products and what stands between two of them.  f32, 4097 tokens,
-// 32 / 2 heads of 128: 317 us, 434 TFLOP/s of the formula and three times that of
-// products; the tensor core is at work 62% of the time, a tile takes 1950 to 2000
+// 32 / 2 heads of 128: 315 us, 437 TFLOP/s of the formula and three times that of
+// products; the tensor core is at work 60% of the time, a tile takes about 2000
 // clocks for 1536 of products.  bf16 at width 256, three prompts of up to 3001
 // tokens behind 500, 16 / 4 heads: 239 us, 1014 TFLOP/s; a tile takes 1600 clocks
 // for 1024 of products: S waits 340 for the one before to be taken, and then runs
@@ -249,8 +250,8 @@ __device__ __forceinline__ bool find_item(const PromptArgs &a, int i, Item &it, 
     return it.found != 0;
 }
 __device__ __forceinline__ bool find_item(const PromptArgs &a, int i, Item &it, int lane, Place &p) {
-    // (From the beginning, four sequences a lane where there are many: 4096
-    // prompts of 8 tokens, 16 / 4 heads of 256, 5.6 ms with one, 2.6 with four.)
+    // (Four sequences a lane where there are many: 4096 prompts of 8 tokens, 16 / 4
+    // heads of 256, f32, 6.0 ms with one, 3.6 with four.)
     return a.nseq > 32 ? find_item<4>(a, i, it, lane, p) : find_item<1>(a, i, it, lane, p);
 }
 // The first number of `given` (a CTA's; -1: no more) that find(number) finds
@@ -321,7 +322,7 @@ constexpr int kSplitThreads = 256;
 
 // One CTA per slot, head, and keys or values: 64 (32) tokens of a sequence into
 // hi and lo tiles.  A sequence's slots begin at first key / tokens + its number.
-// 4097 tokens of 2 heads of 128: 6.5 us (latency: a walk, one round of loads, one
+// 4097 tokens of 2 heads of 128: 8 us (latency: a walk, one round of loads, one
 // of stores).
 template <int D>
 __global__ void __launch_bounds__(kSplitThreads)
@@ -552,7 +553,8 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
     tc_after();
     if (!cm.item.found) {
         // Past the last item: CTAs that have not begun and have none either need
-        // not begin.  (4096 prompts of 8 tokens, f32: 2.4 ms if they do.)
+        // not begin.  (4096 prompts of 8 tokens, 16 / 4 heads of 256, f32: 4.0 ms if
+        // they do, 3.6 so.)
         __syncthreads();  // (all have looked)
         if (w == 0) {
             int n = 0;
@@ -616,7 +618,7 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
     // f32: tile t's state, and whether some tile of the CTA's has tokens apart.
     // (The loops over tiles are there twice: with what such tiles take in the
     // only one, 4097 tokens of 32 / 2 heads of 128 took 326 us on the GPU against
-    // 294 without and 300 now.)
+    // 294 without and 300 so.)
     auto state_of = [&](int t) {
         const TileInfo *p = &a.info[slot0 + (int64_t)t * a.kv_heads];
         return p->kstate | p->vstate;

@@ -10,7 +10,8 @@ shapes, devices) and in the library (ranges, alignment, overlaps, memory).
     logp, entropy, top_logp, top_tokens = kq.token_logprobs(logits, tokens, top=5)
 
 A prompt that continues a cached sequence attends the sequence's keys and
-values, read back in order (kv_read with ctx 0), with their own starts:
+values, read back in order (kv_read with ctx 0, which gives float32: cast them
+for 16-bit queries), with their own starts:
 
     y = kq.prompt_attention(q, k_all, v_all, start, key_start)
 """
