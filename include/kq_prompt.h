@@ -110,7 +110,9 @@ kq_status kq_norm_rope(const kq_norm_part *parts, int n, int type, int out_type,
  * or query, or 2^-39 of a row's largest probability times value, is dropped),
  * so logits may be as large as 2e38, as long as scale * q is below that too.
  * However large a key or value is, rows that do not attend it, or whose
- * probability for it is small enough, keep the bits of what they attend.  A
+ * probability for it is small enough, are as exact as without it.  A row is
+ * divided by its probabilities' sum at the end, so a value's size times the
+ * number of keys (bf16: and 2^8) has to be within f32.  A
  * row that attends a key with an infinity may be NaN where the formula has a
  * weight of zero, and so may one that attends an infinite value of a 16-bit
  * type where its probability is too small for the type.

@@ -90,7 +90,7 @@ struct TileInfo {
 };
 constexpr int kKeysApart = 1, kValuesApart = 2, kSomeNotFinite = 4;
 // Each token's, where they are apart: keys = stored * 2^k, values * 2^15 = stored * 2^v.
-struct TilePowers {
+struct alignas(16) TilePowers {
     int16_t k[64], v[64];
 };
 
@@ -817,6 +817,16 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
             if (count) ek = info[(int64_t)(t1 - 1) * a.kv_heads].ek;
         }
         float m = -INFINITY, l = 0.f;
+        // body(k, its power) for a tile's tokens, eight powers a load
+        auto each_power = [&](const int16_t *powers, auto &&body) {
+#pragma unroll
+            for (int k = 0; k < TK; k += 8) {
+                const int4 x = *reinterpret_cast<const int4 *>(powers + k);
+                const int w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) body(k + 2 * j, (int)(int16_t)w[j]), body(k + 2 * j + 1, w[j] >> 16);
+            }
+        };
         auto step = [&](int i, auto far) {
             constexpr bool kFar = decltype(far)::value;
             const int t = t1 - 1 - i;
@@ -847,11 +857,10 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
             __syncwarp();
             if (lane == 0) kq::mbar_arrive(bar(cm.sfree[i % SB]));
             if (kFar && (state & kKeysApart)) {  // each key's own power of two
-                const int16_t *its = a.powers[slot0 + (int64_t)t * a.kv_heads].k;
-#pragma unroll
-                for (int k = 0; k < TK; ++k)
+                each_power(a.powers[slot0 + (int64_t)t * a.kv_heads].k, [&](int k, int its) {
                     d[k] = __float_as_uint(__uint_as_float(d[k]) *
-                                           __uint_as_float((uint32_t)(127 + min(max(ex - 15 + its[k], -126), 127)) << 23));
+                                           __uint_as_float((uint32_t)(127 + min(max(ex - 15 + its, -126), 127)) << 23));
+                });
                 f = 1.f;
             }
             const int seen = i < edges ? limit + 1 - t * TK : TK;  // columns that the row attends
@@ -919,19 +928,18 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
             if (kFar && (state & kValuesApart)) {
                 // each value's own power of two, by the exponents' bits (what is
                 // not a number stays one)
-                const int16_t *its = a.powers[slot0 + (int64_t)t * a.kv_heads].v;
+                const int16_t *powers = a.powers[slot0 + (int64_t)t * a.kv_heads].v;
                 auto field = [](uint32_t x) { return (int)(x >> 23); };
                 int most = -1000;
-#pragma unroll
-                for (int k = 0; k < TK; ++k)
-                    if (d[k] != 0 && field(d[k]) < 255) most = max(most, field(d[k]) + its[k]);
+                each_power(powers, [&](int k, int its) {
+                    if (d[k] != 0 && field(d[k]) < 255) most = max(most, field(d[k]) + its);
+                });
                 const int ev = max(most - (127 + 14), -96);
                 f = __uint_as_float((uint32_t)(127 + ev - 30) << 23);
-#pragma unroll
-                for (int k = 0; k < TK; ++k) {
-                    const int by = its[k] - ev;
+                each_power(powers, [&](int k, int its) {
+                    const int by = its - ev;
                     if (field(d[k]) < 255) d[k] = d[k] != 0 && field(d[k]) + by > 0 ? d[k] + ((uint32_t)by << 23) : 0u;
-                }
+                });
             }
             if (kTwo && i >= PB) {  // the O before has read P's place
                 wait(cm.pfree[i % PB], i / PB - 1);
