@@ -42,7 +42,7 @@
 //
 // Bound by the products and what stands between two of them.  f32, 4097 tokens,
 // 32 / 2 heads of 128: 315 us, 437 TFLOP/s of the formula and three times that of
-// products; the tensor core is at work 60% of the time, a tile takes about 2000
+// products; the tensor core is at work 61% of the time, a tile takes about 2000
 // clocks for 1536 of products.  bf16 at width 256, three prompts of up to 3001
 // tokens behind 500, 16 / 4 heads: 239 us, 1014 TFLOP/s; a tile takes 1600 clocks
 // for 1024 of products: S waits 340 for the one before to be taken, and then runs
@@ -618,7 +618,7 @@ __global__ void __launch_bounds__(Rows<T, D>::kThreads, 1)
     // f32: tile t's state, and whether some tile of the CTA's has tokens apart.
     // (The loops over tiles are there twice: with what such tiles take in the
     // only one, 4097 tokens of 32 / 2 heads of 128 took 326 us on the GPU against
-    // 294 without and 300 so.)
+    // 294 without and 301 so.)
     auto state_of = [&](int t) {
         const TileInfo *p = &a.info[slot0 + (int64_t)t * a.kv_heads];
         return p->kstate | p->vstate;
